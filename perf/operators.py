@@ -218,7 +218,7 @@ def _prepare_own(st):
     st["handle"] = _Handle(pw, pw.pw_attn_desc(
         L=1, n_heads=c["Hq"], n_kv_heads=c["Hkv"], head_dim=c["D"],
         dtype=pw.PW_BF16 if c["dtype"] == "bf16" else pw.PW_FP16, n_blocks=st["n_blocks"], block_tokens=c["bt"],
-        max_requests=c["R"], max_tokens=st["N"], n_plans=1, device=0))
+        max_requests=c["R"], max_tokens=st["N"], max_shared_tokens=st["N"] if c["prefix"] else 0, n_plans=1, device=0))
     st["step"] = pw.pw_make_step(st["ctx_len"], st["new_len"], st["table"], st["q_start"], st["kv_len"], st["slot"],
                                  st["pos"], max_new=st["max_new"], groups=st.get("groups"),
                                  shared_len=st.get("shared_len"))
