@@ -20,6 +20,7 @@ PW_FLAG_POISON = 1
 PW_ACCUMULATE = 1
 PW_PRENORM = 2
 PW_PAGE_GPU, PW_PAGE_CPU, PW_PAGE_TO_CPU, PW_PAGE_TO_GPU = range(4)
+PW_BF16, PW_FP16 = range(2)
 STATUS_NAMES = {0: "PW_OK", 1: "PW_ERR_INVALID", 2: "PW_ERR_CUDA", 3: "PW_ERR_OOM",
                 4: "PW_ERR_STATE", 5: "PW_ERR_TIMEOUT", 6: "PW_ERR_BUSY",
                 7: "PW_ERR_RANGE"}
@@ -86,8 +87,22 @@ class pw_plan_problem(C.Structure):
                 ("layer", C.c_void_p), ("expert", C.c_void_p), ("M", C.c_void_p)]
 
 
+class pw_attn_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("L", "n_heads", "n_kv_heads", "head_dim", "dtype", "n_blocks", "block_tokens",
+                                       "max_requests", "max_tokens", "max_shared_tokens", "n_plans", "device")]
+
+
+class pw_kv_step(C.Structure):
+    _fields_ = [("R", C.c_int), ("n_tokens", C.c_int), ("max_new", C.c_int), ("table_rows", C.c_int),
+                ("table_stride", C.c_int), ("ctx_len", C.c_void_p), ("new_len", C.c_void_p), ("rows", C.c_void_p),
+                ("table", C.c_void_p), ("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("slot", C.c_void_p),
+                ("pos", C.c_void_p), ("n_groups", C.c_int), ("group_start", C.c_void_p), ("shared_len", C.c_void_p)]
+
+
 _P = C.c_void_p
 _I = C.c_int
+_L = C.c_int64
+_F = C.c_float
 _SIGS = {
     "pw_create": [C.POINTER(pw_desc), C.POINTER(_P)],
     "pw_destroy": [_P],
@@ -128,6 +143,14 @@ _SIGS = {
     "pw_kv_request": [_P, C.c_int64, C.POINTER(C.c_int64), C.POINTER(C.c_int64)],
     "pw_kv_blocks": [_P, C.c_int64, _P, C.c_int64, C.POINTER(C.c_int64)],
     "pw_kv_get_stats": [_P, C.POINTER(pw_kv_stats)],
+    "pw_attn_create": [C.POINTER(pw_attn_desc), C.POINTER(C.c_void_p)],
+    "pw_attn_destroy": [_P],
+    "pw_attn_bind": [_P, _I, _P, _P, _L, _L, _L],
+    "pw_kv_map": [_P, _P, _P, _I, _P],
+    "pw_attn_plan": [_P, _I, _P, _I, _P, _P, _P],
+    "pw_attn_append": [_P, _I, _P, _P, _L, _L, _P, _L, _L, _P],
+    "pw_attn_forward": [_P, _I, _I, _P, _L, _L, _P, _L, _L, _P, _F, _F, _P, _P],
+    "pw_attn_check": [_P, _P],
     "pw_set_profiling": [_P, _I],
     "pw_set_gemv_tokens": [_P, _I],
     "pw_profile_read": [_P, _I, _P],
@@ -152,7 +175,7 @@ def lib():
         for name, args in _SIGS.items():
             f = getattr(L, name)
             f.argtypes = args
-            f.restype = None if name in ("pw_destroy", "pw_kv_destroy") else (C.c_char_p if name in ("pw_last_error", "pw_version") else C.c_int)
+            f.restype = None if name in ("pw_destroy", "pw_kv_destroy", "pw_attn_destroy") else (C.c_char_p if name in ("pw_last_error", "pw_version") else C.c_int)
         _lib = L
     return _lib
 
@@ -503,3 +526,71 @@ def pw_kv_get_stats(kv) -> dict:
     st = pw_kv_stats()
     _check(lib().pw_kv_get_stats(kv, C.byref(st)))
     return {name: getattr(st, name) for name, _ in pw_kv_stats._fields_}
+
+
+# ---------------------------------------------------------------- paged attention
+def pw_attn_create(desc: pw_attn_desc):
+    """An attention handle (pass it to the pw_attn_* calls and pw_kv_map)."""
+    h = C.c_void_p()
+    _check(lib().pw_attn_create(C.byref(desc), C.byref(h)))
+    return h.value
+
+
+def pw_attn_destroy(attn):
+    lib().pw_attn_destroy(attn)
+
+
+def _rows(t):
+    """Address and the strides of [rows][heads][head_dim] (unit last stride)."""
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return t.data_ptr(), a, b
+
+
+def pw_attn_bind(attn, layer, k_cache, v_cache):
+    """Caches as tensors [n_blocks][block_tokens][n_kv_heads][head_dim], views included, of the
+    same strides and a unit last one."""
+    if k_cache.stride() != v_cache.stride() or k_cache.shape != v_cache.shape or k_cache.stride(3) != 1:
+        raise ValueError("the caches must have one shape, the same strides and a contiguous last dimension")
+    _check(lib().pw_attn_bind(attn, layer, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3]))
+
+
+def pw_make_step(ctx_len, new_len, table, q_start, kv_len, slot, pos, max_new, rows=None, groups=None, shared_len=None):
+    """A pw_kv_step over device tensors, which it keeps alive: lengths int32 [R], table int32
+    [rows][blocks], q_start int32 [R + 1], kv_len int32 [R], slot int64 and pos int32 [n_tokens];
+    groups int32 [n_groups + 1] and shared_len int32 [n_groups] for shared prefixes."""
+    s = pw_kv_step(R=ctx_len.numel(), n_tokens=pos.numel(), max_new=int(max_new), table_rows=table.shape[0],
+                   table_stride=table.shape[1], ctx_len=_ptr(ctx_len), new_len=_ptr(new_len), rows=_ptr(rows),
+                   table=_ptr(table), q_start=_ptr(q_start), kv_len=_ptr(kv_len), slot=_ptr(slot), pos=_ptr(pos),
+                   n_groups=0 if groups is None else groups.numel() - 1, group_start=_ptr(groups),
+                   shared_len=_ptr(shared_len))
+    s.refs = (ctx_len, new_len, table, q_start, kv_len, slot, pos, rows, groups, shared_len)
+    return s
+
+
+def pw_kv_map(attn, step, new_ids, stream=None):
+    _check(lib().pw_kv_map(attn, C.addressof(step), _ptr(new_ids), 0 if new_ids is None else new_ids.numel(),
+                           _stream(stream)))
+
+
+def pw_attn_plan(attn, plan, step, window=0, doc_start=None, bidir_len=None, stream=None):
+    _check(lib().pw_attn_plan(attn, plan, C.addressof(step), window, _ptr(doc_start), _ptr(bidir_len),
+                              _stream(stream)))
+
+
+def pw_attn_append(attn, layer, step, k, v, stream=None):
+    """k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last one."""
+    _check(lib().pw_attn_append(attn, layer, C.addressof(step), *_rows(k), *_rows(v), _stream(stream)))
+
+
+def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, slopes=None, stream=None):
+    """q and o: [n_tokens][n_heads][head_dim], any strides with a unit last one; scale defaults to
+    1 / sqrt(head_dim)."""
+    _check(lib().pw_attn_forward(attn, layer, plan, *_rows(q), *_rows(o), _ptr(lse),
+                                 q.shape[2] ** -0.5 if scale is None else scale, softcap, _ptr(slopes),
+                                 _stream(stream)))
+
+
+def pw_attn_check(attn, stream=None):
+    _check(lib().pw_attn_check(attn, _stream(stream)))

@@ -1,0 +1,335 @@
+// pw_attn_api.cpp -- host side of the paged-attention calls of include/pw.h: the handle, its
+// argument checks and launches.  Nothing is allocated after creation.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "pw_attn.h"
+
+using namespace pw;
+
+namespace {
+
+pw_status bad(const char *msg) { return report(nullptr, PW_ERR_INVALID, msg); }
+pw_status cuda_failed(const char *what, int e) {
+  cudaGetLastError();
+  char buf[256];
+  snprintf(buf, sizeof buf, "%s failed: %s", what, cudaGetErrorString((cudaError_t)e));
+  return report(nullptr, PW_ERR_CUDA, buf);
+}
+
+struct Layer {
+  uint16_t *k = nullptr, *v = nullptr;
+  int64_t block_stride = 0, token_stride = 0, head_stride = 0;
+};
+
+struct Plan {
+  bool set = false;
+  pw_kv_step step{};
+  RowBound *bounds = nullptr;  // [max_tokens]
+};
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool good_stride(int64_t s) { return s > 0 && s % 8 == 0; }
+
+int log2_of(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+// Makes the handle's device current for a call and puts the caller's back.
+struct OnDevice {
+  int before = -1;
+  bool ok;
+  explicit OnDevice(int dev) {
+    ok = cudaGetDevice(&before) == cudaSuccess && (before == dev || cudaSetDevice(dev) == cudaSuccess);
+    if (before == dev) before = -1;
+  }
+  ~OnDevice() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+}  // namespace
+
+struct pw_attn {
+  pw_attn_desc d{};
+  int sm_count = 0;
+  std::vector<Layer> layers;
+  std::vector<Plan> plans;
+  std::vector<void *> allocs;
+  int *err = nullptr;
+};
+
+namespace {
+
+pw_status check_step(const pw_attn *a, const pw_kv_step *s) {
+  if (!a || !s) return bad("null argument");
+  if (s->R < 1 || s->R > a->d.max_requests) return bad("R must be in 1..max_requests");
+  if (s->n_tokens < 1 || s->n_tokens > a->d.max_tokens) return bad("n_tokens must be in 1..max_tokens");
+  if (s->max_new < 0) return bad("max_new must not be negative");
+  if (s->table_rows < 1 || s->table_stride < 1) return bad("the table needs rows and entries");
+  if (!s->rows && s->table_rows < s->R) return bad("without `rows` the table needs a row for each request");
+  if ((int64_t)s->table_stride * a->d.block_tokens > INT32_MAX) return bad("a table row holds 2^31 tokens or more");
+  if (!s->ctx_len || !s->new_len || !s->table || !s->q_start || !s->kv_len || !s->slot || !s->pos)
+    return bad("null pointer in the step");
+  if (s->n_groups < 0 || s->n_groups > s->R) return bad("n_groups must be in 0..R");
+  if (s->n_groups > 0) {
+    if (!s->group_start || !s->shared_len) return bad("groups without group_start or shared_len");
+    if (s->n_tokens > a->d.max_shared_tokens) return bad("n_tokens of a step with groups exceeds max_shared_tokens");
+  }
+  return PW_OK;
+}
+
+template <class T>
+bool alloc(pw_attn *a, T **p, size_t n) {
+  void *q = nullptr;
+  if (cudaMalloc(&q, n * sizeof(T) + 16) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  a->allocs.push_back(q);  // capacity reserved at creation
+  *p = static_cast<T *>(q);
+  return true;
+}
+
+pw_status create(const pw_attn_desc &d, pw_attn *a) {
+  a->d = d;
+  a->layers.resize((size_t)d.L);
+  a->plans.resize((size_t)d.n_plans);
+  a->allocs.reserve(64);
+  int e = cudaDeviceGetAttribute(&a->sm_count, cudaDevAttrMultiProcessorCount, d.device);
+  if (e) return cuda_failed("cudaDeviceGetAttribute", e);
+  bool ok = alloc(a, &a->err, 1);
+  for (Plan &p : a->plans) ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens);
+  if (!ok) return report(nullptr, PW_ERR_OOM, "device memory exhausted");
+  if ((e = cudaMemset(a->err, 0, sizeof(int)))) return cuda_failed("cudaMemset", e);
+  if ((e = cudaDeviceSynchronize())) return cuda_failed("cudaDeviceSynchronize", e);
+  return PW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pw_status pw_attn_create(const pw_attn_desc *desc, pw_attn **out) {
+  if (!desc || !out) return bad("null argument");
+  *out = nullptr;
+  const pw_attn_desc &d = *desc;
+  if (d.L < 1 || d.L > 4096) return bad("L must be in 1..4096");
+  if (d.n_kv_heads < 1 || d.n_heads < d.n_kv_heads || d.n_heads % d.n_kv_heads || d.n_heads > 1024)
+    return bad("n_heads must be a multiple of n_kv_heads, at most 1024");
+  if (d.n_heads / d.n_kv_heads > kAttnRows) return bad("at most 128 query heads share a key/value head");
+  if (d.head_dim < 8 || d.head_dim % 8 || d.head_dim > 128) return bad("head_dim must be a multiple of 8 in 8..128");
+  if (d.dtype != PW_BF16 && d.dtype != PW_FP16) return bad("dtype must be PW_BF16 or PW_FP16");
+  if (d.n_blocks < 1) return bad("n_blocks must be positive");
+  if (d.block_tokens != 16 && d.block_tokens != 32 && d.block_tokens != 64 && d.block_tokens != 128)
+    return bad("block_tokens must be 16, 32, 64 or 128");
+  if (d.max_requests < 1 || d.max_requests > kAttnMaxRequests) return bad("max_requests must be in 1..4096");
+  if (d.max_tokens < 1 || d.max_tokens > (1 << 20)) return bad("max_tokens must be in 1..2^20");
+  if (d.max_shared_tokens < 0 || d.max_shared_tokens > d.max_tokens)
+    return bad("max_shared_tokens must be in 0..max_tokens");
+  if (d.n_plans < 1 || d.n_plans > 16) return bad("n_plans must be in 1..16");
+  OnDevice dev(d.device);
+  if (!dev.ok) return cuda_failed("cudaSetDevice", cudaGetLastError());
+  pw_attn *a = new (std::nothrow) pw_attn;
+  if (!a) return report(nullptr, PW_ERR_OOM, "host memory exhausted");
+  pw_status st;
+  try {
+    st = create(d, a);
+  } catch (...) {
+    st = report(nullptr, PW_ERR_OOM, "host memory exhausted");
+  }
+  if (st) {
+    for (void *p : a->allocs) cudaFree(p);
+    delete a;
+    return st;
+  }
+  *out = a;
+  return PW_OK;
+}
+
+void pw_attn_destroy(pw_attn *a) {
+  if (!a) return;
+  OnDevice dev(a->d.device);
+  cudaDeviceSynchronize();
+  for (void *p : a->allocs) cudaFree(p);
+  delete a;
+}
+
+pw_status pw_attn_bind(pw_attn *a, int layer, void *k, void *v, int64_t block_stride, int64_t token_stride,
+                       int64_t head_stride) {
+  if (!a || !k || !v) return bad("null argument");
+  if (layer < 0 || layer >= a->d.L) return bad("layer out of range");
+  if (!aligned16(k) || !aligned16(v)) return bad("cache addresses must be multiples of 16 bytes");
+  if (!good_stride(block_stride) || !good_stride(token_stride) || !good_stride(head_stride))
+    return bad("cache strides must be positive multiples of 8 elements");
+  Layer &l = a->layers[(size_t)layer];
+  l.k = static_cast<uint16_t *>(k);
+  l.v = static_cast<uint16_t *>(v);
+  l.block_stride = block_stride;
+  l.token_stride = token_stride;
+  l.head_stride = head_stride;
+  return PW_OK;
+}
+
+pw_status pw_kv_map(pw_attn *a, const pw_kv_step *s, const int32_t *new_ids, int n_ids, pw_stream stream) {
+  if (pw_status st = check_step(a, s)) return st;
+  if (n_ids < 0 || (n_ids > 0 && !new_ids)) return bad("n_ids ids are needed");
+  OnDevice dev(a->d.device);
+  MapArgs m{};
+  m.R = s->R;
+  m.n_tokens = s->n_tokens;
+  m.table_rows = s->table_rows;
+  m.table_stride = s->table_stride;
+  m.bt = a->d.block_tokens;
+  m.n_blocks = a->d.n_blocks;
+  m.n_ids = n_ids;
+  m.ctx_len = s->ctx_len;
+  m.new_len = s->new_len;
+  m.rows = s->rows;
+  m.new_ids = new_ids;
+  m.table = s->table;
+  m.q_start = s->q_start;
+  m.kv_len = s->kv_len;
+  m.pos = s->pos;
+  m.slot = s->slot;
+  m.err = a->err;
+  if (int e = launch_kv_map(m, stream)) return cuda_failed("pw_kv_map launch", e);
+  return PW_OK;
+}
+
+pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, const int32_t *doc_start,
+                       const int32_t *bidir_len, pw_stream stream) {
+  if (pw_status st = check_step(a, s)) return st;
+  if (plan < 0 || plan >= a->d.n_plans) return bad("plan out of range");
+  if (window < 0) return bad("window must not be negative");
+  OnDevice dev(a->d.device);
+  Plan &p = a->plans[(size_t)plan];
+  PlanArgs g{};
+  g.R = s->R;
+  g.n_tokens = s->n_tokens;
+  g.table_rows = s->table_rows;
+  g.table_stride = s->table_stride;
+  g.bt = a->d.block_tokens;
+  g.ctx_len = s->ctx_len;
+  g.rows = s->rows;
+  g.q_start = s->q_start;
+  g.kv_len = s->kv_len;
+  g.doc_start = doc_start;
+  g.bidir_len = bidir_len;
+  g.window = window;
+  g.bounds = p.bounds;
+  if (int e = launch_attn_plan(g, 1, stream)) return cuda_failed("pw_attn_plan launch", e);
+  p.step = *s;
+  p.set = true;
+  return PW_OK;
+}
+
+pw_status pw_attn_append(pw_attn *a, int layer, const pw_kv_step *s, const void *k, int64_t k_token,
+                         int64_t k_head, const void *v, int64_t v_token, int64_t v_head, pw_stream stream) {
+  if (pw_status st = check_step(a, s)) return st;
+  if (!k || !v) return bad("null argument");
+  if (layer < 0 || layer >= a->d.L) return bad("layer out of range");
+  if (!aligned16(k) || !aligned16(v)) return bad("k and v must be multiples of 16 bytes");
+  if (k_token % 8 || k_head % 8 || v_token % 8 || v_head % 8) return bad("strides must be multiples of 8 elements");
+  const Layer &l = a->layers[(size_t)layer];
+  if (!l.k) return report(nullptr, PW_ERR_STATE, "the layer's cache is not bound");
+  OnDevice dev(a->d.device);
+  AppendArgs g{};
+  g.k = static_cast<const uint16_t *>(k);
+  g.v = static_cast<const uint16_t *>(v);
+  g.k_token = k_token;
+  g.k_head = k_head;
+  g.v_token = v_token;
+  g.v_head = v_head;
+  g.kc = l.k;
+  g.vc = l.v;
+  g.block_stride = l.block_stride;
+  g.token_stride = l.token_stride;
+  g.head_stride = l.head_stride;
+  g.slot = s->slot;
+  g.n_tokens = s->n_tokens;
+  g.n_heads = a->d.n_kv_heads;
+  g.head_dim = a->d.head_dim;
+  g.bt = a->d.block_tokens;
+  g.log_bt = log2_of(a->d.block_tokens);
+  g.n_blocks = a->d.n_blocks;
+  if (int e = launch_attn_append(g, stream)) return cuda_failed("pw_attn_append launch", e);
+  return PW_OK;
+}
+
+pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_t q_token, int64_t q_head,
+                          void *o, int64_t o_token, int64_t o_head, float *lse, float scale, float softcap,
+                          const float *slopes, pw_stream stream) {
+  if (!a || !q || !o) return bad("null argument");
+  if (layer < 0 || layer >= a->d.L) return bad("layer out of range");
+  if (plan < 0 || plan >= a->d.n_plans) return bad("plan out of range");
+  if (!aligned16(q) || !aligned16(o)) return bad("q and o must be multiples of 16 bytes");
+  if (!good_stride(q_token) || !good_stride(q_head) || !good_stride(o_token) || !good_stride(o_head))
+    return bad("strides of q and o must be positive multiples of 8 elements");
+  if (!std::isfinite(scale)) return bad("scale must be finite");
+  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return bad("softcap must be finite and not negative");
+  const Layer &l = a->layers[(size_t)layer];
+  const Plan &p = a->plans[(size_t)plan];
+  if (!l.k) return report(nullptr, PW_ERR_STATE, "the layer's cache is not bound");
+  if (!p.set) return report(nullptr, PW_ERR_STATE, "the plan was never set");
+  OnDevice dev(a->d.device);
+  AttnArgs g{};
+  g.bounds = p.bounds;
+  g.table = p.step.table;
+  g.table_stride = p.step.table_stride;
+  g.n_tokens = p.step.n_tokens;
+  g.n_blocks = a->d.n_blocks;
+  g.log_bt = log2_of(a->d.block_tokens);
+  g.Hq = a->d.n_heads;
+  g.Hkv = a->d.n_kv_heads;
+  g.G = g.Hq / g.Hkv;
+  g.D = a->d.head_dim;
+  g.q = static_cast<const uint16_t *>(q);
+  g.q_token = q_token;
+  g.q_head = q_head;
+  g.o = static_cast<uint16_t *>(o);
+  g.o_token = o_token;
+  g.o_head = o_head;
+  g.kc = l.k;
+  g.vc = l.v;
+  g.block_stride = l.block_stride;
+  g.token_stride = l.token_stride;
+  g.head_stride = l.head_stride;
+  g.lse = lse;
+  g.scale = scale;
+  g.softcap = softcap;
+  g.slopes = slopes;
+  g.err = a->err;
+  g.wait_cycles = kWaitCyclesDefault;
+  if (int e = launch_attn(g, a->d.dtype == PW_BF16, stream)) return cuda_failed("pw_attn_forward launch", e);
+  return PW_OK;
+}
+
+pw_status pw_attn_check(pw_attn *a, pw_stream stream) {
+  if (!a) return bad("null argument");
+  OnDevice dev(a->d.device);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int bits = 0, e;
+  if ((e = cudaMemcpyAsync(&bits, a->err, sizeof bits, cudaMemcpyDeviceToHost, st)))
+    return cuda_failed("cudaMemcpyAsync", e);
+  if ((e = cudaStreamSynchronize(st))) return cuda_failed("cudaStreamSynchronize", e);
+  if (!bits) return PW_OK;
+  if ((e = cudaMemsetAsync(a->err, 0, sizeof bits, st)) || (e = cudaStreamSynchronize(st)))
+    return cuda_failed("cudaMemsetAsync", e);
+  if (bits & kAttnErrWait) return report(nullptr, PW_ERR_TIMEOUT, "a bounded device wait expired; outputs are invalid");
+  char buf[256];
+  snprintf(buf, sizeof buf, "pw_kv_map found:%s%s%s%s", bits & kAttnErrLen ? " a length out of range;" : "",
+           bits & kAttnErrTokens ? " more new tokens than n_tokens;" : "",
+           bits & kAttnErrIds ? " fewer new ids than opened blocks;" : "",
+           bits & kAttnErrBlock ? " a block id or table row out of range;" : "");
+  return report(nullptr, PW_ERR_STATE, buf);
+}
+
+}  // extern "C"

@@ -1,0 +1,210 @@
+// pw_attn_step.cu -- what an engine step needs around its attention: block tables and slot
+// maps from the request lengths, the division of the attention work, and the cache write.
+#include <cuda_runtime.h>
+#include <limits.h>
+
+#include "pw_attn.h"
+#include "pw_device.cuh"
+
+namespace pw {
+
+constexpr int kStepThreads = 256;
+
+// Exclusive prefix sum over the block of one value per thread; *total gets the sum.
+template <int THREADS>
+__device__ __forceinline__ long long block_scan(long long v, long long *total) {
+  __shared__ long long ws[THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += u;
+  }
+  __syncthreads();  // ws of an earlier call has been read
+  if (lane == 31) ws[warp] = inc;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const long long s = ws[w];
+    if (w < warp) before += s;
+    all += s;
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+// The largest i in [0, n) with cum[i] <= t (cum ascending, cum[0] <= t): with equal entries
+// the last of them, so that empty segments are skipped.
+__device__ __forceinline__ int seg_of(const int *cum, int n, int t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int sat(long long v) { return v > INT_MAX ? INT_MAX : (int)v; }
+
+// Block tables and slot maps.  Two exclusive sums over the requests, of the new tokens
+// (q_start) and of the blocks they open, locate everything else: a token's request and an
+// opened block's request are binary searches in them.  Every CTA computes both sums for
+// itself in shared memory (R <= 4096: 16 lengths a thread, which its neighbours have put
+// into L2) and then does its share of the requests, opened blocks and tokens, so one launch
+// without any hand-over between CTAs is enough; the sums cost a CTA less than a second
+// launch would.
+__global__ void __launch_bounds__(kStepThreads) kv_map_kernel(MapArgs a) {
+  extern __shared__ int sh[];
+  int *qs = sh, *bs = sh + a.R + 1;
+  const int tid = threadIdx.x;
+  const int per = (a.R + kStepThreads - 1) / kStepThreads;
+  const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+  const long long cap = (long long)a.table_stride * a.bt;
+  long long nt = 0, nb = 0;
+  int bad = 0;
+  for (int r = r0; r < r1; ++r) {
+    const long long c = a.ctx_len[r], n = a.new_len[r];
+    qs[r] = (int)nt;  // sums within the thread, at most INT_MAX; the threads before are added below
+    bs[r] = sat(nb);
+    // a request with a bad length brings nothing
+    if (c < 0 || n < 0 || c + n > cap) {
+      bad |= kAttnErrLen;
+    } else {
+      nt = min(nt + n, (long long)INT_MAX);
+      nb += (c + n + a.bt - 1) / a.bt - (c + a.bt - 1) / a.bt;
+    }
+  }
+  long long tot_t, tot_b;
+  const long long t0 = block_scan<kStepThreads>(nt, &tot_t);
+  const long long b0 = block_scan<kStepThreads>(nb, &tot_b);
+  for (int r = r0; r < r1; ++r) {
+    qs[r] = sat(qs[r] + t0);
+    bs[r] = sat(bs[r] + b0);
+  }
+  if (tid == 0) {
+    qs[a.R] = sat(tot_t);
+    bs[a.R] = sat(tot_b);
+  }
+  __syncthreads();
+  const int n_new = min(qs[a.R], a.n_tokens), n_open = bs[a.R];
+  if (tot_t > a.n_tokens) bad |= kAttnErrTokens;
+  if (n_open > a.n_ids) bad |= kAttnErrIds;
+  const int gid = blockIdx.x * kStepThreads + tid, step = gridDim.x * kStepThreads;
+  for (int r = gid; r <= a.R; r += step) {
+    a.q_start[r] = min(qs[r], a.n_tokens);
+    if (r < a.R) a.kv_len[r] = a.ctx_len[r] < 0 ? 0 : sat(min(cap, (long long)a.ctx_len[r] + (qs[r + 1] - qs[r])));
+    const int row = r < a.R && a.rows ? a.rows[r] : 0;
+    if (row < 0 || row >= a.table_rows) bad |= kAttnErrBlock;
+  }
+  for (int i = gid; i < n_open; i += step) {
+    const int r = seg_of(bs, a.R, i);
+    const int row = a.rows ? a.rows[r] : r;
+    const int page = (a.ctx_len[r] + a.bt - 1) / a.bt + i - bs[r];
+    int id = i < a.n_ids ? a.new_ids[i] : -1;
+    if (id < 0 || id >= a.n_blocks) {
+      if (i < a.n_ids) bad |= kAttnErrBlock;
+      id = -1;
+    }
+    if (row >= 0 && row < a.table_rows) a.table[(size_t)row * a.table_stride + page] = id;
+  }
+  for (int t = gid; t < a.n_tokens; t += step) {
+    long long slot = -1;
+    int pos = -1;
+    if (t < n_new) {
+      const int r = seg_of(qs, a.R, t);
+      const int row = a.rows ? a.rows[r] : r;
+      const int c = a.ctx_len[r], held = (c + a.bt - 1) / a.bt;
+      pos = c + t - qs[r];
+      const int page = pos / a.bt;
+      int id = -1;
+      if (page < held) {  // a cached block's free end: an entry no thread writes
+        if (row >= 0 && row < a.table_rows) id = a.table[(size_t)row * a.table_stride + page];
+      } else {
+        const int i = bs[r] + page - held;
+        if (i < a.n_ids) id = a.new_ids[i];
+      }
+      if (id >= 0 && id < a.n_blocks)
+        slot = (long long)id * a.bt + pos % a.bt;
+      else if (page < held)
+        bad |= kAttnErrBlock;
+    }
+    a.slot[t] = slot;
+    a.pos[t] = pos;
+  }
+  if (bad) atomicOr(a.err, bad);
+}
+
+int launch_kv_map(const MapArgs &a, void *stream) {
+  const int work = max(max(a.n_tokens, a.n_ids), a.R);
+  const int grid = max(1, min(148, (work + 4 * kStepThreads - 1) / (4 * kStepThreads)));
+  const size_t smem = 2 * sizeof(int) * (size_t)(a.R + 1);
+  kv_map_kernel<<<grid, kStepThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return (int)cudaGetLastError();
+}
+
+// The keys that each row sees (the masks are intervals, so one pair per token).
+__global__ void __launch_bounds__(kStepThreads) attn_bounds_kernel(PlanArgs a) {
+  const long long cap = (long long)a.table_stride * a.bt;
+  const int t = blockIdx.x * kStepThreads + threadIdx.x;
+  if (t >= a.n_tokens) return;
+  RowBound b{0, 0, -1, 0};
+  if (t < a.q_start[a.R]) {
+    const int r = seg_of(a.q_start, a.R, t);
+    const int kv = (int)min((long long)a.kv_len[r], cap);
+    const int row = a.rows ? a.rows[r] : r;
+    b.pos = a.ctx_len[r] + t - a.q_start[r];
+    b.trow = row >= 0 && row < a.table_rows ? row : -1;
+    b.hi = b.pos + 1;
+    if (a.bidir_len) b.hi = max(b.hi, a.bidir_len[r]);
+    b.hi = min(b.hi, kv);
+    if (a.window > 0) b.lo = max(0, b.pos - a.window + 1);
+    if (a.doc_start) b.lo = max(b.lo, a.doc_start[t]);
+    b.lo = min(b.lo, b.hi);
+    if (b.hi <= 0) b.lo = b.hi = 0;
+  }
+  a.bounds[t] = b;
+}
+
+int launch_attn_plan(const PlanArgs &a, int want_bounds, void *stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (want_bounds)
+    attn_bounds_kernel<<<(a.n_tokens + kStepThreads - 1) / kStepThreads, kStepThreads, 0, st>>>(a);
+  return (int)cudaGetLastError();
+}
+
+// The cache write: 16 bytes a thread, both caches in one launch.  A token's row of a cache is
+// n_heads runs of head_dim elements; consecutive threads take consecutive 16-byte pieces of k,
+// then of v, so that reads and writes are whole runs.
+__global__ void __launch_bounds__(kStepThreads) attn_append_kernel(AppendArgs a) {
+  const int vec = a.head_dim / 8, row = a.n_heads * vec;
+  const long long total = 2LL * a.n_tokens * row;
+  for (long long i = (long long)blockIdx.x * kStepThreads + threadIdx.x; i < total;
+       i += (long long)gridDim.x * kStepThreads) {
+    const long long u = i / row;
+    const int w = (int)(i - u * row), h = w / vec, c = w - h * vec;
+    const long long t = u >> 1;
+    const long long slot = a.slot[t];
+    const long long block = slot >> a.log_bt;
+    if (slot < 0 || block >= a.n_blocks) continue;
+    const long long dst = block * a.block_stride + (slot & (a.bt - 1)) * a.token_stride + h * a.head_stride + 8 * c;
+    if (u & 1)
+      *reinterpret_cast<uint4 *>(a.vc + dst) = *reinterpret_cast<const uint4 *>(a.v + t * a.v_token + h * a.v_head + 8 * c);
+    else
+      *reinterpret_cast<uint4 *>(a.kc + dst) = *reinterpret_cast<const uint4 *>(a.k + t * a.k_token + h * a.k_head + 8 * c);
+  }
+}
+
+int launch_attn_append(const AppendArgs &a, void *stream) {
+  const long long total = 2LL * a.n_tokens * a.n_heads * (a.head_dim / 8);
+  const long long want = (total + kStepThreads - 1) / kStepThreads;
+  const int grid = (int)(want < 148 * 8 ? want : 148 * 8);
+  attn_append_kernel<<<grid, kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace pw

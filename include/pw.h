@@ -457,6 +457,118 @@ pw_status pw_kv_request(const pw_kv *kv, int64_t request, int64_t *held, int64_t
 pw_status pw_kv_blocks(const pw_kv *kv, int64_t request, int32_t *ids_out, int64_t capacity, int64_t *n);
 pw_status pw_kv_get_stats(pw_kv *kv, pw_kv_stats *out);
 
+/* ---------------------------------------------------------------- paged attention */
+
+/* The KV blocks that pw_kv_* hands out hold the keys and values that the attention of a layer
+ * reads (the paper's Sec. 3.3 takes the cache and its attention from the serving engine; these
+ * calls have no counterpart there).  One engine step serves R requests; request r has
+ * ctx_len[r] tokens in the cache and brings new_len[r] new ones.  Rows of q, k, v and o are the
+ * new tokens, request after request.  Per step: pw_kv_map, then pw_attn_plan once for each kind
+ * of mask; per layer: pw_attn_append, then pw_attn_forward.  All of them are asynchronous on
+ * `stream`, allocate nothing and read lengths on the device only, so a step can be captured in
+ * a CUDA graph and replayed with new lengths.
+ *
+ * The position of the row t of request r is p = ctx_len[r] + t - q_start[r], and key position j
+ * of its cache lies in block table[row][j / block_tokens] at token j % block_tokens.  The row
+ * sees the keys lo <= j < hi with
+ *   lo = max(0, doc_start[t] if given, p - window + 1 if window > 0),
+ *   hi = min(kv_len[r], max(p + 1, bidir_len[r] if given)),
+ * and, with x_j = scale * (q . k_j), then x_j = softcap * tanh(x_j / softcap) if softcap > 0, then
+ * x_j -= slope[head] * |p - j| if slopes are given,
+ *   o = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)  (natural logarithm).
+ * A row that sees no key gets o = 0 and lse = -infinity.  Keys and values a row does not see do
+ * not reach it, whatever bits they hold.  Products of q and k and the softmax sums are fp32; the
+ * probabilities are rounded to the cache's type for the product with v, which is summed in fp32. */
+enum { PW_BF16 = 0, PW_FP16 = 1 };
+
+typedef struct pw_attn pw_attn;
+
+typedef struct {
+    int L;                /* layers (caches to bind) */
+    int n_heads;          /* query heads, a multiple of n_kv_heads; at most 128 per key/value head */
+    int n_kv_heads;
+    int head_dim;         /* a multiple of 8, at most 128 */
+    int dtype;            /* of q, k, v, o and the caches: PW_BF16 or PW_FP16 */
+    int n_blocks;         /* blocks of each cache; valid block ids are 0 .. n_blocks - 1 */
+    int block_tokens;     /* tokens of a block: 16, 32, 64 or 128 */
+    int max_requests;     /* largest R, at most 4096 */
+    int max_tokens;       /* largest n_tokens, at most 2^20 */
+    int max_shared_tokens;/* largest n_tokens of a step with n_groups > 0 (0: no such steps) */
+    int n_plans;          /* plans kept at a time, 1..16 */
+    int device;           /* CUDA device ordinal */
+} pw_attn_desc;
+
+/* One engine step.  Every pointer is device memory that stays the caller's. */
+typedef struct {
+    int R;                  /* requests, 1 .. max_requests */
+    int n_tokens;           /* rows of slot and pos: at least the sum of new_len.  Rows past that sum
+                               are padding: slot and pos -1, no cache write, o = 0 */
+    int max_new;            /* the largest new_len, or an upper bound of it (it chooses tile sizes;
+                               results do not depend on it) */
+    int table_rows, table_stride; /* rows of table, and entries of a row */
+    const int32_t *ctx_len; /* [R] */
+    const int32_t *new_len; /* [R], each may be 0 */
+    const int32_t *rows;    /* [R] table row of each request, or NULL: request r has row r */
+    int32_t *table;         /* [table_rows][table_stride] block ids; entries of cached tokens are read */
+    int32_t *q_start;       /* [R + 1] first row of each request */
+    int32_t *kv_len;        /* [R] */
+    int64_t *slot;          /* [n_tokens] block id * block_tokens + token within the block */
+    int32_t *pos;           /* [n_tokens] */
+    /* Groups of consecutive requests that share their first tokens: group g is the requests
+     * group_start[g] .. group_start[g + 1] - 1, whose first shared_len[g] tokens (a multiple of
+     * block_tokens, at most each request's ctx_len) lie in the same blocks.  group_start[0] = 0 and
+     * group_start[n_groups] = R; a request alone or a shared_len of 0 is fine.  Those keys are then
+     * read once for the group.  n_groups = 0: none, and both pointers are ignored. */
+    int n_groups;
+    const int32_t *group_start; /* [n_groups + 1] */
+    const int32_t *shared_len;  /* [n_groups] */
+} pw_kv_step;
+
+/* Create an attention handle: plans, split workspace (about 40 MB) and, with max_shared_tokens,
+ * 4 * max_shared_tokens * n_heads * (head_dim + 1) bytes for the shared prefixes' results.  The calls
+ * of one handle run on one stream at a time (its workspace is shared by them), and by one host
+ * thread.  PW_ERR_INVALID on a shape outside the ranges above, PW_ERR_CUDA / PW_ERR_OOM otherwise. */
+pw_status pw_attn_create(const pw_attn_desc *desc, pw_attn **out);
+/* Waits for the device's work and releases the handle.  NULL is ignored. */
+void pw_attn_destroy(pw_attn *a);
+/* The caches of a layer: element (block, token, head, d) of k is k[block * block_stride + token *
+ * token_stride + head * head_stride + d] (strides in elements; v likewise), so a block may keep its
+ * heads or its tokens outermost.  Addresses are multiples of 16 bytes, strides positive multiples of 8.
+ * The memory stays the caller's and outlives the binding; k and v may be bound again. */
+pw_status pw_attn_bind(pw_attn *a, int layer, void *k, void *v, int64_t block_stride, int64_t token_stride,
+                       int64_t head_stride);
+/* Block tables and slot maps of a step, on the device from the lengths: q_start, kv_len, slot, pos, and
+ * the table entries of the blocks that the new tokens open.  new_ids [n_ids] are those blocks' ids,
+ * request after request in the order granted (pw_kv_grow): request r opens
+ * ceil((ctx_len + new_len) / block_tokens) - ceil(ctx_len / block_tokens) blocks.  Ids beyond these are
+ * left alone.  A negative length, too few ids or rows, a table row that is too short or an id outside the
+ * cache is reported by pw_attn_check (PW_ERR_STATE); entries and slots concerned are -1. */
+pw_status pw_kv_map(pw_attn *a, const pw_kv_step *step, const int32_t *new_ids, int n_ids, pw_stream stream);
+/* Lay out the attention work of a mapped step under one mask into plan 0 .. n_plans - 1: per row its keys
+ * [lo, hi), and the division of all key blocks among the SMs.  window >= 0 (0: none).  doc_start [n_tokens]
+ * (NULL: none): position in its request at which the row's document begins, for packed documents.
+ * bidir_len [R] (NULL: none): keys below it are seen by every row of the request.  The plan holds for every
+ * layer of the step with this mask, until the next pw_attn_plan into it; step's table must stay valid. */
+pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *step, int window, const int32_t *doc_start,
+                       const int32_t *bidir_len, pw_stream stream);
+/* Write the step's new keys and values to the layer's cache: row t, head h of k is k[t * k_token +
+ * h * k_head + d] (strides in elements, multiples of 8; addresses multiples of 16 bytes; v likewise).
+ * Rows with slot -1 are skipped. */
+pw_status pw_attn_append(pw_attn *a, int layer, const pw_kv_step *step, const void *k, int64_t k_token,
+                         int64_t k_head, const void *v, int64_t v_token, int64_t v_head, pw_stream stream);
+/* Attention of the step's rows over the layer's cache, which holds the new tokens already: the formula
+ * above.  q and o as k above, over n_heads heads; query head h reads key/value head h / (n_heads /
+ * n_kv_heads).  lse: fp32 [n_tokens][n_heads] or NULL.  scale finite; softcap >= 0 (0: none); slopes: fp32
+ * [n_heads] or NULL.  o may not alias q or the caches.  A block id outside the cache reads as zeros.
+ * PW_ERR_STATE if the plan or the layer's cache was never set. */
+pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_t q_token, int64_t q_head,
+                          void *o, int64_t o_token, int64_t o_head, float *lse, float scale, float softcap,
+                          const float *slopes, pw_stream stream);
+/* Wait for `stream` and report what the handle's calls found since the last check: PW_ERR_TIMEOUT if a
+ * bounded device wait expired, PW_ERR_STATE for the findings of pw_kv_map (message in pw_last_error(NULL)).
+ * Clears what it reports. */
+pw_status pw_attn_check(pw_attn *a, pw_stream stream);
+
 /* ---------------------------------------------------------------- inspection */
 
 /* b-bit codes of a block as the GPU kernels read them (the same device extraction code
