@@ -3,6 +3,7 @@
 
 #include "pw_attn.h"
 #include "pw_device.cuh"
+#include "pw_tc.cuh"
 
 namespace pw {
 
@@ -74,30 +75,697 @@ __device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, i
   *lse = m + logf(l);
 }
 
-template <bool BF>
-__global__ void __launch_bounds__(256) attn_rows_kernel(AttnArgs a) {
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= (long long)a.n_tokens * a.Hq) return;
-  const int t = (int)(w / a.Hq), h = (int)(w - (long long)t * a.Hq), lane = threadIdx.x & 31;
-  const RowBound b = a.bounds[t];
-  float acc[4], lse;
-  row_attention<BF>(a, t, h, b.lo, b.hi, b.trow, b.pos, acc, &lse);
-  if (4 * lane < a.D) {
-    const uint2 out{pack_pair<BF>(acc[0], acc[1]), pack_pair<BF>(acc[2], acc[3])};
-    *reinterpret_cast<uint2 *>(a.o + t * a.o_token + h * a.o_head + 4 * lane) = out;
+// ------------------------------------------------------------------ the tensor-core kernel
+constexpr int kSmemRing = 227 * 1024 - 3072;  // dynamic shared memory: query tiles and the K/V ring
+constexpr uint32_t kTmemColsAttn = 512;
+constexpr uint32_t kSpinNs = 2000;
+
+template <int NS, int DP>
+struct Cfg {
+  static constexpr int kHalves = DP / 64;             // 64-element column blocks of a head
+  static constexpr int kHalfBytes = 128 * 128;        // 128 rows of 128 bytes
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kStages = (kSmemRing - NS * kTileBytes) / kTileBytes;
+  static constexpr int kSmem = (NS + kStages) * kTileBytes;
+  static constexpr int kSoftWarps = 4 * NS;
+  static constexpr int kThreads = kSoftWarps * 32 + 64;
+};
+
+// mbarriers
+template <int STAGES>
+struct Bars {
+  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE, kSF, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kNum = kJoin + 2 };
+};
+
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, kSpinNs)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > a.wait_cycles) break;
   }
-  if (a.lse && lane == 0) a.lse[w] = lse;
+  *abort_flag = 1;
+  atomicOr(a.err, kAttnErrWait);
+  return false;
+}
+__device__ __forceinline__ bool wait_for_all(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag, a));
 }
 
-int launch_attn(const AttnArgs &a, int bf16, void *stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const long long rows = (long long)a.n_tokens * a.Hq;
-  const unsigned grid = (unsigned)((rows + 7) / 8);
-  if (bf16)
-    attn_rows_kernel<true><<<grid, 256, 0, st>>>(a);
-  else
-    attn_rows_kernel<false><<<grid, 256, 0, st>>>(a);
+// A CTA's way through its units: pieces of consecutive key tiles of one (tile, head).
+struct Walk {
+  const AttnArgs &a;
+  AttnStart s;
+  AttnTile t;
+  int n;  // key tiles of this piece
+  __device__ __forceinline__ explicit Walk(const AttnArgs &args) : a(args) { s = a.list.start[blockIdx.x]; }
+  __device__ __forceinline__ bool load() {
+    if (s.n <= 0) return false;
+    const int4 *p = reinterpret_cast<const int4 *>(a.list.tiles + s.tile);
+    const int4 x = p[0], y = p[1];
+    t.tok0 = x.x, t.ntok = x.y, t.trow = x.z, t.klo = x.w;
+    t.khi = y.x, t.kv0 = y.y, t.kv1 = y.z, t.merge = y.w;
+    n = min(t.kv1 - t.kv0 - s.off, s.n);
+    return true;
+  }
+  __device__ __forceinline__ void next() {
+    s.n -= n;
+    s.off += n;
+    if (s.off == t.kv1 - t.kv0) {
+      s.off = 0;
+      if (++s.head == a.Hkv) {
+        s.head = 0;
+        ++s.tile;
+      }
+    }
+  }
+  __device__ __forceinline__ int first() const { return t.kv0 + s.off; }
+  __device__ __forceinline__ bool whole() const { return n == t.kv1 - t.kv0; }
+};
+
+template <int NS, int DP>
+__device__ void produce(const AttnArgs &a, const AttnMaps &maps, uint32_t sm, uint32_t bars, volatile int *abort_flag) {
+  using C = Cfg<NS, DP>;
+  using B = Bars<C::kStages>;
+  const int lane = threadIdx.x & 31;
+  const int bt = 1 << a.log_bt, ppt = kAttnKeys >> a.log_bt;  // blocks of a key tile
+  const int page = lane % ppt, half = lane / ppt;
+  const bool mine = half < C::kHalves;
+  const uint32_t ring = sm + NS * C::kTileBytes;
+  const uint32_t at = (uint32_t)(half * C::kHalfBytes + page * bt * 128);
+  uint32_t fill = 0, pieces = 0;
+  Walk w(a);
+  bool ok = true;
+  for (; ok && w.load(); w.next(), ++pieces) {
+    auto block_of = [&](int kt) {  // the block this lane loads of key tile kt; -1: none of its keys counts
+      const int key0 = kt * kAttnKeys + page * bt;
+      if (!mine || key0 >= w.t.khi || key0 + bt <= w.t.klo) return -1;
+      const int p = key0 >> a.log_bt;
+      int id = -1;
+      if (w.t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)w.t.trow * a.table_stride + p];
+      return id >= 0 && id < a.n_blocks ? id : a.n_blocks;  // out of the map's range: zeros
+    };
+    int id = block_of(w.first());
+    ok = wait_for_all(bars + 8 * B::kQE, (pieces & 1) ^ 1, abort_flag, a);
+    if (!ok) break;
+    const int ns = NS == 2 && w.t.ntok > a.list.tpt ? 2 : 1;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bars + 8 * B::kQF, (uint32_t)(ns * C::kHalves * a.box_tokens * a.G * 128));
+      for (int s = 0; s < ns; ++s)
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_3d(sm + s * C::kTileBytes + h * C::kHalfBytes, &maps.q, 64 * h, w.s.head * a.G,
+                      w.t.tok0 + s * a.list.tpt, bars + 8 * B::kQF);
+    }
+    for (int j = 0; j < w.n; ++j) {
+      const int cur = id;
+      if (j + 1 < w.n) id = block_of(w.first() + j + 1);
+      const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, cur >= 0)) * bt * 128);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t st = fill % C::kStages, use = fill / C::kStages;
+        ok = wait_for_all(bars + 8 * (B::kEmpty + st), (use & 1) ^ 1, abort_flag, a);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (B::kFull + st), bytes);
+        __syncwarp();
+        if (cur >= 0)
+          tma_load_4d(ring + st * C::kTileBytes + at, kv ? &maps.v : &maps.k, 64 * half, 0, w.s.head, cur,
+                      bars + 8 * (B::kFull + st));
+        ++fill;
+      }
+      if (!ok) break;
+    }
+  }
+  if (!ok) {  // given up: wait for what was issued before the shared memory goes away
+    const long long t0 = clock64();
+    for (uint32_t f = fill > (uint32_t)C::kStages ? fill - C::kStages : 0; f < fill; ++f)
+      while (!mbar_try_wait_sleep(bars + 8 * (B::kFull + f % C::kStages), (f / C::kStages) & 1, kSpinNs) &&
+             clock64() - t0 <= a.wait_cycles) {
+      }
+    if (pieces)
+      while (!mbar_try_wait_sleep(bars + 8 * B::kQF, (pieces - 1) & 1, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
+      }
+  }
+}
+
+// S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by one thread.
+template <int NS, int DP, bool BF>
+struct Mma {
+  using C = Cfg<NS, DP>;
+  static __device__ __forceinline__ void qk(uint32_t tmem_s, uint32_t q, uint32_t k) {
+    const uint32_t idesc = idesc_f16_f32(128, kAttnKeys) | (BF ? (1u << 7) | (1u << 10) : 0u);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const uint32_t off = (uint32_t)((i / 4) * C::kHalfBytes + (i % 4) * 32);
+      tc_mma_f16(tmem_s, smem_desc_sw128(q + off, 1024), smem_desc_sw128(k + off, 1024), idesc, i > 0);
+    }
+  }
+  static __device__ __forceinline__ void pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v, bool accumulate) {
+    const uint32_t idesc = idesc_f16_f32(128, DP) | (BF ? (1u << 7) | (1u << 10) : 0u) | (1u << 16);
+#pragma unroll
+    for (int i = 0; i < kAttnKeys / 16; ++i)
+      tc_mma_f16_ta(tmem_o, tmem_p + 8 * i, smem_desc_mn_sw128(v + i * 2048, C::kHalfBytes), idesc,
+                    accumulate || i > 0);
+  }
+};
+
+template <int NS, int DP, bool BF>
+__device__ void issue(const AttnArgs &a, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag) {
+  using C = Cfg<NS, DP>;
+  using B = Bars<C::kStages>;
+  using M = Mma<NS, DP, BF>;
+  const uint32_t ring = sm + NS * C::kTileBytes, o0 = tmem + 256;
+  uint32_t used = 0, pieces = 0, it = 0;
+  uint32_t p_seq[2] = {0, 0};
+  Walk w(a);
+  bool ok = true;
+  auto full = [&](uint32_t f) {
+    const bool r = wait_for(bars + 8 * (B::kFull + f % C::kStages), (f / C::kStages) & 1, abort_flag, a);
+    tc_fence_after();
+    return r;
+  };
+  auto stage = [&](uint32_t f) { return ring + (f % C::kStages) * C::kTileBytes; };
+  auto release = [&](uint32_t f) { tc_commit(bars + 8 * (B::kEmpty + f % C::kStages)); };
+  for (; ok && w.load(); w.next(), ++pieces) {
+    const int n = w.n;
+    ok = wait_for(bars + 8 * B::kQF, pieces & 1, abort_flag, a);
+    if (!ok) break;
+    tc_fence_after();
+    if (NS == 2) {
+      const int ns = w.t.ntok > a.list.tpt ? 2 : 1;
+      if (!(ok = full(used))) break;
+      for (int s = 0; s < ns; ++s) {
+        M::qk(tmem + 128 * s, sm + s * C::kTileBytes, stage(used));
+        tc_commit(bars + 8 * (B::kSF + s));
+      }
+      release(used);
+      if (n == 1) tc_commit(bars + 8 * B::kQE);
+      for (int j = 0; j < n && ok; ++j, used += 2) {
+        if (!(ok = full(used + 1))) break;
+        for (int s = 0; s < ns && ok; ++s) {
+          if (!(ok = wait_for(bars + 8 * (B::kPF + s), p_seq[s] & 1, abort_flag, a))) break;
+          ++p_seq[s];
+          tc_fence_after();
+          M::pv(o0 + 128 * s, tmem + 128 * s, stage(used + 1), j > 0);
+          if (j + 1 < n) {
+            if (s == 0 && !(ok = full(used + 2))) break;
+            M::qk(tmem + 128 * s, sm + s * C::kTileBytes, stage(used + 2));
+            tc_commit(bars + 8 * (B::kSF + s));
+          } else {
+            tc_commit(bars + 8 * (B::kOD + s));
+          }
+        }
+        if (!ok) break;
+        release(used + 1);
+        if (j + 1 < n) {
+          release(used + 2);
+          if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+        }
+      }
+    } else {
+      if (!(ok = full(used))) break;
+      M::qk(tmem + 128 * (it & 1), sm, stage(used));
+      tc_commit(bars + 8 * (B::kSF + (it & 1)));
+      release(used);
+      if (n == 1) tc_commit(bars + 8 * B::kQE);
+      for (int j = 0; j < n; ++j, used += 2, ++it) {
+        const uint32_t b = it & 1;
+        if (j + 1 < n) {
+          if (!(ok = full(used + 2))) break;
+          M::qk(tmem + 128 * (b ^ 1), sm, stage(used + 2));
+          tc_commit(bars + 8 * (B::kSF + (b ^ 1)));
+          release(used + 2);
+          if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+        }
+        if (!(ok = full(used + 1))) break;
+        if (!(ok = wait_for(bars + 8 * (B::kPF + b), p_seq[b] & 1, abort_flag, a))) break;
+        ++p_seq[b];
+        tc_fence_after();
+        M::pv(o0, tmem + 128 * b, stage(used + 1), j > 0);
+        tc_commit(bars + 8 * B::kOD);
+        release(used + 1);
+      }
+    }
+  }
+  // nothing of the tensor cores is in flight when tensor memory is freed
+  tc_commit(bars + 8 * B::kDrain);
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bars + 8 * B::kDrain, 0, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028234e38f; }
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// What a thread knows of its row.
+struct Row {
+  int tok, head;  // query token and head
+  bool valid;
+  int lo, hi;     // its keys within the tile's segment
+  int pos, trow;
+};
+
+// Row results leave here.  Thread-per-row: `get(c, v)` gives 32 unscaled columns from 32 c.  m and l are
+// the row's maximum (log2 units) and sum; the output is get / l.
+template <int DP, bool BF, class Get>
+__device__ __forceinline__ bool emit_row(const AttnArgs &a, const Row &r, bool merge, float m, float l, Get get) {
+  float inv = l == 0.f ? 0.f : 1.f / l;
+  float lse2 = l == 0.f ? -INFINITY : m + lg2(l);
+  float w2 = 0.f;
+  const float *po = nullptr;
+  if (merge && r.valid) {
+    const size_t at = (size_t)r.tok * a.Hq + r.head;
+    const float pl = a.prefix_lse[at];
+    po = a.prefix_o + at * a.D;
+    const float mx = fmaxf(pl, lse2), ms = mx == -INFINITY ? 0.f : mx;
+    const float e1 = ex2(lse2 - ms), e2 = ex2(pl - ms), sum = e1 + e2;
+    const float is = sum == 0.f ? 0.f : 1.f / sum;
+    inv *= e1 * is;
+    w2 = e2 * is;
+    lse2 = sum == 0.f ? -INFINITY : ms + lg2(sum);
+  }
+  bool fin = true;
+#pragma unroll
+  for (int c = 0; c < DP / 32; ++c) {
+    float v[32];
+    get(c, v);
+    if (!r.valid) continue;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= inv;
+    if (po && w2 != 0.f) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        if (32 * c + i < a.D) {
+          const float4 x = *reinterpret_cast<const float4 *>(po + 32 * c + i);
+          v[i] += w2 * x.x;
+          v[i + 1] += w2 * x.y;
+          v[i + 2] += w2 * x.z;
+          v[i + 3] += w2 * x.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (32 * c + i < a.D) fin = fin && finite(v[i]);
+    if (a.to_prefix) {
+      float *d = a.prefix_o + ((size_t)r.tok * a.Hq + r.head) * a.D + 32 * c;
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        if (32 * c + i < a.D) *reinterpret_cast<float4 *>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+      uint16_t *d = a.o + r.tok * a.o_token + r.head * a.o_head + 32 * c;
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        if (32 * c + i < a.D)
+          *reinterpret_cast<uint4 *>(d + i) =
+              make_uint4(pack_pair<BF>(v[i], v[i + 1]), pack_pair<BF>(v[i + 2], v[i + 3]),
+                         pack_pair<BF>(v[i + 4], v[i + 5]), pack_pair<BF>(v[i + 6], v[i + 7]));
+    }
+  }
+  if (r.valid) {
+    if (a.to_prefix)
+      a.prefix_lse[(size_t)r.tok * a.Hq + r.head] = lse2;
+    else if (a.lse)
+      a.lse[(size_t)r.tok * a.Hq + r.head] = lse2 * kLn2;
+  }
+  // a finite sum with an output that is not: a value is infinite or NaN, possibly one that the row does not
+  // see (0 times it in the product with v)
+  return r.valid && !fin && finite(l);
+}
+
+// Rows flagged by emit_row, again from their visible keys alone, by the whole warp.
+template <bool BF>
+__device__ void redo_rows(const AttnArgs &a, unsigned flagged, const Row &r, bool merge) {
+  const int lane = threadIdx.x & 31;
+  while (flagged) {
+    const int src = __ffs(flagged) - 1;
+    flagged &= flagged - 1;
+    const int tok = __shfl_sync(0xffffffffu, r.tok, src), head = __shfl_sync(0xffffffffu, r.head, src);
+    int lo = __shfl_sync(0xffffffffu, r.lo, src), hi = __shfl_sync(0xffffffffu, r.hi, src);
+    const int trow = __shfl_sync(0xffffffffu, r.trow, src), pos = __shfl_sync(0xffffffffu, r.pos, src);
+    if (merge) {  // over the shared prefix too: the row's own bounds
+      const RowBound b = a.bounds[tok];
+      lo = b.lo;
+      hi = b.hi;
+    }
+    float acc[4], lse;
+    row_attention<BF>(a, tok, head, lo, hi, trow, pos, acc, &lse);
+    const size_t at = (size_t)tok * a.Hq + head;
+    if (4 * lane < a.D) {
+      if (a.to_prefix)
+        *reinterpret_cast<float4 *>(a.prefix_o + at * a.D + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      else
+        *reinterpret_cast<uint2 *>(a.o + tok * a.o_token + head * a.o_head + 4 * lane) =
+            make_uint2(pack_pair<BF>(acc[0], acc[1]), pack_pair<BF>(acc[2], acc[3]));
+    }
+  }
+}
+
+template <int NS, int DP, bool BF, bool EXTRA>
+__device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag,
+                       volatile int *last_flag) {
+  using C = Cfg<NS, DP>;
+  using B = Bars<C::kStages>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+  const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+  const uint32_t tmem_o = tmem + 256 + 128 * s + lanes;
+  uint32_t it = 0;        // key tiles of this stream so far
+  uint32_t v_fill = 1;    // ring position of the current tile's V
+  uint32_t o_seen = 0;    // phases of the stream's O barrier known to be complete
+  uint32_t o_done = 0;    // NS == 2: pieces of this stream so far
+  uint32_t joins = 0;     // meetings of the stream's warps so far
+  auto join = [&]() {     // the stream's four warps meet (bounded, as every wait)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (B::kJoin + s));
+    return wait_for_all(bars + 8 * (B::kJoin + s), joins++ & 1, abort_flag, a);
+  };
+  const float sl2 = a.scale * kLog2e;
+  Walk w(a);
+  bool ok = true;
+  for (; ok && w.load(); w.next()) {
+    const int n = w.n;
+    const int ntok = min(a.list.tpt, w.t.ntok - s * a.list.tpt), nrows = ntok * a.G;
+    if (NS == 2 && ntok <= 0) {
+      v_fill += 2 * n;
+      continue;
+    }
+    Row r;
+    r.valid = row < nrows;
+    r.tok = w.t.tok0 + s * a.list.tpt + row / a.G;
+    r.head = w.s.head * a.G + row % a.G;
+    RowBound rb{0, 0, -1, 0};
+    if (r.valid) rb = a.bounds[r.tok];
+    r.lo = max(rb.lo, w.t.klo);
+    r.hi = min(rb.hi, w.t.khi);
+    r.pos = rb.pos;
+    r.trow = w.t.trow;
+    const bool active = 32 * quarter < nrows;
+    const float slope = EXTRA && a.slopes && r.valid ? a.slopes[r.head] * kLog2e : 0.f;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j, ++it, v_fill += 2) {
+      const uint32_t buf = NS == 2 ? (uint32_t)s : (it & 1);
+      const uint32_t par = NS == 2 ? (it & 1) : ((it >> 1) & 1);
+      const uint32_t ts = tmem + 128 * buf + lanes;
+      const int base = (w.first() + j) * kAttnKeys;
+      if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
+      tc_fence_after();
+      if (NS == 1 && it > 0) o_seen = max(o_seen, it - 1);
+      if (s == 0 && (base < w.t.klo || base + kAttnKeys > w.t.khi)) {
+        // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
+        // times what the memory holds may be NaN
+        if (!(ok = wait_for_all(bars + 8 * (B::kFull + v_fill % C::kStages), (v_fill / C::kStages) & 1, abort_flag, a)))
+          break;
+        if (base + row < w.t.klo || base + row >= w.t.khi) {
+          uint8_t *vrow = smp + (NS + v_fill % C::kStages) * C::kTileBytes + row * 128;
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(vrow + h * C::kHalfBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+      }
+      if (active) {
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t *>(x) + 32 * c);
+        tmem_wait_ld();
+        if (EXTRA) {
+          if (a.softcap > 0.f) {
+            const float t2 = 2.f * kLog2e * a.scale / a.softcap, cl = a.softcap * kLog2e;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i] = cl - 2.f * cl * rcp(ex2(x[i] * t2) + 1.f);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i] *= sl2;
+          }
+          if (a.slopes) {
+            const float d0 = (float)(r.pos - base);
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i] -= slope * fabsf(d0 - (float)i);
+          }
+        }
+        const int lo = r.lo - base, hi = r.hi - base;
+        if (__any_sync(0xffffffffu, r.valid && (lo > 0 || hi < kAttnKeys))) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = i >= lo && i < hi ? x[i] : -INFINITY;
+        }
+        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+        for (int i = 4; i < 128; i += 4) {
+          mx0 = fmaxf(mx0, x[i]);
+          mx1 = fmaxf(mx1, x[i + 1]);
+          mx2 = fmaxf(mx2, x[i + 2]);
+          mx3 = fmaxf(mx3, x[i + 3]);
+        }
+        float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        if (!EXTRA) mx *= sl2;
+        if (!r.valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
+        if (j == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+          // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8:
+          // until then probabilities up to 2^8 cost no precision, and the accumulator stays untouched.
+          const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          if (NS == 1) {
+            while (o_seen < it && ok) {
+              ok = wait_for_all(bars + 8 * B::kOD, o_seen & 1, abort_flag, a);
+              ++o_seen;
+            }
+            if (!ok) break;
+            tc_fence_after();
+          }
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            float o[32];
+            tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float *y = x + 32 * c + i;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = ex2(EXTRA ? y[k] - ms : fmaf(y[k], sl2, -ms));
+            s0 += y[0];
+            s1 += y[1];
+            s2 += y[2];
+            s3 += y[3];
+            pk[i / 2] = pack_pair<BF>(y[0], y[1]);
+            pk[i / 2 + 1] = pack_pair<BF>(y[2], y[3]);
+          }
+          tmem_st16(ts + 16 * c, pk);
+        }
+        l += (s0 + s1) + (s2 + s3);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (B::kPF + buf));
+    }
+    if (!ok) break;
+    // the piece's last product
+    if (NS == 2) {
+      ok = wait_for_all(bars + 8 * (B::kOD + s), o_done & 1, abort_flag, a);
+      ++o_done;
+    } else {
+      while (o_seen < it && ok) {
+        ok = wait_for_all(bars + 8 * B::kOD, o_seen & 1, abort_flag, a);
+        ++o_seen;
+      }
+    }
+    if (!ok) break;
+    tc_fence_after();
+    auto from_tmem = [&](int c, float *v) {
+      tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
+      tmem_wait_ld();
+    };
+    const bool merge = w.t.merge && !a.to_prefix && a.prefix_o;
+    if (w.whole()) {
+      if (active) {
+        const bool again = emit_row<DP, BF>(a, r, merge, m, l, from_tmem);
+        const unsigned flagged = __ballot_sync(0xffffffffu, again);
+        if (flagged) redo_rows<BF>(a, flagged, r, merge);
+      }
+    } else {
+      // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up
+      const int cum = a.list.cum[w.s.tile], cost = w.t.kv1 - w.t.kv0;
+      const long long W = (long long)a.list.meta[1] * a.Hkv;
+      const long long ub = (long long)cum * a.Hkv + (long long)w.s.head * cost;
+      const long long P = min((long long)a.ctas, W);
+      const int c0 = (int)(((ub + 1) * P - 1) / W), c1 = (int)(((ub + cost) * P - 1) / W);
+      auto slot_of = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * NS + s; };
+      constexpr int kPart = DP * 128;
+      const size_t my = slot_of(blockIdx.x);
+      if (active) {
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) {
+          float v[32];
+          from_tmem(c, v);
+          if (r.valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((8 * c + i / 4) * 128 + row) * 4),
+                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+          }
+        }
+        if (r.valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
+      }
+      __threadfence();
+      if (!(ok = join())) break;
+      if (row == 0) {
+        int *cnt = a.counters + 2 * c0 + s;
+        const int last = atomicAdd(cnt, 1) == c1 - c0;
+        if (last) *cnt = 0;
+        last_flag[s] = last;
+      }
+      if (!(ok = join())) break;
+      if (last_flag[s]) {
+        __threadfence();
+        if (active) {
+          float mm = -INFINITY, ll = 0.f;
+          if (r.valid) {
+            for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(a.part_ml + slot_of(c) * 128 + row).x);
+            const float ms = mm == -INFINITY ? 0.f : mm;
+            for (int c = c0; c <= c1; ++c) {
+              const float2 ml = __ldcg(a.part_ml + slot_of(c) * 128 + row);
+              ll += ml.y * ex2(ml.x - ms);
+            }
+          }
+          const float ms = mm == -INFINITY ? 0.f : mm;
+          auto from_parts = [&](int c, float *v) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            if (!r.valid) return;
+            for (int p = c0; p <= c1; ++p) {
+              const size_t at = slot_of(p);
+              const float f = ex2(__ldcg(a.part_ml + at * 128 + row).x - ms);
+              const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kPart) + 8 * c * 128 + row;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 y = __ldcg(src + i * 128);
+                v[4 * i] += f * y.x;
+                v[4 * i + 1] += f * y.y;
+                v[4 * i + 2] += f * y.z;
+                v[4 * i + 3] += f * y.w;
+              }
+            }
+          };
+          const bool again = emit_row<DP, BF>(a, r, merge, mm, ll, from_parts);
+          const unsigned flagged = __ballot_sync(0xffffffffu, again);
+          if (flagged) redo_rows<BF>(a, flagged, r, merge);
+        }
+      }
+    }
+  }
+}
+
+template <int NS, int DP, bool BF, bool EXTRA>
+__global__ void __launch_bounds__(Cfg<NS, DP>::kThreads, 1) attn_kernel(const __grid_constant__ AttnMaps maps,
+                                                                       const __grid_constant__ AttnArgs a) {
+  using C = Cfg<NS, DP>;
+  using B = Bars<C::kStages>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bar_mem[B::kNum];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, last_flag[2];
+  const int warp = threadIdx.x >> 5;
+  const uint32_t bars = smem_u32(bar_mem), sm = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bars + 8 * (B::kFull + i), 1);
+      mbar_init(bars + 8 * (B::kEmpty + i), 1);
+    }
+    mbar_init(bars + 8 * B::kQF, 1);
+    mbar_init(bars + 8 * B::kQE, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (B::kSF + i), 1);
+      mbar_init(bars + 8 * (B::kPF + i), 4);
+      mbar_init(bars + 8 * (B::kOD + i), 1);
+      mbar_init(bars + 8 * (B::kJoin + i), 4);
+    }
+    mbar_init(bars + 8 * B::kDrain, 1);
+    abort_flag = (sm & 1023u) != 0u;  // the swizzled tiles are 1 KB-aligned
+    if (abort_flag) atomicOr(a.err, kAttnErrWait);
+    fence_mbar_init();
+  }
+  if (warp == C::kSoftWarps) {
+    tmem_alloc(smem_u32(&tmem_slot), kTmemColsAttn);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (!abort_flag) {
+    if (warp < C::kSoftWarps)
+      soften<NS, DP, BF, EXTRA>(a, smem, sm, bars, tmem, &abort_flag, last_flag);
+    else if (warp == C::kSoftWarps)
+      produce<NS, DP>(a, maps, sm, bars, &abort_flag);
+    else if ((threadIdx.x & 31) == 0)
+      issue<NS, DP, BF>(a, sm, bars, tmem, &abort_flag);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kSoftWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemColsAttn);
+  }
+}
+
+template <int NS, int DP, bool BF, bool EXTRA>
+static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
+  using C = Cfg<NS, DP>;
+  static_assert(C::kStages >= 4, "two key tiles in flight");
+  auto kern = attn_kernel<NS, DP, BF, EXTRA>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  kern<<<a.ctas, C::kThreads, C::kSmem, st>>>(maps, a);
   return (int)cudaGetLastError();
+}
+
+template <int NS, int DP, bool BF>
+static int launch_extra(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
+  // the plain image folds a positive scale into the exponent's multiply-add; caps, biases and other scales
+  // transform the scores first
+  if (a.softcap > 0.f || a.slopes || !(a.scale > 0.f)) return launch_one<NS, DP, BF, true>(a, maps, st);
+  return launch_one<NS, DP, BF, false>(a, maps, st);
+}
+template <int NS, int DP>
+static int launch_type(const AttnArgs &a, const AttnMaps &maps, int bf16, cudaStream_t st) {
+  return bf16 ? launch_extra<NS, DP, true>(a, maps, st) : launch_extra<NS, DP, false>(a, maps, st);
+}
+
+int launch_attn(const AttnArgs &a, const AttnMaps &maps, int bf16, void *stream) {
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.D > 64)
+    return a.list.streams == 2 ? launch_type<2, 128>(a, maps, bf16, st) : launch_type<1, 128>(a, maps, bf16, st);
+  return a.list.streams == 2 ? launch_type<2, 64>(a, maps, bf16, st) : launch_type<1, 64>(a, maps, bf16, st);
 }
 
 }  // namespace pw

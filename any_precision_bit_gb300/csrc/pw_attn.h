@@ -3,6 +3,8 @@
 #include <stdint.h>
 
 #include "../../include/pw.h"
+#include <cuda_runtime.h>
+
 #include "pw_internal.h"
 
 namespace pw {
@@ -40,8 +42,8 @@ struct AttnStart {
   int tile, head, off, n;  // key tile `off` of (tile, head); n key tiles in all
 };
 
-// One list of work.  The units are key tiles, in the order (tile, head, key tile); CTA c of P
-// takes the units [c W / P, (c + 1) W / P) of the W.
+// One list of work.  The units are key tiles, in the order (tile, head, key tile); of the W units
+// CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W if that is less (the rest idle).
 struct AttnList {
   AttnTile *tiles;
   int *cum;          // [tiles + 1] key tiles of one head before each tile
@@ -61,6 +63,7 @@ struct PlanArgs {
   const int *group_start, *shared_len;
   RowBound *bounds;
   AttnList list;
+  int of_groups;  // the list of the groups' shared prefixes, not of the requests
   int ctas, n_kv_heads;
 };
 
@@ -81,11 +84,22 @@ struct AppendArgs {
   int n_tokens, n_heads, head_dim, bt, log_bt, n_blocks;
 };
 
+// Tensor maps of one forward launch: boxes of 64 elements of a head by (Q) the G heads of a
+// key/value head by a tile's tokens, or (K, V) the tokens of a block; 128-byte swizzle, the K-major
+// operand layout of the MMAs.  Elements past head_dim, tokens past n_tokens and blocks past n_blocks
+// read as zeros.
+struct AttnMaps {
+  TmaDesc q, k, v;
+};
+
 struct AttnArgs {
   const RowBound *bounds;
+  AttnList list;
+  int ctas;
   const int *table;
   int table_stride, n_tokens, n_blocks, log_bt;
   int Hq, Hkv, G, D;
+  int box_tokens;  // tokens of one Q box
   const uint16_t *q;
   int64_t q_token, q_head;
   uint16_t *o;
@@ -95,13 +109,23 @@ struct AttnArgs {
   float *lse;
   float scale, softcap;
   const float *slopes;
+  // Results over a shared prefix, normalised, and their log2-sum-exp2: written (to_prefix) or merged
+  // into the rows of tiles with `merge`.
+  float *prefix_o, *prefix_lse;  // [n_tokens][Hq][D], [n_tokens][Hq]
+  int to_prefix;
+  // Partial results of split tiles: two slots a CTA (its last piece and its first) and stream.
+  float *part_o;    // [ctas][2][streams][head_dim padded / 4][128][4]
+  float2 *part_ml;  // [ctas][2][streams][128] running maximum and sum
+  int *counters;    // [ctas][2] arrived pieces of the split tile whose first piece is the CTA's last,
+                    // per stream; zero between launches
   int *err;
   long long wait_cycles;
 };
 
 int launch_kv_map(const MapArgs &a, void *stream);
-int launch_attn_plan(const PlanArgs &a, int want_bounds, void *stream);
+int launch_attn_bounds(const PlanArgs &a, void *stream);
+int launch_attn_list(const PlanArgs &a, void *stream);
 int launch_attn_append(const AppendArgs &a, void *stream);
-int launch_attn(const AttnArgs &a, int bf16, void *stream);
+int launch_attn(const AttnArgs &a, const AttnMaps &maps, int bf16, void *stream);
 
 }  // namespace pw

@@ -1,7 +1,9 @@
 // pw_attn_api.cpp -- host side of the paged-attention calls of include/pw.h: the handle, its
 // argument checks and launches.  Nothing is allocated after creation.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -22,8 +24,36 @@ pw_status cuda_failed(const char *what, int e) {
   return report(nullptr, PW_ERR_CUDA, buf);
 }
 
+// Tensor map of 16-bit elements with the 128-byte swizzle: dim[0] contiguous, the others `stride` elements
+// apart, boxes of box[] elements (64 along dim 0); what lies outside reads as zeros.
+bool encode_map(TmaDesc *out, const void *base, int rank, const cuuint64_t *dim, const int64_t *stride,
+                const cuuint32_t *box) {
+  using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode fn = []() -> Encode {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    return reinterpret_cast<Encode>(p);
+  }();
+  if (!fn) return false;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  cuuint64_t bytes[3];
+  for (int i = 0; i + 1 < rank; ++i) bytes[i] = (cuuint64_t)stride[i] * 2;
+  return fn(reinterpret_cast<CUtensorMap *>(out), CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank,
+            const_cast<void *>(base), dim, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layer {
   uint16_t *k = nullptr, *v = nullptr;
+  TmaDesc map_k, map_v;
   int64_t block_stride = 0, token_stride = 0, head_stride = 0;
 };
 
@@ -31,6 +61,7 @@ struct Plan {
   bool set = false;
   pw_kv_step step{};
   RowBound *bounds = nullptr;  // [max_tokens]
+  AttnList requests{}, groups{};
 };
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -64,6 +95,9 @@ struct pw_attn {
   std::vector<Plan> plans;
   std::vector<void *> allocs;
   int *err = nullptr;
+  float *part_o = nullptr, *prefix_o = nullptr, *prefix_lse = nullptr;
+  float2 *part_ml = nullptr;
+  int *counters = nullptr;
 };
 
 namespace {
@@ -105,10 +139,25 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   a->allocs.reserve(64);
   int e = cudaDeviceGetAttribute(&a->sm_count, cudaDevAttrMultiProcessorCount, d.device);
   if (e) return cuda_failed("cudaDeviceGetAttribute", e);
-  bool ok = alloc(a, &a->err, 1);
-  for (Plan &p : a->plans) ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens);
+  const size_t ctas = (size_t)a->sm_count, dp = d.head_dim > 64 ? 128 : 64;
+  bool ok = alloc(a, &a->err, 1) && alloc(a, &a->counters, 2 * ctas) &&
+            alloc(a, &a->part_o, ctas * 4 * kAttnRows * dp) && alloc(a, &a->part_ml, ctas * 4 * kAttnRows);
+  if (d.max_shared_tokens > 0)
+    ok = ok && alloc(a, &a->prefix_o, (size_t)d.max_shared_tokens * d.n_heads * d.head_dim) &&
+         alloc(a, &a->prefix_lse, (size_t)d.max_shared_tokens * d.n_heads);
+  // a tile holds a token at least, but the last of each segment may be short: requests and the padding, or groups
+  for (Plan &p : a->plans) {
+    ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens);
+    for (AttnList *l : {&p.requests, &p.groups}) {
+      if (l == &p.groups && d.max_shared_tokens == 0) continue;
+      l->max_tiles = d.max_tokens + d.max_requests + 1;
+      ok = ok && alloc(a, &l->tiles, (size_t)l->max_tiles) && alloc(a, &l->cum, (size_t)l->max_tiles + 1) &&
+           alloc(a, &l->start, ctas) && alloc(a, &l->meta, 2);
+    }
+  }
   if (!ok) return report(nullptr, PW_ERR_OOM, "device memory exhausted");
-  if ((e = cudaMemset(a->err, 0, sizeof(int)))) return cuda_failed("cudaMemset", e);
+  if ((e = cudaMemset(a->err, 0, sizeof(int))) || (e = cudaMemset(a->counters, 0, 2 * ctas * sizeof(int))))
+    return cuda_failed("cudaMemset", e);
   if ((e = cudaDeviceSynchronize())) return cuda_failed("cudaDeviceSynchronize", e);
   return PW_OK;
 }
@@ -169,7 +218,18 @@ pw_status pw_attn_bind(pw_attn *a, int layer, void *k, void *v, int64_t block_st
   if (!aligned16(k) || !aligned16(v)) return bad("cache addresses must be multiples of 16 bytes");
   if (!good_stride(block_stride) || !good_stride(token_stride) || !good_stride(head_stride))
     return bad("cache strides must be positive multiples of 8 elements");
+  OnDevice dev(a->d.device);
+  const pw_attn_desc &d = a->d;
+  const cuuint64_t dim[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.block_tokens, (cuuint64_t)d.n_kv_heads,
+                             (cuuint64_t)d.n_blocks};
+  const int64_t stride[3] = {token_stride, head_stride, block_stride};
+  const cuuint32_t box[4] = {64, (cuuint32_t)d.block_tokens, 1, 1};
+  TmaDesc map_k, map_v;
+  if (!encode_map(&map_k, k, 4, dim, stride, box) || !encode_map(&map_v, v, 4, dim, stride, box))
+    return bad("no tensor map can describe this cache (address or strides)");
   Layer &l = a->layers[(size_t)layer];
+  l.map_k = map_k;
+  l.map_v = map_v;
   l.k = static_cast<uint16_t *>(k);
   l.v = static_cast<uint16_t *>(v);
   l.block_stride = block_stride;
@@ -225,7 +285,31 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   g.bidir_len = bidir_len;
   g.window = window;
   g.bounds = p.bounds;
-  if (int e = launch_attn_plan(g, 1, stream)) return cuda_failed("pw_attn_plan launch", e);
+  g.n_groups = s->n_groups;
+  g.group_start = s->group_start;
+  g.shared_len = s->shared_len;
+  g.ctas = a->sm_count;
+  g.n_kv_heads = a->d.n_kv_heads;
+  const int G = a->d.n_heads / a->d.n_kv_heads, most = kAttnRows / G;
+  auto shape = [&](AttnList &l, int tokens) {
+    // two 128-row tiles share each key tile when a segment has rows for them, else one tile runs with its
+    // score buffers doubled
+    tokens = std::max(tokens, 1);
+    l.streams = (int64_t)tokens * G > kAttnRows ? 2 : 1;
+    l.tpt = std::min(most, tokens);
+  };
+  shape(p.requests, s->max_new);
+  shape(p.groups, s->n_tokens);
+  int e = launch_attn_bounds(g, stream);
+  if (!e && s->n_groups) {
+    g.of_groups = 1;
+    g.list = p.groups;
+    e = launch_attn_list(g, stream);
+  }
+  g.of_groups = 0;
+  g.list = p.requests;
+  if (!e) e = launch_attn_list(g, stream);
+  if (e) return cuda_failed("pw_attn_plan launch", e);
   p.step = *s;
   p.set = true;
   return PW_OK;
@@ -308,8 +392,31 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.slopes = slopes;
   g.err = a->err;
   g.wait_cycles = kWaitCyclesDefault;
-  if (int e = launch_attn(g, a->d.dtype == PW_BF16, stream)) return cuda_failed("pw_attn_forward launch", e);
-  return PW_OK;
+  g.part_o = a->part_o;
+  g.part_ml = a->part_ml;
+  g.counters = a->counters;
+  g.ctas = a->sm_count;
+  AttnMaps maps;
+  maps.k = l.map_k;
+  maps.v = l.map_v;
+  const cuuint64_t dim[3] = {(cuuint64_t)g.D, (cuuint64_t)g.Hq, (cuuint64_t)g.n_tokens};
+  const int64_t stride[2] = {q_head, q_token};
+  auto launch = [&](const AttnList &list) -> pw_status {
+    g.list = list;
+    g.box_tokens = list.tpt;
+    const cuuint32_t box[3] = {64, (cuuint32_t)g.G, (cuuint32_t)list.tpt};
+    if (!encode_map(&maps.q, q, 3, dim, stride, box)) return bad("no tensor map can describe q (address or strides)");
+    if (int e = launch_attn(g, maps, a->d.dtype == PW_BF16, stream)) return cuda_failed("pw_attn_forward launch", e);
+    return PW_OK;
+  };
+  if (p.step.n_groups) {
+    g.prefix_o = a->prefix_o;
+    g.prefix_lse = a->prefix_lse;
+    g.to_prefix = 1;
+    if (pw_status st = launch(p.groups)) return st;
+    g.to_prefix = 0;
+  }
+  return launch(p.requests);
 }
 
 pw_status pw_attn_check(pw_attn *a, pw_stream stream) {
@@ -321,7 +428,9 @@ pw_status pw_attn_check(pw_attn *a, pw_stream stream) {
     return cuda_failed("cudaMemcpyAsync", e);
   if ((e = cudaStreamSynchronize(st))) return cuda_failed("cudaStreamSynchronize", e);
   if (!bits) return PW_OK;
-  if ((e = cudaMemsetAsync(a->err, 0, sizeof bits, st)) || (e = cudaStreamSynchronize(st)))
+  if ((e = cudaMemsetAsync(a->err, 0, sizeof bits, st)) ||
+      (e = cudaMemsetAsync(a->counters, 0, 2 * sizeof(int) * (size_t)a->sm_count, st)) ||
+      (e = cudaStreamSynchronize(st)))
     return cuda_failed("cudaMemsetAsync", e);
   if (bits & kAttnErrWait) return report(nullptr, PW_ERR_TIMEOUT, "a bounded device wait expired; outputs are invalid");
   char buf[256];

@@ -170,10 +170,141 @@ __global__ void __launch_bounds__(kStepThreads) attn_bounds_kernel(PlanArgs a) {
   a.bounds[t] = b;
 }
 
-int launch_attn_plan(const PlanArgs &a, int want_bounds, void *stream) {
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (want_bounds)
-    attn_bounds_kernel<<<(a.n_tokens + kStepThreads - 1) / kStepThreads, kStepThreads, 0, st>>>(a);
+int launch_attn_bounds(const PlanArgs &a, void *stream) {
+  attn_bounds_kernel<<<(a.n_tokens + kStepThreads - 1) / kStepThreads, kStepThreads, 0,
+                       reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return (int)cudaGetLastError();
+}
+
+// Segments of a list: requests (and, behind them, the rows that are padding), or groups.
+struct Segment {
+  int tok0, tok1, trow, klo, khi, merge;
+};
+
+__device__ __forceinline__ Segment segment_of(const PlanArgs &a, int i) {
+  Segment g{0, 0, -1, 0, 0, 0};
+  const int n = min(max(a.q_start[a.R], 0), a.n_tokens);
+  const int cap = (int)min((long long)a.table_stride * a.bt, (long long)INT_MAX);
+  int r = i;
+  if (a.of_groups) {
+    r = min(max(a.group_start[i], 0), a.R);
+    const int e = min(max(a.group_start[i + 1], r), a.R);
+    g.tok0 = min(max(a.q_start[r], 0), n);
+    g.tok1 = min(max(a.q_start[e], g.tok0), n);
+    g.khi = min(max(a.shared_len[i], 0), cap);
+    if (r == a.R) return g;
+  } else if (i == a.R) {  // padding rows: no keys
+    g.tok0 = n;
+    g.tok1 = a.n_tokens;
+    return g;
+  } else {
+    g.tok0 = min(max(a.q_start[r], 0), n);
+    g.tok1 = min(max(a.q_start[r + 1], g.tok0), n);
+    g.khi = min(max(a.kv_len[r], 0), cap);
+    if (a.n_groups) {
+      g.klo = min(max(a.shared_len[seg_of(a.group_start, a.n_groups, r)], 0), g.khi);
+      g.merge = 1;
+    }
+  }
+  const int row = a.rows ? a.rows[r] : r;
+  g.trow = row >= 0 && row < a.table_rows ? row : -1;
+  return g;
+}
+
+// One list of work, by one CTA: tiles per segment and their sum; per tile (one warp each) the key
+// tiles that some row of it sees; their sum; and where each of the forward's CTAs begins.
+constexpr int kListThreads = 1024;
+__global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
+  extern __shared__ int cum_tiles[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
+  const int tt = a.list.tpt * a.list.streams;
+  long long before = 0;
+  for (int s0 = 0; s0 < n_seg; s0 += kListThreads) {
+    const int s = s0 + tid;
+    int n = 0;
+    if (s < n_seg) {
+      const Segment g = segment_of(a, s);
+      n = (g.tok1 - g.tok0 + tt - 1) / tt;
+    }
+    long long total;
+    const long long at = block_scan<kListThreads>(n, &total);
+    if (s < n_seg) cum_tiles[s] = (int)(before + at);
+    before += total;
+  }
+  const int n_tiles = (int)min(before, (long long)a.list.max_tiles);
+  __syncthreads();
+  for (int i = warp; i < n_tiles; i += kListThreads / 32) {
+    const int s = seg_of(cum_tiles, n_seg, i);
+    const Segment g = segment_of(a, s);
+    AttnTile t;
+    t.tok0 = g.tok0 + (i - cum_tiles[s]) * tt;
+    t.ntok = min(tt, g.tok1 - t.tok0);
+    t.trow = g.trow;
+    t.klo = g.klo;
+    t.khi = g.khi;
+    t.merge = g.merge;
+    int lo = INT_MAX, hi = 0;
+    for (int j = lane; j < t.ntok; j += 32) {
+      const RowBound b = a.bounds[t.tok0 + j];
+      const int l = max(b.lo, g.klo), h = min(b.hi, g.khi);
+      if (l < h) {
+        lo = min(lo, l);
+        hi = max(hi, h);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    t.kv0 = hi > 0 ? lo / kAttnKeys : g.klo / kAttnKeys;
+    t.kv1 = hi > 0 ? (hi - 1) / kAttnKeys + 1 : t.kv0 + 1;
+    if (lane == 0) {
+      a.list.tiles[i] = t;
+      a.list.cum[i + 1] = t.kv1 - t.kv0;
+    }
+  }
+  __syncthreads();
+  before = 0;
+  for (int i0 = 0; i0 < n_tiles; i0 += kListThreads) {
+    const int i = i0 + tid;
+    const int n = i < n_tiles ? a.list.cum[i + 1] : 0;
+    long long total;
+    const long long at = block_scan<kListThreads>(n, &total);
+    if (i < n_tiles) a.list.cum[i + 1] = sat(before + at + n);
+    before += total;
+  }
+  if (tid == 0) {
+    a.list.cum[0] = 0;
+    a.list.meta[0] = n_tiles;
+    a.list.meta[1] = sat(before);
+  }
+  __syncthreads();
+  const long long W = before * a.n_kv_heads;  // at least one unit: there is a row, and every tile has one
+  for (int c = tid; c < a.ctas; c += kListThreads) {
+    const long long P = min((long long)a.ctas, W);
+    const long long u0 = min(c * W / P, W), u1 = min((c + 1) * W / P, W);
+    AttnStart st{0, 0, 0, (int)(u1 - u0)};
+    if (u1 > u0) {
+      int lo = 0, hi = n_tiles - 1;  // the last tile whose units begin at or before u0
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)a.list.cum[mid] * a.n_kv_heads <= u0)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int cost = a.list.cum[lo + 1] - a.list.cum[lo];
+      const long long rem = u0 - (long long)a.list.cum[lo] * a.n_kv_heads;
+      st.tile = lo;
+      st.head = (int)(rem / cost);
+      st.off = (int)(rem - (long long)st.head * cost);
+    }
+    a.list.start[c] = st;
+  }
+}
+
+int launch_attn_list(const PlanArgs &a, void *stream) {
+  const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
+  attn_list_kernel<<<1, kListThreads, sizeof(int) * (size_t)n_seg, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return (int)cudaGetLastError();
 }
 
