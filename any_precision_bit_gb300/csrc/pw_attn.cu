@@ -302,7 +302,7 @@ __device__ void issue(const AttnArgs &a, uint32_t sm, uint32_t bars, uint32_t tm
         ++p_seq[b];
         tc_fence_after();
         M::pv(o0, tmem + 128 * b, stage(used + 1), j > 0);
-        tc_commit(bars + 8 * B::kOD);
+        tc_commit(bars + 8 * (B::kOD + b));
         release(used + 1);
       }
     }
@@ -365,7 +365,7 @@ __device__ __forceinline__ bool emit_row(const AttnArgs &a, const Row &r, bool m
   for (int c = 0; c < DP / 32; ++c) {
     float v[32];
     get(c, v);
-    if (!r.valid) continue;
+    if (r.valid) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= inv;
     if (po && w2 != 0.f) {
@@ -395,6 +395,7 @@ __device__ __forceinline__ bool emit_row(const AttnArgs &a, const Row &r, bool m
           *reinterpret_cast<uint4 *>(d + i) =
               make_uint4(pack_pair<BF>(v[i], v[i + 1]), pack_pair<BF>(v[i + 2], v[i + 3]),
                          pack_pair<BF>(v[i + 4], v[i + 5]), pack_pair<BF>(v[i + 6], v[i + 7]));
+    }
     }
   }
   if (r.valid) {
@@ -447,7 +448,12 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
   const uint32_t tmem_o = tmem + 256 + 128 * s + lanes;
   uint32_t it = 0;        // key tiles of this stream so far
   uint32_t v_fill = 1;    // ring position of the current tile's V
-  uint32_t o_seen = 0;    // phases of the stream's O barrier known to be complete
+  // NS == 1: P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked
+  // the tile before on the same barrier is known to be complete (the scores of tile t or t + 1 were issued
+  // behind it) and the one after waits for this thread, so the parity cannot be mistaken.
+  auto product_done = [&](uint32_t t) {
+    return wait_for_all(bars + 8 * (B::kOD + (t & 1)), (t >> 1) & 1, abort_flag, a);
+  };
   uint32_t o_done = 0;    // NS == 2: pieces of this stream so far
   uint32_t joins = 0;     // meetings of the stream's warps so far
   auto join = [&]() {     // the stream's four warps meet (bounded, as every wait)
@@ -485,7 +491,6 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
       const int base = (w.first() + j) * kAttnKeys;
       if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
       tc_fence_after();
-      if (NS == 1 && it > 0) o_seen = max(o_seen, it - 1);
       if (s == 0 && (base < w.t.klo || base + kAttnKeys > w.t.khi)) {
         // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
         // times what the memory holds may be NaN
@@ -542,12 +547,9 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
           // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8:
           // until then probabilities up to 2^8 cost no precision, and the accumulator stays untouched.
           const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          // NS == 2: these scores were issued behind the product before, which is therefore done
           if (NS == 1) {
-            while (o_seen < it && ok) {
-              ok = wait_for_all(bars + 8 * B::kOD, o_seen & 1, abort_flag, a);
-              ++o_seen;
-            }
-            if (!ok) break;
+            if (!(ok = product_done(it - 1))) break;
             tc_fence_after();
           }
           m = mn;
@@ -594,14 +596,12 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
       ok = wait_for_all(bars + 8 * (B::kOD + s), o_done & 1, abort_flag, a);
       ++o_done;
     } else {
-      while (o_seen < it && ok) {
-        ok = wait_for_all(bars + 8 * B::kOD, o_seen & 1, abort_flag, a);
-        ++o_seen;
-      }
+      ok = product_done(it - 1);
     }
     if (!ok) break;
     tc_fence_after();
     auto from_tmem = [&](int c, float *v) {
+      __syncwarp();  // a load of the whole warp: lanes without a row come from other branches
       tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
       tmem_wait_ld();
     };
