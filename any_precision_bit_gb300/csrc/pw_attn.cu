@@ -88,13 +88,35 @@ struct Cfg {
   static constexpr int kStages = (kSmemRing - NS * kTileBytes) / kTileBytes;
   static constexpr int kSmem = (NS + kStages) * kTileBytes;
   static constexpr int kSoftWarps = 4 * NS;
-  static constexpr int kThreads = kSoftWarps * 32 + 64;
+  // producer and MMA warps, and (two tiles) two idle warps that complete their warpgroup
+  static constexpr int kThreads = kSoftWarps * 32 + (NS == 2 ? 128 : 64);
 };
+// Two tiles: 384 threads of 168 registers at launch, of which the softmax warps, which hold 128 scores
+// each, need more: 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kRegsSoft = 224, kRegsOther = 56;
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// A piece of work as the producer hands it to the other warps: consecutive key tiles of one (tile, head).
+struct Piece {
+  int n, first;  // key tiles, and the first one (n = 0: no more pieces)
+  int head, tok0, ntok, trow, klo, khi;  // as in AttnTile; head of the keys
+  int fresh;     // other rows than the last piece's
+  int merge;     // merge with the rows' results over their shared prefix
+  int c0, c1;    // CTAs of the (tile, head)'s first and last key tile; equal: the piece is all of it
+};
+constexpr int kPieces = 4;  // pieces handed over ahead
 
 // mbarriers
 template <int STAGES>
 struct Bars {
-  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE, kSF, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kNum = kJoin + 2 };
+  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kNum = kDE + kPieces };
 };
 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
@@ -113,39 +135,93 @@ __device__ __forceinline__ bool wait_for_all(uint32_t bar, uint32_t parity, vola
   return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag, a));
 }
 
-// A CTA's way through its units: pieces of consecutive key tiles of one (tile, head).
-struct Walk {
-  const AttnArgs &a;
-  AttnStart s;
+// A CTA's way through its units: pieces of consecutive key tiles of one (tile, head).  The tile after
+// the current one is fetched ahead of its use.
+__device__ __forceinline__ AttnTile load_tile(const AttnTile *p) {
+  const int4 x = reinterpret_cast<const int4 *>(p)[0], y = reinterpret_cast<const int4 *>(p)[1];
   AttnTile t;
-  int n;  // key tiles of this piece
-  __device__ __forceinline__ explicit Walk(const AttnArgs &args) : a(args) { s = a.list.start[blockIdx.x]; }
+  t.tok0 = x.x, t.ntok = x.y, t.trow = x.z, t.klo = x.w;
+  t.khi = y.x, t.kv0 = y.y, t.kv1 = y.z, t.merge = y.w;
+  return t;
+}
+struct Walk {
+  int tile, head, off, left;  // off and left in units (kAttnPieceCost of them lead each (tile, head))
+  AttnTile t, ahead;
+  int j0, n;  // first key tile of this piece within the tile's, and their number
+  bool fresh; // the tile is another than the last piece's
+  __device__ __forceinline__ explicit Walk(const AttnArgs &a) {
+    const AttnStart s = a.list.start[blockIdx.x];
+    tile = s.tile, head = s.head, off = s.off, left = s.n;
+    fresh = true;
+    if (left > 0) {
+      t = load_tile(a.list.tiles + tile);
+      ahead = load_tile(a.list.tiles + tile + 1);
+    }
+  }
   __device__ __forceinline__ bool load() {
-    if (s.n <= 0) return false;
-    const int4 *p = reinterpret_cast<const int4 *>(a.list.tiles + s.tile);
-    const int4 x = p[0], y = p[1];
-    t.tok0 = x.x, t.ntok = x.y, t.trow = x.z, t.klo = x.w;
-    t.khi = y.x, t.kv0 = y.y, t.kv1 = y.z, t.merge = y.w;
-    n = min(t.kv1 - t.kv0 - s.off, s.n);
+    if (off < kAttnPieceCost) {
+      const int skip = min(kAttnPieceCost - off, left);
+      off += skip;
+      left -= skip;
+    }
+    if (left <= 0) return false;
+    j0 = off - kAttnPieceCost;
+    n = min(t.kv1 - t.kv0 - j0, left);
     return true;
   }
-  __device__ __forceinline__ void next() {
-    s.n -= n;
-    s.off += n;
-    if (s.off == t.kv1 - t.kv0) {
-      s.off = 0;
-      if (++s.head == a.Hkv) {
-        s.head = 0;
-        ++s.tile;
+  __device__ __forceinline__ void next(const AttnArgs &a) {
+    left -= n;
+    off += n;
+    fresh = false;
+    if (off == t.kv1 - t.kv0 + kAttnPieceCost) {
+      off = 0;
+      if (++head == a.Hkv) {
+        head = 0;
+        ++tile;
+        fresh = true;
+        t = ahead;
+        if (left > 0) ahead = load_tile(a.list.tiles + tile + 1);
       }
     }
   }
-  __device__ __forceinline__ int first() const { return t.kv0 + s.off; }
-  __device__ __forceinline__ bool whole() const { return n == t.kv1 - t.kv0; }
+  __device__ __forceinline__ int first() const { return t.kv0 + j0; }
+  __device__ __forceinline__ void describe(const AttnArgs &a, Piece *p) const {
+    int c0 = 0, c1 = 0;
+    if (n != t.kv1 - t.kv0) {
+      const int cost = t.kv1 - t.kv0 + kAttnPieceCost;
+      const long long W = (long long)a.list.meta[1] * a.Hkv, P = min((long long)a.ctas, W);
+      const long long ub = (long long)a.list.cum[tile] * a.Hkv + (long long)head * cost;
+      c0 = (int)(((ub + kAttnPieceCost + 1) * P - 1) / W);
+      c1 = (int)(((ub + cost) * P - 1) / W);
+    }
+    *p = Piece{n, first(), head, t.tok0, t.ntok, t.trow, t.klo, t.khi, fresh, t.merge && !a.to_prefix, c0, c1};
+  }
 };
 
+// Position in the ring of K/V stages.
+template <int STAGES>
+struct Ring {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == STAGES) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Q tiles: with one stream and boxes of at most 64 rows two of them share the query region, so that the
+// next piece's is loaded while the current one is in use.  (The MMAs read 128 rows from either; what
+// lies behind a box's rows gives scores of rows that nobody has.)
+template <int NS>
+__device__ __forceinline__ uint32_t q_buffers(const AttnArgs &a) {
+  return NS == 1 && a.box_tokens * a.G <= 64 ? 2u : 1u;
+}
+constexpr uint32_t kQBuffer = 64 * 128;  // bytes of 64 rows
+
 template <int NS, int DP>
-__device__ void produce(const AttnArgs &a, const AttnMaps &maps, uint32_t sm, uint32_t bars, volatile int *abort_flag) {
+__device__ void produce(const AttnArgs &a, const AttnMaps &maps, Piece *piece, uint32_t sm, uint32_t bars,
+                        volatile int *abort_flag) {
   using C = Cfg<NS, DP>;
   using B = Bars<C::kStages>;
   const int lane = threadIdx.x & 31;
@@ -154,156 +230,214 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, uint32_t sm, ui
   const bool mine = half < C::kHalves;
   const uint32_t ring = sm + NS * C::kTileBytes;
   const uint32_t at = (uint32_t)(half * C::kHalfBytes + page * bt * 128);
-  uint32_t fill = 0, pieces = 0;
+  const uint32_t nq = q_buffers<NS>(a);
+  uint32_t fills = 0, pieces = 0;
+  Ring<C::kStages> r;
   Walk w(a);
   bool ok = true;
-  for (; ok && w.load(); w.next(), ++pieces) {
-    auto block_of = [&](int kt) {  // the block this lane loads of key tile kt; -1: none of its keys counts
-      const int key0 = kt * kAttnKeys + page * bt;
-      if (!mine || key0 >= w.t.khi || key0 + bt <= w.t.klo) return -1;
-      const int p = key0 >> a.log_bt;
-      int id = -1;
-      if (w.t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)w.t.trow * a.table_stride + p];
-      return id >= 0 && id < a.n_blocks ? id : a.n_blocks;  // out of the map's range: zeros
-    };
-    int id = block_of(w.first());
-    ok = wait_for_all(bars + 8 * B::kQE, (pieces & 1) ^ 1, abort_flag, a);
+  // the block this lane loads of a key tile; -1: none of its keys counts
+  auto block_of = [&](const AttnTile &t, int kt) {
+    const int key0 = kt * kAttnKeys + page * bt;
+    if (!mine || key0 >= t.khi || key0 + bt <= t.klo) return -1;
+    const int p = key0 >> a.log_bt;
+    int id = -1;
+    if (t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)t.trow * a.table_stride + p];
+    return id >= 0 && id < a.n_blocks ? id : a.n_blocks;  // out of the map's range: zeros
+  };
+  bool more = w.load();
+  int id = more ? block_of(w.t, w.first()) : -1;
+  // hand over piece `i`, the one the walk is at (or the end)
+  auto publish = [&](uint32_t i) {
+    const uint32_t d = i % kPieces;
+    const bool y = wait_for_all(bars + 8 * (B::kDE + d), ((i / kPieces) & 1) ^ 1, abort_flag, a);
+    if (y && lane == 0) {
+      if (more)
+        w.describe(a, piece + d);
+      else
+        piece[d].n = 0;
+      mbar_arrive(bars + 8 * (B::kDF + d));
+    }
+    return y;
+  };
+  ok = publish(0);
+  while (more && ok) {
+    const uint32_t qb = pieces % nq;
+    ok = wait_for_all(bars + 8 * (B::kQE + qb), ((pieces / nq) & 1) ^ 1, abort_flag, a);
     if (!ok) break;
     const int ns = NS == 2 && w.t.ntok > a.list.tpt ? 2 : 1;
     if (lane == 0) {
-      mbar_arrive_expect_tx(bars + 8 * B::kQF, (uint32_t)(ns * C::kHalves * a.box_tokens * a.G * 128));
+      mbar_arrive_expect_tx(bars + 8 * (B::kQF + qb), (uint32_t)(ns * C::kHalves * a.box_tokens * a.G * 128));
       for (int s = 0; s < ns; ++s)
         for (int h = 0; h < C::kHalves; ++h)
-          tma_load_3d(sm + s * C::kTileBytes + h * C::kHalfBytes, &maps.q, 64 * h, w.s.head * a.G,
-                      w.t.tok0 + s * a.list.tpt, bars + 8 * B::kQF);
+          tma_load_3d(sm + s * C::kTileBytes + h * C::kHalfBytes + qb * kQBuffer, &maps.q, 64 * h, w.head * a.G,
+                      w.t.tok0 + s * a.list.tpt, bars + 8 * (B::kQF + qb));
     }
-    for (int j = 0; j < w.n; ++j) {
+    ++pieces;
+    const int n = w.n, head = w.head;
+    for (int j = 0; j < n; ++j) {
       const int cur = id;
-      if (j + 1 < w.n) id = block_of(w.first() + j + 1);
+      if (j + 1 < n) {
+        id = block_of(w.t, w.first() + j + 1);
+      } else {  // the next piece's first
+        w.next(a);
+        more = w.load();
+        id = more ? block_of(w.t, w.first()) : -1;
+      }
       const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, cur >= 0)) * bt * 128);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t st = fill % C::kStages, use = fill / C::kStages;
-        ok = wait_for_all(bars + 8 * (B::kEmpty + st), (use & 1) ^ 1, abort_flag, a);
+        ok = wait_for_all(bars + 8 * (B::kEmpty + r.st), r.ph ^ 1, abort_flag, a);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (B::kFull + st), bytes);
+        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * (B::kFull + r.st), bytes);
         __syncwarp();
         if (cur >= 0)
-          tma_load_4d(ring + st * C::kTileBytes + at, kv ? &maps.v : &maps.k, 64 * half, 0, w.s.head, cur,
-                      bars + 8 * (B::kFull + st));
-        ++fill;
+          tma_load_4d(ring + r.st * C::kTileBytes + at, kv ? &maps.v : &maps.k, 64 * half, 0, head, cur,
+                      bars + 8 * (B::kFull + r.st));
+        ++fills;
+        r.next();
       }
       if (!ok) break;
     }
+    ok = ok && publish(pieces);
   }
   if (!ok) {  // given up: wait for what was issued before the shared memory goes away
     const long long t0 = clock64();
-    for (uint32_t f = fill > (uint32_t)C::kStages ? fill - C::kStages : 0; f < fill; ++f)
+    for (uint32_t f = fills > (uint32_t)C::kStages ? fills - C::kStages : 0; f < fills; ++f)
       while (!mbar_try_wait_sleep(bars + 8 * (B::kFull + f % C::kStages), (f / C::kStages) & 1, kSpinNs) &&
              clock64() - t0 <= a.wait_cycles) {
       }
-    if (pieces)
-      while (!mbar_try_wait_sleep(bars + 8 * B::kQF, (pieces - 1) & 1, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
+    for (uint32_t q = pieces > nq ? pieces - nq : 0; q < pieces; ++q)
+      while (!mbar_try_wait_sleep(bars + 8 * (B::kQF + q % nq), (q / nq) & 1, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
       }
   }
 }
 
-// S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by one thread.
+// S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by one thread.  The
+// descriptors' low words (address and leading offset) are kept as numbers to which a step's offset is
+// added; the issuing thread has about 60 cycles for each MMA.
 template <int NS, int DP, bool BF>
 struct Mma {
   using C = Cfg<NS, DP>;
+  static constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1 KB atoms, version 1, 128-byte swizzle
+  static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24) | (BF ? (1u << 7) | (1u << 10) : 0u);
+  static __device__ __forceinline__ uint32_t lo_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+  static __device__ __forceinline__ uint32_t lo_mn(uint32_t addr) { return (addr >> 4) | ((C::kHalfBytes >> 4) << 16); }
+  static __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)lo | ((uint64_t)kHi << 32); }
   static __device__ __forceinline__ void qk(uint32_t tmem_s, uint32_t q, uint32_t k) {
-    const uint32_t idesc = idesc_f16_f32(128, kAttnKeys) | (BF ? (1u << 7) | (1u << 10) : 0u);
+    constexpr uint32_t idesc = kIdesc | ((kAttnKeys >> 3) << 17);
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
-      const uint32_t off = (uint32_t)((i / 4) * C::kHalfBytes + (i % 4) * 32);
-      tc_mma_f16(tmem_s, smem_desc_sw128(q + off, 1024), smem_desc_sw128(k + off, 1024), idesc, i > 0);
+      const uint32_t off = (uint32_t)((i / 4) * C::kHalfBytes + (i % 4) * 32) >> 4;
+      tc_mma_f16(tmem_s, desc(q + off), desc(k + off), idesc, i > 0);
     }
   }
-  static __device__ __forceinline__ void pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v, bool accumulate) {
-    const uint32_t idesc = idesc_f16_f32(128, DP) | (BF ? (1u << 7) | (1u << 10) : 0u) | (1u << 16);
+  static __device__ __forceinline__ void pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v, uint32_t accumulate) {
+    constexpr uint32_t idesc = kIdesc | ((DP >> 3) << 17) | (1u << 16);  // B contiguous along N
 #pragma unroll
     for (int i = 0; i < kAttnKeys / 16; ++i)
-      tc_mma_f16_ta(tmem_o, tmem_p + 8 * i, smem_desc_mn_sw128(v + i * 2048, C::kHalfBytes), idesc,
-                    accumulate || i > 0);
+      tc_mma_f16_ta(tmem_o, tmem_p + 8 * i, desc(v + i * (2048 >> 4)), idesc, i > 0 ? 1u : accumulate);
   }
 };
 
 template <int NS, int DP, bool BF>
-__device__ void issue(const AttnArgs &a, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag) {
+__device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag) {
   using C = Cfg<NS, DP>;
   using B = Bars<C::kStages>;
   using M = Mma<NS, DP, BF>;
-  const uint32_t ring = sm + NS * C::kTileBytes, o0 = tmem + 256;
-  uint32_t used = 0, pieces = 0, it = 0;
-  uint32_t p_seq[2] = {0, 0};
-  Walk w(a);
+  constexpr uint32_t kStep = C::kTileBytes >> 4;
+  const uint32_t ring_k = M::lo_k(sm + NS * C::kTileBytes), ring_v = M::lo_mn(sm + NS * C::kTileBytes);
+  const uint32_t o0 = tmem + 256, nq = q_buffers<NS>(a);
+  Ring<C::kStages> r;  // the next stage to be read
+  uint32_t pieces = 0, it = 0, p_par[2] = {0, 0};
   bool ok = true;
-  auto full = [&](uint32_t f) {
-    const bool r = wait_for(bars + 8 * (B::kFull + f % C::kStages), (f / C::kStages) & 1, abort_flag, a);
+  auto full = [&](const Ring<C::kStages> &x) {
+    const bool y = wait_for(bars + 8 * (B::kFull + x.st), x.ph, abort_flag, a);
     tc_fence_after();
-    return r;
+    return y;
   };
-  auto stage = [&](uint32_t f) { return ring + (f % C::kStages) * C::kTileBytes; };
-  auto release = [&](uint32_t f) { tc_commit(bars + 8 * (B::kEmpty + f % C::kStages)); };
-  for (; ok && w.load(); w.next(), ++pieces) {
-    const int n = w.n;
-    ok = wait_for(bars + 8 * B::kQF, pieces & 1, abort_flag, a);
-    if (!ok) break;
-    tc_fence_after();
+  auto release = [&](uint32_t st) { tc_commit(bars + 8 * (B::kEmpty + st)); };
+  for (; ok; ++pieces) {
+    const uint32_t d = pieces % kPieces;
+    if (!wait_for(bars + 8 * (B::kDF + d), (pieces / kPieces) & 1, abort_flag, a)) break;
+    const int n = piece[d].n;
+    const bool two = NS == 2 && piece[d].ntok > a.list.tpt;
+    if (n == 0) break;
+    mbar_arrive(bars + 8 * (B::kDE + d));
+    const uint32_t qb = pieces % nq;
+    const uint32_t q0 = M::lo_k(sm + qb * kQBuffer);
+    ok = wait_for(bars + 8 * (B::kQF + qb), (pieces / nq) & 1, abort_flag, a);
+    if (!ok || !(ok = full(r))) break;
+    uint32_t k_st = r.st;
+    r.next();
     if (NS == 2) {
-      const int ns = w.t.ntok > a.list.tpt ? 2 : 1;
-      if (!(ok = full(used))) break;
-      for (int s = 0; s < ns; ++s) {
-        M::qk(tmem + 128 * s, sm + s * C::kTileBytes, stage(used));
-        tc_commit(bars + 8 * (B::kSF + s));
+      M::qk(tmem, q0, ring_k + k_st * kStep);
+      tc_commit(bars + 8 * B::kSF);
+      if (two) {
+        M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
+        tc_commit(bars + 8 * (B::kSF + 1));
       }
-      release(used);
+      release(k_st);
       if (n == 1) tc_commit(bars + 8 * B::kQE);
-      for (int j = 0; j < n && ok; ++j, used += 2) {
-        if (!(ok = full(used + 1))) break;
-        for (int s = 0; s < ns && ok; ++s) {
-          if (!(ok = wait_for(bars + 8 * (B::kPF + s), p_seq[s] & 1, abort_flag, a))) break;
-          ++p_seq[s];
+      for (int j = 0; j < n; ++j) {
+        const bool more = j + 1 < n;
+        if (!(ok = full(r))) break;
+        const uint32_t v_st = r.st, v = ring_v + v_st * kStep;
+        r.next();
+        if (!(ok = wait_for(bars + 8 * B::kPF, p_par[0], abort_flag, a))) break;
+        p_par[0] ^= 1;
+        tc_fence_after();
+        M::pv(o0, tmem, v, j > 0);
+        if (more) {
+          if (!(ok = full(r))) break;
+          k_st = r.st;
+          r.next();
+          M::qk(tmem, q0, ring_k + k_st * kStep);
+          tc_commit(bars + 8 * B::kSF);
+        } else {
+          tc_commit(bars + 8 * B::kOD);
+        }
+        if (two) {
+          if (!(ok = wait_for(bars + 8 * (B::kPF + 1), p_par[1], abort_flag, a))) break;
+          p_par[1] ^= 1;
           tc_fence_after();
-          M::pv(o0 + 128 * s, tmem + 128 * s, stage(used + 1), j > 0);
-          if (j + 1 < n) {
-            if (s == 0 && !(ok = full(used + 2))) break;
-            M::qk(tmem + 128 * s, sm + s * C::kTileBytes, stage(used + 2));
-            tc_commit(bars + 8 * (B::kSF + s));
+          M::pv(o0 + 128, tmem + 128, v, j > 0);
+          if (more) {
+            M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
+            tc_commit(bars + 8 * (B::kSF + 1));
           } else {
-            tc_commit(bars + 8 * (B::kOD + s));
+            tc_commit(bars + 8 * (B::kOD + 1));
           }
         }
-        if (!ok) break;
-        release(used + 1);
-        if (j + 1 < n) {
-          release(used + 2);
+        release(v_st);
+        if (more) {
+          release(k_st);
           if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
         }
       }
     } else {
-      if (!(ok = full(used))) break;
-      M::qk(tmem + 128 * (it & 1), sm, stage(used));
+      M::qk(tmem + 128 * (it & 1), q0, ring_k + k_st * kStep);
       tc_commit(bars + 8 * (B::kSF + (it & 1)));
-      release(used);
-      if (n == 1) tc_commit(bars + 8 * B::kQE);
-      for (int j = 0; j < n; ++j, used += 2, ++it) {
-        const uint32_t b = it & 1;
+      release(k_st);
+      if (n == 1) tc_commit(bars + 8 * (B::kQE + qb));
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t b = it & 1, v_st = r.st;
+        const Ring<C::kStages> rv = r;
+        r.next();
         if (j + 1 < n) {
-          if (!(ok = full(used + 2))) break;
-          M::qk(tmem + 128 * (b ^ 1), sm, stage(used + 2));
+          if (!(ok = full(r))) break;
+          k_st = r.st;
+          r.next();
+          M::qk(tmem + 128 * (b ^ 1), q0, ring_k + k_st * kStep);
           tc_commit(bars + 8 * (B::kSF + (b ^ 1)));
-          release(used + 2);
-          if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+          release(k_st);
+          if (j + 2 == n) tc_commit(bars + 8 * (B::kQE + qb));
         }
-        if (!(ok = full(used + 1))) break;
-        if (!(ok = wait_for(bars + 8 * (B::kPF + b), p_seq[b] & 1, abort_flag, a))) break;
-        ++p_seq[b];
+        if (!(ok = full(rv))) break;
+        if (!(ok = wait_for(bars + 8 * (B::kPF + b), (it >> 1) & 1, abort_flag, a))) break;
         tc_fence_after();
-        M::pv(o0, tmem + 128 * b, stage(used + 1), j > 0);
+        M::pv(o0, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
         tc_commit(bars + 8 * (B::kOD + b));
-        release(used + 1);
+        release(v_st);
       }
     }
   }
@@ -438,7 +572,7 @@ __device__ void redo_rows(const AttnArgs &a, unsigned flagged, const Row &r, boo
 }
 
 template <int NS, int DP, bool BF, bool EXTRA>
-__device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag,
+__device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem, volatile int *abort_flag,
                        volatile int *last_flag) {
   using C = Cfg<NS, DP>;
   using B = Bars<C::kStages>;
@@ -447,7 +581,8 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
   const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
   const uint32_t tmem_o = tmem + 256 + 128 * s + lanes;
   uint32_t it = 0;        // key tiles of this stream so far
-  uint32_t v_fill = 1;    // ring position of the current tile's V
+  Ring<C::kStages> rv;    // the current tile's V
+  rv.next();
   // NS == 1: P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked
   // the tile before on the same barrier is known to be complete (the scores of tile t or t + 1 were issued
   // behind it) and the one after waits for this thread, so the parity cannot be mistaken.
@@ -462,42 +597,55 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
     return wait_for_all(bars + 8 * (B::kJoin + s), joins++ & 1, abort_flag, a);
   };
   const float sl2 = a.scale * kLog2e;
-  Walk w(a);
-  bool ok = true;
-  for (; ok && w.load(); w.next()) {
-    const int n = w.n;
-    const int ntok = min(a.list.tpt, w.t.ntok - s * a.list.tpt), nrows = ntok * a.G;
+  const int row_tok = s * a.list.tpt + row / a.G;
+  uint32_t pieces = 0;
+  bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
+  RowBound rb{0, 0, -1, 0}, rb_ahead{0, 0, -1, 0};
+  // the row's keys in a piece, fetched while the piece before is in work
+  auto bound_of = [&](const volatile Piece &x) {
+    if (x.n == 0 || !x.fresh) return rb;
+    return row_tok < min(x.ntok, (s + 1) * a.list.tpt) ? a.bounds[x.tok0 + row_tok] : RowBound{0, 0, -1, 0};
+  };
+  if (ok) rb_ahead = bound_of(piece[0]);
+  for (; ok; ++pieces) {
+    const volatile Piece &w = piece[pieces % kPieces];
+    const int n = w.n, klo = w.klo, khi = w.khi, first = w.first;
+    if (n == 0) break;
+    const int ntok = min(a.list.tpt, w.ntok - s * a.list.tpt), nrows = ntok * a.G;
+    rb = rb_ahead;
+    const uint32_t dn = (pieces + 1) % kPieces;
     if (NS == 2 && ntok <= 0) {
-      v_fill += 2 * n;
+      for (int i = 0; i < 2 * n; ++i) rv.next();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+      if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
+      rb_ahead = bound_of(piece[dn]);
       continue;
     }
     Row r;
     r.valid = row < nrows;
-    r.tok = w.t.tok0 + s * a.list.tpt + row / a.G;
-    r.head = w.s.head * a.G + row % a.G;
-    RowBound rb{0, 0, -1, 0};
-    if (r.valid) rb = a.bounds[r.tok];
-    r.lo = max(rb.lo, w.t.klo);
-    r.hi = min(rb.hi, w.t.khi);
+    r.tok = w.tok0 + row_tok;
+    r.head = w.head * a.G + row % a.G;
+    r.lo = max(rb.lo, klo);
+    r.hi = min(rb.hi, khi);
     r.pos = rb.pos;
-    r.trow = w.t.trow;
+    r.trow = w.trow;
     const bool active = 32 * quarter < nrows;
     const float slope = EXTRA && a.slopes && r.valid ? a.slopes[r.head] * kLog2e : 0.f;
     float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j, ++it, v_fill += 2) {
+    for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
       const uint32_t buf = NS == 2 ? (uint32_t)s : (it & 1);
       const uint32_t par = NS == 2 ? (it & 1) : ((it >> 1) & 1);
       const uint32_t ts = tmem + 128 * buf + lanes;
-      const int base = (w.first() + j) * kAttnKeys;
+      const int base = (first + j) * kAttnKeys;
       if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
       tc_fence_after();
-      if (s == 0 && (base < w.t.klo || base + kAttnKeys > w.t.khi)) {
+      if (s == 0 && (base < klo || base + kAttnKeys > khi)) {
         // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
         // times what the memory holds may be NaN
-        if (!(ok = wait_for_all(bars + 8 * (B::kFull + v_fill % C::kStages), (v_fill / C::kStages) & 1, abort_flag, a)))
-          break;
-        if (base + row < w.t.klo || base + row >= w.t.khi) {
-          uint8_t *vrow = smp + (NS + v_fill % C::kStages) * C::kTileBytes + row * 128;
+        if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
+        if (base + row < klo || base + row >= khi) {
+          uint8_t *vrow = smp + (NS + rv.st) * C::kTileBytes + row * 128;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
@@ -591,6 +739,9 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
       if (lane == 0) mbar_arrive(bars + 8 * (B::kPF + buf));
     }
     if (!ok) break;
+    // the next piece has been handed over: its first scores may be on their way
+    if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
+    rb_ahead = bound_of(piece[dn]);
     // the piece's last product
     if (NS == 2) {
       ok = wait_for_all(bars + 8 * (B::kOD + s), o_done & 1, abort_flag, a);
@@ -605,8 +756,9 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
       tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
       tmem_wait_ld();
     };
-    const bool merge = w.t.merge && !a.to_prefix && a.prefix_o;
-    if (w.whole()) {
+    const bool merge = w.merge;
+    const int c0 = w.c0, c1 = w.c1;
+    if (c0 == c1) {
       if (active) {
         const bool again = emit_row<DP, BF>(a, r, merge, m, l, from_tmem);
         const unsigned flagged = __ballot_sync(0xffffffffu, again);
@@ -614,11 +766,6 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
       }
     } else {
       // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up
-      const int cum = a.list.cum[w.s.tile], cost = w.t.kv1 - w.t.kv0;
-      const long long W = (long long)a.list.meta[1] * a.Hkv;
-      const long long ub = (long long)cum * a.Hkv + (long long)w.s.head * cost;
-      const long long P = min((long long)a.ctas, W);
-      const int c0 = (int)(((ub + 1) * P - 1) / W), c1 = (int)(((ub + cost) * P - 1) / W);
       auto slot_of = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * NS + s; };
       constexpr int kPart = DP * 128;
       const size_t my = slot_of(blockIdx.x);
@@ -682,6 +829,8 @@ __device__ void soften(const AttnArgs &a, uint8_t *smp, uint32_t sm, uint32_t ba
         }
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
   }
 }
 
@@ -694,6 +843,7 @@ __global__ void __launch_bounds__(Cfg<NS, DP>::kThreads, 1) attn_kernel(const __
   __shared__ __align__(8) uint64_t bar_mem[B::kNum];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, last_flag[2];
+  __shared__ Piece piece[kPieces];
   const int warp = threadIdx.x >> 5;
   const uint32_t bars = smem_u32(bar_mem), sm = smem_u32(smem);
   if (threadIdx.x == 0) {
@@ -701,15 +851,19 @@ __global__ void __launch_bounds__(Cfg<NS, DP>::kThreads, 1) attn_kernel(const __
       mbar_init(bars + 8 * (B::kFull + i), 1);
       mbar_init(bars + 8 * (B::kEmpty + i), 1);
     }
-    mbar_init(bars + 8 * B::kQF, 1);
-    mbar_init(bars + 8 * B::kQE, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (B::kQF + i), 1);
+      mbar_init(bars + 8 * (B::kQE + i), 1);
       mbar_init(bars + 8 * (B::kSF + i), 1);
       mbar_init(bars + 8 * (B::kPF + i), 4);
       mbar_init(bars + 8 * (B::kOD + i), 1);
       mbar_init(bars + 8 * (B::kJoin + i), 4);
     }
     mbar_init(bars + 8 * B::kDrain, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bars + 8 * (B::kDF + i), 1);
+      mbar_init(bars + 8 * (B::kDE + i), C::kSoftWarps + 1);  // the softmax warps and the MMA thread
+    }
     abort_flag = (sm & 1023u) != 0u;  // the swizzled tiles are 1 KB-aligned
     if (abort_flag) atomicOr(a.err, kAttnErrWait);
     fence_mbar_init();
@@ -722,13 +876,17 @@ __global__ void __launch_bounds__(Cfg<NS, DP>::kThreads, 1) attn_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (!abort_flag) {
-    if (warp < C::kSoftWarps)
-      soften<NS, DP, BF, EXTRA>(a, smem, sm, bars, tmem, &abort_flag, last_flag);
-    else if (warp == C::kSoftWarps)
-      produce<NS, DP>(a, maps, sm, bars, &abort_flag);
-    else if ((threadIdx.x & 31) == 0)
-      issue<NS, DP, BF>(a, sm, bars, tmem, &abort_flag);
+  if (warp < C::kSoftWarps) {
+    if (NS == 2) regs_inc<kRegsSoft>();
+    if (!abort_flag) soften<NS, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+  } else {
+    if (NS == 2) regs_dec<kRegsOther>();
+    if (abort_flag) {
+    } else if (warp == C::kSoftWarps) {
+      produce<NS, DP>(a, maps, piece, sm, bars, &abort_flag);
+    } else if (warp == C::kSoftWarps + 1 && (threadIdx.x & 31) == 0) {
+      issue<NS, DP, BF>(a, piece, sm, bars, tmem, &abort_flag);
+    }
   }
   __syncwarp();
   tc_fence_before();

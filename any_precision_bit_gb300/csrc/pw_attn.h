@@ -12,6 +12,9 @@ namespace pw {
 constexpr int kAttnKeys = 128;         // keys of one key/value tile, the unit of work
 constexpr int kAttnRows = 128;         // query rows of one tile (tensor-memory lanes of an MMA)
 constexpr int kAttnMaxRequests = 4096;
+// Units that a (tile, head) counts for beside its key tiles when the work is divided: the queries' way in,
+// the pipeline's filling and draining, and the result's way out take about as long.
+constexpr int kAttnPieceCost = 2;
 
 // Findings of the device side, reported by pw_attn_check.
 enum {
@@ -39,16 +42,16 @@ struct AttnTile {
 
 // Where a CTA's share of the work begins.
 struct AttnStart {
-  int tile, head, off, n;  // key tile `off` of (tile, head); n key tiles in all
+  int tile, head, off, n;  // unit `off` of (tile, head); n units in all
 };
 
-// One list of work.  The units are key tiles, in the order (tile, head, key tile); of the W units
-// CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W if that is less (the rest idle).
+// One list of work.  In the order (tile, head), each has kAttnPieceCost units without keys and then one for
+// each of its key tiles; of the W units CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W if that is less (the rest idle).
 struct AttnList {
   AttnTile *tiles;
-  int *cum;          // [tiles + 1] key tiles of one head before each tile
+  int *cum;          // [tiles + 1] units of one head before each tile
   AttnStart *start;  // [P]
-  int *meta;         // [0] tiles, [1] key tiles of one head
+  int *meta;         // [0] tiles, [1] units of one head
   int tpt;           // tokens of one 128-row tile
   int streams;       // 128-row tiles of one AttnTile (1 or 2)
   int max_tiles;

@@ -151,7 +151,7 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
     for (AttnList *l : {&p.requests, &p.groups}) {
       if (l == &p.groups && d.max_shared_tokens == 0) continue;
       l->max_tiles = d.max_tokens + d.max_requests + 1;
-      ok = ok && alloc(a, &l->tiles, (size_t)l->max_tiles) && alloc(a, &l->cum, (size_t)l->max_tiles + 1) &&
+      ok = ok && alloc(a, &l->tiles, (size_t)l->max_tiles + 1) && alloc(a, &l->cum, (size_t)l->max_tiles + 1) &&
            alloc(a, &l->start, ctas) && alloc(a, &l->meta, 2);
     }
   }

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     t.kv1 = hi > 0 ? (hi - 1) / kAttnKeys + 1 : t.kv0 + 1;
     if (lane == 0) {
       a.list.tiles[i] = t;
-      a.list.cum[i + 1] = t.kv1 - t.kv0;
+      a.list.cum[i + 1] = t.kv1 - t.kv0 + kAttnPieceCost;
     }
   }
   __syncthreads();
