@@ -312,9 +312,10 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, Piece *piece, u
   }
 }
 
-// S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by one thread.  The
-// descriptors' low words (address and leading offset) are kept as numbers to which a step's offset is
-// added; the issuing thread has about 60 cycles for each MMA.
+// S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by an elected lane of the
+// converged warp, so that the operands stay in the uniform datapath: issued by a lane that ran the loop
+// alone an MMA took 150 cycles, against the 64 that the tensor cores need for one.  The descriptors' low
+// words (address and leading offset) are kept as numbers to which a step's offset is added.
 template <int NS, int DP, bool BF>
 struct Mma {
   using C = Cfg<NS, DP>;
@@ -348,77 +349,94 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
   const uint32_t ring_k = M::lo_k(sm + NS * C::kTileBytes), ring_v = M::lo_mn(sm + NS * C::kTileBytes);
   const uint32_t o0 = tmem + 256, nq = q_buffers<NS>(a);
   Ring<C::kStages> r;  // the next stage to be read
-  uint32_t pieces = 0, it = 0, p_par[2] = {0, 0};
+  uint32_t pieces = 0, it = 0, p_par = 0, p2_par = 0;
   bool ok = true;
-  auto full = [&](const Ring<C::kStages> &x) {
-    const bool y = wait_for(bars + 8 * (B::kFull + x.st), x.ph, abort_flag, a);
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    const bool y = wait_for_all(bars + 8 * bar, par, abort_flag, a);
     tc_fence_after();
     return y;
   };
+  auto full = [&](const Ring<C::kStages> &x) { return wait(B::kFull + x.st, x.ph); };
   auto release = [&](uint32_t st) { tc_commit(bars + 8 * (B::kEmpty + st)); };
   for (; ok; ++pieces) {
     const uint32_t d = pieces % kPieces;
-    if (!wait_for(bars + 8 * (B::kDF + d), (pieces / kPieces) & 1, abort_flag, a)) break;
-    const int n = piece[d].n;
-    const bool two = NS == 2 && piece[d].ntok > a.list.tpt;
+    if (!wait(B::kDF + d, (pieces / kPieces) & 1)) break;
+    const int n = __shfl_sync(0xffffffffu, piece[d].n, 0);
+    const bool two = NS == 2 && __shfl_sync(0xffffffffu, piece[d].ntok, 0) > a.list.tpt;
     if (n == 0) break;
-    mbar_arrive(bars + 8 * (B::kDE + d));
+    if (elect_one()) mbar_arrive(bars + 8 * (B::kDE + d));
+    __syncwarp();
     const uint32_t qb = pieces % nq;
     const uint32_t q0 = M::lo_k(sm + qb * kQBuffer);
-    ok = wait_for(bars + 8 * (B::kQF + qb), (pieces / nq) & 1, abort_flag, a);
-    if (!ok || !(ok = full(r))) break;
+    ok = wait(B::kQF + qb, (pieces / nq) & 1) && full(r);
+    if (!ok) break;
     uint32_t k_st = r.st;
     r.next();
     if (NS == 2) {
-      M::qk(tmem, q0, ring_k + k_st * kStep);
-      tc_commit(bars + 8 * B::kSF);
-      if (two) {
-        M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
-        tc_commit(bars + 8 * (B::kSF + 1));
+      if (elect_one()) {
+        M::qk(tmem, q0, ring_k + k_st * kStep);
+        tc_commit(bars + 8 * B::kSF);
+        if (two) {
+          M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
+          tc_commit(bars + 8 * (B::kSF + 1));
+        }
+        release(k_st);
+        if (n == 1) tc_commit(bars + 8 * B::kQE);
       }
-      release(k_st);
-      if (n == 1) tc_commit(bars + 8 * B::kQE);
+      __syncwarp();
       for (int j = 0; j < n; ++j) {
         const bool more = j + 1 < n;
         if (!(ok = full(r))) break;
         const uint32_t v_st = r.st, v = ring_v + v_st * kStep;
         r.next();
-        if (!(ok = wait_for(bars + 8 * B::kPF, p_par[0], abort_flag, a))) break;
-        p_par[0] ^= 1;
-        tc_fence_after();
-        M::pv(o0, tmem, v, j > 0);
+        if (!(ok = wait(B::kPF, p_par))) break;
         if (more) {
           if (!(ok = full(r))) break;
           k_st = r.st;
           r.next();
-          M::qk(tmem, q0, ring_k + k_st * kStep);
-          tc_commit(bars + 8 * B::kSF);
-        } else {
-          tc_commit(bars + 8 * B::kOD);
         }
-        if (two) {
-          if (!(ok = wait_for(bars + 8 * (B::kPF + 1), p_par[1], abort_flag, a))) break;
-          p_par[1] ^= 1;
-          tc_fence_after();
-          M::pv(o0 + 128, tmem + 128, v, j > 0);
+        if (elect_one()) {
+          M::pv(o0, tmem, v, j > 0);
           if (more) {
-            M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
-            tc_commit(bars + 8 * (B::kSF + 1));
+            M::qk(tmem, q0, ring_k + k_st * kStep);
+            tc_commit(bars + 8 * B::kSF);
           } else {
-            tc_commit(bars + 8 * (B::kOD + 1));
+            tc_commit(bars + 8 * B::kOD);
+          }
+          if (!two) {
+            release(v_st);
+            if (more) release(k_st);
+            if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
           }
         }
-        release(v_st);
-        if (more) {
-          release(k_st);
-          if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+        __syncwarp();
+        if (two) {
+          if (!(ok = wait(B::kPF + 1, p2_par))) break;
+          p2_par ^= 1;
+          if (elect_one()) {
+            M::pv(o0 + 128, tmem + 128, v, j > 0);
+            if (more) {
+              M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
+              tc_commit(bars + 8 * (B::kSF + 1));
+            } else {
+              tc_commit(bars + 8 * (B::kOD + 1));
+            }
+            release(v_st);
+            if (more) release(k_st);
+            if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+          }
+          __syncwarp();
         }
+        p_par ^= 1;
       }
     } else {
-      M::qk(tmem + 128 * (it & 1), q0, ring_k + k_st * kStep);
-      tc_commit(bars + 8 * (B::kSF + (it & 1)));
-      release(k_st);
-      if (n == 1) tc_commit(bars + 8 * (B::kQE + qb));
+      if (elect_one()) {
+        M::qk(tmem + 128 * (it & 1), q0, ring_k + k_st * kStep);
+        tc_commit(bars + 8 * (B::kSF + (it & 1)));
+        release(k_st);
+        if (n == 1) tc_commit(bars + 8 * (B::kQE + qb));
+      }
+      __syncwarp();
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t b = it & 1, v_st = r.st;
         const Ring<C::kStages> rv = r;
@@ -427,22 +445,28 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
           if (!(ok = full(r))) break;
           k_st = r.st;
           r.next();
-          M::qk(tmem + 128 * (b ^ 1), q0, ring_k + k_st * kStep);
-          tc_commit(bars + 8 * (B::kSF + (b ^ 1)));
-          release(k_st);
-          if (j + 2 == n) tc_commit(bars + 8 * (B::kQE + qb));
+          if (elect_one()) {
+            M::qk(tmem + 128 * (b ^ 1), q0, ring_k + k_st * kStep);
+            tc_commit(bars + 8 * (B::kSF + (b ^ 1)));
+            release(k_st);
+            if (j + 2 == n) tc_commit(bars + 8 * (B::kQE + qb));
+          }
+          __syncwarp();
         }
         if (!(ok = full(rv))) break;
-        if (!(ok = wait_for(bars + 8 * (B::kPF + b), (it >> 1) & 1, abort_flag, a))) break;
-        tc_fence_after();
-        M::pv(o0, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
-        tc_commit(bars + 8 * (B::kOD + b));
-        release(v_st);
+        if (!(ok = wait(B::kPF + b, (it >> 1) & 1))) break;
+        if (elect_one()) {
+          M::pv(o0, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
+          tc_commit(bars + 8 * (B::kOD + b));
+          release(v_st);
+        }
+        __syncwarp();
       }
     }
   }
   // nothing of the tensor cores is in flight when tensor memory is freed
-  tc_commit(bars + 8 * B::kDrain);
+  if (elect_one()) tc_commit(bars + 8 * B::kDrain);
+  __syncwarp();
   const long long t0 = clock64();
   while (!mbar_try_wait_sleep(bars + 8 * B::kDrain, 0, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
   }
@@ -884,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<NS, DP>::kThreads, 1) attn_kernel(const __
     if (abort_flag) {
     } else if (warp == C::kSoftWarps) {
       produce<NS, DP>(a, maps, piece, sm, bars, &abort_flag);
-    } else if (warp == C::kSoftWarps + 1 && (threadIdx.x & 31) == 0) {
+    } else if (warp == C::kSoftWarps + 1) {
       issue<NS, DP, BF>(a, piece, sm, bars, tmem, &abort_flag);
     }
   }
