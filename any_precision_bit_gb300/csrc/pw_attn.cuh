@@ -1,0 +1,1183 @@
+// pw_attn.cuh -- attention over the paged key/value cache: the kernel and its launch, instantiated form by
+// form in pw_attn_two.cu, pw_attn_one.cu and pw_attn_spread.cu.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "pw_attn.h"
+#include "pw_device.cuh"
+#include "pw_tc.cuh"
+
+namespace pw {
+
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+  return __half22float2(h);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  uint32_t r;
+  if (BF)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One row (token t, query head h) over the keys [lo, hi) of its table row, by one warp: lane l
+// holds elements 4 l .. 4 l + 3 of the head.  The running maximum and sum of a softmax in fp32;
+// only visible keys and values are read.  acc is the normalised output, *lse the natural
+// log-sum-exp (-inf and zeros for a row without keys).
+template <bool BF>
+__device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, int trow, int pos, float (&acc)[4],
+                              float *lse) {
+  const int lane = threadIdx.x & 31, d = 4 * lane;
+  const bool mine = d < a.D;
+  float qf[4] = {0.f, 0.f, 0.f, 0.f};
+  if (mine) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(a.q + t * a.q_token + h * a.q_head + d);
+    const float2 x = unpack2<BF>(w.x), y = unpack2<BF>(w.y);
+    qf[0] = x.x, qf[1] = x.y, qf[2] = y.x, qf[3] = y.y;
+  }
+  const int hk = h / a.G, mask = (1 << a.log_bt) - 1;
+  const float slope = a.slopes ? a.slopes[h] : 0.f;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+  for (int j = lo; j < hi; ++j) {
+    const int page = j >> a.log_bt;
+    const int id = trow >= 0 && page < a.table_stride ? a.table[(size_t)trow * a.table_stride + page] : -1;
+    uint2 kw{0u, 0u}, vw{0u, 0u};
+    if (mine && id >= 0 && id < a.n_blocks) {
+      const int64_t at = id * a.block_stride + (j & mask) * a.token_stride + hk * a.head_stride + d;
+      kw = *reinterpret_cast<const uint2 *>(a.kc + at);
+      vw = *reinterpret_cast<const uint2 *>(a.vc + at);
+    }
+    const float2 k0 = unpack2<BF>(kw.x), k1 = unpack2<BF>(kw.y);
+    float s = qf[0] * k0.x + qf[1] * k0.y + qf[2] * k1.x + qf[3] * k1.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s *= a.scale;
+    if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
+    if (a.slopes) s -= slope * fabsf((float)(pos - j));
+    const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn;
+    const float f = expf(m - ms), p = expf(s - ms);
+    m = mn;
+    l = l * f + p;
+    const float2 v0 = unpack2<BF>(vw.x), v1 = unpack2<BF>(vw.y);
+    acc[0] = acc[0] * f + p * v0.x;
+    acc[1] = acc[1] * f + p * v0.y;
+    acc[2] = acc[2] * f + p * v1.x;
+    acc[3] = acc[3] * f + p * v1.y;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] *= inv;
+  *lse = m + logf(l);
+}
+
+// ------------------------------------------------------------------ the tensor-core kernel
+constexpr int kSmemRing = 227 * 1024 - 3072;  // dynamic shared memory: query tiles and the K/V ring
+constexpr uint32_t kTmemColsAttn = 512;
+constexpr uint32_t kSpinNs = 2000;
+
+constexpr int kJoinRows = 8;  // rows added up at a time
+
+template <int FORM, int DP>
+struct Cfg {
+  static constexpr int NS = FORM == kTwo ? 2 : 1;
+  static constexpr int kHalves = DP / 64;             // 64-element column blocks of a head
+  static constexpr int kHalfBytes = 128 * 128;        // 128 rows of 128 bytes
+  static constexpr int kTileBytes = kHalves * kHalfBytes;
+  // kSpread: the quarters' results side by side, rows padded against bank conflicts
+  static constexpr int kScratchRow = DP + 4;
+  static constexpr int kScratch = FORM == kSpread ? 4 * kJoinRows * kScratchRow * 4 + 4 * kSpreadRows * 8 : 0;
+  static constexpr int kStages = (kSmemRing - NS * kTileBytes - kScratch) / kTileBytes;
+  static constexpr int kScratchAt = (NS + kStages) * kTileBytes;
+  static constexpr int kSmem = kScratchAt + kScratch;
+  static constexpr int kSoftWarps = 4 * NS;
+  // Producer warps: one for the keys and one for the values, two for each where the memory sets the pace (a
+  // tensor copy takes its lane about 60 cycles, and 16-token blocks make 32 of them for a key tile).
+  static constexpr int kProducers = FORM == kSpread ? 4 : 2;
+  static constexpr int kMmaWarp = kSoftWarps + kProducers;
+  // softmax, producer and MMA warps, and (two tiles) an idle warp that completes its warpgroup
+  static constexpr int kThreads = FORM == kTwo ? 384 : 32 * (kMmaWarp + 1);
+};
+// Two tiles: 384 threads of 168 registers at launch, of which the softmax warps, which hold 128 scores
+// each, need more: 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kRegsSoft = 224, kRegsOther = 56;
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// A piece of work as the producer hands it to the other warps: consecutive key tiles of one (tile, head).
+struct Piece {
+  int n, first;  // key tiles, and the first one (n = 0: no more pieces)
+  int head, tok0, ntok, trow, klo, khi;  // as in AttnTile; head of the keys
+  int fresh;     // other rows than the last piece's
+  int merge;     // merge with the rows' results over their shared prefix
+  int c0, c1;    // CTAs of the (tile, head)'s first and last key tile; equal: the piece is all of it
+};
+constexpr int kPieces = 4;  // pieces handed over ahead
+
+// mbarriers
+template <int STAGES>
+struct Bars {
+  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kNum = kDE + kPieces };
+};
+
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, kSpinNs)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > a.wait_cycles) break;
+  }
+  *abort_flag = 1;
+  atomicOr(a.err, kAttnErrWait);
+  return false;
+}
+__device__ __forceinline__ bool wait_for_all(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag, a));
+}
+
+// A CTA's way through its units: pieces of consecutive key tiles of one (tile, head).  The tile after
+// the current one is fetched ahead of its use.
+__device__ __forceinline__ AttnTile load_tile(const AttnTile *p) {
+  const int4 x = reinterpret_cast<const int4 *>(p)[0], y = reinterpret_cast<const int4 *>(p)[1];
+  AttnTile t;
+  t.tok0 = x.x, t.ntok = x.y, t.trow = x.z, t.klo = x.w;
+  t.khi = y.x, t.kv0 = y.y, t.kv1 = y.z, t.merge = y.w;
+  return t;
+}
+struct Walk {
+  int tile, head, off, left;  // off and left in units (kAttnPieceCost of them lead each (tile, head))
+  AttnTile t, ahead;
+  int j0, n;  // first key tile of this piece within the tile's, and their number
+  bool fresh; // the tile is another than the last piece's
+  __device__ __forceinline__ explicit Walk(const AttnArgs &a) {
+    const AttnStart s = a.list.start[blockIdx.x];
+    tile = s.tile, head = s.head, off = s.off, left = s.n;
+    fresh = true;
+    if (left > 0) {
+      t = load_tile(a.list.tiles + tile);
+      ahead = load_tile(a.list.tiles + tile + 1);
+    }
+  }
+  __device__ __forceinline__ bool load() {
+    if (off < kAttnPieceCost) {
+      const int skip = min(kAttnPieceCost - off, left);
+      off += skip;
+      left -= skip;
+    }
+    if (left <= 0) return false;
+    j0 = off - kAttnPieceCost;
+    n = min(t.kv1 - t.kv0 - j0, left);
+    return true;
+  }
+  __device__ __forceinline__ void next(const AttnArgs &a) {
+    left -= n;
+    off += n;
+    fresh = false;
+    if (off == t.kv1 - t.kv0 + kAttnPieceCost) {
+      off = 0;
+      if (++head == a.Hkv) {
+        head = 0;
+        ++tile;
+        fresh = true;
+        t = ahead;
+        if (left > 0) ahead = load_tile(a.list.tiles + tile + 1);
+      }
+    }
+  }
+  __device__ __forceinline__ int first() const { return t.kv0 + j0; }
+  __device__ __forceinline__ void describe(const AttnArgs &a, Piece *p) const {
+    int c0 = 0, c1 = 0;
+    if (n != t.kv1 - t.kv0) {
+      const int cost = t.kv1 - t.kv0 + kAttnPieceCost;
+      const long long W = (long long)a.list.meta[1] * a.Hkv, P = min((long long)a.ctas, W);
+      const long long ub = (long long)a.list.cum[tile] * a.Hkv + (long long)head * cost;
+      c0 = (int)(((ub + kAttnPieceCost + 1) * P - 1) / W);
+      c1 = (int)(((ub + cost) * P - 1) / W);
+    }
+    *p = Piece{n, first(), head, t.tok0, t.ntok, t.trow, t.klo, t.khi, fresh, t.merge && !a.to_prefix, c0, c1};
+  }
+};
+
+// Position in the ring of K/V stages.
+template <int STAGES>
+struct Ring {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == STAGES) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Query buffers.  Where the boxes leave room (one stream: 64 of a tile's 128 rows; kSpread: 16 of each
+// quarter's 32) a second box is kept behind the first, so that the next piece's queries are loaded while
+// the current one's are in use.  The MMAs read 128 rows from either; what lies between or behind a box's
+// rows gives scores of rows that nobody has.
+template <int FORM>
+__device__ __forceinline__ uint32_t q_buffers(const AttnArgs &a) {
+  const int rows = a.box_tokens * a.G;
+  return FORM == kTwo ? 1u : FORM == kOne ? (rows <= 64 ? 2u : 1u) : (rows <= 16 ? 2u : 1u);
+}
+template <int FORM>
+constexpr uint32_t kQBufferStep = FORM == kSpread ? 16 * 128 : 64 * 128;  // bytes between the two buffers
+
+// A producer warp: the keys (kv = 0) or values of every key tile, or every other box of them; the first of
+// the warps also loads the queries and hands the pieces over.
+template <int FORM, int DP>
+__device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece *piece, uint32_t sm, uint32_t bars,
+                        volatile int *abort_flag) {
+  using C = Cfg<FORM, DP>;
+  constexpr int NS = C::NS;
+  using B = Bars<C::kStages>;
+  constexpr int kShare = C::kProducers / 2;  // warps that share a tile's boxes
+  const int lane = threadIdx.x & 31, kv = self / kShare, share = self % kShare;
+  const bool leads = self == 0;
+  const int bt = 1 << a.log_bt, ppt = kAttnKeys >> a.log_bt;  // blocks of a key tile
+  const int page = lane % ppt, half = lane / ppt;             // this lane's box
+  const bool mine = half < C::kHalves;
+  const bool loads = mine && lane % kShare == share;
+  const uint32_t ring = sm + NS * C::kTileBytes;
+  const uint32_t at = (uint32_t)(half * C::kHalfBytes + page * bt * 128);
+  const uint32_t nq = q_buffers<FORM>(a);
+  const void *map = kv ? &maps.v : &maps.k;
+  uint32_t tiles = 0, pieces = 0;
+  Ring<C::kStages> r;
+  if (kv) r.next();
+  Walk w(a);
+  bool ok = true;
+  // the block of this lane's box of a key tile; -1: none of its keys counts
+  auto block_of = [&](const AttnTile &t, int kt) {
+    const int key0 = kt * kAttnKeys + page * bt;
+    if (!mine || key0 >= t.khi || key0 + bt <= t.klo) return -1;
+    const int p = key0 >> a.log_bt;
+    int id = -1;
+    if (t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)t.trow * a.table_stride + p];
+    return id >= 0 && id < a.n_blocks ? id : a.n_blocks;  // out of the map's range: zeros
+  };
+  bool more = w.load();
+  int id = more ? block_of(w.t, w.first()) : -1;
+  // hand over piece `i`, the one the walk is at (or the end)
+  auto publish = [&](uint32_t i) {
+    const uint32_t d = i % kPieces;
+    const bool y = wait_for_all(bars + 8 * (B::kDE + d), ((i / kPieces) & 1) ^ 1, abort_flag, a);
+    if (y && lane == 0) {
+      if (more)
+        w.describe(a, piece + d);
+      else
+        piece[d].n = 0;
+      mbar_arrive(bars + 8 * (B::kDF + d));
+    }
+    return y;
+  };
+  if (leads) ok = publish(0);
+  while (more && ok) {
+    if (leads) {
+      const uint32_t qb = pieces % nq;
+      ok = wait_for_all(bars + 8 * (B::kQE + qb), ((pieces / nq) & 1) ^ 1, abort_flag, a);
+      if (!ok) break;
+      const int ns = NS == 2 && w.t.ntok > a.list.tpt ? 2 : 1;
+      if (lane == 0) {
+        const int copies = FORM == kSpread ? 4 : ns;
+        mbar_arrive_expect_tx(bars + 8 * (B::kQF + qb), (uint32_t)(copies * C::kHalves * a.box_tokens * a.G * 128));
+        for (int s = 0; s < copies; ++s)
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(sm + s * (FORM == kSpread ? 32 * 128 : C::kTileBytes) + h * C::kHalfBytes +
+                            qb * kQBufferStep<FORM>,
+                        &maps.q, 64 * h, w.head * a.G, FORM == kSpread ? w.t.tok0 : w.t.tok0 + s * a.list.tpt,
+                        bars + 8 * (B::kQF + qb));
+      }
+    }
+    ++pieces;
+    const int n = w.n, head = w.head;
+    for (int j = 0; j < n; ++j) {
+      const int cur = id;
+      if (j + 1 < n) {
+        id = block_of(w.t, w.first() + j + 1);
+      } else {  // the next piece's first
+        w.next(a);
+        more = w.load();
+        id = more ? block_of(w.t, w.first()) : -1;
+      }
+      const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, cur >= 0)) * bt * 128);
+      ok = wait_for_all(bars + 8 * (B::kEmpty + r.st), r.ph ^ 1, abort_flag, a);
+      if (!ok) break;
+      // the barrier's one arrival brings the bytes of all boxes; those of the warp beside may land before it
+      if (share == 0 && lane == 0) mbar_arrive_expect_tx(bars + 8 * (B::kFull + r.st), bytes);
+      __syncwarp();
+      if (loads && cur >= 0)
+        tma_load_4d(ring + r.st * C::kTileBytes + at, map, 64 * half, 0, head, cur, bars + 8 * (B::kFull + r.st));
+      ++tiles;
+      r.next();
+      r.next();
+    }
+    if (leads) ok = ok && publish(pieces);
+  }
+  if (!ok) {  // given up: wait for what was issued before the shared memory goes away
+    const long long t0 = clock64();
+    auto drain = [&](uint32_t bar, uint32_t par) {
+      while (!mbar_try_wait_sleep(bar, par, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
+      }
+    };
+    for (uint32_t t = tiles > (uint32_t)C::kStages ? tiles - C::kStages : 0; t < tiles; ++t) {
+      const uint32_t f = 2 * t + kv;
+      if (f + C::kStages >= 2 * tiles + kv) drain(bars + 8 * (B::kFull + f % C::kStages), (f / C::kStages) & 1);
+    }
+    if (leads)
+      for (uint32_t q = pieces > nq ? pieces - nq : 0; q < pieces; ++q)
+        drain(bars + 8 * (B::kQF + q % nq), (q / nq) & 1);
+  }
+}
+
+// S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by an elected lane of the
+// converged warp, so that the operands stay in the uniform datapath: issued by a lane that ran the loop
+// alone an MMA took 150 cycles, against the 64 that the tensor cores need for one.  The descriptors' low
+// words (address and leading offset) are kept as numbers to which a step's offset is added.
+template <int FORM, int DP, bool BF>
+struct Mma {
+  using C = Cfg<FORM, DP>;
+  static constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1 KB atoms, version 1, 128-byte swizzle
+  static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24) | (BF ? (1u << 7) | (1u << 10) : 0u);
+  static __device__ __forceinline__ uint32_t lo_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+  static __device__ __forceinline__ uint32_t lo_mn(uint32_t addr) { return (addr >> 4) | ((C::kHalfBytes >> 4) << 16); }
+  static __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)lo | ((uint64_t)kHi << 32); }
+  static __device__ __forceinline__ void qk(uint32_t tmem_s, uint32_t q, uint32_t k) {
+    constexpr uint32_t idesc = kIdesc | ((kAttnKeys >> 3) << 17);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const uint32_t off = (uint32_t)((i / 4) * C::kHalfBytes + (i % 4) * 32) >> 4;
+      tc_mma_f16(tmem_s, desc(q + off), desc(k + off), idesc, i > 0);
+    }
+  }
+  static __device__ __forceinline__ void pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v, uint32_t accumulate) {
+    constexpr uint32_t idesc = kIdesc | ((DP >> 3) << 17) | (1u << 16);  // B contiguous along N
+#pragma unroll
+    for (int i = 0; i < kAttnKeys / 16; ++i)
+      tc_mma_f16_ta(tmem_o, tmem_p + 8 * i, desc(v + i * (2048 >> 4)), idesc, i > 0 ? 1u : accumulate);
+  }
+};
+
+template <int FORM, int DP, bool BF>
+__device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag) {
+  using C = Cfg<FORM, DP>;
+  constexpr int NS = C::NS;
+  using B = Bars<C::kStages>;
+  using M = Mma<FORM, DP, BF>;
+  constexpr uint32_t kStep = C::kTileBytes >> 4;
+  const uint32_t ring_k = M::lo_k(sm + NS * C::kTileBytes), ring_v = M::lo_mn(sm + NS * C::kTileBytes);
+  const uint32_t o0 = tmem + 256, nq = q_buffers<FORM>(a);
+  Ring<C::kStages> r;  // the next stage to be read
+  uint32_t pieces = 0, it = 0, p_par = 0, p2_par = 0;
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    const bool y = wait_for_all(bars + 8 * bar, par, abort_flag, a);
+    tc_fence_after();
+    return y;
+  };
+  auto full = [&](const Ring<C::kStages> &x) { return wait(B::kFull + x.st, x.ph); };
+  auto release = [&](uint32_t st) { tc_commit(bars + 8 * (B::kEmpty + st)); };
+  for (; ok; ++pieces) {
+    const uint32_t d = pieces % kPieces;
+    if (!wait(B::kDF + d, (pieces / kPieces) & 1)) break;
+    const int n = __shfl_sync(0xffffffffu, piece[d].n, 0);
+    const bool two = NS == 2 && __shfl_sync(0xffffffffu, piece[d].ntok, 0) > a.list.tpt;
+    if (n == 0) break;
+    if (elect_one()) mbar_arrive(bars + 8 * (B::kDE + d));
+    __syncwarp();
+    const uint32_t qb = pieces % nq;
+    const uint32_t q0 = M::lo_k(sm + qb * kQBufferStep<FORM>);
+    ok = wait(B::kQF + qb, (pieces / nq) & 1) && full(r);
+    if (!ok) break;
+    uint32_t k_st = r.st;
+    r.next();
+    if (NS == 2) {
+      if (elect_one()) {
+        M::qk(tmem, q0, ring_k + k_st * kStep);
+        tc_commit(bars + 8 * B::kSF);
+        if (two) {
+          M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
+          tc_commit(bars + 8 * (B::kSF + 1));
+        }
+        release(k_st);
+        if (n == 1) tc_commit(bars + 8 * B::kQE);
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j) {
+        const bool more = j + 1 < n;
+        if (!(ok = full(r))) break;
+        const uint32_t v_st = r.st, v = ring_v + v_st * kStep;
+        r.next();
+        if (more) {
+          if (!(ok = full(r))) break;
+          k_st = r.st;
+          r.next();
+        }
+        if (!(ok = wait(B::kPF, p_par))) break;
+        if (elect_one()) {
+          M::pv(o0, tmem, v, j > 0);
+          if (more) {
+            M::qk(tmem, q0, ring_k + k_st * kStep);
+            tc_commit(bars + 8 * B::kSF);
+          } else {
+            tc_commit(bars + 8 * B::kOD);
+          }
+          if (!two) {
+            release(v_st);
+            if (more) release(k_st);
+            if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+          }
+        }
+        __syncwarp();
+        if (two) {
+          if (!(ok = wait(B::kPF + 1, p2_par))) break;
+          p2_par ^= 1;
+          if (elect_one()) {
+            M::pv(o0 + 128, tmem + 128, v, j > 0);
+            if (more) {
+              M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
+              tc_commit(bars + 8 * (B::kSF + 1));
+            } else {
+              tc_commit(bars + 8 * (B::kOD + 1));
+            }
+            release(v_st);
+            if (more) release(k_st);
+            if (j + 2 == n) tc_commit(bars + 8 * B::kQE);
+          }
+          __syncwarp();
+        }
+        p_par ^= 1;
+      }
+    } else {
+      if (elect_one()) {
+        M::qk(tmem + 128 * (it & 1), q0, ring_k + k_st * kStep);
+        tc_commit(bars + 8 * (B::kSF + (it & 1)));
+        release(k_st);
+        if (n == 1) tc_commit(bars + 8 * (B::kQE + qb));
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t b = it & 1, v_st = r.st;
+        const Ring<C::kStages> rv = r;
+        r.next();
+        if (j + 1 < n) {
+          if (!(ok = full(r))) break;
+          k_st = r.st;
+          r.next();
+          if (elect_one()) {
+            M::qk(tmem + 128 * (b ^ 1), q0, ring_k + k_st * kStep);
+            tc_commit(bars + 8 * (B::kSF + (b ^ 1)));
+            release(k_st);
+            if (j + 2 == n) tc_commit(bars + 8 * (B::kQE + qb));
+          }
+          __syncwarp();
+        }
+        if (!(ok = full(rv))) break;
+        if (!(ok = wait(B::kPF + b, (it >> 1) & 1))) break;
+        if (elect_one()) {
+          M::pv(o0, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
+          tc_commit(bars + 8 * (B::kOD + b));
+          release(v_st);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // nothing of the tensor cores is in flight when tensor memory is freed
+  if (elect_one()) tc_commit(bars + 8 * B::kDrain);
+  __syncwarp();
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bars + 8 * B::kDrain, 0, kSpinNs) && clock64() - t0 <= a.wait_cycles) {
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028234e38f; }
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Pairs of floats, for the arithmetic that takes two at a time.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int i = 4; i + 8 <= N; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[i + 2 * k], x[i + 2 * k + 1]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], x[N - 4 + k]);  // N = 4 + 8 j + 4
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Scores of the keys base + i to log2 units with cap and bias.  tanh(y) = y P(y^2) with a polynomial of
+// degree 5 (fitted at Chebyshev nodes on |y| <= 3/4; largest error 9.3e-8), on the multiply-add pipe; a
+// warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, whose two special-function
+// operations per score bound the softmax.
+template <int N>
+__device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool valid, float slope, float d0) {
+  const float scale2 = a.scale * kLog2e;
+  if (a.softcap > 0.f) {
+    const float inv = a.scale / a.softcap, cap2 = a.softcap * kLog2e;
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top[k] = max3(top[k], fabsf(x[i + 2 * k]), fabsf(x[i + 2 * k + 1]));
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(inv);
+    if (__any_sync(0xffffffffu, valid && !(most <= 0.75f))) {
+      const float t2 = 2.f * kLog2e * inv;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = cap2 - 2.f * cap2 * rcp(ex2(x[i] * t2) + 1.f);
+    } else {
+      const uint64_t s = pair(inv, inv), c = pair(cap2, cap2);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const uint64_t y = mul2(pair(x[i], x[i + 1]), s), u = mul2(y, y);
+        uint64_t r = pair(-0.004723952151834965f, -0.004723952151834965f);
+        r = fma2(r, u, pair(0.01959378644824028f, 0.01959378644824028f));
+        r = fma2(r, u, pair(-0.053349819034338f, -0.053349819034338f));
+        r = fma2(r, u, pair(0.13325515389442444f, 0.13325515389442444f));
+        r = fma2(r, u, pair(-0.3333296775817871f, -0.3333296775817871f));
+        r = fma2(r, u, pair(1.f, 1.f));
+        unpair(mul2(r, mul2(y, c)), x[i], x[i + 1]);
+      }
+    }
+  } else {
+    const uint64_t s = pair(scale2, scale2);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) unpair(mul2(pair(x[i], x[i + 1]), s), x[i], x[i + 1]);
+  }
+  if (a.slopes) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)i), x[i]);
+  }
+}
+
+// Keys outside [lo, hi) (relative to the first score) do not count.
+template <int N>
+__device__ __forceinline__ void mask_out(float (&x)[N], int lo, int hi) {
+#pragma unroll
+  for (int c = 0; c < N / 32; ++c) {
+    const int l = min(max(lo - 32 * c, 0), 32), h = min(max(hi - 32 * c, 0), 32);
+    // bits l .. h - 1 (none if h <= l)
+    const uint32_t below_h = h == 32 ? 0xffffffffu : (1u << h) - 1u, below_l = l == 32 ? 0xffffffffu : (1u << l) - 1u;
+    const uint32_t seen = below_h & ~below_l;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[32 * c + i] = seen >> i & 1u ? x[32 * c + i] : -INFINITY;
+  }
+}
+
+// 32 scores to probabilities 2^(x scale - m) (EXTRA: 2^(x - m)), packed; their sum in pairs.
+template <bool BF, bool EXTRA>
+__device__ __forceinline__ void exponentials(const float *x, uint64_t scale, uint64_t neg_m, uint32_t (&pk)[16],
+                                             uint64_t (&sum)[2]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float p, q;
+    const uint64_t y = pair(x[i], x[i + 1]);
+    unpair(EXTRA ? add2(y, neg_m) : fma2(y, scale, neg_m), p, q);
+    p = ex2(p);
+    q = ex2(q);
+    sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(p, q));
+    pk[i / 2] = pack_pair<BF>(p, q);
+  }
+}
+
+// How a row's unscaled output v becomes its result: v * inv + w2 * (the row's result over its group's
+// shared prefix, where it has one).  m and l are the row's maximum (log2 units) and sum.
+struct RowOut {
+  float inv, w2, lse2;
+  size_t at;  // the row in [n_tokens][Hq] order
+};
+__device__ __forceinline__ RowOut row_out(const AttnArgs &a, int tok, int head, bool merge, float m, float l) {
+  RowOut r;
+  r.at = (size_t)tok * a.Hq + head;
+  r.inv = l == 0.f ? 0.f : 1.f / l;
+  r.lse2 = l == 0.f ? -INFINITY : m + lg2(l);
+  r.w2 = 0.f;
+  if (merge) {
+    const float pl = a.prefix_lse[r.at];
+    const float mx = fmaxf(pl, r.lse2), ms = mx == -INFINITY ? 0.f : mx;
+    const float e1 = ex2(r.lse2 - ms), e2 = ex2(pl - ms), sum = e1 + e2;
+    const float is = sum == 0.f ? 0.f : 1.f / sum;
+    r.inv *= e1 * is;
+    r.w2 = e2 * is;
+    r.lse2 = sum == 0.f ? -INFINITY : ms + lg2(sum);
+  }
+  return r;
+}
+// N consecutive elements from column c of a row; false if one is not finite.
+template <int N, bool BF>
+__device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, int tok, int head, int c, float (&v)[N]) {
+  static_assert(N % 4 == 0, "stores of 8 or 16 bytes");
+  if (c >= a.D) return true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] *= r.inv;
+  if (r.w2 != 0.f) {
+    const float *po = a.prefix_o + r.at * a.D + c;
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      if (c + i < a.D) {
+        const float4 x = *reinterpret_cast<const float4 *>(po + i);
+        v[i] = fmaf(r.w2, x.x, v[i]);
+        v[i + 1] = fmaf(r.w2, x.y, v[i + 1]);
+        v[i + 2] = fmaf(r.w2, x.z, v[i + 2]);
+        v[i + 3] = fmaf(r.w2, x.w, v[i + 3]);
+      }
+  }
+  bool fin = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (c + i < a.D) fin = fin && finite(v[i]);
+  if (a.to_prefix) {
+    float *d = a.prefix_o + r.at * a.D + c;
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      if (c + i < a.D) *reinterpret_cast<float4 *>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+    uint16_t *d = a.o + tok * a.o_token + head * a.o_head + c;
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8)
+        if (c + i < a.D)
+          *reinterpret_cast<uint4 *>(d + i) =
+              make_uint4(pack_pair<BF>(v[i], v[i + 1]), pack_pair<BF>(v[i + 2], v[i + 3]),
+                         pack_pair<BF>(v[i + 4], v[i + 5]), pack_pair<BF>(v[i + 6], v[i + 7]));
+    } else {
+      *reinterpret_cast<uint2 *>(d) = make_uint2(pack_pair<BF>(v[0], v[1]), pack_pair<BF>(v[2], v[3]));
+    }
+  }
+  return fin;
+}
+__device__ __forceinline__ void store_lse(const AttnArgs &a, const RowOut &r) {
+  if (a.to_prefix)
+    a.prefix_lse[r.at] = r.lse2;
+  else if (a.lse)
+    a.lse[r.at] = r.lse2 * kLn2;
+}
+
+// A row whose sum is finite but whose output is not: a value is infinite or NaN, possibly one that the row
+// does not see (0 times it in the product with v).  Again, from the row's visible keys alone, by the warp.
+template <bool BF>
+__device__ void redo_row(const AttnArgs &a, int tok, int head, const volatile Piece &w) {
+  const int lane = threadIdx.x & 31;
+  const RowBound b = a.bounds[tok];
+  const bool merge = w.merge;  // over the shared prefix too
+  float acc[4], lse;
+  row_attention<BF>(a, tok, head, merge ? b.lo : max(b.lo, w.klo), merge ? b.hi : min(b.hi, w.khi), w.trow, b.pos, acc,
+                    &lse);
+  if (4 * lane < a.D) {
+    if (a.to_prefix)
+      *reinterpret_cast<float4 *>(a.prefix_o + ((size_t)tok * a.Hq + head) * a.D + 4 * lane) =
+          make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else
+      *reinterpret_cast<uint2 *>(a.o + tok * a.o_token + head * a.o_head + 4 * lane) =
+          make_uint2(pack_pair<BF>(acc[0], acc[1]), pack_pair<BF>(acc[2], acc[3]));
+  }
+}
+
+template <int FORM, int DP, bool BF, bool EXTRA>
+__device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
+                       volatile int *abort_flag, volatile int *last_flag) {
+  using C = Cfg<FORM, DP>;
+  using B = Bars<C::kStages>;
+  constexpr int NS = C::NS;
+  constexpr bool SP = FORM == kSpread;
+  constexpr int NC = SP ? 32 : 128;  // scores of a key tile that a thread takes
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = warp >> 2, quarter = warp & 3, thread = 32 * quarter + lane;
+  const int row = SP ? lane : thread, col0 = SP ? 32 * quarter : 0;
+  const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+  const uint32_t tmem_o = tmem + 256 + 128 * s + lanes;
+  uint32_t it = 0;        // key tiles of this stream so far
+  Ring<C::kStages> rv;    // the current tile's V
+  rv.next();
+  // One stream: P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked
+  // the tile before on the same barrier is known to be complete (the scores of tile t or t + 1 were issued
+  // behind it) and the one after waits for this thread, so the parity cannot be mistaken.
+  auto product_done = [&](uint32_t t) {
+    return wait_for_all(bars + 8 * (B::kOD + (t & 1)), (t >> 1) & 1, abort_flag, a);
+  };
+  uint32_t o_done = 0;    // two streams: pieces of this stream so far
+  uint32_t joins = 0;     // meetings of the stream's warps so far
+  auto join = [&]() {     // the stream's four warps meet (bounded, as every wait)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (B::kJoin + s));
+    return wait_for_all(bars + 8 * (B::kJoin + s), joins++ & 1, abort_flag, a);
+  };
+  // a split tile's piece: its partial result has been written; true for the last of its CTAs to come here
+  bool ok = true;
+  auto last_to_arrive = [&](int c0, int c1) {
+    __threadfence();
+    if (!(ok = join())) return false;
+    if (thread == 0) {
+      int *cnt = a.counters + 2 * c0 + s;
+      const int last = atomicAdd(cnt, 1) == c1 - c0;
+      if (last) *cnt = 0;
+      last_flag[s] = last;
+    }
+    if (!(ok = join())) return false;
+    if (!last_flag[s]) return false;
+    __threadfence();
+    return true;
+  };
+  constexpr int kPart = DP * 128;
+  auto slot_of = [&](int c, int c0) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * NS + s; };
+  const float sl2 = a.scale * kLog2e;
+  const int row_tok = s * a.list.tpt + row / a.G;
+  uint32_t pieces = 0;
+  ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
+  RowBound rb{0, 0, -1, 0}, rb_ahead{0, 0, -1, 0};
+  // the row's keys in a piece, fetched while the piece before is in work
+  auto bound_of = [&](const volatile Piece &x) {
+    if (x.n == 0 || !x.fresh) return rb;
+    return row_tok < min(x.ntok, (s + 1) * a.list.tpt) ? a.bounds[x.tok0 + row_tok] : RowBound{0, 0, -1, 0};
+  };
+  if (ok) rb_ahead = bound_of(piece[0]);
+  for (; ok; ++pieces) {
+    const volatile Piece &w = piece[pieces % kPieces];
+    const int n = w.n, first = w.first;
+    if (n == 0) break;
+    const int ntok = min(a.list.tpt, w.ntok - s * a.list.tpt), nrows = ntok * a.G;
+    rb = rb_ahead;
+    const uint32_t dn = (pieces + 1) % kPieces;
+    if (NS == 2 && ntok <= 0) {
+      for (int i = 0; i < 2 * n; ++i) rv.next();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+      if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
+      rb_ahead = bound_of(piece[dn]);
+      continue;
+    }
+    const bool valid = row < nrows;
+    const int lo = max(rb.lo, (int)w.klo), hi = min(rb.hi, (int)w.khi);
+    const bool active = SP || 32 * quarter < nrows;
+    const float slope = EXTRA && a.slopes && valid ? a.slopes[w.head * a.G + row % a.G] * kLog2e : 0.f;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
+      const uint32_t buf = NS == 2 ? (uint32_t)s : (it & 1);
+      const uint32_t par = NS == 2 ? (it & 1) : ((it >> 1) & 1);
+      const uint32_t ts = tmem + 128 * buf + lanes;
+      const int base = (first + j) * kAttnKeys;
+      if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
+      tc_fence_after();
+      if (s == 0 && (base < w.klo || base + kAttnKeys > w.khi)) {
+        // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
+        // times what the memory holds may be NaN
+        if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
+        if (base + thread < w.klo || base + thread >= w.khi) {
+          uint8_t *vrow = smp + (NS + rv.st) * C::kTileBytes + thread * 128;
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(vrow + h * C::kHalfBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+      }
+      if (active) {
+        float x[NC];
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) tmem_ld32(ts + col0 + 32 * c, reinterpret_cast<uint32_t *>(x) + 32 * c);
+        tmem_wait_ld();
+        if (EXTRA) transform<NC>(a, x, valid, slope, (float)(rb.pos - base - col0));
+        const int l0 = lo - base - col0, h0 = hi - base - col0;
+        if (__any_sync(0xffffffffu, valid && (l0 > 0 || h0 < NC))) mask_out<NC>(x, l0, h0);
+        float mx = max_of<NC>(x);
+        if (!EXTRA) mx *= sl2;
+        if (!valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
+        if (j == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+          // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8:
+          // until then probabilities up to 2^8 cost no precision, and the accumulator stays untouched.
+          // Two streams: these scores were issued behind the product before, which is therefore done.
+          const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          if (NS == 1) {
+            if (!(ok = product_done(it - 1))) break;
+            tc_fence_after();
+          }
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            float o[32];
+            tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        const uint64_t scale = pair(sl2, sl2), neg_m = pair(-ms, -ms);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) {
+          uint32_t pk[16];
+          exponentials<BF, EXTRA>(x + 32 * c, scale, neg_m, pk, sum);
+          if (SP) {
+            const uint32_t none[16] = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q != quarter) tmem_st16(ts + 16 * q, none);
+            tmem_st16(ts + 16 * quarter, pk);
+          } else {
+            tmem_st16(ts + 16 * c, pk);
+          }
+        }
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (B::kPF + buf));
+    }
+    if (!ok) break;
+    // the next piece has been handed over: its first scores may be on their way
+    if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
+    rb_ahead = bound_of(piece[dn]);
+    // the piece's last product
+    if (NS == 2) {
+      ok = wait_for_all(bars + 8 * (B::kOD + s), o_done & 1, abort_flag, a);
+      ++o_done;
+    } else {
+      ok = product_done(it - 1);
+    }
+    if (!ok) break;
+    tc_fence_after();
+    auto from_tmem = [&](int c, float (&v)[32]) {
+      __syncwarp();  // a load of the whole warp: lanes without a row come from other branches
+      tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
+      tmem_wait_ld();
+    };
+    const bool merge = w.merge;
+    const int c0 = w.c0, c1 = w.c1;
+    if constexpr (SP) {
+      // Eight rows at a time: the quarters lay their rows side by side, then sixteen threads to a row add
+      // them, relative to the largest of their maxima.
+      float *sh = reinterpret_cast<float *>(smp + C::kScratchAt);
+      float2 *ml = reinterpret_cast<float2 *>(sh + 4 * kJoinRows * C::kScratchRow);
+      constexpr int V = DP / 16;
+      const int c = (thread & 15) * V;
+      ml[quarter * kSpreadRows + lane] = make_float2(m, l);
+      for (int r0 = 0; r0 < nrows && ok; r0 += kJoinRows) {
+        if (r0 > 0 && !(ok = join())) break;  // the rows before have been read
+#pragma unroll
+        for (int k = 0; k < DP / 32; ++k) {
+          float v[32];
+          from_tmem(k, v);
+          if (lane >= r0 && lane < r0 + kJoinRows) {
+            float4 *d = reinterpret_cast<float4 *>(sh + (quarter * kJoinRows + lane - r0) * C::kScratchRow + 32 * k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        if (!(ok = join())) break;
+        const int rr = r0 + (thread >> 4);  // this thread's row and columns c .. c + V - 1
+        const bool mine = rr < nrows;
+        float mm = -INFINITY, ll = 0.f, v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+        if (mine) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mm = fmaxf(mm, ml[q * kSpreadRows + rr].x);
+          const float ms = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 y = ml[q * kSpreadRows + rr];
+            const float f = ex2(y.x - ms);
+            ll = fmaf(f, y.y, ll);
+            const float4 *p = reinterpret_cast<const float4 *>(sh + (q * kJoinRows + rr - r0) * C::kScratchRow + c);
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+              const float4 z = p[i / 4];
+              v[i] = fmaf(f, z.x, v[i]);
+              v[i + 1] = fmaf(f, z.y, v[i + 1]);
+              v[i + 2] = fmaf(f, z.z, v[i + 2]);
+              v[i + 3] = fmaf(f, z.w, v[i + 3]);
+            }
+          }
+        }
+        bool last = c0 == c1;
+        if (!last) {
+          const size_t my = slot_of(blockIdx.x, c0);
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+              __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + rr * DP + c + i),
+                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            if (c == 0) __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
+          }
+          if (r0 + kJoinRows < nrows) continue;
+          last = last_to_arrive(c0, c1);
+          if (!ok) break;
+        }
+        // whole tiles: these eight rows; split tiles: once all pieces are there, all rows
+        for (int q0 = c0 == c1 ? r0 : 0; last && q0 < (c0 == c1 ? min(nrows, r0 + kJoinRows) : nrows); q0 += kJoinRows) {
+          const int ro = q0 + (thread >> 4);
+          const bool use = ro < nrows;
+          if (use && c0 != c1) {
+            mm = -INFINITY;
+            for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, __ldcg(a.part_ml + slot_of(p, c0) * 128 + ro).x);
+            const float ms = mm == -INFINITY ? 0.f : mm;
+            ll = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = 0.f;
+#pragma unroll 4
+            for (int p = c0; p <= c1; ++p) {
+              const size_t at = slot_of(p, c0);
+              const float2 y = __ldcg(a.part_ml + at * 128 + ro);
+              const float f = ex2(y.x - ms);
+              ll = fmaf(f, y.y, ll);
+#pragma unroll
+              for (int i = 0; i < V; i += 4) {
+                const float4 z = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ro * DP + c + i));
+                v[i] = fmaf(f, z.x, v[i]);
+                v[i + 1] = fmaf(f, z.y, v[i + 1]);
+                v[i + 2] = fmaf(f, z.z, v[i + 2]);
+                v[i + 3] = fmaf(f, z.w, v[i + 3]);
+              }
+            }
+          }
+          const int tok = w.tok0 + ro / a.G, head = w.head * a.G + ro % a.G;
+          bool again = false;
+          if (use) {
+            const RowOut out = row_out(a, tok, head, merge, mm, ll);
+            again = !store_cols<V, BF>(a, out, tok, head, c, v) && finite(ll);
+            if (c == 0) store_lse(a, out);
+          }
+          const unsigned flagged = __ballot_sync(0xffffffffu, again);
+          for (int h = 0; h < 2; ++h)  // the warp's two rows
+            if (flagged >> (16 * h) & 0xffffu) {
+              const int rw = q0 + 2 * quarter + h;
+              redo_row<BF>(a, w.tok0 + rw / a.G, w.head * a.G + rw % a.G, w);
+            }
+        }
+      }
+      if (!ok) break;
+    } else {
+      const int tok = w.tok0 + row_tok, head = w.head * a.G + row % a.G;
+      // thread by row: 32 columns at a time from `get`
+      auto emit = [&](float mm, float ll, auto get) {
+        RowOut out{};
+        if (valid) out = row_out(a, tok, head, merge, mm, ll);
+        bool fin = true;
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) {
+          float v[32];
+          get(c, v);
+          if (valid) fin = store_cols<32, BF>(a, out, tok, head, 32 * c, v) && fin;
+        }
+        if (valid) store_lse(a, out);
+        unsigned flagged = __ballot_sync(0xffffffffu, valid && !fin && finite(ll));
+        while (flagged) {
+          const int src = __ffs(flagged) - 1;
+          flagged &= flagged - 1;
+          redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w);
+        }
+      };
+      if (c0 == c1) {
+        if (active) emit(m, l, from_tmem);
+      } else {
+        // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up
+        const size_t my = slot_of(blockIdx.x, c0);
+        if (active) {
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            float v[32];
+            from_tmem(c, v);
+            if (valid) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((8 * c + i / 4) * 128 + row) * 4),
+                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            }
+          }
+          if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
+        }
+        const bool last = last_to_arrive(c0, c1);
+        if (!ok) break;
+        if (last && active) {
+          float mm = -INFINITY, ll = 0.f;
+          if (valid)
+            for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, __ldcg(a.part_ml + slot_of(p, c0) * 128 + row).x);
+          const float ms = mm == -INFINITY ? 0.f : mm;
+          if (valid)
+            for (int p = c0; p <= c1; ++p) {
+              const float2 y = __ldcg(a.part_ml + slot_of(p, c0) * 128 + row);
+              ll = fmaf(ex2(y.x - ms), y.y, ll);
+            }
+          emit(mm, ll, [&](int c, float (&v)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            if (!valid) return;
+            for (int p = c0; p <= c1; ++p) {
+              const size_t at = slot_of(p, c0);
+              const float f = ex2(__ldcg(a.part_ml + at * 128 + row).x - ms);
+              const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kPart) + 8 * c * 128 + row;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 y = __ldcg(src + i * 128);
+                v[4 * i] = fmaf(f, y.x, v[4 * i]);
+                v[4 * i + 1] = fmaf(f, y.y, v[4 * i + 1]);
+                v[4 * i + 2] = fmaf(f, y.z, v[4 * i + 2]);
+                v[4 * i + 3] = fmaf(f, y.w, v[4 * i + 3]);
+              }
+            }
+          });
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+  }
+}
+
+template <int FORM, int DP, bool BF, bool EXTRA>
+__global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const __grid_constant__ AttnMaps maps,
+                                                                       const __grid_constant__ AttnArgs a) {
+  using C = Cfg<FORM, DP>;
+  using B = Bars<C::kStages>;
+  constexpr int NS = C::NS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bar_mem[B::kNum];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, last_flag[2];
+  __shared__ Piece piece[kPieces];
+  const int warp = threadIdx.x >> 5;
+  const uint32_t bars = smem_u32(bar_mem), sm = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bars + 8 * (B::kFull + i), 1);
+      mbar_init(bars + 8 * (B::kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (B::kQF + i), 1);
+      mbar_init(bars + 8 * (B::kQE + i), 1);
+      mbar_init(bars + 8 * (B::kSF + i), 1);
+      mbar_init(bars + 8 * (B::kPF + i), 4);
+      mbar_init(bars + 8 * (B::kOD + i), 1);
+      mbar_init(bars + 8 * (B::kJoin + i), 4);
+    }
+    mbar_init(bars + 8 * B::kDrain, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bars + 8 * (B::kDF + i), 1);
+      mbar_init(bars + 8 * (B::kDE + i), C::kSoftWarps + 1);  // the softmax warps and the MMA thread
+    }
+    abort_flag = (sm & 1023u) != 0u;  // the swizzled tiles are 1 KB-aligned
+    if (abort_flag) atomicOr(a.err, kAttnErrWait);
+    fence_mbar_init();
+  }
+  if (warp == C::kSoftWarps) {
+    tmem_alloc(smem_u32(&tmem_slot), kTmemColsAttn);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp < C::kSoftWarps) {
+    if (NS == 2) regs_inc<kRegsSoft>();
+    if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+  } else {
+    if (NS == 2) regs_dec<kRegsOther>();
+    if (abort_flag) {
+    } else if (warp < C::kMmaWarp) {
+      produce<FORM, DP>(a, maps, warp - C::kSoftWarps, piece, sm, bars, &abort_flag);
+    } else if (warp == C::kMmaWarp) {
+      issue<FORM, DP, BF>(a, piece, sm, bars, tmem, &abort_flag);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kSoftWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemColsAttn);
+  }
+}
+
+template <int FORM, int DP, bool BF, bool EXTRA>
+static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
+  using C = Cfg<FORM, DP>;
+  static_assert(C::kStages >= 4, "two key tiles in flight");
+  auto kern = attn_kernel<FORM, DP, BF, EXTRA>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  kern<<<a.ctas, C::kThreads, C::kSmem, st>>>(maps, a);
+  return (int)cudaGetLastError();
+}
+
+template <int FORM, int DP, bool BF>
+static int launch_extra(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
+  // the plain image folds a positive scale into the exponent's multiply-add; caps, biases and other scales
+  // transform the scores first
+  if (a.softcap > 0.f || a.slopes || !(a.scale > 0.f)) return launch_one<FORM, DP, BF, true>(a, maps, st);
+  return launch_one<FORM, DP, BF, false>(a, maps, st);
+}
+template <int FORM, int DP>
+static int launch_type(const AttnArgs &a, const AttnMaps &maps, int bf16, cudaStream_t st) {
+  return bf16 ? launch_extra<FORM, DP, true>(a, maps, st) : launch_extra<FORM, DP, false>(a, maps, st);
+}
+
+template <int FORM>
+int launch_form(const AttnArgs &a, const AttnMaps &maps, int bf16, cudaStream_t st) {
+  return a.D > 64 ? launch_type<FORM, 128>(a, maps, bf16, st) : launch_type<FORM, 64>(a, maps, bf16, st);
+}
+
+}  // namespace pw

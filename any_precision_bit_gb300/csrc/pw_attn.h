@@ -16,6 +16,17 @@ constexpr int kAttnMaxRequests = 4096;
 // the pipeline's filling and draining, and the result's way out take about as long.
 constexpr int kAttnPieceCost = 2;
 
+// Three forms of the kernel:
+//   kTwo     two 128-row tiles share each key tile: while one tile's scores are in the softmax the
+//            tensor cores work on the other's;
+//   kOne     one tile, its score buffers doubled, so that the next scores are computed during a softmax;
+//   kSpread  one tile of at most 32 rows, which is held four times, once in each lane quarter of tensor
+//            memory: quarter w keeps a softmax over keys 32 w .. 32 w + 31 of every key tile (its
+//            probabilities of the other keys are zeros), and the four results are added at the end.  Four
+//            warps then share the few rows, where in kOne one warp has them all and the others idle.
+enum { kTwo = 2, kOne = 1, kSpread = 4 };
+constexpr int kSpreadRows = 32;
+
 // Findings of the device side, reported by pw_attn_check.
 enum {
   kAttnErrWait = 1,    // a bounded wait expired

@@ -1,0 +1,6 @@
+// pw_attn_two.cu -- the attention kernel with two query tiles to a CTA: prompts, chunks and shared prefixes.
+#include "pw_attn.cuh"
+
+namespace pw {
+template int launch_form<kTwo>(const AttnArgs &, const AttnMaps &, int, cudaStream_t);
+}
