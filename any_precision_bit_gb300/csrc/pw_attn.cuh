@@ -157,6 +157,17 @@ __device__ __forceinline__ AttnTile load_tile(const AttnTile *p) {
   t.khi = y.x, t.kv0 = y.y, t.kv1 = y.z, t.merge = y.w;
   return t;
 }
+// The CTAs that take the first and the last key tile of a (tile, head).
+__device__ __forceinline__ int2 ctas_of(const AttnArgs &a, const AttnTile &t, int tile, int head) {
+  const int cost = t.kv1 - t.kv0 + kAttnPieceCost;
+  const long long W = (long long)a.list.meta[1] * a.Hkv, P = min((long long)a.ctas, W);
+  const long long ub = (long long)a.list.cum[tile] * a.Hkv + (long long)head * cost;
+  return make_int2((int)(((ub + kAttnPieceCost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
+}
+// Slot of a split tile's piece among the partial results: a CTA's last piece, if it begins its tile, or its first.
+__device__ __forceinline__ size_t part_slot(int cta, int c0, int streams, int s) {
+  return ((size_t)cta * 2 + (cta == c0 ? 1 : 0)) * streams + s;
+}
 struct Walk {
   int tile, head, off, left;  // off and left in units (kAttnPieceCost of them lead each (tile, head))
   AttnTile t, ahead;
@@ -199,15 +210,9 @@ struct Walk {
   }
   __device__ __forceinline__ int first() const { return t.kv0 + j0; }
   __device__ __forceinline__ void describe(const AttnArgs &a, Piece *p) const {
-    int c0 = 0, c1 = 0;
-    if (n != t.kv1 - t.kv0) {
-      const int cost = t.kv1 - t.kv0 + kAttnPieceCost;
-      const long long W = (long long)a.list.meta[1] * a.Hkv, P = min((long long)a.ctas, W);
-      const long long ub = (long long)a.list.cum[tile] * a.Hkv + (long long)head * cost;
-      c0 = (int)(((ub + kAttnPieceCost + 1) * P - 1) / W);
-      c1 = (int)(((ub + cost) * P - 1) / W);
-    }
-    *p = Piece{n, first(), head, t.tok0, t.ntok, t.trow, t.klo, t.khi, fresh, t.merge && !a.to_prefix, c0, c1};
+    int2 c = make_int2(0, 0);
+    if (n != t.kv1 - t.kv0) c = ctas_of(a, t, tile, head);
+    *p = Piece{n, first(), head, t.tok0, t.ntok, t.trow, t.klo, t.khi, fresh, t.merge && !a.to_prefix, c.x, c.y};
   }
 };
 
@@ -712,15 +717,15 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, const RowOut &r) {
 
 // A row whose sum is finite but whose output is not: a value is infinite or NaN, possibly one that the row
 // does not see (0 times it in the product with v).  Again, from the row's visible keys alone, by the warp.
+// merge: over the shared prefix too.  Columns c0 .. c1 - 1 are written.
 template <bool BF>
-__device__ void redo_row(const AttnArgs &a, int tok, int head, const volatile Piece &w) {
+__device__ void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi, int trow, bool merge, int c0 = 0,
+                         int c1 = 128) {
   const int lane = threadIdx.x & 31;
   const RowBound b = a.bounds[tok];
-  const bool merge = w.merge;  // over the shared prefix too
   float acc[4], lse;
-  row_attention<BF>(a, tok, head, merge ? b.lo : max(b.lo, w.klo), merge ? b.hi : min(b.hi, w.khi), w.trow, b.pos, acc,
-                    &lse);
-  if (4 * lane < a.D) {
+  row_attention<BF>(a, tok, head, merge ? b.lo : max(b.lo, klo), merge ? b.hi : min(b.hi, khi), trow, b.pos, acc, &lse);
+  if (4 * lane < a.D && 4 * lane >= c0 && 4 * lane < c1) {
     if (a.to_prefix)
       *reinterpret_cast<float4 *>(a.prefix_o + ((size_t)tok * a.Hq + head) * a.D + 4 * lane) =
           make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -776,7 +781,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     return true;
   };
   constexpr int kPart = DP * 128;
-  auto slot_of = [&](int c, int c0) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * NS + s; };
+  auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
   const float sl2 = a.scale * kLog2e;
   const int row_tok = s * a.list.tpt + row / a.G;
   uint32_t pieces = 0;
@@ -960,11 +965,11 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           if (mine) {
 #pragma unroll
             for (int i = 0; i < V; i += 4)
-              __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + rr * DP + c + i),
+              __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((c + i) / 4 * 128 + rr) * 4),
                      make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
             if (c == 0) __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
           }
-          if (r0 + kJoinRows < nrows) continue;
+          if (a.to_prefix || r0 + kJoinRows < nrows) continue;
           last = last_to_arrive(c0, c1);
           if (!ok) break;
         }
@@ -987,7 +992,8 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
               ll = fmaf(f, y.y, ll);
 #pragma unroll
               for (int i = 0; i < V; i += 4) {
-                const float4 z = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ro * DP + c + i));
+                const float4 z =
+                    __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ((c + i) / 4 * 128 + ro) * 4));
                 v[i] = fmaf(f, z.x, v[i]);
                 v[i + 1] = fmaf(f, z.y, v[i + 1]);
                 v[i + 2] = fmaf(f, z.z, v[i + 2]);
@@ -1006,7 +1012,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           for (int h = 0; h < 2; ++h)  // the warp's two rows
             if (flagged >> (16 * h) & 0xffffu) {
               const int rw = q0 + 2 * quarter + h;
-              redo_row<BF>(a, w.tok0 + rw / a.G, w.head * a.G + rw % a.G, w);
+              redo_row<BF>(a, w.tok0 + rw / a.G, w.head * a.G + rw % a.G, w.klo, w.khi, w.trow, merge);
             }
         }
       }
@@ -1029,7 +1035,8 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         while (flagged) {
           const int src = __ffs(flagged) - 1;
           flagged &= flagged - 1;
-          redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w);
+          redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w.klo, w.khi, w.trow,
+                       merge);
         }
       };
       if (c0 == c1) {
@@ -1051,7 +1058,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           }
           if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
         }
-        const bool last = last_to_arrive(c0, c1);
+        const bool last = !a.to_prefix && last_to_arrive(c0, c1);
         if (!ok) break;
         if (last && active) {
           float mm = -INFINITY, ll = 0.f;
@@ -1086,6 +1093,64 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+  }
+}
+
+// Results over shared prefixes: the sum of each split tile's pieces.  A prefix has few tiles in many pieces,
+// and one CTA of the attention kernel adding up a tile's (18 pieces of 64 KB for 256 rows over 4096 keys)
+// took longer than the products; here a CTA takes 16 columns of one tile's 128 rows, a thread a row.
+template <int DP, bool BF>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int kGroups = DP / 16;
+  pdl_trigger();
+  pdl_wait();
+  int i = blockIdx.x;
+  const int c = i % kGroups * 16;
+  i /= kGroups;
+  const int s = i % a.list.streams;
+  i /= a.list.streams;
+  const int head = i % a.Hkv, tile = i / a.Hkv;
+  if (tile >= a.list.meta[0]) return;
+  const AttnTile t = load_tile(a.list.tiles + tile);
+  const int2 ctas = ctas_of(a, t, tile, head);
+  const int row = threadIdx.x, tok = t.tok0 + s * a.list.tpt + row / a.G, h = head * a.G + row % a.G;
+  const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G;
+  if (ctas.x == ctas.y || c >= a.D) return;  // in one piece: its CTA has written the result
+  bool again = false;
+  if (valid) {
+    float m = -INFINITY, l = 0.f, v[16];
+#pragma unroll 4
+    for (int p = ctas.x; p <= ctas.y; ++p)
+      m = fmaxf(m, a.part_ml[part_slot(p, ctas.x, a.list.streams, s) * 128 + row].x);
+    const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int p = ctas.x; p <= ctas.y; ++p) {
+      const size_t at = part_slot(p, ctas.x, a.list.streams, s);
+      const float2 y = a.part_ml[at * 128 + row];
+      const float f = ex2(y.x - ms);
+      l = fmaf(f, y.y, l);
+      const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 z = src[k * 128];
+        v[4 * k] = fmaf(f, z.x, v[4 * k]);
+        v[4 * k + 1] = fmaf(f, z.y, v[4 * k + 1]);
+        v[4 * k + 2] = fmaf(f, z.z, v[4 * k + 2]);
+        v[4 * k + 3] = fmaf(f, z.w, v[4 * k + 3]);
+      }
+    }
+    const RowOut out = row_out(a, tok, h, false, m, l);
+    again = !store_cols<16, BF>(a, out, tok, h, c, v) && finite(l);
+    if (c == 0) store_lse(a, out);
+  }
+  unsigned flagged = __ballot_sync(0xffffffffu, again);
+  while (flagged) {
+    const int src = __ffs(flagged) - 1;
+    flagged &= flagged - 1;
+    redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, false,
+                 c, c + 16);
   }
 }
 
@@ -1132,6 +1197,8 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  pdl_trigger();
+  pdl_wait();  // set up before the previous kernel of the stream has finished; what it wrote is read from here on
   if (warp < C::kSoftWarps) {
     if (NS == 2) regs_inc<kRegsSoft>();
     if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
@@ -1158,9 +1225,14 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
   using C = Cfg<FORM, DP>;
   static_assert(C::kStages >= 4, "two key tiles in flight");
   auto kern = attn_kernel<FORM, DP, BF, EXTRA>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  kern<<<a.ctas, C::kThreads, C::kSmem, st>>>(maps, a);
-  return (int)cudaGetLastError();
+  static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (set != cudaSuccess) return (int)set;
+  if (cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(C::kThreads), (size_t)C::kSmem, st, maps, a)) return (int)e;
+  if (!a.to_prefix) return (int)cudaGetLastError();
+  // tiles that the list can have: whole ones, and the short last one of each group
+  const int tt = a.list.tpt * a.list.streams, tiles = a.n_tokens / tt + a.n_groups;
+  return (int)launch_pdl(attn_join_kernel<DP, BF>, dim3((unsigned)(tiles * a.Hkv * a.list.streams * (DP / 16))),
+                         dim3(128), 0, st, a);
 }
 
 template <int FORM, int DP, bool BF>

@@ -126,7 +126,7 @@ struct AttnArgs {
   // Results over a shared prefix, normalised, and their log2-sum-exp2: written (to_prefix) or merged
   // into the rows of tiles with `merge`.
   float *prefix_o, *prefix_lse;  // [n_tokens][Hq][D], [n_tokens][Hq]
-  int to_prefix;
+  int to_prefix, n_groups;
   // Partial results of split tiles: two slots a CTA (its last piece and its first) and stream.
   float *part_o;    // [ctas][2][streams][head_dim padded / 4][128][4]
   float2 *part_ml;  // [ctas][2][streams][128] running maximum and sum

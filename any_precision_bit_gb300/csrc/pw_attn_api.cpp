@@ -413,6 +413,7 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
     g.prefix_o = a->prefix_o;
     g.prefix_lse = a->prefix_lse;
     g.to_prefix = 1;
+    g.n_groups = p.step.n_groups;
     if (pw_status st = launch(p.groups)) return st;
     g.to_prefix = 0;
   }

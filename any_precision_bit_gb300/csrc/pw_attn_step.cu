@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(kStepThreads) kv_map_kernel(MapArgs a) {
   extern __shared__ int sh[];
   int *qs = sh, *bs = sh + a.R + 1;
   const int tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
   const int per = (a.R + kStepThreads - 1) / kStepThreads;
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
   const long long cap = (long long)a.table_stride * a.bt;
@@ -143,14 +145,15 @@ int launch_kv_map(const MapArgs &a, void *stream) {
   const int work = max(max(a.n_tokens, a.n_ids), a.R);
   const int grid = max(1, min(148, (work + 4 * kStepThreads - 1) / (4 * kStepThreads)));
   const size_t smem = 2 * sizeof(int) * (size_t)(a.R + 1);
-  kv_map_kernel<<<grid, kStepThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return (int)cudaGetLastError();
+  return (int)launch_pdl(kv_map_kernel, dim3(grid), dim3(kStepThreads), smem, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 // The keys that each row sees (the masks are intervals, so one pair per token).
 __global__ void __launch_bounds__(kStepThreads) attn_bounds_kernel(PlanArgs a) {
   const long long cap = (long long)a.table_stride * a.bt;
   const int t = blockIdx.x * kStepThreads + threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
   if (t >= a.n_tokens) return;
   RowBound b{0, 0, -1, 0};
   if (t < a.q_start[a.R]) {
@@ -171,9 +174,8 @@ __global__ void __launch_bounds__(kStepThreads) attn_bounds_kernel(PlanArgs a) {
 }
 
 int launch_attn_bounds(const PlanArgs &a, void *stream) {
-  attn_bounds_kernel<<<(a.n_tokens + kStepThreads - 1) / kStepThreads, kStepThreads, 0,
-                       reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return (int)cudaGetLastError();
+  return (int)launch_pdl(attn_bounds_kernel, dim3((a.n_tokens + kStepThreads - 1) / kStepThreads), dim3(kStepThreads), 0,
+                         reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 // Segments of a list: requests (and, behind them, the rows that are padding), or groups.
@@ -219,6 +221,8 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
   const int tt = a.list.tpt * a.list.streams;
+  pdl_trigger();
+  pdl_wait();
   long long before = 0;
   for (int s0 = 0; s0 < n_seg; s0 += kListThreads) {
     const int s = s0 + tid;
@@ -304,8 +308,8 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
 
 int launch_attn_list(const PlanArgs &a, void *stream) {
   const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
-  attn_list_kernel<<<1, kListThreads, sizeof(int) * (size_t)n_seg, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return (int)cudaGetLastError();
+  return (int)launch_pdl(attn_list_kernel, dim3(1), dim3(kListThreads), sizeof(int) * (size_t)n_seg,
+                         reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 // The cache write: 16 bytes a thread, both caches in one launch.  A token's row of a cache is
@@ -314,6 +318,8 @@ int launch_attn_list(const PlanArgs &a, void *stream) {
 __global__ void __launch_bounds__(kStepThreads) attn_append_kernel(AppendArgs a) {
   const int vec = a.head_dim / 8, row = a.n_heads * vec;
   const long long total = 2LL * a.n_tokens * row;
+  pdl_trigger();
+  pdl_wait();
   for (long long i = (long long)blockIdx.x * kStepThreads + threadIdx.x; i < total;
        i += (long long)gridDim.x * kStepThreads) {
     const long long u = i / row;
@@ -334,8 +340,7 @@ int launch_attn_append(const AppendArgs &a, void *stream) {
   const long long total = 2LL * a.n_tokens * a.n_heads * (a.head_dim / 8);
   const long long want = (total + kStepThreads - 1) / kStepThreads;
   const int grid = (int)(want < 148 * 8 ? want : 148 * 8);
-  attn_append_kernel<<<grid, kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return (int)cudaGetLastError();
+  return (int)launch_pdl(attn_append_kernel, dim3(grid), dim3(kStepThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 }  // namespace pw
