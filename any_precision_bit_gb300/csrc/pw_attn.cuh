@@ -92,16 +92,20 @@ struct Cfg {
   static constexpr int kTileBytes = kHalves * kHalfBytes;
   // kSpread: the quarters' results side by side, rows padded against bank conflicts
   static constexpr int kScratchRow = DP + 4;
-  static constexpr int kScratch = FORM == kSpread ? 4 * kJoinRows * kScratchRow * 4 + 4 * kSpreadRows * 8 : 0;
+  static constexpr int kScratch = FORM == kSpread ? 4 * kJoinRows * kScratchRow * 4 + 2 * 4 * kSpreadRows * 8 : 0;
   static constexpr int kStages = (kSmemRing - NS * kTileBytes - kScratch) / kTileBytes;
   static constexpr int kScratchAt = (NS + kStages) * kTileBytes;
   static constexpr int kSmem = kScratchAt + kScratch;
   static constexpr int kSoftWarps = 4 * NS;
+  // kSpread: four warps add up and write out a piece while the softmax warps are at the next; its outputs
+  // take turns in two accumulators for that (kTwo has no tensor memory left to do so)
+  static constexpr int kFinishWarps = FORM == kSpread ? 4 : 0;
+  static constexpr int kProdWarp = kSoftWarps + kFinishWarps;
   // Producer warps: one for the keys and one for the values, two for each where the memory sets the pace (a
   // tensor copy takes its lane about 60 cycles, and 16-token blocks make 32 of them for a key tile).
   static constexpr int kProducers = FORM == kSpread ? 4 : 2;
-  static constexpr int kMmaWarp = kSoftWarps + kProducers;
-  // softmax, producer and MMA warps, and (two tiles) an idle warp that completes its warpgroup
+  static constexpr int kMmaWarp = kProdWarp + kProducers;
+  // and (two tiles) an idle warp that completes its warpgroup
   static constexpr int kThreads = FORM == kTwo ? 384 : 32 * (kMmaWarp + 1);
 };
 // Two tiles: 384 threads of 168 registers at launch, of which the softmax warps, which hold 128 scores
@@ -129,7 +133,7 @@ constexpr int kPieces = 4;  // pieces handed over ahead
 // mbarriers
 template <int STAGES>
 struct Bars {
-  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kNum = kDE + kPieces };
+  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kOF = kDE + kPieces, kOE = kOF + 2, kML = kOE + 2, kNum = kML + 2 };
 };
 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
@@ -174,13 +178,12 @@ struct Walk {
   int j0, n;  // first key tile of this piece within the tile's, and their number
   bool fresh; // the tile is another than the last piece's
   __device__ __forceinline__ explicit Walk(const AttnArgs &a) {
-    const AttnStart s = a.list.start[blockIdx.x];
-    tile = s.tile, head = s.head, off = s.off, left = s.n;
+    const AttnStart *s = a.list.start + blockIdx.x;
+    const int4 x = *reinterpret_cast<const int4 *>(s);
+    t = load_tile(&s->t);
+    tile = x.x, head = x.y, off = x.z, left = x.w;
     fresh = true;
-    if (left > 0) {
-      t = load_tile(a.list.tiles + tile);
-      ahead = load_tile(a.list.tiles + tile + 1);
-    }
+    if (left > 0) ahead = load_tile(a.list.tiles + tile + 1);
   }
   __device__ __forceinline__ bool load() {
     if (off < kAttnPieceCost) {
@@ -382,6 +385,7 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
   using B = Bars<C::kStages>;
   using M = Mma<FORM, DP, BF>;
   constexpr uint32_t kStep = C::kTileBytes >> 4;
+  constexpr bool SP = FORM == kSpread;
   const uint32_t ring_k = M::lo_k(sm + NS * C::kTileBytes), ring_v = M::lo_mn(sm + NS * C::kTileBytes);
   const uint32_t o0 = tmem + 256, nq = q_buffers<FORM>(a);
   Ring<C::kStages> r;  // the next stage to be read
@@ -403,6 +407,7 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
     if (elect_one()) mbar_arrive(bars + 8 * (B::kDE + d));
     __syncwarp();
     const uint32_t qb = pieces % nq;
+    const uint32_t ob = SP ? pieces & 1 : 0;  // output accumulator
     const uint32_t q0 = M::lo_k(sm + qb * kQBufferStep<FORM>);
     ok = wait(B::kQF + qb, (pieces / nq) & 1) && full(r);
     if (!ok) break;
@@ -490,10 +495,12 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
           __syncwarp();
         }
         if (!(ok = full(rv))) break;
+        if (SP && j == 0 && !(ok = wait(B::kOE + ob, ((pieces >> 1) & 1) ^ 1))) break;
         if (!(ok = wait(B::kPF + b, (it >> 1) & 1))) break;
         if (elect_one()) {
-          M::pv(o0, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
+          M::pv(o0 + 128 * ob, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
           tc_commit(bars + 8 * (B::kOD + b));
+          if (SP && j + 1 == n) tc_commit(bars + 8 * (B::kOF + ob));
           release(v_st);
         }
         __syncwarp();
@@ -735,6 +742,37 @@ __device__ void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi,
   }
 }
 
+// Four warps that finish a row tile together.
+template <int STAGES>
+struct Group {
+  uint32_t bars;
+  int s;           // stream
+  uint32_t joins;  // meetings so far
+  volatile int *abort_flag;
+  // all four meet (bounded, as every wait)
+  __device__ __forceinline__ bool join(const AttnArgs &a) {
+    const uint32_t bar = bars + 8 * (Bars<STAGES>::kJoin + s);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    return wait_for_all(bar, joins++ & 1, abort_flag, a);
+  }
+  // A split tile's piece has been written: true for the last of its CTAs to come here, which may read them all.
+  __device__ __forceinline__ bool last_to_arrive(const AttnArgs &a, int c0, int c1, int thread,
+                                                 volatile int *last_flag, bool &ok) {
+    if (!(ok = join(a))) return false;
+    if (thread == 0) {
+      int *cnt = a.counters + 2 * c0 + s;
+      __threadfence();  // the group's writes, which the meeting has made visible to this thread
+      const int last = atomicAdd(cnt, 1) == c1 - c0;
+      if (last) *cnt = 0;
+      __threadfence();
+      last_flag[s] = last;
+    }
+    if (!(ok = join(a))) return false;
+    return last_flag[s] != 0;
+  }
+};
+
 template <int FORM, int DP, bool BF, bool EXTRA>
 __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
                        volatile int *abort_flag, volatile int *last_flag) {
@@ -747,7 +785,6 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   const int s = warp >> 2, quarter = warp & 3, thread = 32 * quarter + lane;
   const int row = SP ? lane : thread, col0 = SP ? 32 * quarter : 0;
   const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-  const uint32_t tmem_o = tmem + 256 + 128 * s + lanes;
   uint32_t it = 0;        // key tiles of this stream so far
   Ring<C::kStages> rv;    // the current tile's V
   rv.next();
@@ -758,34 +795,13 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     return wait_for_all(bars + 8 * (B::kOD + (t & 1)), (t >> 1) & 1, abort_flag, a);
   };
   uint32_t o_done = 0;    // two streams: pieces of this stream so far
-  uint32_t joins = 0;     // meetings of the stream's warps so far
-  auto join = [&]() {     // the stream's four warps meet (bounded, as every wait)
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (B::kJoin + s));
-    return wait_for_all(bars + 8 * (B::kJoin + s), joins++ & 1, abort_flag, a);
-  };
-  // a split tile's piece: its partial result has been written; true for the last of its CTAs to come here
-  bool ok = true;
-  auto last_to_arrive = [&](int c0, int c1) {
-    __threadfence();
-    if (!(ok = join())) return false;
-    if (thread == 0) {
-      int *cnt = a.counters + 2 * c0 + s;
-      const int last = atomicAdd(cnt, 1) == c1 - c0;
-      if (last) *cnt = 0;
-      last_flag[s] = last;
-    }
-    if (!(ok = join())) return false;
-    if (!last_flag[s]) return false;
-    __threadfence();
-    return true;
-  };
+  Group<C::kStages> group{bars, s, 0, abort_flag};
   constexpr int kPart = DP * 128;
   auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
   const float sl2 = a.scale * kLog2e;
   const int row_tok = s * a.list.tpt + row / a.G;
   uint32_t pieces = 0;
-  ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
+  bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
   RowBound rb{0, 0, -1, 0}, rb_ahead{0, 0, -1, 0};
   // the row's keys in a piece, fetched while the piece before is in work
   auto bound_of = [&](const volatile Piece &x) {
@@ -812,6 +828,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const int lo = max(rb.lo, (int)w.klo), hi = min(rb.hi, (int)w.khi);
     const bool active = SP || 32 * quarter < nrows;
     const float slope = EXTRA && a.slopes && valid ? a.slopes[w.head * a.G + row % a.G] * kLog2e : 0.f;
+    const uint32_t tmem_o = tmem + 256 + 128 * (SP ? pieces & 1 : (uint32_t)s) + lanes;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
       const uint32_t buf = NS == 2 ? (uint32_t)s : (it & 1);
@@ -897,6 +914,18 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     // the next piece has been handed over: its first scores may be on their way
     if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
     rb_ahead = bound_of(piece[dn]);
+    if constexpr (SP) {  // the rest is the finishing warps' work
+      const uint32_t ob = pieces & 1;
+      float2 *ml = reinterpret_cast<float2 *>(smp + C::kScratchAt + 4 * kJoinRows * C::kScratchRow * 4) + ob * 4 * kSpreadRows;
+      if (!(ok = wait_for_all(bars + 8 * (B::kOE + ob), ((pieces >> 1) & 1) ^ 1, abort_flag, a))) break;
+      ml[thread] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + 8 * (B::kML + ob));
+        mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+      }
+      continue;
+    }
     // the piece's last product
     if (NS == 2) {
       ok = wait_for_all(bars + 8 * (B::kOD + s), o_done & 1, abort_flag, a);
@@ -913,111 +942,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     };
     const bool merge = w.merge;
     const int c0 = w.c0, c1 = w.c1;
-    if constexpr (SP) {
-      // Eight rows at a time: the quarters lay their rows side by side, then sixteen threads to a row add
-      // them, relative to the largest of their maxima.
-      float *sh = reinterpret_cast<float *>(smp + C::kScratchAt);
-      float2 *ml = reinterpret_cast<float2 *>(sh + 4 * kJoinRows * C::kScratchRow);
-      constexpr int V = DP / 16;
-      const int c = (thread & 15) * V;
-      ml[quarter * kSpreadRows + lane] = make_float2(m, l);
-      for (int r0 = 0; r0 < nrows && ok; r0 += kJoinRows) {
-        if (r0 > 0 && !(ok = join())) break;  // the rows before have been read
-#pragma unroll
-        for (int k = 0; k < DP / 32; ++k) {
-          float v[32];
-          from_tmem(k, v);
-          if (lane >= r0 && lane < r0 + kJoinRows) {
-            float4 *d = reinterpret_cast<float4 *>(sh + (quarter * kJoinRows + lane - r0) * C::kScratchRow + 32 * k);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
-        if (!(ok = join())) break;
-        const int rr = r0 + (thread >> 4);  // this thread's row and columns c .. c + V - 1
-        const bool mine = rr < nrows;
-        float mm = -INFINITY, ll = 0.f, v[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.f;
-        if (mine) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mm = fmaxf(mm, ml[q * kSpreadRows + rr].x);
-          const float ms = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 y = ml[q * kSpreadRows + rr];
-            const float f = ex2(y.x - ms);
-            ll = fmaf(f, y.y, ll);
-            const float4 *p = reinterpret_cast<const float4 *>(sh + (q * kJoinRows + rr - r0) * C::kScratchRow + c);
-#pragma unroll
-            for (int i = 0; i < V; i += 4) {
-              const float4 z = p[i / 4];
-              v[i] = fmaf(f, z.x, v[i]);
-              v[i + 1] = fmaf(f, z.y, v[i + 1]);
-              v[i + 2] = fmaf(f, z.z, v[i + 2]);
-              v[i + 3] = fmaf(f, z.w, v[i + 3]);
-            }
-          }
-        }
-        bool last = c0 == c1;
-        if (!last) {
-          const size_t my = slot_of(blockIdx.x, c0);
-          if (mine) {
-#pragma unroll
-            for (int i = 0; i < V; i += 4)
-              __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((c + i) / 4 * 128 + rr) * 4),
-                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-            if (c == 0) __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
-          }
-          if (a.to_prefix || r0 + kJoinRows < nrows) continue;
-          last = last_to_arrive(c0, c1);
-          if (!ok) break;
-        }
-        // whole tiles: these eight rows; split tiles: once all pieces are there, all rows
-        for (int q0 = c0 == c1 ? r0 : 0; last && q0 < (c0 == c1 ? min(nrows, r0 + kJoinRows) : nrows); q0 += kJoinRows) {
-          const int ro = q0 + (thread >> 4);
-          const bool use = ro < nrows;
-          if (use && c0 != c1) {
-            mm = -INFINITY;
-            for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, __ldcg(a.part_ml + slot_of(p, c0) * 128 + ro).x);
-            const float ms = mm == -INFINITY ? 0.f : mm;
-            ll = 0.f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.f;
-#pragma unroll 4
-            for (int p = c0; p <= c1; ++p) {
-              const size_t at = slot_of(p, c0);
-              const float2 y = __ldcg(a.part_ml + at * 128 + ro);
-              const float f = ex2(y.x - ms);
-              ll = fmaf(f, y.y, ll);
-#pragma unroll
-              for (int i = 0; i < V; i += 4) {
-                const float4 z =
-                    __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ((c + i) / 4 * 128 + ro) * 4));
-                v[i] = fmaf(f, z.x, v[i]);
-                v[i + 1] = fmaf(f, z.y, v[i + 1]);
-                v[i + 2] = fmaf(f, z.z, v[i + 2]);
-                v[i + 3] = fmaf(f, z.w, v[i + 3]);
-              }
-            }
-          }
-          const int tok = w.tok0 + ro / a.G, head = w.head * a.G + ro % a.G;
-          bool again = false;
-          if (use) {
-            const RowOut out = row_out(a, tok, head, merge, mm, ll);
-            again = !store_cols<V, BF>(a, out, tok, head, c, v) && finite(ll);
-            if (c == 0) store_lse(a, out);
-          }
-          const unsigned flagged = __ballot_sync(0xffffffffu, again);
-          for (int h = 0; h < 2; ++h)  // the warp's two rows
-            if (flagged >> (16 * h) & 0xffffu) {
-              const int rw = q0 + 2 * quarter + h;
-              redo_row<BF>(a, w.tok0 + rw / a.G, w.head * a.G + rw % a.G, w.klo, w.khi, w.trow, merge);
-            }
-        }
-      }
-      if (!ok) break;
-    } else {
+    {
       const int tok = w.tok0 + row_tok, head = w.head * a.G + row % a.G;
       // thread by row: 32 columns at a time from `get`
       auto emit = [&](float mm, float ll, auto get) {
@@ -1058,7 +983,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           }
           if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
         }
-        const bool last = !a.to_prefix && last_to_arrive(c0, c1);
+        const bool last = !a.to_prefix && group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
         if (!ok) break;
         if (last && active) {
           float mm = -INFINITY, ll = 0.f;
@@ -1096,17 +1021,170 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   }
 }
 
+// kSpread: the finishing warps.  Eight rows at a time: the quarters lay their rows side by side, then sixteen
+// threads to a row add them, relative to the largest of their maxima.
+template <int DP, bool BF>
+__device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
+                       volatile int *abort_flag, volatile int *last_flag) {
+  using C = Cfg<kSpread, DP>;
+  using B = Bars<C::kStages>;
+  const int quarter = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, thread = 32 * quarter + lane;
+  float *sh = reinterpret_cast<float *>(smp + C::kScratchAt);
+  constexpr int V = DP / 16, kPart = DP * 128;
+  const int c = (thread & 15) * V;  // this thread's columns c .. c + V - 1
+  auto slot_of = [&](int cta, int c0) { return part_slot(cta, c0, 1, 0); };
+  Group<C::kStages> group{bars, 0, 0, abort_flag};
+  bool ok = true;
+  for (uint32_t pieces = 0; ok; ++pieces) {
+    const uint32_t d = pieces % kPieces, ob = pieces & 1, par = (pieces >> 1) & 1;
+    if (!wait_for_all(bars + 8 * (B::kDF + d), (pieces / kPieces) & 1, abort_flag, a)) break;
+    const volatile Piece &w = piece[d];
+    if (w.n == 0) break;
+    const int nrows = w.ntok * a.G, c0 = w.c0, c1 = w.c1;
+    const bool merge = w.merge;
+    const float2 *ml = reinterpret_cast<const float2 *>(sh + 4 * kJoinRows * C::kScratchRow) + ob * 4 * kSpreadRows;
+    if (!(ok = wait_for_all(bars + 8 * (B::kML + ob), par, abort_flag, a))) break;
+    if (!(ok = wait_for_all(bars + 8 * (B::kOF + ob), par, abort_flag, a))) break;
+    tc_fence_after();
+    const uint32_t tmem_o = tmem + 256 + 128 * ob + ((uint32_t)(32 * quarter) << 16);
+    auto from_tmem = [&](int k, float (&v)[32]) {
+      __syncwarp();
+      tmem_ld32(tmem_o + 32 * k, reinterpret_cast<uint32_t *>(v));
+      tmem_wait_ld();
+    };
+    for (int r0 = 0; r0 < nrows && ok; r0 += kJoinRows) {
+      if (r0 > 0 && !(ok = group.join(a))) break;  // the rows before have been read
+#pragma unroll
+      for (int k = 0; k < DP / 32; ++k) {
+        float v[32];
+        from_tmem(k, v);
+        if (lane >= r0 && lane < r0 + kJoinRows) {
+          float4 *d = reinterpret_cast<float4 *>(sh + (quarter * kJoinRows + lane - r0) * C::kScratchRow + 32 * k);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      if (!(ok = group.join(a))) break;
+      const int rr = r0 + (thread >> 4);  // this thread's row and columns c .. c + V - 1
+      const bool mine = rr < nrows;
+      float mm = -INFINITY, ll = 0.f, v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = 0.f;
+      if (mine) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mm = fmaxf(mm, ml[q * kSpreadRows + rr].x);
+        const float ms = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 y = ml[q * kSpreadRows + rr];
+          const float f = ex2(y.x - ms);
+          ll = fmaf(f, y.y, ll);
+          const float4 *p = reinterpret_cast<const float4 *>(sh + (q * kJoinRows + rr - r0) * C::kScratchRow + c);
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            const float4 z = p[i / 4];
+            v[i] = fmaf(f, z.x, v[i]);
+            v[i + 1] = fmaf(f, z.y, v[i + 1]);
+            v[i + 2] = fmaf(f, z.z, v[i + 2]);
+            v[i + 3] = fmaf(f, z.w, v[i + 3]);
+          }
+        }
+      }
+      bool last = c0 == c1;
+      if (!last) {
+        const size_t my = slot_of(blockIdx.x, c0);
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4)
+            __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((c + i) / 4 * 128 + rr) * 4),
+                   make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+          if (c == 0) __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
+        }
+        if (a.to_prefix || r0 + kJoinRows < nrows) continue;
+        last = group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
+        if (!ok) break;
+      }
+      // whole tiles: these eight rows; split tiles: once all pieces are there, all rows
+      for (int q0 = c0 == c1 ? r0 : 0; last && q0 < (c0 == c1 ? min(nrows, r0 + kJoinRows) : nrows); q0 += kJoinRows) {
+        const int ro = q0 + (thread >> 4);
+        const bool use = ro < nrows;
+        if (use && c0 != c1) {  // running maximum and sums over four pieces at a time
+          mm = -INFINITY;
+          ll = 0.f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] = 0.f;
+          for (int p0 = c0; p0 <= c1; p0 += 4) {
+            float2 y[4];
+            float4 z[4][V / 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool in = p0 + k <= c1;
+              const size_t at = slot_of(in ? p0 + k : c1, c0);
+              y[k] = __ldcg(a.part_ml + at * 128 + ro);
+#pragma unroll
+              for (int i = 0; i < V / 4; ++i)
+                z[k][i] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ((c / 4 + i) * 128 + ro) * 4));
+              if (!in) y[k] = make_float2(-INFINITY, 0.f);
+            }
+            const float mn = fmaxf(fmaxf(fmaxf(mm, y[0].x), fmaxf(y[1].x, y[2].x)), y[3].x);
+            const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(mm - ms);
+            ll *= keep;
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] *= keep;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (p0 + k > c1) break;
+              const float f = ex2(y[k].x - ms);
+              ll = fmaf(f, y[k].y, ll);
+#pragma unroll
+              for (int i = 0; i < V; i += 4) {
+                v[i] = fmaf(f, z[k][i / 4].x, v[i]);
+                v[i + 1] = fmaf(f, z[k][i / 4].y, v[i + 1]);
+                v[i + 2] = fmaf(f, z[k][i / 4].z, v[i + 2]);
+                v[i + 3] = fmaf(f, z[k][i / 4].w, v[i + 3]);
+              }
+            }
+            mm = mn;
+          }
+        }
+        const int tok = w.tok0 + ro / a.G, head = w.head * a.G + ro % a.G;
+        bool again = false;
+        if (use) {
+          const RowOut out = row_out(a, tok, head, merge, mm, ll);
+          again = !store_cols<V, BF>(a, out, tok, head, c, v) && finite(ll);
+          if (c == 0) store_lse(a, out);
+        }
+        const unsigned flagged = __ballot_sync(0xffffffffu, again);
+        for (int h = 0; h < 2; ++h)  // the warp's two rows
+          if (flagged >> (16 * h) & 0xffffu) {
+            const int rw = q0 + 2 * quarter + h;
+            redo_row<BF>(a, w.tok0 + rw / a.G, w.head * a.G + rw % a.G, w.klo, w.khi, w.trow, merge);
+          }
+      }
+    }
+    if (!ok) break;
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bars + 8 * (B::kOE + ob));
+      mbar_arrive(bars + 8 * (B::kDE + d));
+    }
+    ok = group.join(a);  // the shared rows have been read
+  }
+}
+
 // Results over shared prefixes: the sum of each split tile's pieces.  A prefix has few tiles in many pieces,
 // and one CTA of the attention kernel adding up a tile's (18 pieces of 64 KB for 256 rows over 4096 keys)
-// took longer than the products; here a CTA takes 16 columns of one tile's 128 rows, a thread a row.
+// took longer than the products; here a CTA takes 4 columns of one tile's 128 rows, a thread a row, and
+// loads eight pieces at a time.
 template <int DP, bool BF>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int kGroups = DP / 16;
+  constexpr int kBatch = 8;
   pdl_trigger();
   pdl_wait();
   int i = blockIdx.x;
-  const int c = i % kGroups * 16;
-  i /= kGroups;
+  const int c = i % (DP / 4) * 4;
+  i /= DP / 4;
   const int s = i % a.list.streams;
   i /= a.list.streams;
   const int head = i % a.Hkv, tile = i / a.Hkv;
@@ -1118,31 +1196,40 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   if (ctas.x == ctas.y || c >= a.D) return;  // in one piece: its CTA has written the result
   bool again = false;
   if (valid) {
-    float m = -INFINITY, l = 0.f, v[16];
-#pragma unroll 4
-    for (int p = ctas.x; p <= ctas.y; ++p)
-      m = fmaxf(m, a.part_ml[part_slot(p, ctas.x, a.list.streams, s) * 128 + row].x);
-    const float ms = m == -INFINITY ? 0.f : m;
+    // running maximum and sums over batches of pieces
+    float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p0 = ctas.x; p0 <= ctas.y; p0 += kBatch) {
+      float2 y[kBatch];
+      float4 z[kBatch];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 4
-    for (int p = ctas.x; p <= ctas.y; ++p) {
-      const size_t at = part_slot(p, ctas.x, a.list.streams, s);
-      const float2 y = a.part_ml[at * 128 + row];
-      const float f = ex2(y.x - ms);
-      l = fmaf(f, y.y, l);
-      const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 z = src[k * 128];
-        v[4 * k] = fmaf(f, z.x, v[4 * k]);
-        v[4 * k + 1] = fmaf(f, z.y, v[4 * k + 1]);
-        v[4 * k + 2] = fmaf(f, z.z, v[4 * k + 2]);
-        v[4 * k + 3] = fmaf(f, z.w, v[4 * k + 3]);
+      for (int k = 0; k < kBatch; ++k) {
+        const bool in = p0 + k <= ctas.y;
+        const size_t at = part_slot(in ? p0 + k : ctas.y, ctas.x, a.list.streams, s);
+        y[k] = __ldcg(a.part_ml + at * 128 + row);
+        z[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
+        if (!in) y[k] = make_float2(-INFINITY, 0.f);
       }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, y[k].x);
+      const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(m - ms);
+      l *= keep;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] *= keep;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (p0 + k > ctas.y) break;
+        const float f = ex2(y[k].x - ms);
+        l = fmaf(f, y[k].y, l);
+        v[0] = fmaf(f, z[k].x, v[0]);
+        v[1] = fmaf(f, z[k].y, v[1]);
+        v[2] = fmaf(f, z[k].z, v[2]);
+        v[3] = fmaf(f, z[k].w, v[3]);
+      }
+      m = mn;
     }
     const RowOut out = row_out(a, tok, h, false, m, l);
-    again = !store_cols<16, BF>(a, out, tok, h, c, v) && finite(l);
+    again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
     if (c == 0) store_lse(a, out);
   }
   unsigned flagged = __ballot_sync(0xffffffffu, again);
@@ -1150,7 +1237,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const int src = __ffs(flagged) - 1;
     flagged &= flagged - 1;
     redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, false,
-                 c, c + 16);
+                 c, c + 4);
   }
 }
 
@@ -1179,19 +1266,27 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
       mbar_init(bars + 8 * (B::kPF + i), 4);
       mbar_init(bars + 8 * (B::kOD + i), 1);
       mbar_init(bars + 8 * (B::kJoin + i), 4);
+      mbar_init(bars + 8 * (B::kOF + i), 1);
+      mbar_init(bars + 8 * (B::kOE + i), 4);
+      mbar_init(bars + 8 * (B::kML + i), 4);
     }
     mbar_init(bars + 8 * B::kDrain, 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bars + 8 * (B::kDF + i), 1);
-      mbar_init(bars + 8 * (B::kDE + i), C::kSoftWarps + 1);  // the softmax warps and the MMA thread
+      mbar_init(bars + 8 * (B::kDE + i), C::kProdWarp + 1);  // the softmax and finishing warps and the MMA warp
     }
     abort_flag = (sm & 1023u) != 0u;  // the swizzled tiles are 1 KB-aligned
     if (abort_flag) atomicOr(a.err, kAttnErrWait);
     fence_mbar_init();
   }
-  if (warp == C::kSoftWarps) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_slot), kTmemColsAttn);
     tmem_relinquish();
+  }
+  if (threadIdx.x == 32 * C::kProdWarp) {
+    prefetch_tensormap(&maps.q);
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
   }
   tc_fence_before();
   __syncthreads();
@@ -1202,11 +1297,15 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   if (warp < C::kSoftWarps) {
     if (NS == 2) regs_inc<kRegsSoft>();
     if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+  } else if (warp < C::kProdWarp) {
+    if constexpr (FORM == kSpread) {
+      if (!abort_flag) finish<DP, BF>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+    }
   } else {
     if (NS == 2) regs_dec<kRegsOther>();
     if (abort_flag) {
     } else if (warp < C::kMmaWarp) {
-      produce<FORM, DP>(a, maps, warp - C::kSoftWarps, piece, sm, bars, &abort_flag);
+      produce<FORM, DP>(a, maps, warp - C::kProdWarp, piece, sm, bars, &abort_flag);
     } else if (warp == C::kMmaWarp) {
       issue<FORM, DP, BF>(a, piece, sm, bars, tmem, &abort_flag);
     }
@@ -1214,7 +1313,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kSoftWarps) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemColsAttn);
   }
@@ -1231,7 +1330,7 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
   if (!a.to_prefix) return (int)cudaGetLastError();
   // tiles that the list can have: whole ones, and the short last one of each group
   const int tt = a.list.tpt * a.list.streams, tiles = a.n_tokens / tt + a.n_groups;
-  return (int)launch_pdl(attn_join_kernel<DP, BF>, dim3((unsigned)(tiles * a.Hkv * a.list.streams * (DP / 16))),
+  return (int)launch_pdl(attn_join_kernel<DP, BF>, dim3((unsigned)(tiles * a.Hkv * a.list.streams * (DP / 4))),
                          dim3(128), 0, st, a);
 }
 

@@ -54,6 +54,7 @@ struct AttnTile {
 // Where a CTA's share of the work begins.
 struct AttnStart {
   int tile, head, off, n;  // unit `off` of (tile, head); n units in all
+  AttnTile t;              // the tile
 };
 
 // One list of work.  In the order (tile, head), each has kAttnPieceCost units without keys and then one for

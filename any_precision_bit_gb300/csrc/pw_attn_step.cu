@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   for (int c = tid; c < a.ctas; c += kListThreads) {
     const long long P = min((long long)a.ctas, W);
     const long long u0 = min(c * W / P, W), u1 = min((c + 1) * W / P, W);
-    AttnStart st{0, 0, 0, (int)(u1 - u0)};
+    AttnStart st{0, 0, 0, (int)(u1 - u0), {}};
     if (u1 > u0) {
       int lo = 0, hi = n_tiles - 1;  // the last tile whose units begin at or before u0
       while (lo < hi) {
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
       st.tile = lo;
       st.head = (int)(rem / cost);
       st.off = (int)(rem - (long long)st.head * cost);
+      st.t = a.list.tiles[lo];
     }
     a.list.start[c] = st;
   }

@@ -183,4 +183,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
+// Fetch a tensor map ahead of the first copy that uses it.
+__device__ __forceinline__ void prefetch_tensormap(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(tmap) : "memory");
+}
 }  // namespace pw
