@@ -109,8 +109,8 @@ struct Cfg {
   static constexpr int kThreads = FORM == kTwo ? 384 : 32 * (kMmaWarp + 1);
 };
 // Two tiles: 384 threads of 168 registers at launch, of which the softmax warps, which hold 128 scores
-// each, need more: 256 x 224 + 128 x 56 = 384 x 168.
-constexpr int kRegsSoft = 224, kRegsOther = 56;
+// each, need more: 256 x 216 + 128 x 72 = 384 x 168.
+constexpr int kRegsSoft = 216, kRegsOther = 72;
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -176,12 +176,14 @@ struct Walk {
   int tile, head, off, left;  // off and left in units (kAttnPieceCost of them lead each (tile, head))
   AttnTile t, ahead;
   int j0, n;  // first key tile of this piece within the tile's, and their number
+  int2 first_ctas, last_ctas;  // ctas_of for the CTA's first and last piece
   bool fresh; // the tile is another than the last piece's
   __device__ __forceinline__ explicit Walk(const AttnArgs &a) {
     const AttnStart *s = a.list.start + blockIdx.x;
     const int4 x = *reinterpret_cast<const int4 *>(s);
     t = load_tile(&s->t);
     tile = x.x, head = x.y, off = x.z, left = x.w;
+    first_ctas = s->first, last_ctas = s->last;
     fresh = true;
     if (left > 0) ahead = load_tile(a.list.tiles + tile + 1);
   }
@@ -214,7 +216,8 @@ struct Walk {
   __device__ __forceinline__ int first() const { return t.kv0 + j0; }
   __device__ __forceinline__ void describe(const AttnArgs &a, Piece *p) const {
     int2 c = make_int2(0, 0);
-    if (n != t.kv1 - t.kv0) c = ctas_of(a, t, tile, head);
+    // a piece that lacks its tile's beginning is the CTA's first, one that lacks only its end the last
+    if (n != t.kv1 - t.kv0) c = j0 > 0 ? first_ctas : last_ctas;
     *p = Piece{n, first(), head, t.tok0, t.ntok, t.trow, t.klo, t.khi, fresh, t.merge && !a.to_prefix, c.x, c.y};
   }
 };
@@ -291,10 +294,10 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
     }
     return y;
   };
-  if (leads) ok = publish(0);
   while (more && ok) {
     if (leads) {
       const uint32_t qb = pieces % nq;
+      if (!(ok = publish(pieces))) break;
       ok = wait_for_all(bars + 8 * (B::kQE + qb), ((pieces / nq) & 1) ^ 1, abort_flag, a);
       if (!ok) break;
       const int ns = NS == 2 && w.t.ntok > a.list.tpt ? 2 : 1;
@@ -332,8 +335,8 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
       r.next();
       r.next();
     }
-    if (leads) ok = ok && publish(pieces);
   }
+  if (leads && ok) ok = publish(pieces);
   if (!ok) {  // given up: wait for what was issued before the shared memory goes away
     const long long t0 = clock64();
     auto drain = [&](uint32_t bar, uint32_t par) {
@@ -398,22 +401,26 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
   };
   auto full = [&](const Ring<C::kStages> &x) { return wait(B::kFull + x.st, x.ph); };
   auto release = [&](uint32_t st) { tc_commit(bars + 8 * (B::kEmpty + st)); };
-  for (; ok; ++pieces) {
-    const uint32_t d = pieces % kPieces;
-    if (!wait(B::kDF + d, (pieces / kPieces) & 1)) break;
-    const int n = __shfl_sync(0xffffffffu, piece[d].n, 0);
-    const bool two = NS == 2 && __shfl_sync(0xffffffffu, piece[d].ntok, 0) > a.list.tpt;
-    if (n == 0) break;
+  // the next piece's key tiles and whether its second tile has rows; false at the end or when giving up
+  auto next_piece = [&](uint32_t i, int &n, bool &two) {
+    const uint32_t d = i % kPieces;
+    if (!(ok = wait(B::kDF + d, (i / kPieces) & 1))) return false;
+    n = __shfl_sync(0xffffffffu, piece[d].n, 0);
+    two = NS == 2 && __shfl_sync(0xffffffffu, piece[d].ntok, 0) > a.list.tpt;
+    if (n == 0) return false;
     if (elect_one()) mbar_arrive(bars + 8 * (B::kDE + d));
     __syncwarp();
-    const uint32_t qb = pieces % nq;
-    const uint32_t ob = SP ? pieces & 1 : 0;  // output accumulator
-    const uint32_t q0 = M::lo_k(sm + qb * kQBufferStep<FORM>);
-    ok = wait(B::kQF + qb, (pieces / nq) & 1) && full(r);
-    if (!ok) break;
-    uint32_t k_st = r.st;
-    r.next();
-    if (NS == 2) {
+    return ok = wait(B::kQF + i % nq, (i / nq) & 1);
+  };
+  int n = 0;
+  bool two = false;
+  bool more_pieces = next_piece(0, n, two);
+  if constexpr (NS == 2) {
+    for (; more_pieces; more_pieces = next_piece(++pieces, n, two)) {
+      const uint32_t q0 = M::lo_k(sm);
+      if (!(ok = full(r))) break;
+      uint32_t k_st = r.st;
+      r.next();
       if (elect_one()) {
         M::qk(tmem, q0, ring_k + k_st * kStep);
         tc_commit(bars + 8 * B::kSF);
@@ -470,41 +477,52 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
         }
         p_par ^= 1;
       }
-    } else {
+      if (!ok) break;
+    }
+  } else {
+    // The scores of the next key tile, be it of the next piece, are issued before the wait for this tile's
+    // probabilities.
+    uint32_t k_st = 0;
+    int j = 0;  // key tile of the piece
+    auto scores = [&](uint32_t buf, bool last_of_piece, uint32_t qb) {  // of the tile whose keys come next
+      if (!(ok = full(r))) return;
+      k_st = r.st;
+      r.next();
       if (elect_one()) {
-        M::qk(tmem + 128 * (it & 1), q0, ring_k + k_st * kStep);
-        tc_commit(bars + 8 * (B::kSF + (it & 1)));
+        M::qk(tmem + 128 * buf, M::lo_k(sm + qb * kQBufferStep<FORM>), ring_k + k_st * kStep);
+        tc_commit(bars + 8 * (B::kSF + buf));
         release(k_st);
-        if (n == 1) tc_commit(bars + 8 * (B::kQE + qb));
+        if (last_of_piece) tc_commit(bars + 8 * (B::kQE + qb));
       }
       __syncwarp();
-      for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t b = it & 1, v_st = r.st;
-        const Ring<C::kStages> rv = r;
-        r.next();
-        if (j + 1 < n) {
-          if (!(ok = full(r))) break;
-          k_st = r.st;
-          r.next();
-          if (elect_one()) {
-            M::qk(tmem + 128 * (b ^ 1), q0, ring_k + k_st * kStep);
-            tc_commit(bars + 8 * (B::kSF + (b ^ 1)));
-            release(k_st);
-            if (j + 2 == n) tc_commit(bars + 8 * (B::kQE + qb));
-          }
-          __syncwarp();
-        }
-        if (!(ok = full(rv))) break;
-        if (SP && j == 0 && !(ok = wait(B::kOE + ob, ((pieces >> 1) & 1) ^ 1))) break;
-        if (!(ok = wait(B::kPF + b, (it >> 1) & 1))) break;
-        if (elect_one()) {
-          M::pv(o0 + 128 * ob, tmem + 128 * b, ring_v + v_st * kStep, j > 0);
-          tc_commit(bars + 8 * (B::kOD + b));
-          if (SP && j + 1 == n) tc_commit(bars + 8 * (B::kOF + ob));
-          release(v_st);
-        }
-        __syncwarp();
+    };
+    if (more_pieces) scores(0, n == 1, 0);
+    while (ok && more_pieces) {
+      const uint32_t b = it & 1, ob = SP ? pieces & 1 : 0;  // score buffer, output accumulator
+      const Ring<C::kStages> rv = r;                        // this tile's values follow its keys
+      r.next();
+      const bool first = j == 0, last = j + 1 == n;
+      uint32_t of_piece = pieces;
+      if (last) {
+        more_pieces = next_piece(++of_piece, n, two);
+        if (!ok) break;
+        j = 0;
+      } else {
+        ++j;
       }
+      if (more_pieces) scores(b ^ 1, j + 1 == n, of_piece % nq);
+      if (!ok || !(ok = full(rv))) break;
+      if (SP && first && !(ok = wait(B::kOE + ob, ((pieces >> 1) & 1) ^ 1))) break;
+      if (!(ok = wait(B::kPF + b, (it >> 1) & 1))) break;
+      if (elect_one()) {
+        M::pv(o0 + 128 * ob, tmem + 128 * b, ring_v + rv.st * kStep, !first);
+        tc_commit(bars + 8 * (B::kOD + b));
+        if (SP && last) tc_commit(bars + 8 * (B::kOF + ob));
+        release(rv.st);
+      }
+      __syncwarp();
+      pieces = of_piece;
+      ++it;
     }
   }
   // nothing of the tensor cores is in flight when tensor memory is freed
@@ -576,40 +594,40 @@ __device__ __forceinline__ float max_of(const float (&x)[N]) {
 }
 
 // Scores of the keys base + i to log2 units with cap and bias.  tanh(y) = y P(y^2) with a polynomial of
-// degree 5 (fitted at Chebyshev nodes on |y| <= 3/4; largest error 9.3e-8), on the multiply-add pipe; a
-// warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, whose two special-function
-// operations per score bound the softmax.
+// degree 4 (fitted at Chebyshev nodes on |y| <= 1/2; largest error 3.8e-8), on the multiply-add pipe; a
+// warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, with two special-function
+// operations for each score.  (tanh itself in one such operation is off by 2^-11: capped scores, and so
+// probabilities, would lose as much.)
 template <int N>
 __device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool valid, float slope, float d0) {
-  const float scale2 = a.scale * kLog2e;
   if (a.softcap > 0.f) {
-    const float inv = a.scale / a.softcap, cap2 = a.softcap * kLog2e;
+    const float inv = a.inv_cap, cap2 = a.cap2;
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; i += 8)
 #pragma unroll
       for (int k = 0; k < 4; ++k) top[k] = max3(top[k], fabsf(x[i + 2 * k]), fabsf(x[i + 2 * k + 1]));
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(inv);
-    if (__any_sync(0xffffffffu, valid && !(most <= 0.75f))) {
+    if (__any_sync(0xffffffffu, valid && !(most <= 0.5f))) {
       const float t2 = 2.f * kLog2e * inv;
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = cap2 - 2.f * cap2 * rcp(ex2(x[i] * t2) + 1.f);
     } else {
-      const uint64_t s = pair(inv, inv), c = pair(cap2, cap2);
+      const uint64_t s = pair(inv, inv);
+      const float c1 = -0.3333307206630707f * cap2, c2 = 0.13324828445911407f * cap2, c3 = -0.05298924073576927f * cap2,
+                  c4 = 0.017141319811344147f * cap2;
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         const uint64_t y = mul2(pair(x[i], x[i + 1]), s), u = mul2(y, y);
-        uint64_t r = pair(-0.004723952151834965f, -0.004723952151834965f);
-        r = fma2(r, u, pair(0.01959378644824028f, 0.01959378644824028f));
-        r = fma2(r, u, pair(-0.053349819034338f, -0.053349819034338f));
-        r = fma2(r, u, pair(0.13325515389442444f, 0.13325515389442444f));
-        r = fma2(r, u, pair(-0.3333296775817871f, -0.3333296775817871f));
-        r = fma2(r, u, pair(1.f, 1.f));
-        unpair(mul2(r, mul2(y, c)), x[i], x[i + 1]);
+        uint64_t r = fma2(pair(c4, c4), u, pair(c3, c3));
+        r = fma2(r, u, pair(c2, c2));
+        r = fma2(r, u, pair(c1, c1));
+        r = fma2(r, u, pair(cap2, cap2));
+        unpair(mul2(r, y), x[i], x[i + 1]);
       }
     }
   } else {
-    const uint64_t s = pair(scale2, scale2);
+    const uint64_t s = pair(a.scale2, a.scale2);
 #pragma unroll
     for (int i = 0; i < N; i += 2) unpair(mul2(pair(x[i], x[i + 1]), s), x[i], x[i + 1]);
   }
@@ -655,14 +673,13 @@ struct RowOut {
   float inv, w2, lse2;
   size_t at;  // the row in [n_tokens][Hq] order
 };
-__device__ __forceinline__ RowOut row_out(const AttnArgs &a, int tok, int head, bool merge, float m, float l) {
+__device__ __forceinline__ RowOut row_out(const AttnArgs &a, int tok, int head, bool merge, float pl, float m, float l) {
   RowOut r;
   r.at = (size_t)tok * a.Hq + head;
   r.inv = l == 0.f ? 0.f : 1.f / l;
   r.lse2 = l == 0.f ? -INFINITY : m + lg2(l);
   r.w2 = 0.f;
-  if (merge) {
-    const float pl = a.prefix_lse[r.at];
+  if (merge) {  // pl: the row's log2-sum-exp2 over the prefix
     const float mx = fmaxf(pl, r.lse2), ms = mx == -INFINITY ? 0.f : mx;
     const float e1 = ex2(r.lse2 - ms), e2 = ex2(pl - ms), sum = e1 + e2;
     const float is = sum == 0.f ? 0.f : 1.f / sum;
@@ -673,8 +690,10 @@ __device__ __forceinline__ RowOut row_out(const AttnArgs &a, int tok, int head, 
   return r;
 }
 // N consecutive elements from column c of a row; false if one is not finite.
+// `ready`: the row's result over the prefix from column c on, or null to load it here where it counts.
 template <int N, bool BF>
-__device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, int tok, int head, int c, float (&v)[N]) {
+__device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, int tok, int head, int c, float (&v)[N],
+                                           const float4 *ready = nullptr) {
   static_assert(N % 4 == 0, "stores of 8 or 16 bytes");
   if (c >= a.D) return true;
 #pragma unroll
@@ -684,7 +703,7 @@ __device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, i
 #pragma unroll
     for (int i = 0; i < N; i += 4)
       if (c + i < a.D) {
-        const float4 x = *reinterpret_cast<const float4 *>(po + i);
+        const float4 x = ready ? ready[i / 4] : *reinterpret_cast<const float4 *>(po + i);
         v[i] = fmaf(r.w2, x.x, v[i]);
         v[i + 1] = fmaf(r.w2, x.y, v[i + 1]);
         v[i + 2] = fmaf(r.w2, x.z, v[i + 2]);
@@ -798,7 +817,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   Group<C::kStages> group{bars, s, 0, abort_flag};
   constexpr int kPart = DP * 128;
   auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
-  const float sl2 = a.scale * kLog2e;
+  const float sl2 = a.scale2;
   const int row_tok = s * a.list.tpt + row / a.G;
   uint32_t pieces = 0;
   bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
@@ -947,7 +966,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       // thread by row: 32 columns at a time from `get`
       auto emit = [&](float mm, float ll, auto get) {
         RowOut out{};
-        if (valid) out = row_out(a, tok, head, merge, mm, ll);
+        if (valid) out = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, mm, ll);
         bool fin = true;
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
@@ -1043,6 +1062,16 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const int nrows = w.ntok * a.G, c0 = w.c0, c1 = w.c1;
     const bool merge = w.merge;
     const float2 *ml = reinterpret_cast<const float2 *>(sh + 4 * kJoinRows * C::kScratchRow) + ob * 4 * kSpreadRows;
+    // the first eight rows' results over the shared prefix, fetched while the piece is in work
+    float pl = 0.f;
+    float4 po[V / 4];
+    const int row0 = thread >> 4;
+    if (merge && row0 < nrows && c < a.D) {
+      const size_t at = (size_t)(w.tok0 + row0 / a.G) * a.Hq + w.head * a.G + row0 % a.G;
+      pl = a.prefix_lse[at];
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) po[i] = *reinterpret_cast<const float4 *>(a.prefix_o + at * a.D + c + 4 * i);
+    }
     if (!(ok = wait_for_all(bars + 8 * (B::kML + ob), par, abort_flag, a))) break;
     if (!(ok = wait_for_all(bars + 8 * (B::kOF + ob), par, abort_flag, a))) break;
     tc_fence_after();
@@ -1150,8 +1179,10 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         const int tok = w.tok0 + ro / a.G, head = w.head * a.G + ro % a.G;
         bool again = false;
         if (use) {
-          const RowOut out = row_out(a, tok, head, merge, mm, ll);
-          again = !store_cols<V, BF>(a, out, tok, head, c, v) && finite(ll);
+          const bool near = q0 == 0;  // fetched above
+          if (merge && !near) pl = a.prefix_lse[(size_t)tok * a.Hq + head];
+          const RowOut out = row_out(a, tok, head, merge, pl, mm, ll);
+          again = !store_cols<V, BF>(a, out, tok, head, c, v, near ? po : nullptr) && finite(ll);
           if (c == 0) store_lse(a, out);
         }
         const unsigned flagged = __ballot_sync(0xffffffffu, again);
@@ -1228,7 +1259,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
       }
       m = mn;
     }
-    const RowOut out = row_out(a, tok, h, false, m, l);
+    const RowOut out = row_out(a, tok, h, false, 0.f, m, l);
     again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
     if (c == 0) store_lse(a, out);
   }

@@ -55,6 +55,9 @@ struct AttnTile {
 struct AttnStart {
   int tile, head, off, n;  // unit `off` of (tile, head); n units in all
   AttnTile t;              // the tile
+  // CTAs of the first and the last key tile of the (tile, head) that the CTA begins in, and of the one that it
+  // ends in
+  int2 first, last;
 };
 
 // One list of work.  In the order (tile, head), each has kAttnPieceCost units without keys and then one for
@@ -123,6 +126,7 @@ struct AttnArgs {
   int64_t block_stride, token_stride, head_stride;
   float *lse;
   float scale, softcap;
+  float scale2, inv_cap, cap2;  // scale log2 e, scale / softcap, softcap log2 e
   const float *slopes;
   // Results over a shared prefix, normalised, and their log2-sum-exp2: written (to_prefix) or merged
   // into the rows of tiles with `merge`.

@@ -390,6 +390,9 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.scale = scale;
   g.softcap = softcap;
   g.slopes = slopes;
+  g.scale2 = scale * 1.4426950408889634f;
+  g.cap2 = softcap * 1.4426950408889634f;
+  g.inv_cap = softcap > 0.f ? scale / softcap : 0.f;
   g.err = a->err;
   g.wait_cycles = kWaitCyclesDefault;
   g.part_o = a->part_o;

@@ -286,22 +286,30 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   for (int c = tid; c < a.ctas; c += kListThreads) {
     const long long P = min((long long)a.ctas, W);
     const long long u0 = min(c * W / P, W), u1 = min((c + 1) * W / P, W);
-    AttnStart st{0, 0, 0, (int)(u1 - u0), {}};
-    if (u1 > u0) {
-      int lo = 0, hi = n_tiles - 1;  // the last tile whose units begin at or before u0
+    AttnStart st{0, 0, 0, (int)(u1 - u0), {}, {0, 0}, {0, 0}};
+    // the (tile, head) of a unit, and the CTAs of its first and last key tiles
+    auto find = [&](long long u, int &tile, int &head, int &off) {
+      int lo = 0, hi = n_tiles - 1;  // the last tile whose units begin at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((long long)a.list.cum[mid] * a.n_kv_heads <= u0)
+        if ((long long)a.list.cum[mid] * a.n_kv_heads <= u)
           lo = mid;
         else
           hi = mid - 1;
       }
       const int cost = a.list.cum[lo + 1] - a.list.cum[lo];
-      const long long rem = u0 - (long long)a.list.cum[lo] * a.n_kv_heads;
-      st.tile = lo;
-      st.head = (int)(rem / cost);
-      st.off = (int)(rem - (long long)st.head * cost);
-      st.t = a.list.tiles[lo];
+      const long long rem = u - (long long)a.list.cum[lo] * a.n_kv_heads;
+      tile = lo;
+      head = (int)(rem / cost);
+      off = (int)(rem - (long long)head * cost);
+      const long long ub = u - off;
+      return make_int2((int)(((ub + kAttnPieceCost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
+    };
+    if (u1 > u0) {
+      st.first = find(u0, st.tile, st.head, st.off);
+      int tile, head, off;
+      st.last = find(u1 - 1, tile, head, off);
+      st.t = a.list.tiles[st.tile];
     }
     a.list.start[c] = st;
   }
