@@ -161,13 +161,6 @@ __device__ __forceinline__ AttnTile load_tile(const AttnTile *p) {
   t.khi = y.x, t.kv0 = y.y, t.kv1 = y.z, t.merge = y.w;
   return t;
 }
-// The CTAs that take the first and the last key tile of a (tile, head).
-__device__ __forceinline__ int2 ctas_of(const AttnArgs &a, const AttnTile &t, int tile, int head) {
-  const int cost = t.kv1 - t.kv0 + kAttnPieceCost;
-  const long long W = (long long)a.list.meta[1] * a.Hkv, P = min((long long)a.ctas, W);
-  const long long ub = (long long)a.list.cum[tile] * a.Hkv + (long long)head * cost;
-  return make_int2((int)(((ub + kAttnPieceCost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
-}
 // Slot of a split tile's piece among the partial results: a CTA's last piece, if it begins its tile, or its first.
 __device__ __forceinline__ size_t part_slot(int cta, int c0, int streams, int s) {
   return ((size_t)cta * 2 + (cta == c0 ? 1 : 0)) * streams + s;
@@ -176,7 +169,7 @@ struct Walk {
   int tile, head, off, left;  // off and left in units (kAttnPieceCost of them lead each (tile, head))
   AttnTile t, ahead;
   int j0, n;  // first key tile of this piece within the tile's, and their number
-  int2 first_ctas, last_ctas;  // ctas_of for the CTA's first and last piece
+  int2 first_ctas, last_ctas;  // see AttnStart
   bool fresh; // the tile is another than the last piece's
   __device__ __forceinline__ explicit Walk(const AttnArgs &a) {
     const AttnStart *s = a.list.start + blockIdx.x;
@@ -246,7 +239,7 @@ __device__ __forceinline__ uint32_t q_buffers(const AttnArgs &a) {
 template <int FORM>
 constexpr uint32_t kQBufferStep = FORM == kSpread ? 16 * 128 : 64 * 128;  // bytes between the two buffers
 
-// A producer warp: the keys (kv = 0) or values of every key tile, or every other box of them; the first of
+// A producer warp: the keys (kv = 0) or values of every key tile, or every other box of them; the last of
 // the warps also loads the queries and hands the pieces over.
 template <int FORM, int DP>
 __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece *piece, uint32_t sm, uint32_t bars,
@@ -256,7 +249,7 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   using B = Bars<C::kStages>;
   constexpr int kShare = C::kProducers / 2;  // warps that share a tile's boxes
   const int lane = threadIdx.x & 31, kv = self / kShare, share = self % kShare;
-  const bool leads = self == 0;
+  const bool leads = self == C::kProducers - 1;  // values are needed later than keys
   const int bt = 1 << a.log_bt, ppt = kAttnKeys >> a.log_bt;  // blocks of a key tile
   const int page = lane % ppt, half = lane / ppt;             // this lane's box
   const bool mine = half < C::kHalves;
@@ -954,6 +947,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     }
     if (!ok) break;
     tc_fence_after();
+    if (a.after_prefix) pdl_wait();  // (returns at once but the first time)
     auto from_tmem = [&](int c, float (&v)[32]) {
       __syncwarp();  // a load of the whole warp: lanes without a row come from other branches
       tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
@@ -1054,6 +1048,21 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   auto slot_of = [&](int cta, int c0) { return part_slot(cta, c0, 1, 0); };
   Group<C::kStages> group{bars, 0, 0, abort_flag};
   bool ok = true;
+  const int row0 = thread >> 4, tok0 = row0 / a.G, head0 = row0 - tok0 * a.G;  // the first eight rows: this thread's
+  // their results over the shared prefix, fetched a piece ahead where the next one is known by then
+  float pl = 0.f;
+  float4 po[V / 4];
+  uint32_t fetched = 0;  // pieces up to here
+  auto fetch = [&](const volatile Piece &w) {
+    if (w.n && w.merge && row0 < w.ntok * a.G && c < a.D) {
+      const size_t at = (size_t)(w.tok0 + tok0) * a.Hq + w.head * a.G + head0;
+      pl = a.prefix_lse[at];
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) po[i] = *reinterpret_cast<const float4 *>(a.prefix_o + at * a.D + c + 4 * i);
+    }
+    ++fetched;
+  };
+  if (a.after_prefix) pdl_wait();
   for (uint32_t pieces = 0; ok; ++pieces) {
     const uint32_t d = pieces % kPieces, ob = pieces & 1, par = (pieces >> 1) & 1;
     if (!wait_for_all(bars + 8 * (B::kDF + d), (pieces / kPieces) & 1, abort_flag, a)) break;
@@ -1062,16 +1071,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const int nrows = w.ntok * a.G, c0 = w.c0, c1 = w.c1;
     const bool merge = w.merge;
     const float2 *ml = reinterpret_cast<const float2 *>(sh + 4 * kJoinRows * C::kScratchRow) + ob * 4 * kSpreadRows;
-    // the first eight rows' results over the shared prefix, fetched while the piece is in work
-    float pl = 0.f;
-    float4 po[V / 4];
-    const int row0 = thread >> 4;
-    if (merge && row0 < nrows && c < a.D) {
-      const size_t at = (size_t)(w.tok0 + row0 / a.G) * a.Hq + w.head * a.G + row0 % a.G;
-      pl = a.prefix_lse[at];
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) po[i] = *reinterpret_cast<const float4 *>(a.prefix_o + at * a.D + c + 4 * i);
-    }
+    if (fetched == pieces) fetch(w);
     if (!(ok = wait_for_all(bars + 8 * (B::kML + ob), par, abort_flag, a))) break;
     if (!(ok = wait_for_all(bars + 8 * (B::kOF + ob), par, abort_flag, a))) break;
     tc_fence_after();
@@ -1176,10 +1176,10 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
             mm = mn;
           }
         }
-        const int tok = w.tok0 + ro / a.G, head = w.head * a.G + ro % a.G;
+        const bool near = q0 == 0;  // fetched above
+        const int tok = w.tok0 + (near ? tok0 : ro / a.G), head = w.head * a.G + (near ? head0 : ro % a.G);
         bool again = false;
         if (use) {
-          const bool near = q0 == 0;  // fetched above
           if (merge && !near) pl = a.prefix_lse[(size_t)tok * a.Hq + head];
           const RowOut out = row_out(a, tok, head, merge, pl, mm, ll);
           again = !store_cols<V, BF>(a, out, tok, head, c, v, near ? po : nullptr) && finite(ll);
@@ -1200,6 +1200,8 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       mbar_arrive(bars + 8 * (B::kOE + ob));
       mbar_arrive(bars + 8 * (B::kDE + d));
     }
+    const uint32_t dn = (pieces + 1) % kPieces;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1))) fetch(piece[dn]);
     ok = group.join(a);  // the shared rows have been read
   }
 }
@@ -1207,10 +1209,10 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 // Results over shared prefixes: the sum of each split tile's pieces.  A prefix has few tiles in many pieces,
 // and one CTA of the attention kernel adding up a tile's (18 pieces of 64 KB for 256 rows over 4096 keys)
 // took longer than the products; here a CTA takes 4 columns of one tile's 128 rows, a thread a row, and
-// loads eight pieces at a time.
+// loads ten pieces at a time.
 template <int DP, bool BF>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 10;  // (in flight together; 18 pieces are two batches)
   pdl_trigger();
   pdl_wait();
   int i = blockIdx.x;
@@ -1219,9 +1221,9 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   const int s = i % a.list.streams;
   i /= a.list.streams;
   const int head = i % a.Hkv, tile = i / a.Hkv;
-  if (tile >= a.list.meta[0]) return;
   const AttnTile t = load_tile(a.list.tiles + tile);
-  const int2 ctas = ctas_of(a, t, tile, head);
+  const int2 ctas = a.list.ctas[tile * a.Hkv + head];
+  if (tile >= a.list.meta[0]) return;
   const int row = threadIdx.x, tok = t.tok0 + s * a.list.tpt + row / a.G, h = head * a.G + row % a.G;
   const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G;
   if (ctas.x == ctas.y || c >= a.D) return;  // in one piece: its CTA has written the result
@@ -1323,8 +1325,13 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  pdl_trigger();
-  pdl_wait();  // set up before the previous kernel of the stream has finished; what it wrote is read from here on
+  // Set up before the previous kernels of the stream have finished; what they wrote is read from here on.  Behind
+  // the kernels over the shared prefixes only the finishing code waits: those kernels write nothing that the
+  // others read, and whatever ran before them is complete, since the first of them lets its successor begin only
+  // once its own wait is over (and that one its own, this).
+  if (!a.to_prefix) pdl_trigger();
+  if (!a.after_prefix) pdl_wait();
+  if (a.to_prefix) pdl_trigger();
   if (warp < C::kSoftWarps) {
     if (NS == 2) regs_inc<kRegsSoft>();
     if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);

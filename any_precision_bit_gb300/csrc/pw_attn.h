@@ -66,6 +66,7 @@ struct AttnList {
   AttnTile *tiles;
   int *cum;          // [tiles + 1] units of one head before each tile
   AttnStart *start;  // [P]
+  int2 *ctas;        // [tiles][Hkv] CTAs of the first and the last key tile; null: not wanted
   int *meta;         // [0] tiles, [1] units of one head
   int tpt;           // tokens of one 128-row tile
   int streams;       // 128-row tiles of one AttnTile (1 or 2)
@@ -131,7 +132,7 @@ struct AttnArgs {
   // Results over a shared prefix, normalised, and their log2-sum-exp2: written (to_prefix) or merged
   // into the rows of tiles with `merge`.
   float *prefix_o, *prefix_lse;  // [n_tokens][Hq][D], [n_tokens][Hq]
-  int to_prefix, n_groups;
+  int to_prefix, after_prefix, n_groups;
   // Partial results of split tiles: two slots a CTA (its last piece and its first) and stream.
   float *part_o;    // [ctas][2][streams][head_dim padded / 4][128][4]
   float2 *part_ml;  // [ctas][2][streams][128] running maximum and sum

@@ -150,7 +150,14 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
     ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens);
     for (AttnList *l : {&p.requests, &p.groups}) {
       if (l == &p.groups && d.max_shared_tokens == 0) continue;
-      l->max_tiles = d.max_tokens + d.max_requests + 1;
+      if (l == &p.groups) {
+        // full tiles of at least 128 / G tokens (or of all a step's), and the short last one of each group
+        const int G = d.n_heads / d.n_kv_heads;
+        l->max_tiles = d.max_shared_tokens / std::min(kAttnRows / G, d.max_shared_tokens) + d.max_requests;
+        ok = ok && alloc(a, &l->ctas, ((size_t)l->max_tiles + 1) * d.n_kv_heads);
+      } else {
+        l->max_tiles = d.max_tokens + d.max_requests + 1;
+      }
       ok = ok && alloc(a, &l->tiles, (size_t)l->max_tiles + 1) && alloc(a, &l->cum, (size_t)l->max_tiles + 1) &&
            alloc(a, &l->start, ctas) && alloc(a, &l->meta, 2);
     }
@@ -419,6 +426,7 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
     g.n_groups = p.step.n_groups;
     if (pw_status st = launch(p.groups)) return st;
     g.to_prefix = 0;
+    g.after_prefix = 1;
   }
   return launch(p.requests);
 }

@@ -283,8 +283,17 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   }
   __syncthreads();
   const long long W = before * a.n_kv_heads;  // at least one unit: there is a row, and every tile has one
+  const long long P = min((long long)a.ctas, W);
+  // CTAs of the first and the last key tile of a (tile, head) whose units begin at ub
+  auto ctas_of = [&](long long ub, int cost) {
+    return make_int2((int)(((ub + kAttnPieceCost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
+  };
+  if (a.list.ctas)
+    for (int i = tid; i < n_tiles * a.n_kv_heads; i += kListThreads) {
+      const int tile = i / a.n_kv_heads, cost = a.list.cum[tile + 1] - a.list.cum[tile];
+      a.list.ctas[i] = ctas_of((long long)a.list.cum[tile] * a.n_kv_heads + (long long)(i - tile * a.n_kv_heads) * cost, cost);
+    }
   for (int c = tid; c < a.ctas; c += kListThreads) {
-    const long long P = min((long long)a.ctas, W);
     const long long u0 = min(c * W / P, W), u1 = min((c + 1) * W / P, W);
     AttnStart st{0, 0, 0, (int)(u1 - u0), {}, {0, 0}, {0, 0}};
     // the (tile, head) of a unit, and the CTAs of its first and last key tiles
@@ -302,8 +311,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
       tile = lo;
       head = (int)(rem / cost);
       off = (int)(rem - (long long)head * cost);
-      const long long ub = u - off;
-      return make_int2((int)(((ub + kAttnPieceCost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
+      return ctas_of(u - off, cost);
     };
     if (u1 > u0) {
       st.first = find(u0, st.tile, st.head, st.off);
