@@ -7,6 +7,12 @@
 #include "pw_device.cuh"
 #include "pw_tc.cuh"
 
+// Code that hardly ever runs is kept out of line, since the instructions of the roles of a CTA share their
+// cache; but not in kTwo, whose warps trade registers, which excludes calls.
+#ifndef PW_RARE
+#define PW_RARE __noinline__
+#endif
+
 namespace pw {
 
 template <bool BF>
@@ -136,17 +142,20 @@ struct Bars {
   enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kOF = kDE + kPieces, kOE = kOF + 2, kML = kOE + 2, kNum = kML + 2 };
 };
 
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
-  if (mbar_try_wait(bar, parity)) return true;
+static __device__ PW_RARE bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
+                                       long long cycles) {
   const long long t0 = clock64();
   for (;;) {
     if (mbar_try_wait_sleep(bar, parity, kSpinNs)) return true;
     if (*abort_flag) return false;
-    if (clock64() - t0 > a.wait_cycles) break;
+    if (clock64() - t0 > cycles) break;
   }
   *abort_flag = 1;
-  atomicOr(a.err, kAttnErrWait);
+  atomicOr(err, kAttnErrWait);
   return false;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, a.err, a.wait_cycles);
 }
 __device__ __forceinline__ bool wait_for_all(uint32_t bar, uint32_t parity, volatile int *abort_flag, const AttnArgs &a) {
   return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag, a));
@@ -669,13 +678,13 @@ struct RowOut {
 __device__ __forceinline__ RowOut row_out(const AttnArgs &a, int tok, int head, bool merge, float pl, float m, float l) {
   RowOut r;
   r.at = (size_t)tok * a.Hq + head;
-  r.inv = l == 0.f ? 0.f : 1.f / l;
+  r.inv = l == 0.f ? 0.f : rcp(l);
   r.lse2 = l == 0.f ? -INFINITY : m + lg2(l);
   r.w2 = 0.f;
   if (merge) {  // pl: the row's log2-sum-exp2 over the prefix
     const float mx = fmaxf(pl, r.lse2), ms = mx == -INFINITY ? 0.f : mx;
     const float e1 = ex2(r.lse2 - ms), e2 = ex2(pl - ms), sum = e1 + e2;
-    const float is = sum == 0.f ? 0.f : 1.f / sum;
+    const float is = sum == 0.f ? 0.f : rcp(sum);
     r.inv *= e1 * is;
     r.w2 = e2 * is;
     r.lse2 = sum == 0.f ? -INFINITY : ms + lg2(sum);
@@ -738,7 +747,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, const RowOut &r) {
 // does not see (0 times it in the product with v).  Again, from the row's visible keys alone, by the warp.
 // merge: over the shared prefix too.  Columns c0 .. c1 - 1 are written.
 template <bool BF>
-__device__ void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi, int trow, bool merge, int c0 = 0,
+static __device__ PW_RARE void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi, int trow, bool merge, int c0 = 0,
                          int c1 = 128) {
   const int lane = threadIdx.x & 31;
   const RowBound b = a.bounds[tok];
@@ -886,7 +895,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           }
           m = mn;
           l *= f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
             float o[32];
             tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
@@ -956,34 +965,13 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const bool merge = w.merge;
     const int c0 = w.c0, c1 = w.c1;
     {
-      const int tok = w.tok0 + row_tok, head = w.head * a.G + row % a.G;
-      // thread by row: 32 columns at a time from `get`
-      auto emit = [&](float mm, float ll, auto get) {
-        RowOut out{};
-        if (valid) out = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, mm, ll);
-        bool fin = true;
-#pragma unroll
-        for (int c = 0; c < DP / 32; ++c) {
-          float v[32];
-          get(c, v);
-          if (valid) fin = store_cols<32, BF>(a, out, tok, head, 32 * c, v) && fin;
-        }
-        if (valid) store_lse(a, out);
-        unsigned flagged = __ballot_sync(0xffffffffu, valid && !fin && finite(ll));
-        while (flagged) {
-          const int src = __ffs(flagged) - 1;
-          flagged &= flagged - 1;
-          redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w.klo, w.khi, w.trow,
-                       merge);
-        }
-      };
-      if (c0 == c1) {
-        if (active) emit(m, l, from_tmem);
-      } else {
-        // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up
+      bool out = true;  // this CTA writes the result
+      if (c0 != c1) {
+        // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up, in
+        // tensor memory again (results over a shared prefix: attn_join_kernel does)
         const size_t my = slot_of(blockIdx.x, c0);
         if (active) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
             float v[32];
             from_tmem(c, v);
@@ -996,36 +984,63 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           }
           if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
         }
-        const bool last = !a.to_prefix && group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
+        out = !a.to_prefix && group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
         if (!ok) break;
-        if (last && active) {
-          float mm = -INFINITY, ll = 0.f;
+        if (out && active) {
+          m = -INFINITY;
+          l = 0.f;
           if (valid)
-            for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, __ldcg(a.part_ml + slot_of(p, c0) * 128 + row).x);
-          const float ms = mm == -INFINITY ? 0.f : mm;
+            for (int p = c0; p <= c1; ++p) m = fmaxf(m, __ldcg(a.part_ml + slot_of(p, c0) * 128 + row).x);
+          const float ms = m == -INFINITY ? 0.f : m;
           if (valid)
             for (int p = c0; p <= c1; ++p) {
               const float2 y = __ldcg(a.part_ml + slot_of(p, c0) * 128 + row);
-              ll = fmaf(ex2(y.x - ms), y.y, ll);
+              l = fmaf(ex2(y.x - ms), y.y, l);
             }
-          emit(mm, ll, [&](int c, float (&v)[32]) {
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c) {
+            float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            if (!valid) return;
-            for (int p = c0; p <= c1; ++p) {
-              const size_t at = slot_of(p, c0);
-              const float f = ex2(__ldcg(a.part_ml + at * 128 + row).x - ms);
-              const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kPart) + 8 * c * 128 + row;
+            if (valid)
+#pragma unroll 1
+              for (int p = c0; p <= c1; ++p) {
+                const size_t at = slot_of(p, c0);
+                const float f = ex2(__ldcg(a.part_ml + at * 128 + row).x - ms);
+                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kPart) + 8 * c * 128 + row;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 y = __ldcg(src + i * 128);
-                v[4 * i] = fmaf(f, y.x, v[4 * i]);
-                v[4 * i + 1] = fmaf(f, y.y, v[4 * i + 1]);
-                v[4 * i + 2] = fmaf(f, y.z, v[4 * i + 2]);
-                v[4 * i + 3] = fmaf(f, y.w, v[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) {
+                  const float4 y = __ldcg(src + i * 128);
+                  v[4 * i] = fmaf(f, y.x, v[4 * i]);
+                  v[4 * i + 1] = fmaf(f, y.y, v[4 * i + 1]);
+                  v[4 * i + 2] = fmaf(f, y.z, v[4 * i + 2]);
+                  v[4 * i + 3] = fmaf(f, y.w, v[4 * i + 3]);
+                }
               }
-            }
-          });
+            __syncwarp();
+            tmem_st32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
+          }
+          tmem_wait_st();
+        }
+      }
+      if (out && active) {  // a thread's row, 32 columns at a time
+        const int tok = w.tok0 + row_tok, head = w.head * a.G + row % a.G;
+        RowOut ro{};
+        if (valid) ro = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, m, l);
+        bool fin = true;
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          float v[32];
+          from_tmem(c, v);
+          if (valid) fin = store_cols<32, BF>(a, ro, tok, head, 32 * c, v) && fin;
+        }
+        if (valid) store_lse(a, ro);
+        unsigned flagged = __ballot_sync(0xffffffffu, valid && !fin && finite(l));
+        while (flagged) {
+          const int src = __ffs(flagged) - 1;
+          flagged &= flagged - 1;
+          redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w.klo, w.khi, w.trow,
+                       merge);
         }
       }
     }
@@ -1186,6 +1201,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           if (c == 0) store_lse(a, out);
         }
         const unsigned flagged = __ballot_sync(0xffffffffu, again);
+#pragma unroll 1
         for (int h = 0; h < 2; ++h)  // the warp's two rows
           if (flagged >> (16 * h) & 0xffffu) {
             const int rw = q0 + 2 * quarter + h;
@@ -1211,7 +1227,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 // took longer than the products; here a CTA takes 4 columns of one tile's 128 rows, a thread a row, and
 // loads ten pieces at a time.
 template <int DP, bool BF>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kBatch = 10;  // (in flight together; 18 pieces are two batches)
   pdl_trigger();
   pdl_wait();
