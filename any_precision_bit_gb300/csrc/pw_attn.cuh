@@ -139,7 +139,7 @@ constexpr int kPieces = 4;  // pieces handed over ahead
 // mbarriers
 template <int STAGES>
 struct Bars {
-  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kOF = kDE + kPieces, kOE = kOF + 2, kML = kOE + 2, kNum = kML + 2 };
+  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kOF = kDE + kPieces, kOE = kOF + 2, kML = kOE + 2, kPE = kML + 2, kNum = kPE + 2 };
 };
 
 static __device__ PW_RARE bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
@@ -355,6 +355,9 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   }
 }
 
+// kTwo: 16-key steps of a key tile whose probabilities are handed over early.
+constexpr int kEarly = 6;
+
 // S = Q K^T (128 rows by 128 keys) and O += P V (P in tensor memory), issued by an elected lane of the
 // converged warp, so that the operands stay in the uniform datapath: issued by a lane that ran the loop
 // alone an MMA took 150 cycles, against the 64 that the tensor cores need for one.  The descriptors' low
@@ -375,10 +378,12 @@ struct Mma {
       tc_mma_f16(tmem_s, desc(q + off), desc(k + off), idesc, i > 0);
     }
   }
+  // steps (of 16 keys) from .. to - 1
+  template <int FROM = 0, int TO = kAttnKeys / 16>
   static __device__ __forceinline__ void pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v, uint32_t accumulate) {
     constexpr uint32_t idesc = kIdesc | ((DP >> 3) << 17) | (1u << 16);  // B contiguous along N
 #pragma unroll
-    for (int i = 0; i < kAttnKeys / 16; ++i)
+    for (int i = FROM; i < TO; ++i)
       tc_mma_f16_ta(tmem_o, tmem_p + 8 * i, desc(v + i * (2048 >> 4)), idesc, i > 0 ? 1u : accumulate);
   }
 };
@@ -444,9 +449,13 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
           k_st = r.st;
           r.next();
         }
+        // the product with the first keys' probabilities while the softmax is at the last ones'
+        if (!(ok = wait(B::kPE, p_par))) break;
+        if (elect_one()) M::template pv<0, kEarly>(o0, tmem, v, j > 0);
+        __syncwarp();
         if (!(ok = wait(B::kPF, p_par))) break;
         if (elect_one()) {
-          M::pv(o0, tmem, v, j > 0);
+          M::template pv<kEarly, kAttnKeys / 16>(o0, tmem, v, 1);
           if (more) {
             M::qk(tmem, q0, ring_k + k_st * kStep);
             tc_commit(bars + 8 * B::kSF);
@@ -461,10 +470,13 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
         }
         __syncwarp();
         if (two) {
+          if (!(ok = wait(B::kPE + 1, p2_par))) break;
+          if (elect_one()) M::template pv<0, kEarly>(o0 + 128, tmem + 128, v, j > 0);
+          __syncwarp();
           if (!(ok = wait(B::kPF + 1, p2_par))) break;
           p2_par ^= 1;
           if (elect_one()) {
-            M::pv(o0 + 128, tmem + 128, v, j > 0);
+            M::template pv<kEarly, kAttnKeys / 16>(o0 + 128, tmem + 128, v, 1);
             if (more) {
               M::qk(tmem + 128, q0 + kStep, ring_k + k_st * kStep);
               tc_commit(bars + 8 * (B::kSF + 1));
@@ -921,11 +933,19 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           } else {
             tmem_st16(ts + 16 * c, pk);
           }
+          if (NS == 2 && 2 * (c + 1) == kEarly) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (B::kPE + s));
+          }
         }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
         tmem_wait_st();
+      } else if (NS == 2 && lane == 0) {
+        mbar_arrive(bars + 8 * (B::kPE + s));
       }
       tc_fence_before();
       __syncwarp();
@@ -1318,6 +1338,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
       mbar_init(bars + 8 * (B::kOF + i), 1);
       mbar_init(bars + 8 * (B::kOE + i), 4);
       mbar_init(bars + 8 * (B::kML + i), 4);
+      mbar_init(bars + 8 * (B::kPE + i), 4);
     }
     mbar_init(bars + 8 * B::kDrain, 1);
     for (int i = 0; i < kPieces; ++i) {
