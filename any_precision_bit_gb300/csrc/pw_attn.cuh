@@ -814,6 +814,10 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   constexpr int NS = C::NS;
   constexpr bool SP = FORM == kSpread;
   constexpr int NC = SP ? 32 : 128;  // scores of a key tile that a thread takes
+  // Of which this many at a time.  Capped and biased scores go through tensor memory once more, in two halves:
+  // all 128 at a time their arithmetic spilled registers and filled the instruction cache (chunks-docs-cap
+  // 70.7 us, in halves 67.9); plain scores lose more by the second read (prompt-8192 413 us, in halves 444).
+  constexpr int CH = SP ? 32 : EXTRA ? 64 : 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = warp >> 2, quarter = warp & 3, thread = 32 * quarter + lane;
   const int row = SP ? lane : thread, col0 = SP ? 32 * quarter : 0;
@@ -884,14 +888,26 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         fence_async_smem();
       }
       if (active) {
-        float x[NC];
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) tmem_ld32(ts + col0 + 32 * c, reinterpret_cast<uint32_t *>(x) + 32 * c);
-        tmem_wait_ld();
-        if (EXTRA) transform<NC>(a, x, valid, slope, (float)(rb.pos - base - col0));
         const int l0 = lo - base - col0, h0 = hi - base - col0;
-        if (__any_sync(0xffffffffu, valid && (l0 > 0 || h0 < NC))) mask_out<NC>(x, l0, h0);
-        float mx = max_of<NC>(x);
+        const bool edge = __any_sync(0xffffffffu, valid && (l0 > 0 || h0 < NC));
+        float x[CH], mx = -INFINITY;
+        auto load = [&](int c) {
+#pragma unroll
+          for (int i = 0; i < CH; i += 32) tmem_ld32(ts + col0 + c + i, reinterpret_cast<uint32_t *>(x) + i);
+          tmem_wait_ld();
+        };
+#pragma unroll 1
+        for (int c = 0; c < NC; c += CH) {
+          load(c);
+          if (EXTRA) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - col0 - c));
+          if (edge) mask_out<CH>(x, l0 - c, h0 - c);
+          mx = fmaxf(mx, max_of<CH>(x));
+          if (EXTRA && CH < NC) {
+#pragma unroll
+            for (int i = 0; i < CH; i += 32) tmem_st32(ts + c + i, reinterpret_cast<uint32_t *>(x) + i);
+          }
+        }
+        if (EXTRA && CH < NC) tmem_wait_st();
         if (!EXTRA) mx *= sl2;
         if (!valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
         if (j == 0) {
@@ -920,24 +936,28 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         const float ms = m == -INFINITY ? 0.f : m;
         const uint64_t scale = pair(sl2, sl2), neg_m = pair(-ms, -ms);
         uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int c0 = 0; c0 < NC; c0 += CH) {
+          if (CH < NC) load(c0);  // as transformed
 #pragma unroll
-        for (int c = 0; c < NC / 32; ++c) {
-          uint32_t pk[16];
-          exponentials<BF, EXTRA>(x + 32 * c, scale, neg_m, pk, sum);
-          if (SP) {
-            const uint32_t none[16] = {};
+          for (int c = 0; c < CH / 32; ++c) {
+            uint32_t pk[16];
+            exponentials<BF, EXTRA>(x + 32 * c, scale, neg_m, pk, sum);
+            if (SP) {
+              const uint32_t none[16] = {};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (q != quarter) tmem_st16(ts + 16 * q, none);
-            tmem_st16(ts + 16 * quarter, pk);
-          } else {
-            tmem_st16(ts + 16 * c, pk);
-          }
-          if (NS == 2 && 2 * (c + 1) == kEarly) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + 8 * (B::kPE + s));
+              for (int q = 0; q < 4; ++q)
+                if (q != quarter) tmem_st16(ts + 16 * q, none);
+              tmem_st16(ts + 16 * quarter, pk);
+            } else {
+              tmem_st16(ts + c0 / 2 + 16 * c, pk);
+            }
+            if (NS == 2 && c0 / 16 + 2 * (c + 1) == kEarly) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bars + 8 * (B::kPE + s));
+            }
           }
         }
         float s0, s1;
