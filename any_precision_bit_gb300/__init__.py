@@ -529,6 +529,28 @@ def pw_kv_get_stats(kv) -> dict:
 
 
 # ---------------------------------------------------------------- paged attention
+# (Called once or several times a layer, so argument marshalling is kept short here.)
+def _addr(t):
+    """Address of a contiguous device tensor, or None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t):
+    """Address and the strides of [rows][heads][head_dim] (unit last stride)."""
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return t.data_ptr(), a, b
+
+
+def _cuda_stream(s):
+    return None if s is None else getattr(s, "cuda_stream", s)
+
+
 def pw_attn_create(desc: pw_attn_desc):
     """An attention handle (pass it to the pw_attn_* calls and pw_kv_map)."""
     h = C.c_void_p()
@@ -538,14 +560,6 @@ def pw_attn_create(desc: pw_attn_desc):
 
 def pw_attn_destroy(attn):
     lib().pw_attn_destroy(attn)
-
-
-def _rows(t):
-    """Address and the strides of [rows][heads][head_dim] (unit last stride)."""
-    a, b, c = t.stride()
-    if c != 1:
-        raise ValueError("the last dimension must be contiguous")
-    return t.data_ptr(), a, b
 
 
 def pw_attn_bind(attn, layer, k_cache, v_cache):
@@ -561,36 +575,44 @@ def pw_make_step(ctx_len, new_len, table, q_start, kv_len, slot, pos, max_new, r
     [rows][blocks], q_start int32 [R + 1], kv_len int32 [R], slot int64 and pos int32 [n_tokens];
     groups int32 [n_groups + 1] and shared_len int32 [n_groups] for shared prefixes."""
     s = pw_kv_step(R=ctx_len.numel(), n_tokens=pos.numel(), max_new=int(max_new), table_rows=table.shape[0],
-                   table_stride=table.shape[1], ctx_len=_ptr(ctx_len), new_len=_ptr(new_len), rows=_ptr(rows),
-                   table=_ptr(table), q_start=_ptr(q_start), kv_len=_ptr(kv_len), slot=_ptr(slot), pos=_ptr(pos),
-                   n_groups=0 if groups is None else groups.numel() - 1, group_start=_ptr(groups),
-                   shared_len=_ptr(shared_len))
+                   table_stride=table.shape[1], ctx_len=_addr(ctx_len), new_len=_addr(new_len), rows=_addr(rows),
+                   table=_addr(table), q_start=_addr(q_start), kv_len=_addr(kv_len), slot=_addr(slot), pos=_addr(pos),
+                   n_groups=0 if groups is None else groups.numel() - 1, group_start=_addr(groups),
+                   shared_len=_addr(shared_len))
     s.refs = (ctx_len, new_len, table, q_start, kv_len, slot, pos, rows, groups, shared_len)
+    s.address = C.addressof(s)
     return s
 
 
 def pw_kv_map(attn, step, new_ids, stream=None):
-    _check(lib().pw_kv_map(attn, C.addressof(step), _ptr(new_ids), 0 if new_ids is None else new_ids.numel(),
-                           _stream(stream)))
+    st = lib().pw_kv_map(attn, step.address, _addr(new_ids), 0 if new_ids is None else new_ids.numel(),
+                         _cuda_stream(stream))
+    if st:
+        _check(st)
 
 
 def pw_attn_plan(attn, plan, step, window=0, doc_start=None, bidir_len=None, stream=None):
-    _check(lib().pw_attn_plan(attn, plan, C.addressof(step), window, _ptr(doc_start), _ptr(bidir_len),
-                              _stream(stream)))
+    st = lib().pw_attn_plan(attn, plan, step.address, window, _addr(doc_start), _addr(bidir_len), _cuda_stream(stream))
+    if st:
+        _check(st)
 
 
 def pw_attn_append(attn, layer, step, k, v, stream=None):
     """k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last one."""
-    _check(lib().pw_attn_append(attn, layer, C.addressof(step), *_rows(k), *_rows(v), _stream(stream)))
+    st = lib().pw_attn_append(attn, layer, step.address, *_rows(k), *_rows(v), _cuda_stream(stream))
+    if st:
+        _check(st)
 
 
 def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, slopes=None, stream=None):
     """q and o: [n_tokens][n_heads][head_dim], any strides with a unit last one; scale defaults to
     1 / sqrt(head_dim)."""
-    _check(lib().pw_attn_forward(attn, layer, plan, *_rows(q), *_rows(o), _ptr(lse),
-                                 q.shape[2] ** -0.5 if scale is None else scale, softcap, _ptr(slopes),
-                                 _stream(stream)))
+    st = lib().pw_attn_forward(attn, layer, plan, *_rows(q), *_rows(o), _addr(lse),
+                               q.shape[2] ** -0.5 if scale is None else scale, softcap, _addr(slopes),
+                               _cuda_stream(stream))
+    if st:
+        _check(st)
 
 
 def pw_attn_check(attn, stream=None):
-    _check(lib().pw_attn_check(attn, _stream(stream)))
+    _check(lib().pw_attn_check(attn, _cuda_stream(stream)))

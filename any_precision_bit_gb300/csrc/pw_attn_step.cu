@@ -218,7 +218,7 @@ __device__ __forceinline__ Segment segment_of(const PlanArgs &a, int i) {
 constexpr int kListThreads = 1024;
 __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   extern __shared__ int cum_tiles[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
   const int tt = a.list.tpt * a.list.streams;
   pdl_trigger();
@@ -238,7 +238,11 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   }
   const int n_tiles = (int)min(before, (long long)a.list.max_tiles);
   __syncthreads();
-  for (int i = warp; i < n_tiles; i += kListThreads / 32) {
+  // lanes that look through a tile's tokens: one where they are few (a decode step's)
+  const int wide = tt > 4 ? 32 : 1;
+  for (int i0 = 0; i0 < n_tiles; i0 += kListThreads / wide) {
+    const int i = i0 + tid / wide;
+    if (i >= n_tiles) break;  // (whole warps, or with one lane to a tile nothing that meets follows)
     const int s = seg_of(cum_tiles, n_seg, i);
     const Segment g = segment_of(a, s);
     AttnTile t;
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     t.khi = g.khi;
     t.merge = g.merge;
     int lo = INT_MAX, hi = 0;
-    for (int j = lane; j < t.ntok; j += 32) {
+    for (int j = wide == 32 ? lane : 0; j < t.ntok; j += wide) {
       const RowBound b = a.bounds[t.tok0 + j];
       const int l = max(b.lo, g.klo), h = min(b.hi, g.khi);
       if (l < h) {
@@ -257,11 +261,13 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
         hi = max(hi, h);
       }
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (wide == 32) {
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+    }
     t.kv0 = hi > 0 ? lo / kAttnKeys : g.klo / kAttnKeys;
     t.kv1 = hi > 0 ? (hi - 1) / kAttnKeys + 1 : t.kv0 + 1;
-    if (lane == 0) {
+    if (wide == 1 || lane == 0) {
       a.list.tiles[i] = t;
       a.list.cum[i + 1] = t.kv1 - t.kv0 + kAttnPieceCost;
     }
@@ -329,35 +335,50 @@ int launch_attn_list(const PlanArgs &a, void *stream) {
                          reinterpret_cast<cudaStream_t>(stream), a);
 }
 
-// The cache write: 16 bytes a thread, both caches in one launch.  A token's row of a cache is
-// n_heads runs of head_dim elements; consecutive threads take consecutive 16-byte pieces of k,
-// then of v, so that reads and writes are whole runs.
-__global__ void __launch_bounds__(kStepThreads) attn_append_kernel(AppendArgs a) {
+// The cache write.  A token is 2 n_heads head_dim elements, of k and then of v, in pieces of 16 bytes; a
+// thread keeps its piece and goes through the tokens four at a time, so that the divisions that find the
+// piece are done once and four loads are under way together.  Consecutive threads take consecutive pieces:
+// reads and writes are whole runs of a head, or of all heads where the cache keeps them side by side.
+constexpr int kAppendTokens = 4;
+__global__ void __launch_bounds__(kStepThreads) attn_append_kernel(AppendArgs a, int lanes) {
   const int vec = a.head_dim / 8, row = a.n_heads * vec;
-  const long long total = 2LL * a.n_tokens * row;
+  const int sub = threadIdx.x / lanes, per = kStepThreads / lanes;  // token within the block's `per` tokens
   pdl_trigger();
   pdl_wait();
-  for (long long i = (long long)blockIdx.x * kStepThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kStepThreads) {
-    const long long u = i / row;
-    const int w = (int)(i - u * row), h = w / vec, c = w - h * vec;
-    const long long t = u >> 1;
-    const long long slot = a.slot[t];
-    const long long block = slot >> a.log_bt;
-    if (slot < 0 || block >= a.n_blocks) continue;
-    const long long dst = block * a.block_stride + (slot & (a.bt - 1)) * a.token_stride + h * a.head_stride + 8 * c;
-    if (u & 1)
-      *reinterpret_cast<uint4 *>(a.vc + dst) = *reinterpret_cast<const uint4 *>(a.v + t * a.v_token + h * a.v_head + 8 * c);
-    else
-      *reinterpret_cast<uint4 *>(a.kc + dst) = *reinterpret_cast<const uint4 *>(a.k + t * a.k_token + h * a.k_head + 8 * c);
+  if (sub >= per) return;
+  const int stride = gridDim.x * per;
+  for (int w = threadIdx.x - sub * lanes; w < 2 * row; w += lanes) {
+    const bool val = w >= row;
+    const int x = val ? w - row : w, h = x / vec, c = 8 * (x - h * vec);
+    const uint16_t *src = val ? a.v + h * a.v_head + c : a.k + h * a.k_head + c;
+    uint16_t *dst = (val ? a.vc : a.kc) + h * a.head_stride + c;
+    const int64_t step = val ? a.v_token : a.k_token;
+    for (int t0 = blockIdx.x * per + sub; t0 < a.n_tokens; t0 += kAppendTokens * stride) {
+      int64_t slot[kAppendTokens];
+      uint4 data[kAppendTokens];
+#pragma unroll
+      for (int i = 0; i < kAppendTokens; ++i) {
+        const int64_t t = t0 + (int64_t)i * stride;
+        slot[i] = t < a.n_tokens ? a.slot[t] : -1;
+        if (slot[i] >> a.log_bt >= a.n_blocks) slot[i] = -1;
+        if (slot[i] >= 0) data[i] = *reinterpret_cast<const uint4 *>(src + t * step);
+      }
+#pragma unroll
+      for (int i = 0; i < kAppendTokens; ++i)
+        if (slot[i] >= 0)
+          *reinterpret_cast<uint4 *>(dst + (slot[i] >> a.log_bt) * a.block_stride + (slot[i] & (a.bt - 1)) * a.token_stride) =
+              data[i];
+    }
   }
 }
 
 int launch_attn_append(const AppendArgs &a, void *stream) {
-  const long long total = 2LL * a.n_tokens * a.n_heads * (a.head_dim / 8);
-  const long long want = (total + kStepThreads - 1) / kStepThreads;
-  const int grid = (int)(want < 148 * 8 ? want : 148 * 8);
-  return (int)launch_pdl(attn_append_kernel, dim3(grid), dim3(kStepThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  const int pieces = 2 * a.n_heads * (a.head_dim / 8);
+  const int lanes = pieces < kStepThreads ? pieces : kStepThreads, per = kStepThreads / lanes;
+  // enough blocks to fill the SMs; a step of few tokens gets one token (of each `per`) a block
+  const int want = (a.n_tokens + per - 1) / per, most = 152 * 8;
+  return (int)launch_pdl(attn_append_kernel, dim3(want < most ? want : most), dim3(kStepThreads), 0,
+                         reinterpret_cast<cudaStream_t>(stream), a, lanes);
 }
 
 }  // namespace pw
