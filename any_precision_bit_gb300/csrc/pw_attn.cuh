@@ -562,6 +562,8 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// row / G for the rows of a tile: a multiplication by ceil(65536 / G) is exact below 65536 / G.
+__device__ __forceinline__ int over_g(const AttnArgs &a, int row) { return (int)((uint32_t)row * a.g_magic >> 16); }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028234e38f; }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -593,6 +595,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y, float z) {  // NaN if one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 template <int N>
@@ -724,10 +731,16 @@ __device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, i
         v[i + 3] = fmaf(r.w2, x.w, v[i + 3]);
       }
   }
-  bool fin = true;
+  // the largest magnitude, NaN if one is (elements past head_dim are zeros, or NaN times them: not looked at)
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (c + i < a.D) fin = fin && finite(v[i]);
+  for (int i = 0; i < N; i += 8) {
+    float t8 = max_nan(max_nan(fabsf(v[i]), fabsf(v[i + 1]), fabsf(v[i + 2])), fabsf(v[i + 3]), top);
+    if constexpr (N % 8 == 0)
+      t8 = max_nan(max_nan(fabsf(v[i + 4]), fabsf(v[i + 5]), fabsf(v[i + 6])), fabsf(v[i + 7]), t8);
+    if (c + i < a.D) top = t8;
+  }
+  const bool fin = finite(top);
   if (a.to_prefix) {
     float *d = a.prefix_o + r.at * a.D + c;
 #pragma unroll
@@ -795,10 +808,11 @@ struct Group {
     if (!(ok = join(a))) return false;
     if (thread == 0) {
       int *cnt = a.counters + 2 * c0 + s;
-      __threadfence();  // the group's writes, which the meeting has made visible to this thread
-      const int last = atomicAdd(cnt, 1) == c1 - c0;
+      // releases the group's writes, which the meeting has made visible to this thread, and acquires the others'
+      int before;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;\n" : "=r"(before) : "l"(cnt) : "memory");
+      const int last = before == c1 - c0;
       if (last) *cnt = 0;
-      __threadfence();
       last_flag[s] = last;
     }
     if (!(ok = join(a))) return false;
@@ -836,7 +850,8 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   constexpr int kPart = DP * 128;
   auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
   const float sl2 = a.scale2;
-  const int row_tok = s * a.list.tpt + row / a.G;
+  const int row_t = over_g(a, row), row_h = row - row_t * a.G;  // the row's token in its tile, and head
+  const int row_tok = s * a.list.tpt + row_t;
   uint32_t pieces = 0;
   bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
   RowBound rb{0, 0, -1, 0}, rb_ahead{0, 0, -1, 0};
@@ -864,7 +879,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const bool valid = row < nrows;
     const int lo = max(rb.lo, (int)w.klo), hi = min(rb.hi, (int)w.khi);
     const bool active = SP || 32 * quarter < nrows;
-    const float slope = EXTRA && a.slopes && valid ? a.slopes[w.head * a.G + row % a.G] * kLog2e : 0.f;
+    const float slope = EXTRA && a.slopes && valid ? a.slopes[w.head * a.G + row_h] * kLog2e : 0.f;
     const uint32_t tmem_o = tmem + 256 + 128 * (SP ? pieces & 1 : (uint32_t)s) + lanes;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
@@ -1064,7 +1079,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         }
       }
       if (out && active) {  // a thread's row, 32 columns at a time
-        const int tok = w.tok0 + row_tok, head = w.head * a.G + row % a.G;
+        const int tok = w.tok0 + row_tok, head = w.head * a.G + row_h;
         RowOut ro{};
         if (valid) ro = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, m, l);
         bool fin = true;
@@ -1103,7 +1118,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   auto slot_of = [&](int cta, int c0) { return part_slot(cta, c0, 1, 0); };
   Group<C::kStages> group{bars, 0, 0, abort_flag};
   bool ok = true;
-  const int row0 = thread >> 4, tok0 = row0 / a.G, head0 = row0 - tok0 * a.G;  // the first eight rows: this thread's
+  const int row0 = thread >> 4, tok0 = over_g(a, row0), head0 = row0 - tok0 * a.G;  // the first eight rows: this thread's
   // their results over the shared prefix, fetched a piece ahead where the next one is known by then
   float pl = 0.f;
   float4 po[V / 4];
@@ -1232,7 +1247,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           }
         }
         const bool near = q0 == 0;  // fetched above
-        const int tok = w.tok0 + (near ? tok0 : ro / a.G), head = w.head * a.G + (near ? head0 : ro % a.G);
+        const int ro_t = over_g(a, ro), tok = w.tok0 + ro_t, head = w.head * a.G + ro - ro_t * a.G;
         bool again = false;
         if (use) {
           if (merge && !near) pl = a.prefix_lse[(size_t)tok * a.Hq + head];
@@ -1241,12 +1256,14 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           if (c == 0) store_lse(a, out);
         }
         const unsigned flagged = __ballot_sync(0xffffffffu, again);
+        if (flagged) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h)  // the warp's two rows
-          if (flagged >> (16 * h) & 0xffffu) {
-            const int rw = q0 + 2 * quarter + h;
-            redo_row<BF>(a, w.tok0 + rw / a.G, w.head * a.G + rw % a.G, w.klo, w.khi, w.trow, merge);
-          }
+          for (int h = 0; h < 2; ++h)  // the warp's two rows
+            if (flagged >> (16 * h) & 0xffffu) {
+              const int rw = q0 + 2 * quarter + h, rw_t = over_g(a, rw);
+              redo_row<BF>(a, w.tok0 + rw_t, w.head * a.G + rw - rw_t * a.G, w.klo, w.khi, w.trow, merge);
+            }
+        }
       }
     }
     if (!ok) break;
@@ -1264,39 +1281,56 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 
 // Results over shared prefixes: the sum of each split tile's pieces.  A prefix has few tiles in many pieces,
 // and one CTA of the attention kernel adding up a tile's (18 pieces of 64 KB for 256 rows over 4096 keys)
-// took longer than the products; here a CTA takes 4 columns of one tile's 128 rows, a thread a row, and
-// loads ten pieces at a time.
+// took longer than the products; here a CTA takes 4 columns of one tile's 128 rows, a thread a row, with
+// eight pieces under way.
+template <bool BF>
+static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned flagged, int tok, int h, const AttnTile &t, int c) {
+  while (flagged) {
+    const int src = __ffs(flagged) - 1;
+    flagged &= flagged - 1;
+    redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, false,
+                 c, c + 4);
+  }
+}
 template <int DP, bool BF>
 static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int kBatch = 10;  // (in flight together; 18 pieces are two batches)
+  constexpr int kBatch = 8;
   pdl_trigger();
   pdl_wait();
   int i = blockIdx.x;
   const int c = i % (DP / 4) * 4;
   i /= DP / 4;
-  const int s = i % a.list.streams;
-  i /= a.list.streams;
-  const int head = i % a.Hkv, tile = i / a.Hkv;
+  const int s = a.list.streams == 2 ? i & 1 : 0;
+  if (a.list.streams == 2) i >>= 1;
+  const int tile = i / a.Hkv, head = i - tile * a.Hkv;
   const AttnTile t = load_tile(a.list.tiles + tile);
-  const int2 ctas = a.list.ctas[tile * a.Hkv + head];
-  if (tile >= a.list.meta[0]) return;
-  const int row = threadIdx.x, tok = t.tok0 + s * a.list.tpt + row / a.G, h = head * a.G + row % a.G;
+  const int2 ctas = a.list.ctas[i];
+  if (tile >= a.list.meta[0] || ctas.x == ctas.y || c >= a.D) return;  // (in one piece: its CTA has written the result)
+  const int row = threadIdx.x, row_t = over_g(a, row);
+  const int tok = t.tok0 + s * a.list.tpt + row_t, h = head * a.G + row - row_t * a.G;
   const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G;
-  if (ctas.x == ctas.y || c >= a.D) return;  // in one piece: its CTA has written the result
   bool again = false;
   if (valid) {
-    // running maximum and sums over batches of pieces
-    float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p0 = ctas.x; p0 <= ctas.y; p0 += kBatch) {
+    // the first piece is its CTA's last, the others their CTAs' first (see part_slot): two slots apart
+    const size_t at = part_slot(ctas.x, ctas.x, a.list.streams, s), next = part_slot(ctas.x + 1, ctas.x, a.list.streams, s);
+    const int step = 2 * a.list.streams;
+    const float2 *pm = a.part_ml + next * 128 + row;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + next * (DP * 128)) + c / 4 * 128 + row;
+    float2 y0 = __ldcg(a.part_ml + at * 128 + row);
+    float4 v0 = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
+    float m = y0.x, l = y0.y, v[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll 1
+    for (int p = ctas.x + 1; p <= ctas.y; p += kBatch, pm += kBatch * step * 128, po += (size_t)kBatch * step * DP * 32) {
       float2 y[kBatch];
       float4 z[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const bool in = p0 + k <= ctas.y;
-        const size_t at = part_slot(in ? p0 + k : ctas.y, ctas.x, a.list.streams, s);
-        y[k] = __ldcg(a.part_ml + at * 128 + row);
-        z[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
-        if (!in) y[k] = make_float2(-INFINITY, 0.f);
+        y[k] = make_float2(-INFINITY, 0.f);
+        z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p + k <= ctas.y) {
+          y[k] = __ldcg(pm + k * step * 128);
+          z[k] = __ldcg(po + (size_t)k * step * DP * 32);
+        }
       }
       float mn = m;
 #pragma unroll
@@ -1307,7 +1341,6 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
       for (int k = 0; k < 4; ++k) v[k] *= keep;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (p0 + k > ctas.y) break;
         const float f = ex2(y[k].x - ms);
         l = fmaf(f, y[k].y, l);
         v[0] = fmaf(f, z[k].x, v[0]);
@@ -1321,13 +1354,8 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
     again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
     if (c == 0) store_lse(a, out);
   }
-  unsigned flagged = __ballot_sync(0xffffffffu, again);
-  while (flagged) {
-    const int src = __ffs(flagged) - 1;
-    flagged &= flagged - 1;
-    redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, false,
-                 c, c + 4);
-  }
+  const unsigned flagged = __ballot_sync(0xffffffffu, again);
+  if (flagged) redo_join<BF>(a, flagged, tok, h, t, c);
 }
 
 template <int FORM, int DP, bool BF, bool EXTRA>

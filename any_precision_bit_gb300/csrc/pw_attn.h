@@ -118,6 +118,7 @@ struct AttnArgs {
   const int *table;
   int table_stride, n_tokens, n_blocks, log_bt;
   int Hq, Hkv, G, D;
+  unsigned g_magic;  // ceil(65536 / G)
   int box_tokens;  // tokens of one Q box
   const uint16_t *q;
   int64_t q_token, q_head;

@@ -382,6 +382,7 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.Hkv = a->d.n_kv_heads;
   g.G = g.Hq / g.Hkv;
   g.D = a->d.head_dim;
+  g.g_magic = (65536u + (unsigned)g.G - 1u) / (unsigned)g.G;
   g.q = static_cast<const uint16_t *>(q);
   g.q_token = q_token;
   g.q_head = q_head;
