@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "pw_attn.h"
 #include "pw_device.cuh"
 #include "pw_tc.cuh"
@@ -175,7 +177,8 @@ __device__ __forceinline__ size_t part_slot(int cta, int c0, int streams, int s)
   return ((size_t)cta * 2 + (cta == c0 ? 1 : 0)) * streams + s;
 }
 struct Walk {
-  int tile, head, off, left;  // off and left in units (kAttnPieceCost of them lead each (tile, head))
+  int tile, head, off, left;  // off and left in units
+  int cost;                   // units that lead each (tile, head)
   AttnTile t, ahead;
   int j0, n;  // first key tile of this piece within the tile's, and their number
   int2 first_ctas, last_ctas;  // see AttnStart
@@ -186,17 +189,18 @@ struct Walk {
     t = load_tile(&s->t);
     tile = x.x, head = x.y, off = x.z, left = x.w;
     first_ctas = s->first, last_ctas = s->last;
+    cost = a.list.piece_cost;
     fresh = true;
     if (left > 0) ahead = load_tile(a.list.tiles + tile + 1);
   }
   __device__ __forceinline__ bool load() {
-    if (off < kAttnPieceCost) {
-      const int skip = min(kAttnPieceCost - off, left);
+    if (off < cost) {
+      const int skip = min(cost - off, left);
       off += skip;
       left -= skip;
     }
     if (left <= 0) return false;
-    j0 = off - kAttnPieceCost;
+    j0 = off - cost;
     n = min(t.kv1 - t.kv0 - j0, left);
     return true;
   }
@@ -204,7 +208,7 @@ struct Walk {
     left -= n;
     off += n;
     fresh = false;
-    if (off == t.kv1 - t.kv0 + kAttnPieceCost) {
+    if (off == t.kv1 - t.kv0 + cost) {
       off = 0;
       if (++head == a.Hkv) {
         head = 0;
@@ -658,9 +662,9 @@ __device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool
   }
 }
 
-// Keys outside [lo, hi) (relative to the first score) do not count.
+// Keys outside [lo, hi) (relative to the first score) get `value`.
 template <int N>
-__device__ __forceinline__ void mask_out(float (&x)[N], int lo, int hi) {
+__device__ __forceinline__ void mask_out(float (&x)[N], int lo, int hi, float value) {
 #pragma unroll
   for (int c = 0; c < N / 32; ++c) {
     const int l = min(max(lo - 32 * c, 0), 32), h = min(max(hi - 32 * c, 0), 32);
@@ -668,7 +672,7 @@ __device__ __forceinline__ void mask_out(float (&x)[N], int lo, int hi) {
     const uint32_t below_h = h == 32 ? 0xffffffffu : (1u << h) - 1u, below_l = l == 32 ? 0xffffffffu : (1u << l) - 1u;
     const uint32_t seen = below_h & ~below_l;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[32 * c + i] = seen >> i & 1u ? x[32 * c + i] : -INFINITY;
+    for (int i = 0; i < 32; ++i) x[32 * c + i] = seen >> i & 1u ? x[32 * c + i] : value;
   }
 }
 
@@ -914,8 +918,10 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 #pragma unroll 1
         for (int c = 0; c < NC; c += CH) {
           load(c);
+          // (hidden scores, which may come from unwritten memory, have no say in how the tile's are capped)
+          if (EXTRA && edge && a.softcap > 0.f) mask_out<CH>(x, l0 - c, h0 - c, 0.f);
           if (EXTRA) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - col0 - c));
-          if (edge) mask_out<CH>(x, l0 - c, h0 - c);
+          if (edge) mask_out<CH>(x, l0 - c, h0 - c, -INFINITY);
           mx = fmaxf(mx, max_of<CH>(x));
           if (EXTRA && CH < NC) {
 #pragma unroll
@@ -1447,8 +1453,12 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
   using C = Cfg<FORM, DP>;
   static_assert(C::kStages >= 4, "two key tiles in flight");
   auto kern = attn_kernel<FORM, DP, BF, EXTRA>;
-  static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (set != cudaSuccess) return (int)set;
+  static std::atomic<uint64_t> done{0};  // devices whose limit has been raised
+  const uint64_t bit = 1ull << (a.device & 63);
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) return (int)e;
+    if (a.device < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  }
   if (cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(C::kThreads), (size_t)C::kSmem, st, maps, a)) return (int)e;
   if (!a.to_prefix) return (int)cudaGetLastError();
   // tiles that the list can have: whole ones, and the short last one of each group

@@ -12,10 +12,6 @@ namespace pw {
 constexpr int kAttnKeys = 128;         // keys of one key/value tile, the unit of work
 constexpr int kAttnRows = 128;         // query rows of one tile (tensor-memory lanes of an MMA)
 constexpr int kAttnMaxRequests = 4096;
-// Units that a (tile, head) counts for beside its key tiles when the work is divided: the queries' way in,
-// the pipeline's filling and draining, and the result's way out take about as long.
-constexpr int kAttnPieceCost = 2;
-
 // Three forms of the kernel:
 //   kTwo     two 128-row tiles share each key tile: while one tile's scores are in the softmax the
 //            tensor cores work on the other's;
@@ -60,7 +56,7 @@ struct AttnStart {
   int2 first, last;
 };
 
-// One list of work.  In the order (tile, head), each has kAttnPieceCost units without keys and then one for
+// One list of work.  In the order (tile, head), each has piece_cost units without keys and then one for
 // each of its key tiles; of the W units CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W if that is less (the rest idle).
 struct AttnList {
   AttnTile *tiles;
@@ -70,6 +66,8 @@ struct AttnList {
   int *meta;         // [0] tiles, [1] units of one head
   int tpt;           // tokens of one 128-row tile
   int streams;       // 128-row tiles of one AttnTile (1 or 2)
+  int piece_cost;    // units that a (tile, head) counts for beside its key tiles when the work is divided: the
+                     // queries' way in, the pipeline's filling and draining, the result's way out
   int max_tiles;
 };
 
@@ -114,7 +112,7 @@ struct AttnMaps {
 struct AttnArgs {
   const RowBound *bounds;
   AttnList list;
-  int ctas;
+  int ctas, device;
   const int *table;
   int table_stride, n_tokens, n_blocks, log_bt;
   int Hq, Hkv, G, D;

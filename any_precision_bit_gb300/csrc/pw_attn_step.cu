@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     t.kv1 = hi > 0 ? (hi - 1) / kAttnKeys + 1 : t.kv0 + 1;
     if (wide == 1 || lane == 0) {
       a.list.tiles[i] = t;
-      a.list.cum[i + 1] = t.kv1 - t.kv0 + kAttnPieceCost;
+      a.list.cum[i + 1] = t.kv1 - t.kv0 + a.list.piece_cost;
     }
   }
   __syncthreads();
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   const long long P = min((long long)a.ctas, W);
   // CTAs of the first and the last key tile of a (tile, head) whose units begin at ub
   auto ctas_of = [&](long long ub, int cost) {
-    return make_int2((int)(((ub + kAttnPieceCost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
+    return make_int2((int)(((ub + a.list.piece_cost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
   };
   if (a.list.ctas)
     for (int i = tid; i < n_tiles * a.n_kv_heads; i += kListThreads) {

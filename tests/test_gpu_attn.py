@@ -195,6 +195,23 @@ def test_calls_repeat_bit_for_bit_and_follow_new_lengths():
     s.close()
 
 
+@pytest.mark.parametrize("group_start", [None, [0, 3]])
+@pytest.mark.parametrize("kw", [dict(), dict(window=40, softcap=30.0), dict(softcap=2.0), dict(slopes=[0.3] * 8)])
+def test_bits_do_not_depend_on_unwritten_memory(kw, group_start):
+    """Whatever the cache holds behind the written tokens, and whatever ran before: the same bits."""
+    ref = None
+    for fill in (float("nan"), 0.0, 1e30, -3.0):
+        s = Step([80, 80, 80], [13, 1, 50], Hq=8, Hkv=2, D=32, seed=3, group_start=group_start, prefix=80)
+        for c in s.kv:
+            c[s.torch.isnan(c)] = fill
+        s.map_and_append()
+        for _ in range(10):
+            got = s.forward(**kw)
+            ref = ref or got
+            assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
+        s.close()
+
+
 def test_step_in_a_cuda_graph_follows_the_lengths():
     import torch
     s = Step([100, 40], [1, 1], D=64, spare_ids=2)
@@ -301,3 +318,75 @@ def test_refusals_of_the_calls():
     pw.pw_attn_check(s.attn)
     s.close()
     assert not bad
+
+
+@pytest.mark.parametrize("rows", [1, 8, 9, 16, 17, 32, 33, 64, 65, 127, 128, 129, 256, 257])
+@pytest.mark.parametrize("dtype,D,mask", [("bf16", 128, {}), ("fp16", 64, dict(softcap=6.0)),
+                                          ("bf16", 64, dict(window=70)), ("fp16", 128, dict(softcap=3.0, slopes=True))])
+def test_row_counts_around_the_tile_sizes(rows, dtype, D, mask):
+    """One request with `rows` new tokens (unshared heads: as many rows in a tile) behind a cache, beside
+    one with a single token."""
+    s = Step([150, 333], [rows, 1], Hq=2, Hkv=2, D=D, dtype=dtype, bt=32, seed=rows, qscale=2.5)
+    s.map_and_append()
+    s.compare(**_mask(s, **mask))
+    s.close()
+
+
+@pytest.mark.parametrize("new", [1, 2, 30])
+def test_many_requests_share_the_sms(new):
+    """More pieces than SMs, most of them short, some tiles split."""
+    rng = np.random.default_rng(new)
+    R = 150 if new < 30 else 40
+    s = Step(rng.integers(0, 700, size=R), [new] * R, Hq=8, Hkv=4, D=64, dtype="fp16")
+    s.map_and_append()
+    s.compare()
+    s.compare(window=200, softcap=15.0)
+    s.close()
+
+
+def test_capped_scores_beyond_the_polynomial():
+    """Scores of several times the cap: the tanh is at its ends."""
+    s = Step([300, 20], [3, 140], D=64, dtype="fp16", qscale=30.0)
+    s.map_and_append()
+    s.compare(softcap=4.0)
+    s.close()
+
+
+def test_blocks_beyond_32_bit_offsets():
+    """Block ids whose elements lie past 2^32 in the cache."""
+    import torch
+
+    import any_precision_bit_gb300 as pw
+    n_blocks, bt, Hkv, D = 40000, 128, 8, 128
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 25 GB")
+    k = torch.empty(n_blocks, bt, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    table = torch.tensor([[39990, 5, 33000]], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    rows = [torch.randn(300, Hkv, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    q = torch.randn(300, Hkv, D, generator=g).to(torch.bfloat16).cuda()
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    a = pw.pw_attn_create(pw.pw_attn_desc(L=1, n_heads=Hkv, n_kv_heads=Hkv, head_dim=D, dtype=0, n_blocks=n_blocks,
+                                          block_tokens=bt, max_requests=1, max_tokens=300, max_shared_tokens=0, n_plans=1,
+                                          device=0))
+    pw.pw_attn_bind(a, 0, k, v)
+    step = pw.pw_make_step(i32(1), i32(1) + 300, table, i32(2), i32(1), torch.zeros(300, dtype=torch.int64, device="cuda"),
+                           i32(300), max_new=300)
+    ids = table[0].clone()
+    table.fill_(-1)
+    torch.cuda.synchronize()
+    pw.pw_kv_map(a, step, ids)
+    pw.pw_attn_append(a, 0, step, *rows)
+    pw.pw_attn_plan(a, 0, step)
+    o = torch.empty_like(q)
+    pw.pw_attn_forward(a, 0, 0, q, o)
+    pw.pw_attn_check(a)
+    assert torch.equal(torch.cat([k[i] for i in (39990, 5, 33000)])[:300], rows[0])
+    x = torch.einsum("thd,jhd->htj", q.double(), rows[0].double()) / D ** 0.5
+    x = x.masked_fill(torch.ones(300, 300, dtype=torch.bool, device="cuda").triu(1), -np.inf)
+    p = torch.softmax(x, -1)
+    want = torch.einsum("htj,jhd->thd", p, rows[1].double())
+    size = torch.einsum("htj,jhd->thd", p, rows[1].double().abs())
+    assert bool(((o.double() - want).abs() <= 2.0 ** -8 * (want.abs() + size) + 1e-4 * size).all())
+    pw.pw_attn_destroy(a)
