@@ -881,7 +881,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       continue;
     }
     const bool valid = row < nrows;
-    const int lo = max(rb.lo, (int)w.klo), hi = min(rb.hi, (int)w.khi);
+    const int klo = w.klo, khi = w.khi, lo = max(rb.lo, klo), hi = min(rb.hi, khi);
     const bool active = SP || 32 * quarter < nrows;
     const float slope = EXTRA && a.slopes && valid ? a.slopes[w.head * a.G + row_h] * kLog2e : 0.f;
     const uint32_t tmem_o = tmem + 256 + 128 * (SP ? pieces & 1 : (uint32_t)s) + lanes;
@@ -893,11 +893,11 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       const int base = (first + j) * kAttnKeys;
       if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
       tc_fence_after();
-      if (s == 0 && (base < w.klo || base + kAttnKeys > w.khi)) {
+      if (s == 0 && (base < klo || base + kAttnKeys > khi)) {
         // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
         // times what the memory holds may be NaN
         if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
-        if (base + thread < w.klo || base + thread >= w.khi) {
+        if (base + thread < klo || base + thread >= khi) {
           uint8_t *vrow = smp + (NS + rv.st) * C::kTileBytes + thread * 128;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
@@ -1419,10 +1419,10 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   // Set up before the previous kernels of the stream have finished; what they wrote is read from here on.  Behind
   // the kernels over the shared prefixes only the finishing code waits: those kernels write nothing that the
   // others read, and whatever ran before them is complete, since the first of them lets its successor begin only
-  // once its own wait is over (and that one its own, this).
+  // at its end.  (At its end, because the successor's many small CTAs would otherwise crowd the SMs that are done
+  // first.)
   if (!a.to_prefix) pdl_trigger();
   if (!a.after_prefix) pdl_wait();
-  if (a.to_prefix) pdl_trigger();
   if (warp < C::kSoftWarps) {
     if (NS == 2) regs_inc<kRegsSoft>();
     if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
