@@ -1,5 +1,5 @@
 // pw_attn.cuh -- attention over the paged key/value cache: the kernel and its launch, instantiated form by
-// form in pw_attn_two.cu, pw_attn_one.cu and pw_attn_spread.cu.
+// form in pw_attn_two.cu and pw_attn_spread.cu.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr int kTileBytes = kHalves * kHalfBytes;
   // kSpread: the quarters' results side by side, rows padded against bank conflicts
   static constexpr int kScratchRow = DP + 4;
-  static constexpr int kScratch = FORM == kSpread ? 4 * kJoinRows * kScratchRow * 4 + 2 * 4 * kSpreadRows * 8 : 0;
+  static constexpr int kScratch = FORM == kSpread ? 4 * kJoinRows * kScratchRow * 4 + 2 * 4 * 32 * 8 : 0;
   static constexpr int kStages = (kSmemRing - NS * kTileBytes - kScratch) / kTileBytes;
   static constexpr int kScratchAt = (NS + kStages) * kTileBytes;
   static constexpr int kSmem = kScratchAt + kScratch;
@@ -240,17 +240,12 @@ struct Ring {
   }
 };
 
-// Query buffers.  Where the boxes leave room (one stream: 64 of a tile's 128 rows; kSpread: 16 of each
-// quarter's 32) a second box is kept behind the first, so that the next piece's queries are loaded while
-// the current one's are in use.  The MMAs read 128 rows from either; what lies between or behind a box's
-// rows gives scores of rows that nobody has.
+// Query buffers.  kSpread keeps a second box (of at most 16 rows) behind the first in each quarter's 32 rows, so
+// that the next piece's queries are loaded while the current one's are in use.  (The MMAs read 128 rows from
+// either; what lies between or behind a box's rows gives scores of rows that nobody has.)
 template <int FORM>
-__device__ __forceinline__ uint32_t q_buffers(const AttnArgs &a) {
-  const int rows = a.box_tokens * a.G;
-  return FORM == kTwo ? 1u : FORM == kOne ? (rows <= 64 ? 2u : 1u) : (rows <= 16 ? 2u : 1u);
-}
-template <int FORM>
-constexpr uint32_t kQBufferStep = FORM == kSpread ? 16 * 128 : 64 * 128;  // bytes between the two buffers
+constexpr uint32_t kQBuffers = FORM == kSpread ? 2 : 1;
+constexpr uint32_t kQBufferStep = kSpreadRows * 128;  // bytes between the two
 
 // A producer warp: the keys (kv = 0) or values of every key tile, or every other box of them; the last of
 // the warps also loads the queries and hands the pieces over.
@@ -269,7 +264,7 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   const bool loads = mine && lane % kShare == share;
   const uint32_t ring = sm + NS * C::kTileBytes;
   const uint32_t at = (uint32_t)(half * C::kHalfBytes + page * bt * 128);
-  const uint32_t nq = q_buffers<FORM>(a);
+  constexpr uint32_t nq = kQBuffers<FORM>;
   const void *map = kv ? &maps.v : &maps.k;
   uint32_t tiles = 0, pieces = 0;
   Ring<C::kStages> r;
@@ -306,14 +301,14 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
       if (!(ok = publish(pieces))) break;
       ok = wait_for_all(bars + 8 * (B::kQE + qb), ((pieces / nq) & 1) ^ 1, abort_flag, a);
       if (!ok) break;
-      const int ns = NS == 2 && w.t.ntok > a.list.tpt ? 2 : 1;
+      const int ns = FORM == kTwo && w.t.ntok > a.list.tpt ? 2 : 1;
       if (lane == 0) {
         const int copies = FORM == kSpread ? 4 : ns;
         mbar_arrive_expect_tx(bars + 8 * (B::kQF + qb), (uint32_t)(copies * C::kHalves * a.box_tokens * a.G * 128));
         for (int s = 0; s < copies; ++s)
           for (int h = 0; h < C::kHalves; ++h)
             tma_load_3d(sm + s * (FORM == kSpread ? 32 * 128 : C::kTileBytes) + h * C::kHalfBytes +
-                            qb * kQBufferStep<FORM>,
+                            qb * kQBufferStep,
                         &maps.q, 64 * h, w.head * a.G, FORM == kSpread ? w.t.tok0 : w.t.tok0 + s * a.list.tpt,
                         bars + 8 * (B::kQF + qb));
       }
@@ -401,7 +396,8 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
   constexpr uint32_t kStep = C::kTileBytes >> 4;
   constexpr bool SP = FORM == kSpread;
   const uint32_t ring_k = M::lo_k(sm + NS * C::kTileBytes), ring_v = M::lo_mn(sm + NS * C::kTileBytes);
-  const uint32_t o0 = tmem + 256, nq = q_buffers<FORM>(a);
+  const uint32_t o0 = tmem + 256;
+  constexpr uint32_t nq = kQBuffers<FORM>;
   Ring<C::kStages> r;  // the next stage to be read
   uint32_t pieces = 0, it = 0, p_par = 0, p2_par = 0;
   bool ok = true;
@@ -417,7 +413,7 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
     const uint32_t d = i % kPieces;
     if (!(ok = wait(B::kDF + d, (i / kPieces) & 1))) return false;
     n = __shfl_sync(0xffffffffu, piece[d].n, 0);
-    two = NS == 2 && __shfl_sync(0xffffffffu, piece[d].ntok, 0) > a.list.tpt;
+    two = !SP && __shfl_sync(0xffffffffu, piece[d].ntok, 0) > a.list.tpt;
     if (n == 0) return false;
     if (elect_one()) mbar_arrive(bars + 8 * (B::kDE + d));
     __syncwarp();
@@ -426,7 +422,7 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
   int n = 0;
   bool two = false;
   bool more_pieces = next_piece(0, n, two);
-  if constexpr (NS == 2) {
+  if constexpr (!SP) {
     for (; more_pieces; more_pieces = next_piece(++pieces, n, two)) {
       const uint32_t q0 = M::lo_k(sm);
       if (!(ok = full(r))) break;
@@ -507,7 +503,7 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
       k_st = r.st;
       r.next();
       if (elect_one()) {
-        M::qk(tmem + 128 * buf, M::lo_k(sm + qb * kQBufferStep<FORM>), ring_k + k_st * kStep);
+        M::qk(tmem + 128 * buf, M::lo_k(sm + qb * kQBufferStep), ring_k + k_st * kStep);
         tc_commit(bars + 8 * (B::kSF + buf));
         release(k_st);
         if (last_of_piece) tc_commit(bars + 8 * (B::kQE + qb));
@@ -516,7 +512,7 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
     };
     if (more_pieces) scores(0, n == 1, 0);
     while (ok && more_pieces) {
-      const uint32_t b = it & 1, ob = SP ? pieces & 1 : 0;  // score buffer, output accumulator
+      const uint32_t b = it & 1, ob = pieces & 1;  // score buffer, output accumulator
       const Ring<C::kStages> rv = r;                        // this tile's values follow its keys
       r.next();
       const bool first = j == 0, last = j + 1 == n;
@@ -530,12 +526,12 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
       }
       if (more_pieces) scores(b ^ 1, j + 1 == n, of_piece % nq);
       if (!ok || !(ok = full(rv))) break;
-      if (SP && first && !(ok = wait(B::kOE + ob, ((pieces >> 1) & 1) ^ 1))) break;
+      if (first && !(ok = wait(B::kOE + ob, ((pieces >> 1) & 1) ^ 1))) break;
       if (!(ok = wait(B::kPF + b, (it >> 1) & 1))) break;
       if (elect_one()) {
         M::pv(o0 + 128 * ob, tmem + 128 * b, ring_v + rv.st * kStep, !first);
         tc_commit(bars + 8 * (B::kOD + b));
-        if (SP && last) tc_commit(bars + 8 * (B::kOF + ob));
+        if (last) tc_commit(bars + 8 * (B::kOF + ob));
         release(rv.st);
       }
       __syncwarp();
@@ -843,13 +839,13 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   uint32_t it = 0;        // key tiles of this stream so far
   Ring<C::kStages> rv;    // the current tile's V
   rv.next();
-  // One stream: P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked
+  // kSpread: P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked
   // the tile before on the same barrier is known to be complete (the scores of tile t or t + 1 were issued
   // behind it) and the one after waits for this thread, so the parity cannot be mistaken.
   auto product_done = [&](uint32_t t) {
     return wait_for_all(bars + 8 * (B::kOD + (t & 1)), (t >> 1) & 1, abort_flag, a);
   };
-  uint32_t o_done = 0;    // two streams: pieces of this stream so far
+  uint32_t o_done = 0;    // kTwo: pieces of this stream so far
   Group<C::kStages> group{bars, s, 0, abort_flag};
   constexpr int kPart = DP * 128;
   auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
@@ -872,7 +868,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const int ntok = min(a.list.tpt, w.ntok - s * a.list.tpt), nrows = ntok * a.G;
     rb = rb_ahead;
     const uint32_t dn = (pieces + 1) % kPieces;
-    if (NS == 2 && ntok <= 0) {
+    if (!SP && ntok <= 0) {
       for (int i = 0; i < 2 * n; ++i) rv.next();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
@@ -887,8 +883,8 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const uint32_t tmem_o = tmem + 256 + 128 * (SP ? pieces & 1 : (uint32_t)s) + lanes;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
-      const uint32_t buf = NS == 2 ? (uint32_t)s : (it & 1);
-      const uint32_t par = NS == 2 ? (it & 1) : ((it >> 1) & 1);
+      const uint32_t buf = !SP ? (uint32_t)s : (it & 1);
+      const uint32_t par = !SP ? (it & 1) : ((it >> 1) & 1);
       const uint32_t ts = tmem + 128 * buf + lanes;
       const int base = (first + j) * kAttnKeys;
       if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
@@ -936,9 +932,9 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
           // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8:
           // until then probabilities up to 2^8 cost no precision, and the accumulator stays untouched.
-          // Two streams: these scores were issued behind the product before, which is therefore done.
+          // kTwo: these scores were issued behind the product before, which is therefore done.
           const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2(m - mn);
-          if (NS == 1) {
+          if (SP) {
             if (!(ok = product_done(it - 1))) break;
             tc_fence_after();
           }
@@ -973,7 +969,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
             } else {
               tmem_st16(ts + c0 / 2 + 16 * c, pk);
             }
-            if (NS == 2 && c0 / 16 + 2 * (c + 1) == kEarly) {
+            if (!SP && c0 / 16 + 2 * (c + 1) == kEarly) {
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
@@ -985,7 +981,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
         tmem_wait_st();
-      } else if (NS == 2 && lane == 0) {
+      } else if (!SP && lane == 0) {
         mbar_arrive(bars + 8 * (B::kPE + s));
       }
       tc_fence_before();
@@ -998,7 +994,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     rb_ahead = bound_of(piece[dn]);
     if constexpr (SP) {  // the rest is the finishing warps' work
       const uint32_t ob = pieces & 1;
-      float2 *ml = reinterpret_cast<float2 *>(smp + C::kScratchAt + 4 * kJoinRows * C::kScratchRow * 4) + ob * 4 * kSpreadRows;
+      float2 *ml = reinterpret_cast<float2 *>(smp + C::kScratchAt + 4 * kJoinRows * C::kScratchRow * 4) + ob * 4 * 32;
       if (!(ok = wait_for_all(bars + 8 * (B::kOE + ob), ((pieces >> 1) & 1) ^ 1, abort_flag, a))) break;
       ml[thread] = make_float2(m, l);
       __syncwarp();
@@ -1008,14 +1004,8 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       }
       continue;
     }
-    // the piece's last product
-    if (NS == 2) {
-      ok = wait_for_all(bars + 8 * (B::kOD + s), o_done & 1, abort_flag, a);
-      ++o_done;
-    } else {
-      ok = product_done(it - 1);
-    }
-    if (!ok) break;
+    // kTwo: the piece's last product
+    if (!(ok = wait_for_all(bars + 8 * (B::kOD + s), o_done++ & 1, abort_flag, a))) break;
     tc_fence_after();
     if (a.after_prefix) pdl_wait();  // (returns at once but the first time)
     auto from_tmem = [&](int c, float (&v)[32]) {
@@ -1025,84 +1015,82 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     };
     const bool merge = w.merge;
     const int c0 = w.c0, c1 = w.c1;
-    {
-      bool out = true;  // this CTA writes the result
-      if (c0 != c1) {
-        // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up, in
-        // tensor memory again (results over a shared prefix: attn_join_kernel does)
-        const size_t my = slot_of(blockIdx.x, c0);
-        if (active) {
-#pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
-            float v[32];
-            from_tmem(c, v);
-            if (valid) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((8 * c + i / 4) * 128 + row) * 4),
-                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-            }
-          }
-          if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
-        }
-        out = !a.to_prefix && group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
-        if (!ok) break;
-        if (out && active) {
-          m = -INFINITY;
-          l = 0.f;
-          if (valid)
-            for (int p = c0; p <= c1; ++p) m = fmaxf(m, __ldcg(a.part_ml + slot_of(p, c0) * 128 + row).x);
-          const float ms = m == -INFINITY ? 0.f : m;
-          if (valid)
-            for (int p = c0; p <= c1; ++p) {
-              const float2 y = __ldcg(a.part_ml + slot_of(p, c0) * 128 + row);
-              l = fmaf(ex2(y.x - ms), y.y, l);
-            }
-#pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            if (valid)
-#pragma unroll 1
-              for (int p = c0; p <= c1; ++p) {
-                const size_t at = slot_of(p, c0);
-                const float f = ex2(__ldcg(a.part_ml + at * 128 + row).x - ms);
-                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kPart) + 8 * c * 128 + row;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 y = __ldcg(src + i * 128);
-                  v[4 * i] = fmaf(f, y.x, v[4 * i]);
-                  v[4 * i + 1] = fmaf(f, y.y, v[4 * i + 1]);
-                  v[4 * i + 2] = fmaf(f, y.z, v[4 * i + 2]);
-                  v[4 * i + 3] = fmaf(f, y.w, v[4 * i + 3]);
-                }
-              }
-            __syncwarp();
-            tmem_st32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
-          }
-          tmem_wait_st();
-        }
-      }
-      if (out && active) {  // a thread's row, 32 columns at a time
-        const int tok = w.tok0 + row_tok, head = w.head * a.G + row_h;
-        RowOut ro{};
-        if (valid) ro = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, m, l);
-        bool fin = true;
+    bool out = true;  // this CTA writes the result
+    if (c0 != c1) {
+      // a piece of a tile: its partial result goes to this CTA's slot, and whoever arrives last adds all up, in
+      // tensor memory again (or attn_join_kernel does)
+      const size_t my = slot_of(blockIdx.x, c0);
+      if (active) {
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
           float v[32];
           from_tmem(c, v);
-          if (valid) fin = store_cols<32, BF>(a, ro, tok, head, 32 * c, v) && fin;
+          if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((8 * c + i / 4) * 128 + row) * 4),
+                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+          }
         }
-        if (valid) store_lse(a, ro);
-        unsigned flagged = __ballot_sync(0xffffffffu, valid && !fin && finite(l));
-        while (flagged) {
-          const int src = __ffs(flagged) - 1;
-          flagged &= flagged - 1;
-          redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w.klo, w.khi, w.trow,
-                       merge);
+        if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
+      }
+      out = !a.join && group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
+      if (!ok) break;
+      if (out && active) {
+        m = -INFINITY;
+        l = 0.f;
+        if (valid)
+          for (int p = c0; p <= c1; ++p) m = fmaxf(m, __ldcg(a.part_ml + slot_of(p, c0) * 128 + row).x);
+        const float ms = m == -INFINITY ? 0.f : m;
+        if (valid)
+          for (int p = c0; p <= c1; ++p) {
+            const float2 y = __ldcg(a.part_ml + slot_of(p, c0) * 128 + row);
+            l = fmaf(ex2(y.x - ms), y.y, l);
+          }
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          if (valid)
+#pragma unroll 1
+            for (int p = c0; p <= c1; ++p) {
+              const size_t at = slot_of(p, c0);
+              const float f = ex2(__ldcg(a.part_ml + at * 128 + row).x - ms);
+              const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kPart) + 8 * c * 128 + row;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 y = __ldcg(src + i * 128);
+                v[4 * i] = fmaf(f, y.x, v[4 * i]);
+                v[4 * i + 1] = fmaf(f, y.y, v[4 * i + 1]);
+                v[4 * i + 2] = fmaf(f, y.z, v[4 * i + 2]);
+                v[4 * i + 3] = fmaf(f, y.w, v[4 * i + 3]);
+              }
+            }
+          __syncwarp();
+          tmem_st32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(v));
         }
+        tmem_wait_st();
+      }
+    }
+    if (out && active) {  // a thread's row, 32 columns at a time
+      const int tok = w.tok0 + row_tok, head = w.head * a.G + row_h;
+      RowOut ro{};
+      if (valid) ro = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, m, l);
+      bool fin = true;
+#pragma unroll 1
+      for (int c = 0; c < DP / 32; ++c) {
+        float v[32];
+        from_tmem(c, v);
+        if (valid) fin = store_cols<32, BF>(a, ro, tok, head, 32 * c, v) && fin;
+      }
+      if (valid) store_lse(a, ro);
+      unsigned flagged = __ballot_sync(0xffffffffu, valid && !fin && finite(l));
+      while (flagged) {
+        const int src = __ffs(flagged) - 1;
+        flagged &= flagged - 1;
+        redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w.klo, w.khi, w.trow,
+                     merge);
       }
     }
     __syncwarp();
@@ -1146,7 +1134,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     if (w.n == 0) break;
     const int nrows = w.ntok * a.G, c0 = w.c0, c1 = w.c1;
     const bool merge = w.merge;
-    const float2 *ml = reinterpret_cast<const float2 *>(sh + 4 * kJoinRows * C::kScratchRow) + ob * 4 * kSpreadRows;
+    const float2 *ml = reinterpret_cast<const float2 *>(sh + 4 * kJoinRows * C::kScratchRow) + ob * 4 * 32;
     if (fetched == pieces) fetch(w);
     if (!(ok = wait_for_all(bars + 8 * (B::kML + ob), par, abort_flag, a))) break;
     if (!(ok = wait_for_all(bars + 8 * (B::kOF + ob), par, abort_flag, a))) break;
@@ -1177,11 +1165,11 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       for (int i = 0; i < V; ++i) v[i] = 0.f;
       if (mine) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mm = fmaxf(mm, ml[q * kSpreadRows + rr].x);
+        for (int q = 0; q < 4; ++q) mm = fmaxf(mm, ml[q * 32 + rr].x);
         const float ms = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float2 y = ml[q * kSpreadRows + rr];
+          const float2 y = ml[q * 32 + rr];
           const float f = ex2(y.x - ms);
           ll = fmaf(f, y.y, ll);
           const float4 *p = reinterpret_cast<const float4 *>(sh + (q * kJoinRows + rr - r0) * C::kScratchRow + c);
@@ -1205,7 +1193,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
           if (c == 0) __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
         }
-        if (a.to_prefix || r0 + kJoinRows < nrows) continue;
+        if (a.join || r0 + kJoinRows < nrows) continue;
         last = group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
         if (!ok) break;
       }
@@ -1285,83 +1273,84 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   }
 }
 
-// Results over shared prefixes: the sum of each split tile's pieces.  A prefix has few tiles in many pieces,
-// and one CTA of the attention kernel adding up a tile's (18 pieces of 64 KB for 256 rows over 4096 keys)
-// took longer than the products; here a CTA takes 4 columns of one tile's 128 rows, a thread a row, with
-// eight pieces under way.
+// The sum of each split tile's pieces, where tiles are few and their pieces many: one CTA of the attention
+// kernel adding up a tile's (18 pieces of 64 KB for 256 rows over a prefix of 4096 keys) took longer than the
+// products.  Here a CTA takes 4 columns of a tile's 128 rows at a time, a thread a row, with eight pieces under
+// way.
 template <bool BF>
-static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned flagged, int tok, int h, const AttnTile &t, int c) {
+static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned flagged, int tok, int h, const AttnTile &t,
+                                              bool merge, int c) {
   while (flagged) {
     const int src = __ffs(flagged) - 1;
     flagged &= flagged - 1;
-    redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, false,
+    redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, merge,
                  c, c + 4);
   }
 }
 template <int DP, bool BF>
 static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 8, kCols = DP / 4;
   pdl_trigger();
   pdl_wait();
-  int i = blockIdx.x;
-  const int c = i % (DP / 4) * 4;
-  i /= DP / 4;
-  const int s = a.list.streams == 2 ? i & 1 : 0;
-  if (a.list.streams == 2) i >>= 1;
-  const int tile = i / a.Hkv, head = i - tile * a.Hkv;
-  const AttnTile t = load_tile(a.list.tiles + tile);
-  const int2 ctas = a.list.ctas[i];
-  if (tile >= a.list.meta[0] || ctas.x == ctas.y || c >= a.D) return;  // (in one piece: its CTA has written the result)
-  const int row = threadIdx.x, row_t = over_g(a, row);
-  const int tok = t.tok0 + s * a.list.tpt + row_t, h = head * a.G + row - row_t * a.G;
-  const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G;
-  bool again = false;
-  if (valid) {
-    // the first piece is its CTA's last, the others their CTAs' first (see part_slot): two slots apart
-    const size_t at = part_slot(ctas.x, ctas.x, a.list.streams, s), next = part_slot(ctas.x + 1, ctas.x, a.list.streams, s);
-    const int step = 2 * a.list.streams;
-    const float2 *pm = a.part_ml + next * 128 + row;
-    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + next * (DP * 128)) + c / 4 * 128 + row;
-    float2 y0 = __ldcg(a.part_ml + at * 128 + row);
-    float4 v0 = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
-    float m = y0.x, l = y0.y, v[4] = {v0.x, v0.y, v0.z, v0.w};
+  const int streams = a.list.streams, row = threadIdx.x, row_t = over_g(a, row), row_h = row - row_t * a.G;
+  const int n = a.list.meta[2] * streams * kCols;
 #pragma unroll 1
-    for (int p = ctas.x + 1; p <= ctas.y; p += kBatch, pm += kBatch * step * 128, po += (size_t)kBatch * step * DP * 32) {
-      float2 y[kBatch];
-      float4 z[kBatch];
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int c = i % kCols * 4, s = streams == 2 ? i / kCols & 1 : 0;
+    const AttnSplit *sp = a.list.splits + (streams == 2 ? i / (2 * kCols) : i / kCols);
+    const AttnTile t = load_tile(&sp->t);
+    const int4 x = *reinterpret_cast<const int4 *>(&sp->head);
+    const int c0 = x.y, c1 = x.z, tok = t.tok0 + s * a.list.tpt + row_t, h = x.x * a.G + row_h;
+    const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G && c < a.D, merge = t.merge && !a.to_prefix;
+    bool again = false;
+    if (valid) {
+      // the first piece is its CTA's last, the others their CTAs' first (see part_slot): two slots apart
+      const size_t at = part_slot(c0, c0, streams, s), next = part_slot(c0 + 1, c0, streams, s);
+      const int step = 2 * streams;
+      const float2 *pm = a.part_ml + next * 128 + row;
+      const float4 *po = reinterpret_cast<const float4 *>(a.part_o + next * (DP * 128)) + c / 4 * 128 + row;
+      const float2 y0 = __ldcg(a.part_ml + at * 128 + row);
+      const float4 v0 = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
+      const float pl = merge ? a.prefix_lse[(size_t)tok * a.Hq + h] : 0.f;
+      float m = y0.x, l = y0.y, v[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll 1
+      for (int p = c0 + 1; p <= c1; p += kBatch, pm += kBatch * step * 128, po += (size_t)kBatch * step * DP * 32) {
+        float2 y[kBatch];
+        float4 z[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        y[k] = make_float2(-INFINITY, 0.f);
-        z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p + k <= ctas.y) {
-          y[k] = __ldcg(pm + k * step * 128);
-          z[k] = __ldcg(po + (size_t)k * step * DP * 32);
+        for (int k = 0; k < kBatch; ++k) {
+          y[k] = make_float2(-INFINITY, 0.f);
+          z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p + k <= c1) {
+            y[k] = __ldcg(pm + k * step * 128);
+            z[k] = __ldcg(po + (size_t)k * step * DP * 32);
+          }
         }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, y[k].x);
+        const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(m - ms);
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] *= keep;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float f = ex2(y[k].x - ms);
+          l = fmaf(f, y[k].y, l);
+          v[0] = fmaf(f, z[k].x, v[0]);
+          v[1] = fmaf(f, z[k].y, v[1]);
+          v[2] = fmaf(f, z[k].z, v[2]);
+          v[3] = fmaf(f, z[k].w, v[3]);
+        }
+        m = mn;
       }
-      float mn = m;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, y[k].x);
-      const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(m - ms);
-      l *= keep;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] *= keep;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float f = ex2(y[k].x - ms);
-        l = fmaf(f, y[k].y, l);
-        v[0] = fmaf(f, z[k].x, v[0]);
-        v[1] = fmaf(f, z[k].y, v[1]);
-        v[2] = fmaf(f, z[k].z, v[2]);
-        v[3] = fmaf(f, z[k].w, v[3]);
-      }
-      m = mn;
+      const RowOut out = row_out(a, tok, h, merge, pl, m, l);
+      again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
+      if (c == 0) store_lse(a, out);
     }
-    const RowOut out = row_out(a, tok, h, false, 0.f, m, l);
-    again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
-    if (c == 0) store_lse(a, out);
+    const unsigned flagged = __ballot_sync(0xffffffffu, again);
+    if (flagged) redo_join<BF>(a, flagged, tok, h, t, merge, c);
   }
-  const unsigned flagged = __ballot_sync(0xffffffffu, again);
-  if (flagged) redo_join<BF>(a, flagged, tok, h, t, c);
 }
 
 template <int FORM, int DP, bool BF, bool EXTRA>
@@ -1369,7 +1358,6 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
                                                                        const __grid_constant__ AttnArgs a) {
   using C = Cfg<FORM, DP>;
   using B = Bars<C::kStages>;
-  constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar_mem[B::kNum];
   __shared__ uint32_t tmem_slot;
@@ -1421,17 +1409,17 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   // others read, and whatever ran before them is complete, since the first of them lets its successor begin only
   // at its end.  (At its end, because the successor's many small CTAs would otherwise crowd the SMs that are done
   // first.)
-  if (!a.to_prefix) pdl_trigger();
+  if (!a.join) pdl_trigger();
   if (!a.after_prefix) pdl_wait();
   if (warp < C::kSoftWarps) {
-    if (NS == 2) regs_inc<kRegsSoft>();
+    if (FORM == kTwo) regs_inc<kRegsSoft>();
     if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
   } else if (warp < C::kProdWarp) {
     if constexpr (FORM == kSpread) {
       if (!abort_flag) finish<DP, BF>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
     }
   } else {
-    if (NS == 2) regs_dec<kRegsOther>();
+    if (FORM == kTwo) regs_dec<kRegsOther>();
     if (abort_flag) {
     } else if (warp < C::kMmaWarp) {
       produce<FORM, DP>(a, maps, warp - C::kProdWarp, piece, sm, bars, &abort_flag);
@@ -1460,11 +1448,8 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
     if (a.device < 64) done.fetch_or(bit, std::memory_order_relaxed);
   }
   if (cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(C::kThreads), (size_t)C::kSmem, st, maps, a)) return (int)e;
-  if (!a.to_prefix) return (int)cudaGetLastError();
-  // tiles that the list can have: whole ones, and the short last one of each group
-  const int tt = a.list.tpt * a.list.streams, tiles = a.n_tokens / tt + a.n_groups;
-  return (int)launch_pdl(attn_join_kernel<DP, BF>, dim3((unsigned)(tiles * a.Hkv * a.list.streams * (DP / 4))),
-                         dim3(128), 0, st, a);
+  if (!a.join) return (int)cudaGetLastError();
+  return (int)launch_pdl(attn_join_kernel<DP, BF>, dim3(4 * a.ctas), dim3(128), 0, st, a);
 }
 
 template <int FORM, int DP, bool BF>

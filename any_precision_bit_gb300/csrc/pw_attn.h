@@ -12,16 +12,19 @@ namespace pw {
 constexpr int kAttnKeys = 128;         // keys of one key/value tile, the unit of work
 constexpr int kAttnRows = 128;         // query rows of one tile (tensor-memory lanes of an MMA)
 constexpr int kAttnMaxRequests = 4096;
-// Three forms of the kernel:
+// Two forms of the kernel:
 //   kTwo     two 128-row tiles share each key tile: while one tile's scores are in the softmax the
 //            tensor cores work on the other's;
-//   kOne     one tile, its score buffers doubled, so that the next scores are computed during a softmax;
-//   kSpread  one tile of at most 32 rows, which is held four times, once in each lane quarter of tensor
+//   kSpread  one tile of at most 16 rows, which is held four times, once in each lane quarter of tensor
 //            memory: quarter w keeps a softmax over keys 32 w .. 32 w + 31 of every key tile (its
 //            probabilities of the other keys are zeros), and the four results are added at the end.  Four
-//            warps then share the few rows, where in kOne one warp has them all and the others idle.
-enum { kTwo = 2, kOne = 1, kSpread = 4 };
-constexpr int kSpreadRows = 32;
+//            warps then share the few rows, the scores of the next key tile are computed during a
+//            softmax, and four more warps finish a piece during the next.
+// Measured with one form and the other, 64 requests (us): 4 rows behind 256 .. 8192 keys 178 in kSpread
+// and 188 in kTwo, behind 16 .. 700 keys 27.5 and 34.1; 16 rows behind up to 4096 keys 103 and 107; 32 rows,
+// where kSpread has no second query buffer, 65 and 64.
+enum { kTwo = 2, kSpread = 4 };
+constexpr int kSpreadRows = 16;
 
 // Findings of the device side, reported by pw_attn_check.
 enum {
@@ -56,14 +59,20 @@ struct AttnStart {
   int2 first, last;
 };
 
+// A (tile, head) that is split among the CTAs c0 .. c1, c1 > c0.
+struct AttnSplit {
+  AttnTile t;
+  int head, c0, c1, pad;
+};
+
 // One list of work.  In the order (tile, head), each has piece_cost units without keys and then one for
 // each of its key tiles; of the W units CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W if that is less (the rest idle).
 struct AttnList {
   AttnTile *tiles;
   int *cum;          // [tiles + 1] units of one head before each tile
   AttnStart *start;  // [P]
-  int2 *ctas;        // [tiles][Hkv] CTAs of the first and the last key tile; null: not wanted
-  int *meta;         // [0] tiles, [1] units of one head
+  AttnSplit *splits; // [P], of which meta[2] are set
+  int *meta;         // [0] tiles, [1] units of one head, [2] splits
   int tpt;           // tokens of one 128-row tile
   int streams;       // 128-row tiles of one AttnTile (1 or 2)
   int piece_cost;    // units that a (tile, head) counts for beside its key tiles when the work is divided: the
@@ -131,7 +140,8 @@ struct AttnArgs {
   // Results over a shared prefix, normalised, and their log2-sum-exp2: written (to_prefix) or merged
   // into the rows of tiles with `merge`.
   float *prefix_o, *prefix_lse;  // [n_tokens][Hq][D], [n_tokens][Hq]
-  int to_prefix, after_prefix, n_groups;
+  int to_prefix, after_prefix;
+  int join;  // pieces of split tiles are added up by attn_join_kernel, not by the last of their CTAs
   // Partial results of split tiles: two slots a CTA (its last piece and its first) and stream.
   float *part_o;    // [ctas][2][streams][head_dim padded / 4][128][4]
   float2 *part_ml;  // [ctas][2][streams][128] running maximum and sum

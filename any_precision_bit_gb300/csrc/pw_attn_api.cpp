@@ -16,6 +16,8 @@ using namespace pw;
 
 namespace {
 
+constexpr int kJoinPieces = 2;
+
 pw_status bad(const char *msg) { return report(nullptr, PW_ERR_INVALID, msg); }
 pw_status cuda_failed(const char *what, int e) {
   cudaGetLastError();
@@ -154,12 +156,11 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
         // full tiles of at least 128 / G tokens (or of all a step's), and the short last one of each group
         const int G = d.n_heads / d.n_kv_heads;
         l->max_tiles = d.max_shared_tokens / std::min(kAttnRows / G, d.max_shared_tokens) + d.max_requests;
-        ok = ok && alloc(a, &l->ctas, ((size_t)l->max_tiles + 1) * d.n_kv_heads);
       } else {
         l->max_tiles = d.max_tokens + d.max_requests + 1;
       }
       ok = ok && alloc(a, &l->tiles, (size_t)l->max_tiles + 1) && alloc(a, &l->cum, (size_t)l->max_tiles + 1) &&
-           alloc(a, &l->start, ctas) && alloc(a, &l->meta, 2);
+           alloc(a, &l->start, ctas) && alloc(a, &l->meta, 3) && alloc(a, &l->splits, ctas);
     }
   }
   if (!ok) return report(nullptr, PW_ERR_OOM, "device memory exhausted");
@@ -299,10 +300,8 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   g.n_kv_heads = a->d.n_kv_heads;
   const int G = a->d.n_heads / a->d.n_kv_heads, most = kAttnRows / G;
   auto shape = [&](AttnList &l, int tokens) {
-    // two 128-row tiles share each key tile when a segment has rows for them, else one tile runs with its
-    // score buffers doubled
     tokens = std::max(tokens, 1);
-    l.streams = (int64_t)tokens * G > kAttnRows ? 2 : 1;
+    l.streams = (int64_t)tokens * G > kSpreadRows ? 2 : 1;  // the kernel's form: see pw_attn.h
     l.tpt = std::min(most, tokens);
     // measured: two tiles, 8192-token prompt 479, 417, 395, 397, 401 us at 1 to 5 and packed chunks 66, 66, 68,
     // 71, 73 us; few rows, 160 windowed requests 137, 137, 138 us at 1 to 3
@@ -427,12 +426,14 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   if (p.step.n_groups) {
     g.prefix_o = a->prefix_o;
     g.prefix_lse = a->prefix_lse;
-    g.to_prefix = 1;
-    g.n_groups = p.step.n_groups;
+    g.to_prefix = g.join = 1;
     if (pw_status st = launch(p.groups)) return st;
     g.to_prefix = 0;
     g.after_prefix = 1;
   }
+  // where the two-tile form has so few tiles that each is split among many CTAs on average
+  const int tiles = p.step.n_tokens / (p.requests.tpt * p.requests.streams) + p.step.R;
+  g.join = p.requests.streams == 2 && (int64_t)tiles * g.Hkv * kJoinPieces <= g.ctas;
   return launch(p.requests);
 }
 

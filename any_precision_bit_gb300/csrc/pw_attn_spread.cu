@@ -1,4 +1,4 @@
-// pw_attn_spread.cu -- the attention kernel with at most 32 query rows: single tokens.
+// pw_attn_spread.cu -- the attention kernel with at most 16 query rows to a tile: single tokens and drafts.
 #include "pw_attn.cuh"
 
 namespace pw {

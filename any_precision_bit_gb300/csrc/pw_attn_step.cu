@@ -294,11 +294,9 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   auto ctas_of = [&](long long ub, int cost) {
     return make_int2((int)(((ub + a.list.piece_cost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
   };
-  if (a.list.ctas)
-    for (int i = tid; i < n_tiles * a.n_kv_heads; i += kListThreads) {
-      const int tile = i / a.n_kv_heads, cost = a.list.cum[tile + 1] - a.list.cum[tile];
-      a.list.ctas[i] = ctas_of((long long)a.list.cum[tile] * a.n_kv_heads + (long long)(i - tile * a.n_kv_heads) * cost, cost);
-    }
+  __shared__ int n_splits;
+  if (tid == 0) n_splits = 0;
+  __syncthreads();
   for (int c = tid; c < a.ctas; c += kListThreads) {
     const long long u0 = min(c * W / P, W), u1 = min((c + 1) * W / P, W);
     AttnStart st{0, 0, 0, (int)(u1 - u0), {}, {0, 0}, {0, 0}};
@@ -324,9 +322,13 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
       int tile, head, off;
       st.last = find(u1 - 1, tile, head, off);
       st.t = a.list.tiles[st.tile];
+      if (st.last.x == c && st.last.y > c)  // split, from here on (their order does not matter)
+        a.list.splits[atomicAdd(&n_splits, 1)] = AttnSplit{a.list.tiles[tile], head, c, st.last.y, 0};
     }
     a.list.start[c] = st;
   }
+  __syncthreads();
+  if (tid == 0) a.list.meta[2] = n_splits;
 }
 
 int launch_attn_list(const PlanArgs &a, void *stream) {

@@ -1,4 +1,4 @@
-// pw_attn_two.cu -- the attention kernel with two query tiles to a CTA: prompts, chunks and shared prefixes.
+// pw_attn_two.cu -- the attention kernel with two query tiles to a CTA.
 #define PW_RARE __forceinline__
 #include "pw_attn.cuh"
 
