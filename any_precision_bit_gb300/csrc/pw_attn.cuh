@@ -1107,7 +1107,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   using B = Bars<C::kStages>;
   const int quarter = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, thread = 32 * quarter + lane;
   float *sh = reinterpret_cast<float *>(smp + C::kScratchAt);
-  constexpr int V = DP / 16, kPart = DP * 128;
+  constexpr int V = DP / 16, kPart = DP * 128, kBatch = 8;
   const int c = (thread & 15) * V;  // this thread's columns c .. c + V - 1
   auto slot_of = [&](int cta, int c0) { return part_slot(cta, c0, 1, 0); };
   Group<C::kStages> group{bars, 0, 0, abort_flag};
@@ -1199,47 +1199,90 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       }
       // whole tiles: these eight rows; split tiles: once all pieces are there, all rows
       for (int q0 = c0 == c1 ? r0 : 0; last && q0 < (c0 == c1 ? min(nrows, r0 + kJoinRows) : nrows); q0 += kJoinRows) {
-        const int ro = q0 + (thread >> 4);
-        const bool use = ro < nrows;
-        if (use && c0 != c1) {  // running maximum and sums over four pieces at a time
+        int slot = thread >> 4, share = 0;  // (row, share of its pieces)
+        if (c0 != c1) {
+          // running maximum and sums, eight pieces under way; where rows are few, several threads share one's pieces
+          const int shares = nrows > 4 ? 1 : nrows > 2 ? 2 : nrows > 1 ? 4 : 8, rows = kJoinRows / shares;
+          share = slot / rows;
+          slot -= share * rows;
+          const int ro = q0 + slot;
           mm = -INFINITY;
           ll = 0.f;
 #pragma unroll
           for (int i = 0; i < V; ++i) v[i] = 0.f;
-          for (int p0 = c0; p0 <= c1; p0 += 4) {
-            float2 y[4];
-            float4 z[4][V / 4];
+          if (ro < nrows) {
+#pragma unroll 1
+            for (int p0 = c0 + share; p0 <= c1; p0 += kBatch * shares) {
+              float2 y[kBatch];
+              float4 z[kBatch][V / 4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool in = p0 + k <= c1;
-              const size_t at = slot_of(in ? p0 + k : c1, c0);
-              y[k] = __ldcg(a.part_ml + at * 128 + ro);
+              for (int k = 0; k < kBatch; ++k) {
+                y[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-              for (int i = 0; i < V / 4; ++i)
-                z[k][i] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ((c / 4 + i) * 128 + ro) * 4));
-              if (!in) y[k] = make_float2(-INFINITY, 0.f);
-            }
-            const float mn = fmaxf(fmaxf(fmaxf(mm, y[0].x), fmaxf(y[1].x, y[2].x)), y[3].x);
-            const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(mm - ms);
-            ll *= keep;
+                for (int i = 0; i < V / 4; ++i) z[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int p = p0 + k * shares;
+                if (p <= c1) {
+                  const size_t at = slot_of(p, c0);
+                  y[k] = __ldcg(a.part_ml + at * 128 + ro);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] *= keep;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (p0 + k > c1) break;
-              const float f = ex2(y[k].x - ms);
-              ll = fmaf(f, y[k].y, ll);
-#pragma unroll
-              for (int i = 0; i < V; i += 4) {
-                v[i] = fmaf(f, z[k][i / 4].x, v[i]);
-                v[i + 1] = fmaf(f, z[k][i / 4].y, v[i + 1]);
-                v[i + 2] = fmaf(f, z[k][i / 4].z, v[i + 2]);
-                v[i + 3] = fmaf(f, z[k][i / 4].w, v[i + 3]);
+                  for (int i = 0; i < V / 4; ++i)
+                    z[k][i] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kPart + ((c / 4 + i) * 128 + ro) * 4));
+                }
               }
+              float mn = mm;
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, y[k].x);
+              const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(mm - ms);
+              ll *= keep;
+#pragma unroll
+              for (int i = 0; i < V; ++i) v[i] *= keep;
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const float f = ex2(y[k].x - ms);
+                ll = fmaf(f, y[k].y, ll);
+#pragma unroll
+                for (int i = 0; i < V; i += 4) {
+                  v[i] = fmaf(f, z[k][i / 4].x, v[i]);
+                  v[i + 1] = fmaf(f, z[k][i / 4].y, v[i + 1]);
+                  v[i + 2] = fmaf(f, z[k][i / 4].z, v[i + 2]);
+                  v[i + 3] = fmaf(f, z[k][i / 4].w, v[i + 3]);
+                }
+              }
+              mm = mn;
             }
-            mm = mn;
+          }
+          if (shares > 1) {  // the shares' sums side by side, as the quarters' before
+            float2 *share_ml = reinterpret_cast<float2 *>(sh + kJoinRows * C::kScratchRow);
+            if (share > 0) {
+#pragma unroll
+              for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4 *>(sh + (share * rows + slot) * C::kScratchRow + c + i) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              if (c == 0) share_ml[share * rows + slot] = make_float2(mm, ll);
+            }
+            if (!(ok = group.join(a))) break;
+            if (share == 0) {
+              float mn = mm;
+#pragma unroll 1
+              for (int k = 1; k < shares; ++k) mn = fmaxf(mn, share_ml[k * rows + slot].x);
+              const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(mm - ms);
+              ll *= keep;
+#pragma unroll
+              for (int i = 0; i < V; ++i) v[i] *= keep;
+#pragma unroll 1
+              for (int k = 1; k < shares; ++k) {
+                const float2 y = share_ml[k * rows + slot];
+                const float f = ex2(y.x - ms);
+                ll = fmaf(f, y.y, ll);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = fmaf(f, sh[(k * rows + slot) * C::kScratchRow + c + i], v[i]);
+              }
+              mm = mn;
+            }
           }
         }
+        const int ro = q0 + slot;
+        const bool use = share == 0 && ro < nrows;
         const bool near = q0 == 0;  // fetched above
         const int ro_t = over_g(a, ro), tok = w.tok0 + ro_t, head = w.head * a.G + ro - ro_t * a.G;
         bool again = false;
@@ -1275,8 +1318,8 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 
 // The sum of each split tile's pieces, where tiles are few and their pieces many: one CTA of the attention
 // kernel adding up a tile's (18 pieces of 64 KB for 256 rows over a prefix of 4096 keys) took longer than the
-// products.  Here a CTA takes 4 columns of a tile's 128 rows at a time, a thread a row, with eight pieces under
-// way.
+// products.  Here a CTA takes 4 columns of a tile's rows at a time, a thread a row, with eight pieces under way;
+// of kSpread's 16 rows eight threads share each, its pieces dealt out among them.
 template <bool BF>
 static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned flagged, int tok, int h, const AttnTile &t,
                                               bool merge, int c) {
@@ -1287,44 +1330,52 @@ static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned flagge
                  c, c + 4);
   }
 }
-template <int DP, bool BF>
+template <int FORM, int DP, bool BF>
 static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kBatch = 8, kCols = DP / 4;
+  constexpr int kRows = FORM == kSpread ? kSpreadRows : 128, kShare = 128 / kRows;
+  __shared__ float4 sum_v[kShare][kRows];
+  __shared__ float2 sum_ml[kShare][kRows];
   pdl_trigger();
   pdl_wait();
-  const int streams = a.list.streams, row = threadIdx.x, row_t = over_g(a, row), row_h = row - row_t * a.G;
+  const int streams = FORM == kTwo ? 2 : 1, share = threadIdx.x / kRows, row = threadIdx.x % kRows, row_t = over_g(a, row), row_h = row - row_t * a.G;
   const int n = a.list.meta[2] * streams * kCols;
 #pragma unroll 1
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int c = i % kCols * 4, s = streams == 2 ? i / kCols & 1 : 0;
-    const AttnSplit *sp = a.list.splits + (streams == 2 ? i / (2 * kCols) : i / kCols);
+    const int c = i % kCols * 4, s = i / kCols % streams;
+    const AttnSplit *sp = a.list.splits + i / (streams * kCols);
     const AttnTile t = load_tile(&sp->t);
     const int4 x = *reinterpret_cast<const int4 *>(&sp->head);
     const int c0 = x.y, c1 = x.z, tok = t.tok0 + s * a.list.tpt + row_t, h = x.x * a.G + row_h;
     const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G && c < a.D, merge = t.merge && !a.to_prefix;
     bool again = false;
+    float pl = 0.f, m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     if (valid) {
-      // the first piece is its CTA's last, the others their CTAs' first (see part_slot): two slots apart
-      const size_t at = part_slot(c0, c0, streams, s), next = part_slot(c0 + 1, c0, streams, s);
-      const int step = 2 * streams;
-      const float2 *pm = a.part_ml + next * 128 + row;
-      const float4 *po = reinterpret_cast<const float4 *>(a.part_o + next * (DP * 128)) + c / 4 * 128 + row;
-      const float2 y0 = __ldcg(a.part_ml + at * 128 + row);
-      const float4 v0 = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
-      const float pl = merge ? a.prefix_lse[(size_t)tok * a.Hq + h] : 0.f;
-      float m = y0.x, l = y0.y, v[4] = {v0.x, v0.y, v0.z, v0.w};
+      // pieces of this thread: the CTAs c0 + share, c0 + share + kShare, ...; all but c0's are their CTAs' first (see
+      // part_slot), two slots apart
+      const int step = 2 * streams * kShare;
+      auto load = [&](size_t at, float2 &y, float4 &z) {
+        y = __ldcg(a.part_ml + at * 128 + row);
+        z = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * (DP * 128)) + c / 4 * 128 + row);
+      };
+      float2 y0 = make_float2(-INFINITY, 0.f);
+      float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c0 + share <= c1) load(part_slot(c0 + share, c0, streams, s), y0, v0);
+      const size_t next = part_slot(c0 + share + kShare, c0, streams, s);
+      if (merge && share == 0) pl = a.prefix_lse[(size_t)tok * a.Hq + h];
+      m = y0.x;
+      l = y0.y;
+      v[0] = v0.x, v[1] = v0.y, v[2] = v0.z, v[3] = v0.w;
+      size_t at = next;
 #pragma unroll 1
-      for (int p = c0 + 1; p <= c1; p += kBatch, pm += kBatch * step * 128, po += (size_t)kBatch * step * DP * 32) {
+      for (int p = c0 + share + kShare; p <= c1; p += kBatch * kShare, at += kBatch * step) {
         float2 y[kBatch];
         float4 z[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           y[k] = make_float2(-INFINITY, 0.f);
           z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (p + k <= c1) {
-            y[k] = __ldcg(pm + k * step * 128);
-            z[k] = __ldcg(po + (size_t)k * step * DP * 32);
-          }
+          if (p + k * kShare <= c1) load(at + k * step, y[k], z[k]);
         }
         float mn = m;
 #pragma unroll
@@ -1344,6 +1395,37 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
         }
         m = mn;
       }
+      if (kShare > 1) {
+        sum_ml[share][row] = make_float2(m, l);
+        sum_v[share][row] = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    if (kShare > 1) {
+      __syncthreads();
+      if (valid && share == 0) {
+        float mn = m;
+#pragma unroll
+        for (int k = 1; k < kShare; ++k) mn = fmaxf(mn, sum_ml[k][row].x);
+        const float ms = mn == -INFINITY ? 0.f : mn, keep = ex2(m - ms);
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] *= keep;
+#pragma unroll
+        for (int k = 1; k < kShare; ++k) {
+          const float2 y = sum_ml[k][row];
+          const float4 z = sum_v[k][row];
+          const float f = ex2(y.x - ms);
+          l = fmaf(f, y.y, l);
+          v[0] = fmaf(f, z.x, v[0]);
+          v[1] = fmaf(f, z.y, v[1]);
+          v[2] = fmaf(f, z.z, v[2]);
+          v[3] = fmaf(f, z.w, v[3]);
+        }
+        m = mn;
+      }
+      __syncthreads();
+    }
+    if (valid && share == 0) {
       const RowOut out = row_out(a, tok, h, merge, pl, m, l);
       again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
       if (c == 0) store_lse(a, out);
@@ -1449,7 +1531,7 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
   }
   if (cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(C::kThreads), (size_t)C::kSmem, st, maps, a)) return (int)e;
   if (!a.join) return (int)cudaGetLastError();
-  return (int)launch_pdl(attn_join_kernel<DP, BF>, dim3(4 * a.ctas), dim3(128), 0, st, a);
+  return (int)launch_pdl(attn_join_kernel<FORM, DP, BF>, dim3(4 * a.ctas), dim3(128), 0, st, a);
 }
 
 template <int FORM, int DP, bool BF>

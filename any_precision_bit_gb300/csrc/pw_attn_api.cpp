@@ -16,7 +16,11 @@ using namespace pw;
 
 namespace {
 
-constexpr int kJoinPieces = 2;
+// Measured (us), pieces added up by the last CTA to arrive and by attn_join_kernel.  Two tiles: 64 new tokens behind
+// 32000 71 and 39, 100 behind 1000 28 and 16, 256 behind 32000 (4 pieces a tile) 104 and 96, 700 in three
+// requests (1.5 pieces) 28.8 and 31.7.  Few rows: one request behind 131000 with one key/value head 55 and 23, behind
+// 32000 with two 32 and 16, with four 28 and 21; with eight (8 pieces by this count) behind 517 10.9 and 12.4.
+constexpr int kJoinTwo = 2, kJoinSpread = 16;
 
 pw_status bad(const char *msg) { return report(nullptr, PW_ERR_INVALID, msg); }
 pw_status cuda_failed(const char *what, int e) {
@@ -431,9 +435,10 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
     g.to_prefix = 0;
     g.after_prefix = 1;
   }
-  // where the two-tile form has so few tiles that each is split among many CTAs on average
+  // Where tiles are few, each is split among many CTAs, and a kernel of its own adds up the pieces: from so many
+  // pieces a tile on average.
   const int tiles = p.step.n_tokens / (p.requests.tpt * p.requests.streams) + p.step.R;
-  g.join = p.requests.streams == 2 && (int64_t)tiles * g.Hkv * kJoinPieces <= g.ctas;
+  g.join = (int64_t)tiles * g.Hkv * (p.requests.streams == 2 ? kJoinTwo : kJoinSpread) <= g.ctas;
   return launch(p.requests);
 }
 
