@@ -566,6 +566,9 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ int over_g(const AttnArgs &a, int row) { return (int)((uint32_t)row * a.g_magic >> 16); }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.4028234e38f; }
 
+// What happens to the scores besides a positive scale.
+enum { kPlain, kCapped, kGeneral };
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Pairs of floats, for the arithmetic that takes two at a time.
@@ -614,7 +617,17 @@ __device__ __forceinline__ float max_of(const float (&x)[N]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Scores of the keys base + i to log2 units with cap and bias.  tanh(y) = y P(y^2) with a polynomial of
+template <int N>
+__device__ __forceinline__ float largest_magnitude(const float (&x)[N]) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = max3(top[k], fabsf(x[i + 2 * k]), fabsf(x[i + 2 * k + 1]));
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// kGeneral: scores of the keys base + i to log2 units with cap and bias.  tanh(y) = y P(y^2) with a polynomial of
 // degree 4 (fitted at Chebyshev nodes on |y| <= 1/2; largest error 3.8e-8), on the multiply-add pipe; a
 // warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, with two special-function
 // operations for each score.  (tanh itself in one such operation is off by 2^-11: capped scores, and so
@@ -623,12 +636,7 @@ template <int N>
 __device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool valid, float slope, float d0) {
   if (a.softcap > 0.f) {
     const float inv = a.inv_cap, cap2 = a.cap2;
-    float top[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; i += 8)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top[k] = max3(top[k], fabsf(x[i + 2 * k]), fabsf(x[i + 2 * k + 1]));
-    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(inv);
+    const float most = largest_magnitude(x) * fabsf(inv);
     if (__any_sync(0xffffffffu, valid && !(most <= 0.5f))) {
       const float t2 = 2.f * kLog2e * inv;
 #pragma unroll
@@ -672,15 +680,42 @@ __device__ __forceinline__ void mask_out(float (&x)[N], int lo, int hi, float va
   }
 }
 
-// 32 scores to probabilities 2^(x scale - m) (EXTRA: 2^(x - m)), packed; their sum in pairs.
-template <bool BF, bool EXTRA>
+// kCapped: N raw scores to exponents cap(x) - m.  With the scale folded into the polynomial's coefficients
+// (a.cap_poly) that is six operations a pair, the last of which subtracts m: the maximum of capped scores is the
+// cap of the largest, so that m is known before.
+__device__ __forceinline__ float cap_one(const AttnArgs &a, float x, bool wide) {
+  if (wide) return a.cap2 - 2.f * a.cap2 * rcp(ex2(x * (2.f * kLog2e) * a.inv_cap) + 1.f);
+  const float u = x * x;
+  return x * fmaf(fmaf(fmaf(fmaf(a.cap_poly[4], u, a.cap_poly[3]), u, a.cap_poly[2]), u, a.cap_poly[1]), u, a.cap_poly[0]);
+}
+template <int N>
+__device__ __forceinline__ void cap_exponents(const AttnArgs &a, float (&x)[N], bool wide, float m) {
+  if (wide) {
+    const float t2 = 2.f * kLog2e * a.inv_cap, top = a.cap2 - m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fmaf(-2.f * a.cap2, rcp(ex2(x[i] * t2) + 1.f), top);
+  } else {
+    const uint64_t k4 = pair(a.cap_poly[4], a.cap_poly[4]), k3 = pair(a.cap_poly[3], a.cap_poly[3]),
+                   k2 = pair(a.cap_poly[2], a.cap_poly[2]), k1 = pair(a.cap_poly[1], a.cap_poly[1]),
+                   k0 = pair(a.cap_poly[0], a.cap_poly[0]), neg_m = pair(-m, -m);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t y = pair(x[i], x[i + 1]), u = mul2(y, y);
+      const uint64_t r = fma2(fma2(fma2(fma2(k4, u, k3), u, k2), u, k1), u, k0);
+      unpair(fma2(r, y, neg_m), x[i], x[i + 1]);
+    }
+  }
+}
+// 32 scores to probabilities, packed, and their sum in pairs: 2^(x scale - m) (kPlain), 2^(x - m) (kGeneral), or 2^x of
+// exponents (kCapped).
+template <bool BF, int MODE>
 __device__ __forceinline__ void exponentials(const float *x, uint64_t scale, uint64_t neg_m, uint32_t (&pk)[16],
                                              uint64_t (&sum)[2]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     float p, q;
     const uint64_t y = pair(x[i], x[i + 1]);
-    unpair(EXTRA ? add2(y, neg_m) : fma2(y, scale, neg_m), p, q);
+    unpair(MODE == kCapped ? y : MODE == kGeneral ? add2(y, neg_m) : fma2(y, scale, neg_m), p, q);
     p = ex2(p);
     q = ex2(q);
     sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(p, q));
@@ -820,7 +855,7 @@ struct Group {
   }
 };
 
-template <int FORM, int DP, bool BF, bool EXTRA>
+template <int FORM, int DP, bool BF, int MODE>
 __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
                        volatile int *abort_flag, volatile int *last_flag) {
   using C = Cfg<FORM, DP>;
@@ -831,7 +866,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   // Of which this many at a time.  Capped and biased scores go through tensor memory once more, in two halves:
   // all 128 at a time their arithmetic spilled registers and filled the instruction cache (chunks-docs-cap
   // 70.7 us, in halves 67.9); plain scores lose more by the second read (prompt-8192 413 us, in halves 444).
-  constexpr int CH = SP ? 32 : EXTRA ? 64 : 128;
+  constexpr int CH = SP ? 32 : MODE != kPlain ? 64 : 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = warp >> 2, quarter = warp & 3, thread = 32 * quarter + lane;
   const int row = SP ? lane : thread, col0 = SP ? 32 * quarter : 0;
@@ -879,7 +914,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const bool valid = row < nrows;
     const int klo = w.klo, khi = w.khi, lo = max(rb.lo, klo), hi = min(rb.hi, khi);
     const bool active = SP || 32 * quarter < nrows;
-    const float slope = EXTRA && a.slopes && valid ? a.slopes[w.head * a.G + row_h] * kLog2e : 0.f;
+    const float slope = MODE == kGeneral && a.slopes && valid ? a.slopes[w.head * a.G + row_h] * kLog2e : 0.f;
     const uint32_t tmem_o = tmem + 256 + 128 * (SP ? pieces & 1 : (uint32_t)s) + lanes;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
@@ -911,21 +946,25 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           for (int i = 0; i < CH; i += 32) tmem_ld32(ts + col0 + c + i, reinterpret_cast<uint32_t *>(x) + i);
           tmem_wait_ld();
         };
+        float top = 0.f;
 #pragma unroll 1
         for (int c = 0; c < NC; c += CH) {
           load(c);
           // (hidden scores, which may come from unwritten memory, have no say in how the tile's are capped)
-          if (EXTRA && edge && a.softcap > 0.f) mask_out<CH>(x, l0 - c, h0 - c, 0.f);
-          if (EXTRA) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - col0 - c));
+          if (MODE != kPlain && edge && a.softcap > 0.f) mask_out<CH>(x, l0 - c, h0 - c, 0.f);
+          if (MODE == kCapped) top = fmaxf(top, largest_magnitude(x));
+          if (MODE == kGeneral) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - col0 - c));
           if (edge) mask_out<CH>(x, l0 - c, h0 - c, -INFINITY);
           mx = fmaxf(mx, max_of<CH>(x));
-          if (EXTRA && CH < NC) {
+          if (MODE == kGeneral && CH < NC) {
 #pragma unroll
             for (int i = 0; i < CH; i += 32) tmem_st32(ts + c + i, reinterpret_cast<uint32_t *>(x) + i);
           }
         }
-        if (EXTRA && CH < NC) tmem_wait_st();
-        if (!EXTRA) mx *= sl2;
+        if (MODE == kGeneral && CH < NC) tmem_wait_st();
+        const bool wide = MODE == kCapped && __any_sync(0xffffffffu, valid && !(top * a.inv_cap <= 0.5f));
+        if (MODE == kPlain) mx *= a.scale2;
+        if (MODE == kCapped) mx = mx == -INFINITY ? mx : cap_one(a, mx, wide);
         if (!valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
         if (j == 0) {
           m = mx;
@@ -955,11 +994,15 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         uint64_t sum[2] = {0, 0};
 #pragma unroll 1
         for (int c0 = 0; c0 < NC; c0 += CH) {
-          if (CH < NC) load(c0);  // as transformed
+          if (CH < NC) load(c0);  // (kGeneral: as transformed)
+          if (MODE == kCapped) {
+            cap_exponents<CH>(a, x, wide, ms);
+            if (edge) mask_out<CH>(x, l0 - c0, h0 - c0, -INFINITY);
+          }
 #pragma unroll
           for (int c = 0; c < CH / 32; ++c) {
             uint32_t pk[16];
-            exponentials<BF, EXTRA>(x + 32 * c, scale, neg_m, pk, sum);
+            exponentials<BF, MODE>(x + 32 * c, scale, neg_m, pk, sum);
             if (SP) {
               const uint32_t none[16] = {};
 #pragma unroll
@@ -1435,7 +1478,7 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
   }
 }
 
-template <int FORM, int DP, bool BF, bool EXTRA>
+template <int FORM, int DP, bool BF, int MODE>
 __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const __grid_constant__ AttnMaps maps,
                                                                        const __grid_constant__ AttnArgs a) {
   using C = Cfg<FORM, DP>;
@@ -1495,7 +1538,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   if (!a.after_prefix) pdl_wait();
   if (warp < C::kSoftWarps) {
     if (FORM == kTwo) regs_inc<kRegsSoft>();
-    if (!abort_flag) soften<FORM, DP, BF, EXTRA>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+    if (!abort_flag) soften<FORM, DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
   } else if (warp < C::kProdWarp) {
     if constexpr (FORM == kSpread) {
       if (!abort_flag) finish<DP, BF>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
@@ -1518,11 +1561,11 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   }
 }
 
-template <int FORM, int DP, bool BF, bool EXTRA>
+template <int FORM, int DP, bool BF, int MODE>
 static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
   using C = Cfg<FORM, DP>;
   static_assert(C::kStages >= 4, "two key tiles in flight");
-  auto kern = attn_kernel<FORM, DP, BF, EXTRA>;
+  auto kern = attn_kernel<FORM, DP, BF, MODE>;
   static std::atomic<uint64_t> done{0};  // devices whose limit has been raised
   const uint64_t bit = 1ull << (a.device & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
@@ -1535,15 +1578,16 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
 }
 
 template <int FORM, int DP, bool BF>
-static int launch_extra(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
-  // the plain image folds a positive scale into the exponent's multiply-add; caps, biases and other scales
-  // transform the scores first
-  if (a.softcap > 0.f || a.slopes || !(a.scale > 0.f)) return launch_one<FORM, DP, BF, true>(a, maps, st);
-  return launch_one<FORM, DP, BF, false>(a, maps, st);
+static int launch_mode(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
+  // kPlain folds a positive scale into the exponent's multiply-add; caps alone have the form above (for scales whose
+  // ninth power is far from what fp32 holds), and everything else transforms the scores first
+  if (!(a.softcap > 0.f) && !a.slopes && a.scale > 0.f) return launch_one<FORM, DP, BF, kPlain>(a, maps, st);
+  if (!a.slopes && a.inv_cap >= 1e-3f && a.inv_cap <= 1e2f) return launch_one<FORM, DP, BF, kCapped>(a, maps, st);
+  return launch_one<FORM, DP, BF, kGeneral>(a, maps, st);
 }
 template <int FORM, int DP>
 static int launch_type(const AttnArgs &a, const AttnMaps &maps, int bf16, cudaStream_t st) {
-  return bf16 ? launch_extra<FORM, DP, true>(a, maps, st) : launch_extra<FORM, DP, false>(a, maps, st);
+  return bf16 ? launch_mode<FORM, DP, true>(a, maps, st) : launch_mode<FORM, DP, false>(a, maps, st);
 }
 
 template <int FORM>

@@ -136,6 +136,7 @@ struct AttnArgs {
   float *lse;
   float scale, softcap;
   float scale2, inv_cap, cap2;  // scale log2 e, scale / softcap, softcap log2 e
+  float cap_poly[5];            // cap2 tanh(inv_cap x) as x times a polynomial of x^2
   const float *slopes;
   // Results over a shared prefix, normalised, and their log2-sum-exp2: written (to_prefix) or merged
   // into the rows of tiles with `merge`.

@@ -408,6 +408,10 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.scale2 = scale * 1.4426950408889634f;
   g.cap2 = softcap * 1.4426950408889634f;
   g.inv_cap = softcap > 0.f ? scale / softcap : 0.f;
+  // tanh(y) = y P(y^2), |y| <= 1/2 (see pw_attn.cuh)
+  const double poly[5] = {1.0, -0.3333307206630707, 0.13324828445911407, -0.05298924073576927, 0.017141319811344147};
+  double power = (double)g.cap2 * g.inv_cap;
+  for (int i = 0; i < 5; ++i, power *= (double)g.inv_cap * g.inv_cap) g.cap_poly[i] = (float)(poly[i] * power);
   g.err = a->err;
   g.wait_cycles = kWaitCyclesDefault;
   g.part_o = a->part_o;
