@@ -1,5 +1,22 @@
 // pw_attn.cuh -- attention over the paged key/value cache: the kernel and its launch, instantiated form by
 // form in pw_attn_two.cu and pw_attn_spread.cu.
+//
+// For a query row q with keys lo <= j < hi, x_j = scale q.k_j (capped, biased) and o = sum_j e^{x_j} v_j / sum_j
+// e^{x_j}, in one pass over the keys: with m a running reference, l = sum 2^{x_j log2 e - m} and O = sum
+// 2^{x_j log2 e - m} v_j; where the maximum outgrows m, l and O are scaled by 2^{m - m'}.  Two partial results of a
+// row join in the same way.
+//
+// A CTA (one to an SM) goes through its share of the units (a tile of 128 keys against a tile of query rows of one
+// key/value head, see AttnList).  Warps have roles: producers copy queries, keys and values to shared memory block by
+// block (TMA through the block table, 128-byte swizzle); one warp issues S = Q K^T and O += P V, S, P and O in tensor
+// memory (S and P share columns); softmax warps turn S into P, a lane a row; and a piece of a tile's keys ends in the
+// result, or in a partial one that is added up with the others' (the last CTA to arrive, or attn_join_kernel).
+//
+// Memory bounds the few-row form: 64 rows of 4 behind 0.26 to 8 thousand keys move 1.13 GB in 172 to 178 us, 6.4 to
+// 6.6 TB/s; two producer warps (one for K, one for V) reached 5.2 TB/s, the copies' issue being their limit.  The
+// two-tile form runs an 8192-token prompt of 32/8 heads of 128 at 1.42 PFLOP/s (387 us): a stream waits for its own
+// products (512 + 512 cycles and 350 of latency) behind its softmax (1800 cycles), and tensor memory has no room for a
+// second score buffer beside two streams' S and O.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -141,9 +158,27 @@ constexpr int kPieces = 4;  // pieces handed over ahead
 // mbarriers
 template <int STAGES>
 struct Bars {
-  enum { kFull = 0, kEmpty = STAGES, kQF = 2 * STAGES, kQE = kQF + 2, kSF = kQE + 2, kPF = kSF + 2, kOD = kPF + 2, kDrain = kOD + 2, kJoin, kDF = kJoin + 2, kDE = kDF + kPieces, kOF = kDE + kPieces, kOE = kOF + 2, kML = kOE + 2, kPE = kML + 2, kNum = kPE + 2 };
+  enum {
+    kFull = 0,               // a stage's keys or values have landed
+    kEmpty = STAGES,         // ... have been read by the MMAs
+    kQF = 2 * STAGES,        // a query buffer has landed
+    kQE = kQF + 2,           // ... its last scores are issued and done
+    kSF = kQE + 2,           // scores are in tensor memory (kTwo: of a stream; kSpread: of even and odd key tiles)
+    kPF = kSF + 2,           // probabilities are (four warps)
+    kPE = kPF + 2,           // kTwo: those of the first keys
+    kOD = kPE + 2,           // P V done: kTwo, a stream's last of a piece; kSpread, of an even or odd key tile
+    kOF = kOD + 2,           // kSpread: an output accumulator holds a piece's result
+    kOE = kOF + 2,           // ... has been read
+    kML = kOE + 2,           // ... the piece's maxima and sums are in shared memory
+    kJoin = kML + 2,         // four warps meet (a stream's, or the finishing warps)
+    kDF = kJoin + 2,         // a piece has been handed over
+    kDE = kDF + kPieces,     // ... every reader is done with it
+    kDrain = kDE + kPieces,  // the MMA warp's last commit
+    kNum
+  };
 };
 
+// Bounded wait on an mbarrier phase: false once the launch's limit is over or another warp has given up.
 static __device__ PW_RARE bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
                                        long long cycles) {
   const long long t0 = clock64();

@@ -288,8 +288,8 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     a.list.meta[1] = sat(before);
   }
   __syncthreads();
-  const long long W = before * a.n_kv_heads;  // at least one unit: there is a row, and every tile has one
-  const long long P = min((long long)a.ctas, W);
+  const long long W = before * a.n_kv_heads;  // (0 for groups without new tokens)
+  const long long P = max(1LL, min((long long)a.ctas, W));
   // CTAs of the first and the last key tile of a (tile, head) whose units begin at ub
   auto ctas_of = [&](long long ub, int cost) {
     return make_int2((int)(((ub + a.list.piece_cost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));

@@ -174,6 +174,14 @@ def test_shared_prefix(new, group_start, prefix, mask):
     s.close()
 
 
+@pytest.mark.parametrize("new", [[0, 0, 0], [0, 2, 0]])
+def test_shared_prefix_of_requests_without_new_tokens(new):
+    s = Step([48, 70, 33], new, Hq=4, Hkv=1, D=64, group_start=[0, 1, 3], prefix=[48, 32], pad=3)
+    s.map_and_append()
+    s.compare()
+    s.close()
+
+
 def test_long_context_is_split():
     s = Step([20000], [1], Hq=2, Hkv=1, D=64, bt=64)
     s.map_and_append()
