@@ -151,6 +151,7 @@ _SIGS = {
     "pw_attn_append": [_P, _I, _P, _P, _L, _L, _P, _L, _L, _P],
     "pw_attn_forward": [_P, _I, _I, _P, _L, _L, _P, _L, _L, _P, _F, _F, _P, _P],
     "pw_attn_check": [_P, _P],
+    "pw_attn_set_fault": [_P, _I, _I],
     "pw_set_profiling": [_P, _I],
     "pw_set_gemv_tokens": [_P, _I],
     "pw_profile_read": [_P, _I, _P],
@@ -616,3 +617,7 @@ def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, 
 
 def pw_attn_check(attn, stream=None):
     _check(lib().pw_attn_check(attn, _cuda_stream(stream)))
+
+
+def pw_attn_set_fault(attn, kind, n):
+    _check(lib().pw_attn_set_fault(attn, kind, n))

@@ -149,7 +149,8 @@ struct AttnArgs {
   int *counters;    // [ctas][2] arrived pieces of the split tile whose first piece is the CTA's last,
                     // per stream; zero between launches
   int *err;
-  long long wait_cycles;
+  long long wait_cycles;  // bounded device waits give up after this many SM cycles
+  int withhold;           // testing: see produce()
 };
 
 int launch_kv_map(const MapArgs &a, void *stream);

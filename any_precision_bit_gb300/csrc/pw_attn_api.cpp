@@ -104,6 +104,8 @@ struct pw_attn {
   float *part_o = nullptr, *prefix_o = nullptr, *prefix_lse = nullptr;
   float2 *part_ml = nullptr;
   int *counters = nullptr;
+  long long wait_cycles = kWaitCyclesDefault;
+  int fault_withhold = 0;  // testing: the next forward withholds one device barrier arrival
 };
 
 namespace {
@@ -413,7 +415,9 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   double power = (double)g.cap2 * g.inv_cap;
   for (int i = 0; i < 5; ++i, power *= (double)g.inv_cap * g.inv_cap) g.cap_poly[i] = (float)(poly[i] * power);
   g.err = a->err;
-  g.wait_cycles = kWaitCyclesDefault;
+  g.wait_cycles = a->wait_cycles;
+  g.withhold = a->fault_withhold;
+  a->fault_withhold = 0;
   g.part_o = a->part_o;
   g.part_ml = a->part_ml;
   g.counters = a->counters;
@@ -444,6 +448,18 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   const int tiles = p.step.n_tokens / (p.requests.tpt * p.requests.streams) + p.step.R;
   g.join = (int64_t)tiles * g.Hkv * (p.requests.streams == 2 ? kJoinTwo : kJoinSpread) <= g.ctas;
   return launch(p.requests);
+}
+
+pw_status pw_attn_set_fault(pw_attn *a, int kind, int n) {
+  if (!a) return bad("null argument");
+  if (n < 0 || (kind != 4 && kind != 5)) return bad("kind 4 or 5 and n >= 0");
+  if (kind == 4) {
+    a->fault_withhold = n != 0;
+  } else {
+    // cycles at the highest SM clock, so the wait lasts at least n microseconds
+    a->wait_cycles = n ? 2100LL * n : kWaitCyclesDefault;
+  }
+  return PW_OK;
 }
 
 pw_status pw_attn_check(pw_attn *a, pw_stream stream) {

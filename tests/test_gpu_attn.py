@@ -292,6 +292,30 @@ def test_findings_of_the_map_are_reported_once():
     finding(many_tokens, "more new tokens")
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [70, 1, 4]])
+@pytest.mark.parametrize("groups", [False, True])
+def test_an_expired_device_wait_is_reported_once(new, groups):
+    """One arrival withheld and a short limit (2 ms): PW_ERR_TIMEOUT once, then results as before."""
+    kw = dict(group_start=[0, 3], prefix=64) if groups else {}
+    s = Step([100, 400, 64], new, Hq=4, Hkv=2, D=64, **kw)
+    s.map_and_append()
+    s.compare()
+    s.pw.pw_attn_set_fault(s.attn, 5, 2000)
+    s.pw.pw_attn_set_fault(s.attn, 4, 1)
+    o = s.torch.empty(s.N, s.Hq, s.D, dtype=s.dt, device="cuda")
+    s.pw.pw_attn_forward(s.attn, 0, 0, s.q, o)
+    with pytest.raises(s.pw.PwError) as e:
+        s.pw.pw_attn_check(s.attn)
+    assert e.value.status == s.pw.PW_ERR_TIMEOUT
+    s.pw.pw_attn_check(s.attn)
+    s.pw.pw_attn_set_fault(s.attn, 5, 0)
+    s.compare()
+    s.compare(window=33)
+    with pytest.raises(s.pw.PwError):
+        s.pw.pw_attn_set_fault(s.attn, 1, 1)
+    s.close()
+
+
 def test_refusals_of_the_calls():
     import torch
     s = Step([20], [2], D=64)
