@@ -1003,11 +1003,15 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         if (MODE == kPlain) mx *= a.scale2;
         if (MODE == kCapped) mx = mx == -INFINITY ? mx : cap_one(a, mx, wide);
         if (!valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
+        // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8: until then
+        // the accumulator stays untouched.  fp16 probabilities lie as high as its range allows, in 2^7 .. 2^15 for
+        // the largest, so that what is 2^-21 of it still has all its bits and 2^-32 of it is not lost: many small
+        // ones behind a large one (of a small value) make up the result.
+        constexpr float kAbove = BF ? 0.f : 7.f;
+        mx -= kAbove;
         if (j == 0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-          // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8:
-          // until then probabilities up to 2^8 cost no precision, and the accumulator stays untouched.
           // kTwo: these scores were issued behind the product before, which is therefore done.
           const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2(m - mn);
           if (SP) {

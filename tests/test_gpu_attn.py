@@ -422,3 +422,32 @@ def test_blocks_beyond_32_bit_offsets():
     size = torch.einsum("htj,jhd->thd", p, rows[1].double().abs())
     assert bool(((o.double() - want).abs() <= 2.0 ** -8 * (want.abs() + size) + 1e-4 * size).all())
     pw.pw_attn_destroy(a)
+
+
+@pytest.mark.parametrize("new", [1, 3, 300])
+@pytest.mark.parametrize("mask", [{}, dict(softcap=40.0), dict(slopes=True)])
+def test_small_probabilities_behind_a_large_one(new, mask):
+    """A first key that takes nearly all the weight and whose value is zero: the result is what the others'
+    probabilities, about 2^-25 of the largest, add up to.  The largest is 2^7 or more before it is rounded to fp16,
+    so a probability is off by 2^-11 of itself or 2^-32 of the largest."""
+    R = 160 if new < 100 else 12
+    s = Step([300] * R, [new] * R, D=64, dtype="fp16", bt=16)
+    first = s.torch.as_tensor(s.table0[:, 0].astype(np.int64)).cuda()
+    for c, rest, top in ((s.kv[0], 0.0, 2.1875), (s.kv[1], 16.0, 0.0)):
+        c.nan_to_num_(0.0).fill_(rest)
+        c[first, 0] = top
+    s.q.fill_(1.0)  # the first key's score is 64 * 2.1875 / 8 = 17.5, the others' are 0
+    s.k.fill_(0.0)
+    s.v.fill_(16.0)
+    s.map_and_append()
+    kw = dict(mask)
+    if kw.pop("slopes", None):
+        kw["slopes"] = np.full(s.Hq, 2.0 ** -12)
+    got, _ = s.forward(**kw)
+    o, _, absum, _, where = s.expect(**kw)
+    keys = max(hi - lo for _, _, lo, hi in where)
+    # (scores are fp32: 17.5 log2 e with an error of 2^-22 or so, far below 2^-11; results below 2^-14 are subnormal)
+    tol = 2.0 ** -11 * (np.abs(o) + absum) + 1e-4 * absum + keys * 2.0 ** -32 * 16.0 + 2.0 ** -25
+    assert (o[:, :, 0] > 20 * tol[:, :, 0]).all()
+    assert (np.abs(got - o) <= tol).all(), float((np.abs(got - o) / tol).max())
+    s.close()
