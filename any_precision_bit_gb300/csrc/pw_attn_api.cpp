@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -283,8 +284,6 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   if (pw_status st = check_step(a, s)) return st;
   if (plan < 0 || plan >= a->d.n_plans) return bad("plan out of range");
   if (window < 0) return bad("window must not be negative");
-  OnDevice dev(a->d.device);
-  Plan &p = a->plans[(size_t)plan];
   PlanArgs g{};
   g.R = s->R;
   g.n_tokens = s->n_tokens;
@@ -299,7 +298,6 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   g.doc_start = doc_start;
   g.bidir_len = bidir_len;
   g.window = window;
-  g.bounds = p.bounds;
   g.n_groups = s->n_groups;
   g.group_start = s->group_start;
   g.shared_len = s->shared_len;
@@ -314,8 +312,23 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
     // 71, 73 us; few rows, 160 windowed requests 137, 137, 138 us at 1 to 3
     l.piece_cost = l.streams == 2 ? 3 : 2;
   };
-  shape(p.requests, s->max_new);
-  shape(p.groups, s->n_tokens);
+  // The lists sum up key tiles (and a piece's cost) over all tiles of rows in 31 bits, as they do an SM's share over
+  // the heads.
+  const int64_t keys = ((int64_t)s->table_stride * a->d.block_tokens + kAttnKeys - 1) / kAttnKeys;
+  auto countable = [&](const AttnList &l, int segments) {
+    const int64_t sum = (s->n_tokens / (l.tpt * l.streams) + (int64_t)segments) * (keys + l.piece_cost);
+    return sum <= INT32_MAX && sum * a->d.n_kv_heads / a->sm_count < INT32_MAX;
+  };
+  AttnList requests = a->plans[(size_t)plan].requests, groups = a->plans[(size_t)plan].groups;
+  shape(requests, s->max_new);
+  shape(groups, s->n_tokens);
+  if (!countable(requests, s->R + 1) || (s->n_groups && !countable(groups, s->n_groups)))
+    return bad("table_stride is too long for this many tokens (2^31 key tiles or more)");
+  OnDevice dev(a->d.device);
+  Plan &p = a->plans[(size_t)plan];
+  p.requests = requests;
+  p.groups = groups;
+  g.bounds = p.bounds;
   int e = launch_attn_bounds(g, stream);
   if (!e && s->n_groups) {
     g.of_groups = 1;
@@ -410,7 +423,7 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.slopes = slopes;
   g.scale2 = scale * 1.4426950408889634f;
   g.cap2 = softcap * 1.4426950408889634f;
-  g.inv_cap = softcap > 0.f ? scale / softcap : 0.f;
+  g.inv_cap = softcap > 0.f ? std::clamp(scale / softcap, -FLT_MAX, FLT_MAX) : 0.f;  // (0 scores stay 0)
   // tanh(y) = y P(y^2), |y| <= 1/2 (see pw_attn.cuh)
   const double poly[5] = {1.0, -0.3333307206630707, 0.13324828445911407, -0.05298924073576927, 0.017141319811344147};
   double power = (double)g.cap2 * g.inv_cap;

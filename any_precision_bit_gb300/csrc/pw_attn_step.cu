@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kStepThreads) kv_map_kernel(MapArgs a) {
     const int row = r < a.R && a.rows ? a.rows[r] : 0;
     if (row < 0 || row >= a.table_rows) bad |= kAttnErrBlock;
   }
-  for (int i = gid; i < n_open; i += step) {
-    const int r = seg_of(bs, a.R, i);
+  for (long long j = gid; j < n_open; j += step) {  // (n_open may be anything below 2^31)
+    const int i = (int)j, r = seg_of(bs, a.R, i);
     const int row = a.rows ? a.rows[r] : r;
     const int page = (a.ctx_len[r] + a.bt - 1) / a.bt + i - bs[r];
     int id = i < a.n_ids ? a.new_ids[i] : -1;

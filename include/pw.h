@@ -548,7 +548,9 @@ pw_status pw_kv_map(pw_attn *a, const pw_kv_step *step, const int32_t *new_ids, 
  * [lo, hi), and the division of all key blocks among the SMs.  window >= 0 (0: none).  doc_start [n_tokens]
  * (NULL: none): position in its request at which the row's document begins, for packed documents.
  * bidir_len [R] (NULL: none): keys below it are seen by every row of the request.  The plan holds for every
- * layer of the step with this mask, until the next pw_attn_plan into it; step's table must stay valid. */
+ * layer of the step with this mask, until the next pw_attn_plan into it; step's table must stay valid.
+ * PW_ERR_INVALID also where table_stride and n_tokens allow for 2^31 or more key tiles of 128 over all tiles of
+ * rows (a tile is 256 / (n_heads / n_kv_heads) tokens of a request, or max_new where that is less). */
 pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *step, int window, const int32_t *doc_start,
                        const int32_t *bidir_len, pw_stream stream);
 /* Write the step's new keys and values to the layer's cache: row t, head h of k is k[t * k_token +

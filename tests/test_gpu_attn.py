@@ -451,3 +451,21 @@ def test_small_probabilities_behind_a_large_one(new, mask):
     assert (o[:, :, 0] > 20 * tol[:, :, 0]).all()
     assert (np.abs(got - o) <= tol).all(), float((np.abs(got - o) / tol).max())
     s.close()
+
+
+def test_plan_refuses_more_work_than_it_can_count():
+    """Key tiles are counted in 31 bits over all tiles of rows."""
+    import torch
+    s = Step([20] * 4, [300] * 4, D=64)
+    s.map_and_append()
+    s.pw.pw_attn_plan(s.attn, 0, s.step)
+    stride = s.step.table_stride
+    s.step.table_stride = (2 ** 31 - 1) // s.bt  # 2^24 key tiles a row
+    s.step.max_new = 1  # a token a tile: 1200 tiles
+    with pytest.raises(s.pw.PwError) as e:
+        s.pw.pw_attn_plan(s.attn, 0, s.step)
+    assert e.value.status == s.pw.PW_ERR_INVALID
+    s.step.table_stride, s.step.max_new = stride, 300
+    torch.cuda.synchronize()
+    s.compare()
+    s.close()
