@@ -531,20 +531,24 @@ def pw_kv_get_stats(kv) -> dict:
 
 # ---------------------------------------------------------------- paged attention
 # (Called once or several times a layer, so argument marshalling is kept short here.)
-def _addr(t):
-    """Address of a contiguous device tensor, or None."""
+_attn_shapes = {}  # handle: (n_heads, n_kv_heads, head_dim, desc, {plan: its step's n_tokens})
+
+
+def _addr(t, size=4, n=0):
+    """Address of a contiguous device tensor of at least n elements of `size` bytes, or None."""
     if t is None:
         return None
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
+    if not t.is_contiguous() or t.element_size() != size or t.numel() < n or not t.is_cuda:
+        raise ValueError(f"needs a contiguous device tensor of {n} or more elements of {size} bytes")
     return t.data_ptr()
 
 
-def _rows(t):
-    """Address and the strides of [rows][heads][head_dim] (unit last stride)."""
+def _rows(t, n, heads, dim):
+    """Address and the strides of [n or more rows][heads][dim] (unit last stride)."""
+    rows, h, d = t.shape
     a, b, c = t.stride()
-    if c != 1:
-        raise ValueError("the last dimension must be contiguous")
+    if rows < n or h != heads or d != dim or c != 1 or t.element_size() != 2 or not t.is_cuda:
+        raise ValueError(f"needs a device tensor [{n}][{heads}][{dim}] of 16-bit elements, the last dimension contiguous")
     return t.data_ptr(), a, b
 
 
@@ -556,18 +560,25 @@ def pw_attn_create(desc: pw_attn_desc):
     """An attention handle (pass it to the pw_attn_* calls and pw_kv_map)."""
     h = C.c_void_p()
     _check(lib().pw_attn_create(C.byref(desc), C.byref(h)))
+    kept = pw_attn_desc.from_buffer_copy(desc)
+    _attn_shapes[h.value] = kept.n_heads, kept.n_kv_heads, kept.head_dim, kept, {}
     return h.value
 
 
 def pw_attn_destroy(attn):
+    _attn_shapes.pop(attn, None)
     lib().pw_attn_destroy(attn)
 
 
 def pw_attn_bind(attn, layer, k_cache, v_cache):
     """Caches as tensors [n_blocks][block_tokens][n_kv_heads][head_dim], views included, of the
     same strides and a unit last one."""
-    if k_cache.stride() != v_cache.stride() or k_cache.shape != v_cache.shape or k_cache.stride(3) != 1:
-        raise ValueError("the caches must have one shape, the same strides and a contiguous last dimension")
+    d = _attn_shapes[attn][3]
+    for c in (k_cache, v_cache):
+        if tuple(c.shape) != (d.n_blocks, d.block_tokens, d.n_kv_heads, d.head_dim) or c.element_size() != 2 or not c.is_cuda:
+            raise ValueError("the caches must be device tensors of the handle's shape and 16-bit elements")
+    if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+        raise ValueError("the caches must have the same strides and a contiguous last dimension")
     _check(lib().pw_attn_bind(attn, layer, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3]))
 
 
@@ -575,11 +586,11 @@ def pw_make_step(ctx_len, new_len, table, q_start, kv_len, slot, pos, max_new, r
     """A pw_kv_step over device tensors, which it keeps alive: lengths int32 [R], table int32
     [rows][blocks], q_start int32 [R + 1], kv_len int32 [R], slot int64 and pos int32 [n_tokens];
     groups int32 [n_groups + 1] and shared_len int32 [n_groups] for shared prefixes."""
-    s = pw_kv_step(R=ctx_len.numel(), n_tokens=pos.numel(), max_new=int(max_new), table_rows=table.shape[0],
-                   table_stride=table.shape[1], ctx_len=_addr(ctx_len), new_len=_addr(new_len), rows=_addr(rows),
-                   table=_addr(table), q_start=_addr(q_start), kv_len=_addr(kv_len), slot=_addr(slot), pos=_addr(pos),
-                   n_groups=0 if groups is None else groups.numel() - 1, group_start=_addr(groups),
-                   shared_len=_addr(shared_len))
+    R, n, n_groups = ctx_len.numel(), pos.numel(), 0 if groups is None else groups.numel() - 1
+    s = pw_kv_step(R=R, n_tokens=n, max_new=int(max_new), table_rows=table.shape[0], table_stride=table.shape[1],
+                   ctx_len=_addr(ctx_len), new_len=_addr(new_len, n=R), rows=_addr(rows, n=R), table=_addr(table),
+                   q_start=_addr(q_start, n=R + 1), kv_len=_addr(kv_len, n=R), slot=_addr(slot, 8, n), pos=_addr(pos),
+                   n_groups=n_groups, group_start=_addr(groups), shared_len=_addr(shared_len, n=n_groups))
     s.refs = (ctx_len, new_len, table, q_start, kv_len, slot, pos, rows, groups, shared_len)
     s.address = C.addressof(s)
     return s
@@ -593,14 +604,18 @@ def pw_kv_map(attn, step, new_ids, stream=None):
 
 
 def pw_attn_plan(attn, plan, step, window=0, doc_start=None, bidir_len=None, stream=None):
-    st = lib().pw_attn_plan(attn, plan, step.address, window, _addr(doc_start), _addr(bidir_len), _cuda_stream(stream))
+    st = lib().pw_attn_plan(attn, plan, step.address, window, _addr(doc_start, n=step.n_tokens), _addr(bidir_len, n=step.R),
+                            _cuda_stream(stream))
     if st:
         _check(st)
+    _attn_shapes[attn][4][plan] = step.n_tokens
 
 
 def pw_attn_append(attn, layer, step, k, v, stream=None):
     """k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last one."""
-    st = lib().pw_attn_append(attn, layer, step.address, *_rows(k), *_rows(v), _cuda_stream(stream))
+    _, h, d, _, _ = _attn_shapes[attn]
+    n = step.n_tokens
+    st = lib().pw_attn_append(attn, layer, step.address, *_rows(k, n, h, d), *_rows(v, n, h, d), _cuda_stream(stream))
     if st:
         _check(st)
 
@@ -608,9 +623,10 @@ def pw_attn_append(attn, layer, step, k, v, stream=None):
 def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, slopes=None, stream=None):
     """q and o: [n_tokens][n_heads][head_dim], any strides with a unit last one; scale defaults to
     1 / sqrt(head_dim)."""
-    st = lib().pw_attn_forward(attn, layer, plan, *_rows(q), *_rows(o), _addr(lse),
-                               q.shape[2] ** -0.5 if scale is None else scale, softcap, _addr(slopes),
-                               _cuda_stream(stream))
+    h, _, d, _, plans = _attn_shapes[attn]
+    n = plans.get(plan, 0)
+    st = lib().pw_attn_forward(attn, layer, plan, *_rows(q, n, h, d), *_rows(o, n, h, d), _addr(lse, n=n * h),
+                               d ** -0.5 if scale is None else scale, softcap, _addr(slopes, n=h), _cuda_stream(stream))
     if st:
         _check(st)
 

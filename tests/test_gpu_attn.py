@@ -469,3 +469,41 @@ def test_plan_refuses_more_work_than_it_can_count():
     torch.cuda.synchronize()
     s.compare()
     s.close()
+
+
+def test_refusals_of_tensors_that_do_not_fit():
+    """Tensors of another shape, type or device than the handle and the step ask for never reach a kernel."""
+    import torch
+    s = Step([20, 7], [2, 3], D=64)
+    pw = s.pw
+    s.map_and_append()
+    pw.pw_attn_plan(s.attn, 0, s.step)
+    o = torch.empty(s.N, s.Hq, s.D, dtype=s.dt, device="cuda")
+    lse = torch.empty(s.N, s.Hq, device="cuda")
+    i32 = torch.zeros(s.N, dtype=torch.int32, device="cuda")
+    wrong = [
+        lambda: pw.pw_attn_append(s.attn, 0, s.step, s.k[:-1], s.v),
+        lambda: pw.pw_attn_append(s.attn, 0, s.step, s.k, s.v[:, :1]),
+        lambda: pw.pw_attn_append(s.attn, 0, s.step, s.k.float(), s.v),
+        lambda: pw.pw_attn_append(s.attn, 0, s.step, s.k, s.v.cpu()),
+        lambda: pw.pw_attn_forward(s.attn, 0, 0, s.q[1:], o),
+        lambda: pw.pw_attn_forward(s.attn, 0, 0, s.q, o[..., :32]),
+        lambda: pw.pw_attn_forward(s.attn, 0, 0, s.q, o.float()),
+        lambda: pw.pw_attn_forward(s.attn, 0, 0, s.q, o, lse=lse[:-1]),
+        lambda: pw.pw_attn_forward(s.attn, 0, 0, s.q, o, lse=lse.double()),
+        lambda: pw.pw_attn_forward(s.attn, 0, 0, s.q, o, slopes=lse[0, :-1]),
+        lambda: pw.pw_attn_plan(s.attn, 0, s.step, doc_start=i32[1:]),
+        lambda: pw.pw_attn_plan(s.attn, 0, s.step, bidir_len=i32[:1]),
+        lambda: pw.pw_attn_bind(s.attn, 0, s.kv[0][1:], s.kv[1][1:]),
+        lambda: pw.pw_attn_bind(s.attn, 0, s.kv[0].float(), s.kv[1].float()),
+        lambda: pw.pw_make_step(i32[:2], i32[:1], s.table, s.q_start, s.kv_len, s.slot, s.pos, max_new=3),
+        lambda: pw.pw_make_step(i32[:2], i32[:2], s.table, s.q_start[:-1], s.kv_len, s.slot, s.pos, max_new=3),
+        lambda: pw.pw_make_step(i32[:2], i32[:2], s.table, s.q_start, s.kv_len, s.slot.int(), s.pos, max_new=3),
+        lambda: pw.pw_make_step(i32[:2], i32[:2], s.table.long(), s.q_start, s.kv_len, s.slot, s.pos, max_new=3),
+        lambda: pw.pw_make_step(i32[:2].cpu(), i32[:2], s.table, s.q_start, s.kv_len, s.slot, s.pos, max_new=3),
+    ]
+    for call in wrong:
+        with pytest.raises(ValueError):
+            call()
+    s.compare()
+    s.close()
