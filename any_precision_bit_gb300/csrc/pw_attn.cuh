@@ -9,7 +9,7 @@
 // A CTA (one to an SM) goes through its share of the units (a tile of 128 keys against a tile of query rows of one
 // key/value head, see AttnList).  Warps have roles: producers copy queries, keys and values to shared memory block by
 // block (TMA through the block table, 128-byte swizzle); one warp issues S = Q K^T and O += P V, S, P and O in tensor
-// memory (S and P share columns); softmax warps turn S into P, a lane a row; and a piece of a tile's keys ends in the
+// memory (S and P share columns); softmax warps turn S into P; and a piece of a tile's keys ends in the
 // result, or in a partial one that is added up with the others' (the last CTA to arrive, or attn_join_kernel).
 //
 // Memory bounds the few-row form: 64 rows of 4 behind 0.26 to 8 thousand keys move 1.13 GB in 172 to 178 us, 6.4 to
@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "pw_attn.h"
 #include "pw_device.cuh"
@@ -669,7 +670,8 @@ __device__ __forceinline__ float largest_magnitude(const float (&x)[N]) {
 // warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, with two special-function
 // operations for each score.  (tanh itself in one such operation is off by 2^-11: capped scores, and so
 // probabilities, would lose as much.)
-template <int N>
+// Scores are consecutive keys, or (PAIRS) pairs of them eight apart.
+template <int N, bool PAIRS = false>
 __device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool valid, float slope, float d0) {
   if (a.softcap > 0.f) {
     const float inv = a.inv_cap, cap2 = a.cap2;
@@ -699,7 +701,7 @@ __device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool
   }
   if (a.slopes) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)i), x[i]);
+    for (int i = 0; i < N; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)(PAIRS ? 8 * (i / 2) + i % 2 : i)), x[i]);
   }
 }
 
@@ -743,13 +745,32 @@ __device__ __forceinline__ void cap_exponents(const AttnArgs &a, float (&x)[N], 
     }
   }
 }
-// 32 scores to probabilities, packed, and their sum in pairs: 2^(x scale - m) (kPlain), 2^(x - m) (kGeneral), or 2^x of
+// The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8: until then the
+// accumulator stays untouched.  fp16 probabilities lie as high as its range allows, in 2^7 .. 2^15 for the largest, so
+// that what is 2^-21 of it still has all its bits and 2^-32 of it is not lost: many small ones behind a large one (of
+// a small value) make up the result.
+template <bool BF>
+constexpr float kAbove = BF ? 0.f : 7.f;
+
+// Zeros for the value of a key tile's key `thread`, where it lies outside [klo, khi).
+template <class C>
+__device__ __forceinline__ void hide_value(uint8_t *v, int thread, int base, int klo, int khi) {
+  if (base + thread < klo || base + thread >= khi) {
+#pragma unroll
+    for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4 *>(v + h * C::kHalfBytes + thread * 128 + 16 * i) = make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
+}
+// N scores to probabilities, packed, and their sum in pairs: 2^(x scale - m) (kPlain), 2^(x - m) (kGeneral), or 2^x of
 // exponents (kCapped).
-template <bool BF, int MODE>
-__device__ __forceinline__ void exponentials(const float *x, uint64_t scale, uint64_t neg_m, uint32_t (&pk)[16],
+template <bool BF, int MODE, int N>
+__device__ __forceinline__ void exponentials(const float *x, uint64_t scale, uint64_t neg_m, uint32_t (&pk)[N / 2],
                                              uint64_t (&sum)[2]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  for (int i = 0; i < N; i += 2) {
     float p, q;
     const uint64_t y = pair(x[i], x[i + 1]);
     unpair(MODE == kCapped ? y : MODE == kGeneral ? add2(y, neg_m) : fma2(y, scale, neg_m), p, q);
@@ -892,32 +913,26 @@ struct Group {
   }
 };
 
-template <int FORM, int DP, bool BF, int MODE>
+// kTwo: the softmax warps of two streams, which write their rows' results, too.
+template <int DP, bool BF, int MODE>
 __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
                        volatile int *abort_flag, volatile int *last_flag) {
-  using C = Cfg<FORM, DP>;
+  using C = Cfg<kTwo, DP>;
   using B = Bars<C::kStages>;
   constexpr int NS = C::NS;
-  constexpr bool SP = FORM == kSpread;
-  constexpr int NC = SP ? 32 : 128;  // scores of a key tile that a thread takes
+  constexpr int NC = 128;  // scores of a key tile that a thread takes
   // Of which this many at a time.  Capped and biased scores go through tensor memory once more, in two halves:
   // all 128 at a time their arithmetic spilled registers and filled the instruction cache (chunks-docs-cap
   // 70.7 us, in halves 67.9); plain scores lose more by the second read (prompt-8192 413 us, in halves 444).
-  constexpr int CH = SP ? 32 : MODE != kPlain ? 64 : 128;
+  constexpr int CH = MODE != kPlain ? 64 : 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = warp >> 2, quarter = warp & 3, thread = 32 * quarter + lane;
-  const int row = SP ? lane : thread, col0 = SP ? 32 * quarter : 0;
+  const int row = thread;
   const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
   uint32_t it = 0;        // key tiles of this stream so far
   Ring<C::kStages> rv;    // the current tile's V
   rv.next();
-  // kSpread: P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked
-  // the tile before on the same barrier is known to be complete (the scores of tile t or t + 1 were issued
-  // behind it) and the one after waits for this thread, so the parity cannot be mistaken.
-  auto product_done = [&](uint32_t t) {
-    return wait_for_all(bars + 8 * (B::kOD + (t & 1)), (t >> 1) & 1, abort_flag, a);
-  };
-  uint32_t o_done = 0;    // kTwo: pieces of this stream so far
+  uint32_t o_done = 0;    // pieces of this stream so far
   Group<C::kStages> group{bars, s, 0, abort_flag};
   constexpr int kPart = DP * 128;
   auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
@@ -940,7 +955,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const int ntok = min(a.list.tpt, w.ntok - s * a.list.tpt), nrows = ntok * a.G;
     rb = rb_ahead;
     const uint32_t dn = (pieces + 1) % kPieces;
-    if (!SP && ntok <= 0) {
+    if (ntok <= 0) {
       for (int i = 0; i < 2 * n; ++i) rv.next();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
@@ -950,37 +965,27 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     }
     const bool valid = row < nrows;
     const int klo = w.klo, khi = w.khi, lo = max(rb.lo, klo), hi = min(rb.hi, khi);
-    const bool active = SP || 32 * quarter < nrows;
+    const bool active = 32 * quarter < nrows;
     const float slope = MODE == kGeneral && a.slopes && valid ? a.slopes[w.head * a.G + row_h] * kLog2e : 0.f;
-    const uint32_t tmem_o = tmem + 256 + 128 * (SP ? pieces & 1 : (uint32_t)s) + lanes;
+    const uint32_t tmem_o = tmem + 256 + 128 * (uint32_t)s + lanes, ts = tmem + 128 * (uint32_t)s + lanes;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
-      const uint32_t buf = !SP ? (uint32_t)s : (it & 1);
-      const uint32_t par = !SP ? (it & 1) : ((it >> 1) & 1);
-      const uint32_t ts = tmem + 128 * buf + lanes;
       const int base = (first + j) * kAttnKeys;
-      if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), par, abort_flag, a))) break;
+      if (!(ok = wait_for_all(bars + 8 * (B::kSF + s), it & 1, abort_flag, a))) break;
       tc_fence_after();
       if (s == 0 && (base < klo || base + kAttnKeys > khi)) {
         // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
         // times what the memory holds may be NaN
         if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
-        if (base + thread < klo || base + thread >= khi) {
-          uint8_t *vrow = smp + (NS + rv.st) * C::kTileBytes + thread * 128;
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(vrow + h * C::kHalfBytes + 16 * i) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
+        hide_value<C>(smp + (NS + rv.st) * C::kTileBytes, thread, base, klo, khi);
       }
       if (active) {
-        const int l0 = lo - base - col0, h0 = hi - base - col0;
+        const int l0 = lo - base, h0 = hi - base;
         const bool edge = __any_sync(0xffffffffu, valid && (l0 > 0 || h0 < NC));
         float x[CH], mx = -INFINITY;
         auto load = [&](int c) {
 #pragma unroll
-          for (int i = 0; i < CH; i += 32) tmem_ld32(ts + col0 + c + i, reinterpret_cast<uint32_t *>(x) + i);
+          for (int i = 0; i < CH; i += 32) tmem_ld32(ts + c + i, reinterpret_cast<uint32_t *>(x) + i);
           tmem_wait_ld();
         };
         float top = 0.f;
@@ -990,7 +995,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           // (hidden scores, which may come from unwritten memory, have no say in how the tile's are capped)
           if (MODE != kPlain && edge && a.softcap > 0.f) mask_out<CH>(x, l0 - c, h0 - c, 0.f);
           if (MODE == kCapped) top = fmaxf(top, largest_magnitude(x));
-          if (MODE == kGeneral) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - col0 - c));
+          if (MODE == kGeneral) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - c));
           if (edge) mask_out<CH>(x, l0 - c, h0 - c, -INFINITY);
           mx = fmaxf(mx, max_of<CH>(x));
           if (MODE == kGeneral && CH < NC) {
@@ -1003,21 +1008,12 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         if (MODE == kPlain) mx *= a.scale2;
         if (MODE == kCapped) mx = mx == -INFINITY ? mx : cap_one(a, mx, wide);
         if (!valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
-        // The maximum subtracted from the scores is renewed only when it has grown by a factor of 2^8: until then
-        // the accumulator stays untouched.  fp16 probabilities lie as high as its range allows, in 2^7 .. 2^15 for
-        // the largest, so that what is 2^-21 of it still has all its bits and 2^-32 of it is not lost: many small
-        // ones behind a large one (of a small value) make up the result.
-        constexpr float kAbove = BF ? 0.f : 7.f;
-        mx -= kAbove;
+        mx -= kAbove<BF>;
         if (j == 0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-          // kTwo: these scores were issued behind the product before, which is therefore done.
+          // (these scores were issued behind the product before, which is therefore done)
           const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2(m - mn);
-          if (SP) {
-            if (!(ok = product_done(it - 1))) break;
-            tc_fence_after();
-          }
           m = mn;
           l *= f;
 #pragma unroll 1
@@ -1043,17 +1039,9 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 #pragma unroll
           for (int c = 0; c < CH / 32; ++c) {
             uint32_t pk[16];
-            exponentials<BF, MODE>(x + 32 * c, scale, neg_m, pk, sum);
-            if (SP) {
-              const uint32_t none[16] = {};
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (q != quarter) tmem_st16(ts + 16 * q, none);
-              tmem_st16(ts + 16 * quarter, pk);
-            } else {
-              tmem_st16(ts + c0 / 2 + 16 * c, pk);
-            }
-            if (!SP && c0 / 16 + 2 * (c + 1) == kEarly) {
+            exponentials<BF, MODE, 32>(x + 32 * c, scale, neg_m, pk, sum);
+            tmem_st16(ts + c0 / 2 + 16 * c, pk);
+            if (c0 / 16 + 2 * (c + 1) == kEarly) {
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
@@ -1065,30 +1053,18 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
         tmem_wait_st();
-      } else if (!SP && lane == 0) {
+      } else if (lane == 0) {
         mbar_arrive(bars + 8 * (B::kPE + s));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (B::kPF + buf));
+      if (lane == 0) mbar_arrive(bars + 8 * (B::kPF + s));
     }
     if (!ok) break;
     // the next piece has been handed over: its first scores may be on their way
     if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
     rb_ahead = bound_of(piece[dn]);
-    if constexpr (SP) {  // the rest is the finishing warps' work
-      const uint32_t ob = pieces & 1;
-      float2 *ml = reinterpret_cast<float2 *>(smp + C::kScratchAt + 4 * kJoinRows * C::kScratchRow * 4) + ob * 4 * 32;
-      if (!(ok = wait_for_all(bars + 8 * (B::kOE + ob), ((pieces >> 1) & 1) ^ 1, abort_flag, a))) break;
-      ml[thread] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + 8 * (B::kML + ob));
-        mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
-      }
-      continue;
-    }
-    // kTwo: the piece's last product
+    // the piece's last product
     if (!(ok = wait_for_all(bars + 8 * (B::kOD + s), o_done++ & 1, abort_flag, a))) break;
     tc_fence_after();
     if (a.after_prefix) pdl_wait();  // (returns at once but the first time)
@@ -1179,6 +1155,200 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+  }
+}
+
+// kSpread: the softmax warps.  A quarter's 16 rows by its 32 keys lie over its warp as the tensor cores' fragments:
+// thread t holds eight scores of row t / 4 and, where a tile has more than eight rows, eight of the row eight
+// below.  (A lane a row, half of a warp's lanes or more would have nothing to do.)  Four threads share a row: its
+// maximum is made common to them when it is renewed, which each of them may ask for, and its sum at a piece's end.
+template <int DP, bool BF, int MODE>
+__device__ void soften_few(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
+                           volatile int *abort_flag) {
+  using C = Cfg<kSpread, DP>;
+  using B = Bars<C::kStages>;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, thread = 32 * quarter + lane;
+  const int col0 = 32 * quarter + 2 * (lane & 3);  // this thread's keys: col0 + 8 k and the one after, k = 0 .. 3
+  const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+  uint32_t it = 0, pieces = 0;  // key tiles, pieces so far
+  Ring<C::kStages> rv;          // the current tile's V
+  rv.next();
+  // P V of key tile t is complete.  Even and odd tiles have a barrier each: when this is asked the tile before on
+  // the same barrier is known to be complete (the scores of tile t or t + 1 were issued behind it) and the one after
+  // waits for this thread, so the parity cannot be mistaken.
+  auto product_done = [&](uint32_t t) {
+    return wait_for_all(bars + 8 * (B::kOD + (t & 1)), (t >> 1) & 1, abort_flag, a);
+  };
+  int row_t[2], row_h[2];  // the rows' tokens in their tile, and heads
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = lane / 4 + 8 * h;
+    row_t[h] = over_g(a, row);
+    row_h[h] = row - row_t[h] * a.G;
+  }
+  bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
+  RowBound rb[2] = {{0, 0, -1, 0}, {0, 0, -1, 0}}, ahead[2] = {{0, 0, -1, 0}, {0, 0, -1, 0}};
+  // the rows' keys in a piece, fetched while the piece before is in work
+  auto fetch = [&](const volatile Piece &x) {
+    const bool fresh = x.n != 0 && x.fresh;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ahead[h] = rb[h];
+      if (fresh) ahead[h] = row_t[h] < x.ntok ? a.bounds[x.tok0 + row_t[h]] : RowBound{0, 0, -1, 0};
+    }
+  };
+  if (ok) fetch(piece[0]);
+  for (; ok; ++pieces) {
+    const volatile Piece &w = piece[pieces % kPieces];
+    const int n = w.n, first = w.first;
+    if (n == 0) break;
+    const int ntok = w.ntok, klo = w.klo, khi = w.khi;
+    const bool both = ntok * a.G > 8;
+    bool valid[2];
+    int lo[2], hi[2];
+    float slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      rb[h] = ahead[h];
+      valid[h] = row_t[h] < ntok;
+      lo[h] = max(rb[h].lo, klo);
+      hi[h] = min(rb[h].hi, khi);
+      slope[h] = MODE == kGeneral && a.slopes && valid[h] ? a.slopes[w.head * a.G + row_h[h]] * kLog2e : 0.f;
+    }
+    const uint32_t tmem_o = tmem + 256 + 128 * (pieces & 1) + lanes;
+    // The scores s of a key tile, of the first eight rows or of all sixteen.
+    auto tile = [&](auto rows, const uint32_t (&sc)[16], uint32_t ts, int base, bool begins) {
+      constexpr int H = decltype(rows)::value;
+      float x[H][8], mx[H];
+      uint32_t seen[H];  // bits 8 k + e: this thread's keys that the row sees
+      bool edge = false, wide = false;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[h][i] = __uint_as_float(sc[4 * (i / 2) + 2 * h + i % 2]);
+        const int l0 = lo[h] - base - 32 * quarter, h0 = hi[h] - base - 32 * quarter;
+        const int from = min(max(l0, 0), 32), to = min(max(h0, 0), 32);
+        const uint32_t below_to = to == 32 ? 0xffffffffu : (1u << to) - 1u;
+        const uint32_t below_from = from == 32 ? 0xffffffffu : (1u << from) - 1u;
+        seen[h] = (below_to & ~below_from) >> (2 * (lane & 3));
+        edge = edge || (valid[h] && (l0 > 0 || h0 < 32));
+      }
+      edge = __any_sync(0xffffffffu, edge);
+      auto hide = [&](int h, float value) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[h][i] = seen[h] >> (8 * (i / 2) + i % 2) & 1u ? x[h][i] : value;
+      };
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        // (hidden scores, which may come from unwritten memory, have no say in how the tile's are capped)
+        if (MODE != kPlain && edge && a.softcap > 0.f) hide(h, 0.f);
+        if (MODE == kCapped) wide = wide || (valid[h] && !(largest_magnitude(x[h]) * a.inv_cap <= 0.5f));
+        if (MODE == kGeneral) transform<8, true>(a, x[h], valid[h], slope[h], (float)(rb[h].pos - base - col0));
+        if (edge) hide(h, -INFINITY);
+        mx[h] = max_of(x[h]);
+      }
+      if (MODE == kCapped) wide = __any_sync(0xffffffffu, wide);
+      bool grown = false;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        if (MODE == kPlain) mx[h] *= a.scale2;
+        if (MODE == kCapped) mx[h] = mx[h] == -INFINITY ? mx[h] : cap_one(a, mx[h], wide);
+        mx[h] -= kAbove<BF>;
+        if (!valid[h]) mx[h] = -INFINITY;  // rows of nobody: no rescaling on their account
+        grown = grown || mx[h] > m[h] + 8.f;
+      }
+      if (begins || __any_sync(0xffffffffu, grown)) {
+        float f[2] = {1.f, 1.f};
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+          const float mn = fmaxf(m[h], mx[h]);
+          f[h] = mn == -INFINITY ? 1.f : ex2(m[h] - mn);
+          m[h] = mn;
+          l[h] *= f[h];
+        }
+        if (!begins) {
+          if (!(ok = product_done(it - 1))) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[16];
+            tmem_ld_16x32(tmem_o + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i / 2 % 2]);
+            tmem_st_16x32(tmem_o + 32 * c, o);
+          }
+        }
+      }
+      uint32_t p[8] = {};
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const float ms = m[h] == -INFINITY ? 0.f : m[h];
+        if (MODE == kCapped) {
+          cap_exponents<8>(a, x[h], wide, ms);
+          if (edge) hide(h, -INFINITY);
+        }
+        uint32_t pk[4];
+        uint64_t sum[2] = {0, 0};
+        exponentials<BF, MODE, 8>(x[h], pair(a.scale2, a.scale2), pair(-ms, -ms), pk, sum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[2 * i + h] = pk[i];
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l[h] += s0 + s1;
+      }
+      const uint32_t none[8] = {};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q != quarter) tmem_st_16x16(ts + 16 * q, none);
+      tmem_st_16x16(ts + 16 * quarter, p);
+      tmem_wait_st();
+    };
+    for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
+      const uint32_t buf = it & 1, ts = tmem + 128 * buf + lanes;
+      const int base = (first + j) * kAttnKeys;
+      if (!(ok = wait_for_all(bars + 8 * (B::kSF + buf), (it >> 1) & 1, abort_flag, a))) break;
+      tc_fence_after();
+      if (base < klo || base + kAttnKeys > khi) {
+        // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
+        // times what the memory holds may be NaN
+        if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
+        hide_value<C>(smp + (1 + rv.st) * C::kTileBytes, thread, base, klo, khi);
+        __syncwarp();
+      }
+      uint32_t sc[16];
+      tmem_ld_16x32(ts + 32 * quarter, sc);
+      tmem_wait_ld();
+      if (both)
+        tile(std::integral_constant<int, 2>{}, sc, ts, base, j == 0);
+      else
+        tile(std::integral_constant<int, 1>{}, sc, ts, base, j == 0);
+      if (!ok) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (B::kPF + buf));
+    }
+    if (!ok) break;
+    // the next piece has been handed over: its first scores may be on their way
+    const uint32_t dn = (pieces + 1) % kPieces;
+    if (!(ok = wait_for_all(bars + 8 * (B::kDF + dn), ((pieces + 1) / kPieces) & 1, abort_flag, a))) break;
+    fetch(piece[dn]);
+    const uint32_t ob = pieces & 1;  // the rest is the finishing warps' work
+    float2 *ml = reinterpret_cast<float2 *>(smp + C::kScratchAt + 4 * kJoinRows * C::kScratchRow * 4) + ob * 4 * 32;
+    if (!(ok = wait_for_all(bars + 8 * (B::kOE + ob), ((pieces >> 1) & 1) ^ 1, abort_flag, a))) break;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if ((lane & 3) == 0) ml[32 * quarter + lane / 4 + 8 * h] = make_float2(m[h], l[h]);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bars + 8 * (B::kML + ob));
+      mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+    }
   }
 }
 
@@ -1579,7 +1749,12 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   if (!a.after_prefix) pdl_wait();
   if (warp < C::kSoftWarps) {
     if (FORM == kTwo) regs_inc<kRegsSoft>();
-    if (!abort_flag) soften<FORM, DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+    if (!abort_flag) {
+      if constexpr (FORM == kSpread)
+        soften_few<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag);
+      else
+        soften<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+    }
   } else if (warp < C::kProdWarp) {
     if constexpr (FORM == kSpread) {
       if (!abort_flag) finish<DP, BF>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
