@@ -23,6 +23,14 @@ namespace {
 // 32000 with two 32 and 16, with four 28 and 21; with eight (8 pieces by this count) behind 517 10.9 and 12.4.
 constexpr int kJoinTwo = 2, kJoinSpread = 16;
 
+// Where heads stand side by side in a cache and do not fill 256 bytes, a copy that has L2 fetch 256 bytes brings part of
+// the next head, too, whose turn on this SM comes a whole row of keys later.  While all SMs' keys of a head fit into
+// this many bytes of L2 that is a gain; beyond, most of it is fetched twice and 64 bytes are better.  Measured, 80
+// requests of 16 heads of 64 and a window (us, 256 and 64 bytes): 300 keys 46 and 49, 1024 (40 MB) 94 and 97, 1500
+// (58 MB) 130 and 124, 4096 339 and 275; 8 heads of 96: 300 keys 42 and 42, 1024 (60 MB) 87 and 77, 3000 212 and 162.
+// Rows of 256 bytes, or heads outermost: both alike (8 heads of 128 212 and 214).
+constexpr int64_t kReuseBytes = 48 << 20;
+
 pw_status bad(const char *msg) { return report(nullptr, PW_ERR_INVALID, msg); }
 pw_status cuda_failed(const char *what, int e) {
   cudaGetLastError();
@@ -34,7 +42,7 @@ pw_status cuda_failed(const char *what, int e) {
 // Tensor map of 16-bit elements with the 128-byte swizzle: dim[0] contiguous, the others `stride` elements
 // apart, boxes of box[] elements (64 along dim 0); what lies outside reads as zeros.
 bool encode_map(TmaDesc *out, const void *base, int rank, const cuuint64_t *dim, const int64_t *stride,
-                const cuuint32_t *box) {
+                const cuuint32_t *box, CUtensorMapL2promotion fetch = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -54,19 +62,20 @@ bool encode_map(TmaDesc *out, const void *base, int rank, const cuuint64_t *dim,
   for (int i = 0; i + 1 < rank; ++i) bytes[i] = (cuuint64_t)stride[i] * 2;
   return fn(reinterpret_cast<CUtensorMap *>(out), CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank,
             const_cast<void *>(base), dim, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_SWIZZLE_128B, fetch,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Layer {
   uint16_t *k = nullptr, *v = nullptr;
-  TmaDesc map_k, map_v;
+  TmaDesc map_k[2], map_v[2];  // L2 fetches 256 bytes, or 64 (see kReuseBytes)
   int64_t block_stride = 0, token_stride = 0, head_stride = 0;
 };
 
 struct Plan {
   bool set = false;
   pw_kv_step step{};
+  int64_t reach = 0;           // keys that a row sees at most
   RowBound *bounds = nullptr;  // [max_tokens]
   AttnList requests{}, groups{};
 };
@@ -239,12 +248,13 @@ pw_status pw_attn_bind(pw_attn *a, int layer, void *k, void *v, int64_t block_st
                              (cuuint64_t)d.n_blocks};
   const int64_t stride[3] = {token_stride, head_stride, block_stride};
   const cuuint32_t box[4] = {64, (cuuint32_t)d.block_tokens, 1, 1};
-  TmaDesc map_k, map_v;
-  if (!encode_map(&map_k, k, 4, dim, stride, box) || !encode_map(&map_v, v, 4, dim, stride, box))
-    return bad("no tensor map can describe this cache (address or strides)");
-  Layer &l = a->layers[(size_t)layer];
-  l.map_k = map_k;
-  l.map_v = map_v;
+  Layer n = a->layers[(size_t)layer], &l = a->layers[(size_t)layer];
+  for (int i = 0; i < 2; ++i) {
+    const auto fetch = i ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    if (!encode_map(&n.map_k[i], k, 4, dim, stride, box, fetch) || !encode_map(&n.map_v[i], v, 4, dim, stride, box, fetch))
+      return bad("no tensor map can describe this cache (address or strides)");
+  }
+  l = n;
   l.k = static_cast<uint16_t *>(k);
   l.v = static_cast<uint16_t *>(v);
   l.block_stride = block_stride;
@@ -326,6 +336,7 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
     return bad("table_stride is too long for this many tokens (2^31 key tiles or more)");
   OnDevice dev(a->d.device);
   Plan &p = a->plans[(size_t)plan];
+  p.reach = std::min((int64_t)s->table_stride * a->d.block_tokens, window ? (int64_t)window + s->max_new : INT64_MAX);
   p.requests = requests;
   p.groups = groups;
   g.bounds = p.bounds;
@@ -437,8 +448,10 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.counters = a->counters;
   g.ctas = a->sm_count;
   AttnMaps maps;
-  maps.k = l.map_k;
-  maps.v = l.map_v;
+  const bool apart = l.token_stride != g.D && g.D % 128;
+  const int fetch = apart && p.reach * g.D * 4 * a->sm_count > kReuseBytes;
+  maps.k = l.map_k[fetch];
+  maps.v = l.map_v[fetch];
   const cuuint64_t dim[3] = {(cuuint64_t)g.D, (cuuint64_t)g.Hq, (cuuint64_t)g.n_tokens};
   const int64_t stride[2] = {q_head, q_token};
   auto launch = [&](const AttnList &list) -> pw_status {
