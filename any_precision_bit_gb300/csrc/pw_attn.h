@@ -18,8 +18,8 @@ constexpr int kAttnMaxRequests = 4096;
 //   kSpread  one tile of at most 16 rows, which is held four times, once in each lane quarter of tensor
 //            memory: quarter w keeps a softmax over keys 32 w .. 32 w + 31 of every key tile (its
 //            probabilities of the other keys are zeros), and the four results are added at the end.  Four
-//            warps then share the few rows (eight or sixteen scores a thread), the scores of the next key tile are computed during a
-//            softmax, and four more warps finish a piece during the next.
+//            warps then share the few rows (eight or sixteen scores a thread), the scores of the next key
+//            tile are computed during a softmax, and four more warps finish a piece during the next.
 // Measured with one form and the other, 64 requests (us, launch included): 4 rows behind 256 .. 8192 keys 189 in
 // kSpread and 201 in kTwo, behind 16 .. 700 keys 36 and 46; 4 rows of 64 with capped scores behind up to 4096
 // keys 126 and 249; 16 rows behind as many 111 and 120; 32 rows, where kSpread has no second query buffer, 65 and 64.
