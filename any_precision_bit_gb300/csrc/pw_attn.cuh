@@ -219,11 +219,11 @@ struct Walk {
   int j0, n;  // first key tile of this piece within the tile's, and their number
   int2 first_ctas, last_ctas;  // see AttnStart
   bool fresh; // the tile is another than the last piece's
-  __device__ __forceinline__ explicit Walk(const AttnArgs &a) {
+  __device__ __forceinline__ Walk(const AttnArgs &a, bool fits) {
     const AttnStart *s = a.list.start + blockIdx.x;
     const int4 x = *reinterpret_cast<const int4 *>(s);
     t = load_tile(&s->t);
-    tile = x.x, head = x.y, off = x.z, left = x.w;
+    tile = x.x, head = x.y, off = x.z, left = fits ? x.w : 0;
     first_ctas = s->first, last_ctas = s->last;
     cost = a.list.piece_cost;
     fresh = true;
@@ -263,6 +263,15 @@ struct Walk {
     *p = Piece{n, first(), head, t.tok0, t.ntok, t.trow, t.klo, t.khi, fresh, t.merge && !a.to_prefix, c.x, c.y};
   }
 };
+
+// The plan on the device is the one that this launch was made for.
+__device__ __forceinline__ bool plan_fits(const AttnArgs &a) {
+  const int4 x = reinterpret_cast<const int4 *>(a.planned)[0], y = reinterpret_cast<const int4 *>(a.planned)[1];
+  const AttnShape &s = a.shape;
+  const uint64_t table = (uint64_t)(uint32_t)y.z | (uint64_t)(uint32_t)y.w << 32;
+  return x.x == s.tpt && x.y == s.streams && x.z == s.group_tpt && x.w == s.group_streams && y.x == s.n_tokens &&
+         y.y == s.table_stride && table == reinterpret_cast<uint64_t>(s.table);
+}
 
 // Position in the ring of K/V stages.
 template <int STAGES>
@@ -306,7 +315,14 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   Ring<C::kStages> r;
   if (kv) r.next();
   const int first_id = a.list.start[blockIdx.x].ids[page];
-  Walk w(a);
+  // (where the plan does not fit there are no pieces, and the other warps find none)
+  const bool fits = plan_fits(a);
+  Walk w(a, fits);
+  if (!fits && leads) {
+    if (a.after_prefix) pdl_wait();  // as every launch before its end
+    if (lane == 0) atomicOr(a.err, kAttnErrPlan);
+    __syncwarp();
+  }
   bool ok = true;
   // the block of this lane's box of a key tile; -1: none of its keys counts
   auto block_of = [&](const AttnTile &t, int kt, bool at_start = false) {
@@ -1592,6 +1608,7 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
   __shared__ float2 sum_ml[kShare][kRows];
   pdl_trigger();
   pdl_wait();
+  if (!plan_fits(a)) return;  // (reported by attn_kernel)
   const int streams = FORM == kTwo ? 2 : 1, share = threadIdx.x / kRows, row = threadIdx.x % kRows, row_t = over_g(a, row), row_h = row - row_t * a.G;
   const int n = a.list.meta[2] * streams * kCols;
 #pragma unroll 1

@@ -33,7 +33,20 @@ enum {
   kAttnErrTokens = 4,  // new tokens beyond n_tokens
   kAttnErrIds = 8,     // fewer new ids than opened blocks
   kAttnErrBlock = 16,  // a block id or a table row out of range
+  kAttnErrPlan = 32,   // a forward met a plan of another shape than it was launched for
 };
+
+// What a forward's launch takes from the plan by value, beside the lists that lie on the device.  The plan's
+// kernels leave it beside the lists; a launch that finds another one there (a captured forward replayed after the
+// plan was laid out again, or a captured plan that has not been replayed) would read past its tiles, the rows of
+// q and o or the table, so it writes nothing and reports kAttnErrPlan.
+struct alignas(16) AttnShape {
+  int tpt, streams;              // of the requests' list (streams 0: never laid out)
+  int group_tpt, group_streams;  // of the groups' (0: no groups)
+  int n_tokens, table_stride;
+  const int *table;
+};
+static_assert(sizeof(AttnShape) == 32, "two 16-byte loads");
 
 // Keys a row may see, and where: [lo, hi) of table row trow (-1: none), at position pos.
 struct RowBound {
@@ -91,6 +104,7 @@ struct PlanArgs {
   RowBound *bounds;
   AttnList list;
   int of_groups;  // the list of the groups' shared prefixes, not of the requests
+  AttnShape shape, *shape_out;  // left by the kernel that lays out the requests' list, the plan's last
   int ctas, n_kv_heads;
 };
 
@@ -122,6 +136,8 @@ struct AttnMaps {
 struct AttnArgs {
   const RowBound *bounds;
   AttnList list;
+  AttnShape shape;           // as launched
+  const AttnShape *planned;  // as laid out
   int ctas, device;
   const int *table;
   int table_stride, n_tokens, n_blocks, log_bt;

@@ -77,7 +77,17 @@ struct Plan {
   pw_kv_step step{};
   int64_t reach = 0;           // keys that a row sees at most
   RowBound *bounds = nullptr;  // [max_tokens]
+  AttnShape *shape = nullptr;  // as laid out on the device
   AttnList requests{}, groups{};
+
+  AttnShape launch_shape() const {
+    AttnShape s{requests.tpt, requests.streams, 0, 0, step.n_tokens, step.table_stride, step.table};
+    if (step.n_groups) {
+      s.group_tpt = groups.tpt;
+      s.group_streams = groups.streams;
+    }
+    return s;
+  }
 };
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -165,7 +175,7 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
          alloc(a, &a->prefix_lse, (size_t)d.max_shared_tokens * d.n_heads);
   // a tile holds a token at least, but the last of each segment may be short: requests and the padding, or groups
   for (Plan &p : a->plans) {
-    ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens);
+    ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens) && alloc(a, &p.shape, 1);
     for (AttnList *l : {&p.requests, &p.groups}) {
       if (l == &p.groups && d.max_shared_tokens == 0) continue;
       if (l == &p.groups) {
@@ -182,6 +192,8 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   if (!ok) return report(nullptr, PW_ERR_OOM, "device memory exhausted");
   if ((e = cudaMemset(a->err, 0, sizeof(int))) || (e = cudaMemset(a->counters, 0, 2 * ctas * sizeof(int))))
     return cuda_failed("cudaMemset", e);
+  for (Plan &p : a->plans)
+    if ((e = cudaMemset(p.shape, 0, sizeof(AttnShape)))) return cuda_failed("cudaMemset", e);
   if ((e = cudaDeviceSynchronize())) return cuda_failed("cudaDeviceSynchronize", e);
   return PW_OK;
 }
@@ -337,9 +349,13 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   OnDevice dev(a->d.device);
   Plan &p = a->plans[(size_t)plan];
   p.reach = std::min((int64_t)s->table_stride * a->d.block_tokens, window ? (int64_t)window + s->max_new : INT64_MAX);
+  p.set = false;
   p.requests = requests;
   p.groups = groups;
+  p.step = *s;
   g.bounds = p.bounds;
+  g.shape = p.launch_shape();
+  g.shape_out = p.shape;
   int e = launch_attn_bounds(g, stream);
   if (!e && s->n_groups) {
     g.of_groups = 1;
@@ -350,7 +366,6 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   g.list = p.requests;
   if (!e) e = launch_attn_list(g, stream);
   if (e) return cuda_failed("pw_attn_plan launch", e);
-  p.step = *s;
   p.set = true;
   return PW_OK;
 }
@@ -406,6 +421,8 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   OnDevice dev(a->d.device);
   AttnArgs g{};
   g.bounds = p.bounds;
+  g.shape = p.launch_shape();
+  g.planned = p.shape;
   g.table = p.step.table;
   g.table_stride = p.step.table_stride;
   g.n_tokens = p.step.n_tokens;
@@ -503,11 +520,14 @@ pw_status pw_attn_check(pw_attn *a, pw_stream stream) {
       (e = cudaStreamSynchronize(st)))
     return cuda_failed("cudaMemsetAsync", e);
   if (bits & kAttnErrWait) return report(nullptr, PW_ERR_TIMEOUT, "a bounded device wait expired; outputs are invalid");
-  char buf[256];
-  snprintf(buf, sizeof buf, "pw_kv_map found:%s%s%s%s", bits & kAttnErrLen ? " a length out of range;" : "",
+  char buf[384];
+  snprintf(buf, sizeof buf, "%s%s%s%s%s%s", bits & ~kAttnErrPlan ? "pw_kv_map found:" : "",
+           bits & kAttnErrLen ? " a length out of range;" : "",
            bits & kAttnErrTokens ? " more new tokens than n_tokens;" : "",
            bits & kAttnErrIds ? " fewer new ids than opened blocks;" : "",
-           bits & kAttnErrBlock ? " a block id or table row out of range;" : "");
+           bits & kAttnErrBlock ? " a block id or table row out of range;" : "",
+           bits & kAttnErrPlan ? " a forward's plan is laid out for other tile sizes, n_tokens, table or groups than it was "
+                                 "launched with: it wrote nothing" : "");
   return report(nullptr, PW_ERR_STATE, buf);
 }
 

@@ -335,7 +335,10 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     a.list.start[c] = st;
   }
   __syncthreads();
-  if (tid == 0) a.list.meta[2] = n_splits;
+  if (tid == 0) {
+    a.list.meta[2] = n_splits;
+    if (!a.of_groups) *a.shape_out = a.shape;
+  }
 }
 
 int launch_attn_list(const PlanArgs &a, void *stream) {

@@ -549,6 +549,10 @@ pw_status pw_kv_map(pw_attn *a, const pw_kv_step *step, const int32_t *new_ids, 
  * (NULL: none): position in its request at which the row's document begins, for packed documents.
  * bidir_len [R] (NULL: none): keys below it are seen by every row of the request.  The plan holds for every
  * layer of the step with this mask, until the next pw_attn_plan into it; step's table must stay valid.
+ * A captured pw_attn_forward may be replayed after its plan was laid out again with the same max_new, n_tokens, table,
+ * table_stride and presence of groups, and follows the new lengths and masks.  After one with others (as far as they
+ * change the tiles), or while a captured pw_attn_plan has not been replayed, it writes nothing and pw_attn_check
+ * reports PW_ERR_STATE.
  * PW_ERR_INVALID also where table_stride and n_tokens allow for 2^31 or more key tiles of 128 over all tiles of
  * rows (a tile is 256 / (n_heads / n_kv_heads) tokens of a request, or max_new where that is less). */
 pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *step, int window, const int32_t *doc_start,
@@ -572,7 +576,8 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
  * give up after about n microseconds (0: the default, about 2 s).  PW_ERR_INVALID for another kind or n < 0. */
 pw_status pw_attn_set_fault(pw_attn *a, int kind, int n);
 /* Wait for `stream` and report what the handle's calls found since the last check: PW_ERR_TIMEOUT if a
- * bounded device wait expired, PW_ERR_STATE for the findings of pw_kv_map (message in pw_last_error(NULL)).
+ * bounded device wait expired, PW_ERR_STATE for the findings of pw_kv_map and for a forward whose plan was laid out
+ * anew for another shape (message in pw_last_error(NULL)).
  * Clears what it reports. */
 pw_status pw_attn_check(pw_attn *a, pw_stream stream);
 
