@@ -314,7 +314,6 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   uint32_t tiles = 0, pieces = 0;
   Ring<C::kStages> r;
   if (kv) r.next();
-  const int first_id = a.list.start[blockIdx.x].ids[page];
   // (where the plan does not fit there are no pieces, and the other warps find none)
   const bool fits = plan_fits(a);
   Walk w(a, fits);
@@ -325,16 +324,16 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   }
   bool ok = true;
   // the block of this lane's box of a key tile; -1: none of its keys counts
-  auto block_of = [&](const AttnTile &t, int kt, bool at_start = false) {
+  auto block_of = [&](const AttnTile &t, int kt) {
     const int key0 = kt * kAttnKeys + page * bt;
     if (!mine || key0 >= t.khi || key0 + bt <= t.klo) return -1;
     const int p = key0 >> a.log_bt;
-    int id = at_start ? first_id : -1;
-    if (!at_start && t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)t.trow * a.table_stride + p];
+    int id = -1;
+    if (t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)t.trow * a.table_stride + p];
     return id >= 0 && id < a.n_blocks ? id : a.n_blocks;  // out of the map's range: zeros
   };
   bool more = w.load();
-  int id = more ? block_of(w.t, w.first(), true) : -1;
+  int id = more ? block_of(w.t, w.first()) : -1;
   // hand over piece `i`, the one the walk is at (or the end)
   auto publish = [&](uint32_t i) {
     const uint32_t d = i % kPieces;

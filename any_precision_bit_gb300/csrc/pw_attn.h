@@ -70,7 +70,6 @@ struct AttnStart {
   // CTAs of the first and the last key tile of the (tile, head) that the CTA begins in, and of the one that it
   // ends in
   int2 first, last;
-  int ids[8];              // table entries of its first key tile (16-token blocks have eight)
 };
 
 // A (tile, head) that is split among the CTAs c0 .. c1, c1 > c0.
@@ -96,7 +95,7 @@ struct AttnList {
 
 struct PlanArgs {
   int R, n_tokens, table_rows, table_stride, bt;
-  const int *ctx_len, *rows, *q_start, *kv_len, *table;
+  const int *ctx_len, *rows, *q_start, *kv_len;
   const int *doc_start, *bidir_len;
   int window;
   int n_groups;

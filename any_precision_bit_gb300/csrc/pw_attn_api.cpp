@@ -313,7 +313,6 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, co
   g.table_stride = s->table_stride;
   g.bt = a->d.block_tokens;
   g.ctx_len = s->ctx_len;
-  g.table = s->table;
   g.rows = s->rows;
   g.q_start = s->q_start;
   g.kv_len = s->kv_len;

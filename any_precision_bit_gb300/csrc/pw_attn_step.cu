@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   __syncthreads();
   for (int c = tid; c < a.ctas; c += kListThreads) {
     const long long u0 = min(c * W / P, W), u1 = min((c + 1) * W / P, W);
-    AttnStart st{0, 0, 0, (int)(u1 - u0), {}, {0, 0}, {0, 0}, {}};
+    AttnStart st{0, 0, 0, (int)(u1 - u0), {}, {0, 0}, {0, 0}};
     // the (tile, head) of a unit, and the CTAs of its first and last key tiles
     auto find = [&](long long u, int &tile, int &head, int &off) {
       int lo = 0, hi = n_tiles - 1;  // the last tile whose units begin at or before u
@@ -322,13 +322,6 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
       int tile, head, off;
       st.last = find(u1 - 1, tile, head, off);
       st.t = a.list.tiles[st.tile];
-      const int ppt = kAttnKeys / a.bt, page = (st.t.kv0 + max(st.off - a.list.piece_cost, 0)) * ppt;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        st.ids[i] = -1;
-        if (i < ppt && st.t.trow >= 0 && page + i < a.table_stride)
-          st.ids[i] = a.table[(size_t)st.t.trow * a.table_stride + page + i];
-      }
       if (st.last.x == c && st.last.y > c)  // split, from here on (their order does not matter)
         a.list.splits[atomicAdd(&n_splits, 1)] = AttnSplit{a.list.tiles[tile], head, c, st.last.y, 0};
     }

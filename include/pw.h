@@ -548,7 +548,8 @@ pw_status pw_kv_map(pw_attn *a, const pw_kv_step *step, const int32_t *new_ids, 
  * [lo, hi), and the division of all key blocks among the SMs.  window >= 0 (0: none).  doc_start [n_tokens]
  * (NULL: none): position in its request at which the row's document begins, for packed documents.
  * bidir_len [R] (NULL: none): keys below it are seen by every row of the request.  The plan holds for every
- * layer of the step with this mask, until the next pw_attn_plan into it; step's table must stay valid.
+ * layer of the step with this mask, until the next pw_attn_plan into it; step's table must stay valid, and
+ * its entries are read by each pw_attn_forward: a block may be moved in between.
  * A captured pw_attn_forward may be replayed after its plan was laid out again with the same max_new, n_tokens, table,
  * table_stride and presence of groups, and follows the new lengths and masks.  After one with others (as far as they
  * change the tiles), or while a captured pw_attn_plan has not been replayed, it writes nothing and pw_attn_check
