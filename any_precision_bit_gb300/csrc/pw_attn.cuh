@@ -51,56 +51,109 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return r;
 }
 
-// One row (token t, query head h) over the keys [lo, hi) of its table row, by one warp: lane l
-// holds elements 4 l .. 4 l + 3 of the head.  The running maximum and sum of a softmax in fp32;
-// only visible keys and values are read.  acc is the normalised output, *lse the natural
-// log-sum-exp (-inf and zeros for a row without keys).
-template <bool BF>
-__device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, int trow, int pos, float (&acc)[4],
-                              float *lse) {
-  const int lane = threadIdx.x & 31, d = 4 * lane;
-  const bool mine = d < a.D;
-  float qf[4] = {0.f, 0.f, 0.f, 0.f};
-  if (mine) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(a.q + t * a.q_token + h * a.q_head + d);
-    const float2 x = unpack2<BF>(w.x), y = unpack2<BF>(w.y);
-    qf[0] = x.x, qf[1] = x.y, qf[2] = y.x, qf[3] = y.y;
-  }
+// One row (token t, query head h) over the keys [lo, hi) of its table row, by one warp, for rows that the
+// tensor cores cannot do (see redo_row): eight lanes share a key, lane l its elements 8 (l % 8) .. + 7 and 64 + 8 (l % 8)
+// .. + 7, and 4 KEYS keys are under way at a time, KEYS to each quarter of the warp.  Each quarter has the running
+// maximum and sum of a softmax over its keys in fp32, which are joined at the end; only visible keys and values are
+// read.  acc is the normalised output in all lanes (zeros for a row without keys).
+template <bool BF, int KEYS>
+__device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, int trow, int pos, float (&acc)[16]) {
+  const int lane = threadIdx.x & 31, sub = lane >> 3, d = 8 * (lane & 7);
   const int hk = h / a.G, mask = (1 << a.log_bt) - 1;
+  auto spread = [](const uint4 &w, float *x) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = unpack2<BF>(u[i]);
+      x[2 * i] = y.x;
+      x[2 * i + 1] = y.y;
+    }
+  };
+  // Loads are made from the cache's or the table's beginning where there is nothing to load, and replaced by zeros: no
+  // branch keeps one from being issued behind another.
+  const bool has[2] = {d < a.D, d + 64 < a.D};
+  const int col[2] = {has[0] ? d : 0, has[1] ? d + 64 : 0};
+  auto zeros_but = [](bool keep, uint4 w) { return keep ? w : make_uint4(0, 0, 0, 0); };
+  float q[16];
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+    spread(zeros_but(has[half], *reinterpret_cast<const uint4 *>(a.q + t * a.q_token + h * a.q_head + col[half])), q + 8 * half);
+  const int *table = a.table + (trow >= 0 ? (size_t)trow * a.table_stride : 0);
+  auto block_of = [&](int j) {
+    const int page = j >> a.log_bt;
+    const bool in = j < hi && trow >= 0 && page < a.table_stride;
+    const int id = table[in ? page : 0];
+    return in && id >= 0 && id < a.n_blocks ? id : -1;
+  };
   const float slope = a.slopes ? a.slopes[h] : 0.f;
   float m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int page = j >> a.log_bt;
-    const int id = trow >= 0 && page < a.table_stride ? a.table[(size_t)trow * a.table_stride + page] : -1;
-    uint2 kw{0u, 0u}, vw{0u, 0u};
-    if (mine && id >= 0 && id < a.n_blocks) {
-      const int64_t at = id * a.block_stride + (j & mask) * a.token_stride + hk * a.head_stride + d;
-      kw = *reinterpret_cast<const uint2 *>(a.kc + at);
-      vw = *reinterpret_cast<const uint2 *>(a.vc + at);
-    }
-    const float2 k0 = unpack2<BF>(kw.x), k1 = unpack2<BF>(kw.y);
-    float s = qf[0] * k0.x + qf[1] * k0.y + qf[2] * k1.x + qf[3] * k1.y;
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int j0 = lo; j0 < hi; j0 += 4 * KEYS) {
+    uint4 k[KEYS][2], v[KEYS][2];
+    int id[KEYS];
+    bool there[KEYS];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale;
-    if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-    if (a.slopes) s -= slope * fabsf((float)(pos - j));
-    const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = expf(m - ms), p = expf(s - ms);
+    for (int u = 0; u < KEYS; ++u) id[u] = block_of(j0 + 4 * u + sub);
+#pragma unroll
+    for (int u = 0; u < KEYS; ++u) {
+      there[u] = id[u] >= 0;
+      const int64_t at = there[u] ? id[u] * a.block_stride + ((j0 + 4 * u + sub) & mask) * a.token_stride + hk * a.head_stride : 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        k[u][half] = *reinterpret_cast<const uint4 *>(a.kc + at + col[half]);
+        v[u][half] = *reinterpret_cast<const uint4 *>(a.vc + at + col[half]);
+      }
+    }
+    float s[KEYS], mn = m;
+#pragma unroll
+    for (int u = 0; u < KEYS; ++u) {
+      float x[16], y = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) spread(zeros_but(there[u] && has[half], k[u][half]), x + 8 * half);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y = fmaf(q[i], x[i], y);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      y *= a.scale;
+      if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
+      const int j = j0 + 4 * u + sub;
+      if (a.slopes) y -= slope * fabsf((float)(pos - j));
+      s[u] = j < hi ? y : -INFINITY;
+      mn = fmaxf(mn, s[u]);
+    }
+    const float ms = mn == -INFINITY ? 0.f : mn, f = expf(m - ms);
     m = mn;
-    l = l * f + p;
-    const float2 v0 = unpack2<BF>(vw.x), v1 = unpack2<BF>(vw.y);
-    acc[0] = acc[0] * f + p * v0.x;
-    acc[1] = acc[1] * f + p * v0.y;
-    acc[2] = acc[2] * f + p * v1.x;
-    acc[3] = acc[3] * f + p * v1.y;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] *= f;
+#pragma unroll
+    for (int u = 0; u < KEYS; ++u) {
+      const float p = expf(s[u] - ms);
+      l += p;
+      float x[16];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) spread(zeros_but(there[u] && has[half], v[u][half]), x + 8 * half);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = fmaf(p, x[i], acc[i]);
+    }
   }
+  // the quarters' results
+  float top = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  const float f = expf(m - (top == -INFINITY ? 0.f : top));
+  l *= f;
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] *= inv;
-  *lse = m + logf(l);
+  for (int i = 0; i < 16; ++i) {
+    float x = acc[i] * f;
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    x += __shfl_xor_sync(0xffffffffu, x, 16);
+    acc[i] = x * inv;
+  }
 }
 
 // ------------------------------------------------------------------ the tensor-core kernel
@@ -818,15 +871,33 @@ __device__ __forceinline__ RowOut row_out(const AttnArgs &a, int tok, int head, 
   }
   return r;
 }
-// N consecutive elements from column c of a row; false if one is not finite.
-// `ready`: the row's result over the prefix from column c on, or null to load it here where it counts.
+// The largest magnitude of the first n of N elements (n a multiple of 8, or N = 4), NaN if one of them is.  (Columns
+// past head_dim are zeros, or NaN times them: not looked at.)
+template <int N>
+__device__ __forceinline__ float largest_before(const float *v, int n) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    float t8 = max_nan(max_nan(fabsf(v[i]), fabsf(v[i + 1]), fabsf(v[i + 2])), fabsf(v[i + 3]), top);
+    if constexpr (N % 8 == 0)
+      t8 = max_nan(max_nan(fabsf(v[i + 4]), fabsf(v[i + 5]), fabsf(v[i + 6])), fabsf(v[i + 7]), t8);
+    if (i < n) top = t8;
+  }
+  return top;
+}
+// N consecutive elements from column c of a row; false if one is not finite (by the row's own keys: its result over a
+// shared prefix may be).
+// `ready`: the row's result over the prefix from column c on, or null to load it here where it counts.  hold: what is
+// not finite is not stored.
 template <int N, bool BF>
 __device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, int tok, int head, int c, float (&v)[N],
-                                           const float4 *ready = nullptr) {
+                                           const float4 *ready = nullptr, bool hold = false) {
   static_assert(N % 4 == 0, "stores of 8 or 16 bytes");
   if (c >= a.D) return true;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] *= r.inv;
+  const bool fin = finite(largest_before<N>(v, a.D - c));
+  if (hold && !fin) return false;
   if (r.w2 != 0.f) {
     const float *po = a.prefix_o + r.at * a.D + c;
 #pragma unroll
@@ -839,16 +910,6 @@ __device__ __forceinline__ bool store_cols(const AttnArgs &a, const RowOut &r, i
         v[i + 3] = fmaf(r.w2, x.w, v[i + 3]);
       }
   }
-  // the largest magnitude, NaN if one is (elements past head_dim are zeros, or NaN times them: not looked at)
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    float t8 = max_nan(max_nan(fabsf(v[i]), fabsf(v[i + 1]), fabsf(v[i + 2])), fabsf(v[i + 3]), top);
-    if constexpr (N % 8 == 0)
-      t8 = max_nan(max_nan(fabsf(v[i + 4]), fabsf(v[i + 5]), fabsf(v[i + 6])), fabsf(v[i + 7]), t8);
-    if (c + i < a.D) top = t8;
-  }
-  const bool fin = finite(top);
   if (a.to_prefix) {
     float *d = a.prefix_o + r.at * a.D + c;
 #pragma unroll
@@ -878,22 +939,74 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, const RowOut &r) {
 
 // A row whose sum is finite but whose output is not: a value is infinite or NaN, possibly one that the row
 // does not see (0 times it in the product with v).  Again, from the row's visible keys alone, by the warp.
-// merge: over the shared prefix too.  Columns c0 .. c1 - 1 are written.
-template <bool BF>
-static __device__ PW_RARE void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi, int trow, bool merge, int c0 = 0,
-                         int c1 = 128) {
+// merge: over the shared prefix too.  Columns 4 g .. 4 g + 3 are written for the bits g of `groups`.
+template <bool BF, int KEYS>
+static __device__ PW_RARE void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi, int trow, bool merge,
+                                        uint32_t groups = ~0u) {
   const int lane = threadIdx.x & 31;
   const RowBound b = a.bounds[tok];
-  float acc[4], lse;
-  row_attention<BF>(a, tok, head, merge ? b.lo : max(b.lo, klo), merge ? b.hi : min(b.hi, khi), trow, b.pos, acc, &lse);
-  if (4 * lane < a.D && 4 * lane >= c0 && 4 * lane < c1) {
+  float acc[16];
+  row_attention<BF, KEYS>(a, tok, head, merge ? b.lo : max(b.lo, klo), merge ? b.hi : min(b.hi, khi), trow, b.pos, acc);
+  if (lane >= 8) return;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const int c = i / 8 * 64 + 8 * lane + i % 8;
+    if (c >= a.D || !(groups >> (c / 4) & 1u)) continue;
     if (a.to_prefix)
-      *reinterpret_cast<float4 *>(a.prefix_o + ((size_t)tok * a.Hq + head) * a.D + 4 * lane) =
-          make_float4(acc[0], acc[1], acc[2], acc[3]);
+      *reinterpret_cast<float4 *>(a.prefix_o + ((size_t)tok * a.Hq + head) * a.D + c) =
+          make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     else
-      *reinterpret_cast<uint2 *>(a.o + tok * a.o_token + head * a.o_head + 4 * lane) =
-          make_uint2(pack_pair<BF>(acc[0], acc[1]), pack_pair<BF>(acc[2], acc[3]));
+      *reinterpret_cast<uint2 *>(a.o + tok * a.o_token + head * a.o_head + c) =
+          make_uint2(pack_pair<BF>(acc[i], acc[i + 1]), pack_pair<BF>(acc[i + 2], acc[i + 3]));
   }
+}
+
+// Such a row takes as long as its keys are many, and a pipeline of bounded waits cannot stop for it: within
+// attn_kernel it is marked, once its output is written, and computed again when the CTA's pieces are done.
+static __device__ __forceinline__ void mark_row(const AttnArgs &a, int tok, int head, volatile int *marked) {
+  const size_t at = (size_t)tok * a.Hq + head;
+  __threadfence();  // another CTA that has a piece of the tile may be the one that takes the row
+  atomicOr(a.marks + (at >> 5), 1u << (at & 31));
+  *marked = 1;
+}
+// By the first `warps` of a CTA whose pieces are done, rows dealt out among them.  A CTA looks at the rows of all its pieces;
+// the one that finished a tile has a piece of it, and whoever clears a row's mark computes it.
+template <bool BF, int KEYS>
+static __device__ PW_RARE void redo_marked(const AttnArgs &a, int warps) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Walk w(a, true);
+  while (w.load()) {
+    const AttnTile t = w.t;
+    const bool merge = t.merge && !a.to_prefix;
+    const int rows = t.ntok * a.G;
+    for (int r0 = 0; r0 < rows; r0 += 32 * warps) {
+      const int r = r0 + lane * warps + warp, tok = t.tok0 + r / a.G, head = w.head * a.G + r % a.G;
+      bool mine = false;
+      if (r < rows) {
+        const size_t at = (size_t)tok * a.Hq + head;
+        const uint32_t bit = 1u << (at & 31);
+        mine = (__ldcg(a.marks + (at >> 5)) & bit) && (atomicAnd(a.marks + (at >> 5), ~bit) & bit);
+        if (mine) __threadfence();
+      }
+      unsigned flagged = __ballot_sync(0xffffffffu, mine);
+      __syncwarp();
+      while (flagged) {
+        const int src = __ffs(flagged) - 1;
+        flagged &= flagged - 1;
+        redo_row<BF, KEYS>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), t.klo, t.khi, t.trow,
+                        merge);
+      }
+    }
+    w.next(a);
+  }
+}
+
+// Bit i of sixteen as bit 2 i.
+__device__ __forceinline__ uint32_t every_other(uint32_t x) {
+  x = (x | x << 8) & 0x00ff00ffu;
+  x = (x | x << 4) & 0x0f0f0f0fu;
+  x = (x | x << 2) & 0x33333333u;
+  return (x | x << 1) & 0x55555555u;
 }
 
 // Four warps that finish a row tile together.
@@ -931,7 +1044,7 @@ struct Group {
 // kTwo: the softmax warps of two streams, which write their rows' results, too.
 template <int DP, bool BF, int MODE>
 __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
-                       volatile int *abort_flag, volatile int *last_flag) {
+                       volatile int *abort_flag, volatile int *last_flag, volatile int *marked) {
   using C = Cfg<kTwo, DP>;
   using B = Bars<C::kStages>;
   constexpr int NS = C::NS;
@@ -1096,10 +1209,17 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       // tensor memory again (or attn_join_kernel does)
       const size_t my = slot_of(blockIdx.x, c0);
       if (active) {
+        uint32_t odd = 0;
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
           float v[32];
           from_tmem(c, v);
+          if (a.join) {
+            uint32_t o = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o |= finite(largest_before<4>(v + 4 * i, 4)) ? 0u : 1u << i;
+            odd |= o << (8 * c);
+          }
           if (valid) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -1107,7 +1227,10 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
                      make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
           }
         }
-        if (valid) __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
+        if (valid) {
+          __stcg(a.part_ml + my * 128 + row, make_float2(m, l));
+          if (a.join) a.part_odd[my * 128 + row] = odd;
+        }
       }
       out = !a.join && group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
       if (!ok) break;
@@ -1160,13 +1283,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         if (valid) fin = store_cols<32, BF>(a, ro, tok, head, 32 * c, v) && fin;
       }
       if (valid) store_lse(a, ro);
-      unsigned flagged = __ballot_sync(0xffffffffu, valid && !fin && finite(l));
-      while (flagged) {
-        const int src = __ffs(flagged) - 1;
-        flagged &= flagged - 1;
-        redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), w.klo, w.khi, w.trow,
-                     merge);
-      }
+      if (valid && !fin && finite(l)) mark_row(a, tok, head, marked);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
@@ -1371,7 +1488,7 @@ __device__ void soften_few(const AttnArgs &a, const volatile Piece *piece, uint8
 // threads to a row add them, relative to the largest of their maxima.
 template <int DP, bool BF>
 __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
-                       volatile int *abort_flag, volatile int *last_flag) {
+                       volatile int *abort_flag, volatile int *last_flag, volatile int *marked) {
   using C = Cfg<kSpread, DP>;
   using B = Bars<C::kStages>;
   const int quarter = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, thread = 32 * quarter + lane;
@@ -1455,12 +1572,20 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       bool last = c0 == c1;
       if (!last) {
         const size_t my = slot_of(blockIdx.x, c0);
+        // the threads of a row, one half of the warp, with columns that are not finite
+        uint32_t odd[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+          odd[i] = __ballot_sync(0xffffffffu, !finite(largest_before<4>(v + 4 * i, 4))) >> (lane & 16) & 0xffffu;
         if (mine) {
 #pragma unroll
           for (int i = 0; i < V; i += 4)
             __stcg(reinterpret_cast<float4 *>(a.part_o + my * kPart + ((c + i) / 4 * 128 + rr) * 4),
                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-          if (c == 0) __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
+          if (c == 0) {
+            __stcg(a.part_ml + my * 128 + rr, make_float2(mm, ll));
+            if (a.join) a.part_odd[my * 128 + rr] = V == 4 ? odd[0] : every_other(odd[0]) | every_other(odd[V / 4 - 1]) << 1;
+          }
         }
         if (a.join || r0 + kJoinRows < nrows) continue;
         last = group.last_to_arrive(a, c0, c1, thread, last_flag, ok);
@@ -1562,13 +1687,12 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           if (c == 0) store_lse(a, out);
         }
         const unsigned flagged = __ballot_sync(0xffffffffu, again);
-        if (flagged) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h)  // the warp's two rows
-            if (flagged >> (16 * h) & 0xffffu) {
-              const int rw = q0 + 2 * quarter + h, rw_t = over_g(a, rw);
-              redo_row<BF>(a, w.tok0 + rw_t, w.head * a.G + rw - rw_t * a.G, w.klo, w.khi, w.trow, merge);
-            }
+        if (__builtin_expect(flagged != 0, 0)) {
+          __syncwarp();  // the row's stores come before its mark
+          if (lane % 16 == 0 && (flagged >> lane & 0xffffu)) {
+            const int rw = q0 + 2 * quarter + lane / 16, rw_t = rw / a.G;
+            mark_row(a, w.tok0 + rw_t, w.head * a.G + rw - rw_t * a.G, marked);
+          }
         }
       }
     }
@@ -1585,22 +1709,42 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   }
 }
 
+// Rows of this warp whose columns are not finite: bit `it` of `todo` for the CTA's piece of work number `it`.  Those columns
+// were not stored.  Where pieces of the row are not finite, all CTAs that have such columns of it find the same ones, and
+// one of them computes the row, once; where only the sum overflowed each does so for its columns.
+template <int COLS, bool BF>
+static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned todo, int streams) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int it = 0; it < 16; ++it) {
+    const int i = blockIdx.x + it * gridDim.x, col = i % COLS, s = i / COLS % streams;
+#pragma unroll 1
+    for (unsigned left = __ballot_sync(0xffffffffu, todo >> it & 1u); left; left &= left - 1) {
+      const AttnSplit *sp = a.list.splits + i / (streams * COLS);
+      const AttnTile t = load_tile(&sp->t);
+      const int row = (threadIdx.x & ~31) + __ffs(left) - 1, row_t = over_g(a, row);
+      uint32_t odd = 0;
+      for (int p = sp->c0 + lane; p <= sp->c1; p += 32) odd |= a.part_odd[part_slot(p, sp->c0, streams, s) * 128 + row];
+      odd = __reduce_or_sync(0xffffffffu, odd) & (0xffffffffu >> (32 - a.D / 4));
+      uint32_t groups = 1u << col;
+      if (odd & groups) {
+        groups = odd;
+        for (int k = row % __popc(odd); k > 0; --k) odd &= odd - 1;  // rows are dealt out among the CTAs
+        if (__ffs(odd) - 1 != col) continue;
+      }
+      redo_row<BF, 1>(a, t.tok0 + s * a.list.tpt + row_t, sp->head * a.G + row - row_t * a.G, t.klo, t.khi, t.trow,
+                      t.merge && !a.to_prefix, groups);
+    }
+  }
+}
 // The sum of each split tile's pieces, where tiles are few and their pieces many: one CTA of the attention
 // kernel adding up a tile's (18 pieces of 64 KB for 256 rows over a prefix of 4096 keys) took longer than the
 // products.  Here a CTA takes 4 columns of a tile's rows at a time, a thread a row, with eight pieces under way;
-// of kSpread's 16 rows eight threads share each, its pieces dealt out among them.
-template <bool BF>
-static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned flagged, int tok, int h, const AttnTile &t,
-                                              bool merge, int c) {
-  while (flagged) {
-    const int src = __ffs(flagged) - 1;
-    flagged &= flagged - 1;
-    redo_row<BF>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), t.klo, t.khi, t.trow, merge,
-                 c, c + 4);
-  }
-}
+// of kSpread's 16 rows eight threads share each, its pieces dealt out among them.  (At most 72 registers, so that the
+// next kernel's CTAs find room beside these; rows to be computed again take few keys at a time for it, and are done
+// behind the loop.  With the 128 registers that four times as many keys take, 64 requests behind a shared prefix of 4096 were 4 us slower.)
 template <int FORM, int DP, bool BF>
-static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+static __global__ void __launch_bounds__(128, 7) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kBatch = 8, kCols = DP / 4;
   constexpr int kRows = FORM == kSpread ? kSpreadRows : 128, kShare = 128 / kRows;
   __shared__ float4 sum_v[kShare][kRows];
@@ -1610,15 +1754,16 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
   if (!plan_fits(a)) return;  // (reported by attn_kernel)
   const int streams = FORM == kTwo ? 2 : 1, share = threadIdx.x / kRows, row = threadIdx.x % kRows, row_t = over_g(a, row), row_h = row - row_t * a.G;
   const int n = a.list.meta[2] * streams * kCols;
+  // Rows to be computed again, by this CTA's tiles: what is done for them stays out of this loop's registers.
+  unsigned todo = 0;
 #pragma unroll 1
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+  for (int i = blockIdx.x, it = 0; i < n; i += gridDim.x, ++it) {
     const int c = i % kCols * 4, s = i / kCols % streams;
     const AttnSplit *sp = a.list.splits + i / (streams * kCols);
     const AttnTile t = load_tile(&sp->t);
     const int4 x = *reinterpret_cast<const int4 *>(&sp->head);
     const int c0 = x.y, c1 = x.z, tok = t.tok0 + s * a.list.tpt + row_t, h = x.x * a.G + row_h;
     const bool valid = row < min(a.list.tpt, t.ntok - s * a.list.tpt) * a.G && c < a.D, merge = t.merge && !a.to_prefix;
-    bool again = false;
     float pl = 0.f, m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     if (valid) {
       // pieces of this thread: the CTAs c0 + share, c0 + share + kShare, ...; all but c0's are their CTAs' first (see
@@ -1697,12 +1842,12 @@ static __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_cons
     }
     if (valid && share == 0) {
       const RowOut out = row_out(a, tok, h, merge, pl, m, l);
-      again = !store_cols<4, BF>(a, out, tok, h, c, v) && finite(l);
+      const bool sums = finite(l);
+      if (!store_cols<4, BF>(a, out, tok, h, c, v, nullptr, sums) && sums) todo |= 1u << it;
       if (c == 0) store_lse(a, out);
     }
-    const unsigned flagged = __ballot_sync(0xffffffffu, again);
-    if (flagged) redo_join<BF>(a, flagged, tok, h, t, merge, c);
   }
+  if (__any_sync(0xffffffffu, todo != 0)) redo_join<kCols, BF>(a, todo, streams);
 }
 
 template <int FORM, int DP, bool BF, int MODE>
@@ -1713,7 +1858,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar_mem[B::kNum];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, last_flag[2];
+  __shared__ int abort_flag, last_flag[2], marked;
   __shared__ Piece piece[kPieces];
   const int warp = threadIdx.x >> 5;
   const uint32_t bars = smem_u32(bar_mem), sm = smem_u32(smem);
@@ -1739,6 +1884,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
       mbar_init(bars + 8 * (B::kDF + i), 1);
       mbar_init(bars + 8 * (B::kDE + i), C::kProdWarp + 1);  // the softmax and finishing warps and the MMA warp
     }
+    marked = 0;
     abort_flag = (sm & 1023u) != 0u;  // the swizzled tiles are 1 KB-aligned
     if (abort_flag) atomicOr(a.err, kAttnErrWait);
     fence_mbar_init();
@@ -1769,11 +1915,17 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
       if constexpr (FORM == kSpread)
         soften_few<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag);
       else
-        soften<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+        soften<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag, last_flag, &marked);
+    }
+    if constexpr (FORM == kTwo) {  // (here, where a warp has the registers for it)
+      static_assert(FORM != kTwo || C::kSoftWarps == 8, "a barrier of 256 threads");
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      if (__all_sync(0xffffffffu, marked && !abort_flag)) redo_marked<BF, 2>(a, C::kSoftWarps);
     }
   } else if (warp < C::kProdWarp) {
     if constexpr (FORM == kSpread) {
-      if (!abort_flag) finish<DP, BF>(a, piece, smem, bars, tmem, &abort_flag, last_flag);
+      if (!abort_flag) finish<DP, BF>(a, piece, smem, bars, tmem, &abort_flag, last_flag, &marked);
     }
   } else {
     if (FORM == kTwo) regs_dec<kRegsOther>();
@@ -1790,7 +1942,9 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemColsAttn);
+    __syncwarp();
   }
+  if (FORM == kSpread && __all_sync(0xffffffffu, marked && !abort_flag)) redo_marked<BF, 1>(a, C::kThreads / 32);
 }
 
 template <int FORM, int DP, bool BF, int MODE>
@@ -1806,6 +1960,8 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
   }
   if (cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(C::kThreads), (size_t)C::kSmem, st, maps, a)) return (int)e;
   if (!a.join) return (int)cudaGetLastError();
+  // (a split ends a CTA's share, so that there are at most a.ctas of them with two streams of 32 column groups each: not
+  // more than 16 pieces of work for a CTA here, as redo_join counts on)
   return (int)launch_pdl(attn_join_kernel<FORM, DP, BF>, dim3(4 * a.ctas), dim3(128), 0, st, a);
 }
 

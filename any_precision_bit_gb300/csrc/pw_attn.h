@@ -162,8 +162,10 @@ struct AttnArgs {
   // Partial results of split tiles: two slots a CTA (its last piece and its first) and stream.
   float *part_o;    // [ctas][2][streams][head_dim padded / 4][128][4]
   float2 *part_ml;  // [ctas][2][streams][128] running maximum and sum
+  uint32_t *part_odd;  // [ctas][2][streams][128] bit g: columns 4 g .. 4 g + 3 of a row's piece are not finite (with `join`)
   int *counters;    // [ctas][2] arrived pieces of the split tile whose first piece is the CTA's last,
                     // per stream; zero between launches
+  uint32_t *marks;  // a bit for each row [n_tokens][Hq]: to be computed again by attn_kernel; zero between launches
   int *err;
   long long wait_cycles;  // bounded device waits give up after this many SM cycles
   int withhold;           // testing: see produce()

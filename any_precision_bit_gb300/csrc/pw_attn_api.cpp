@@ -124,6 +124,8 @@ struct pw_attn {
   float *part_o = nullptr, *prefix_o = nullptr, *prefix_lse = nullptr;
   float2 *part_ml = nullptr;
   int *counters = nullptr;
+  uint32_t *marks = nullptr, *part_odd = nullptr;
+  size_t mark_words = 0;
   long long wait_cycles = kWaitCyclesDefault;
   int fault_withhold = 0;  // testing: the next forward withholds one device barrier arrival
 };
@@ -168,8 +170,10 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   int e = cudaDeviceGetAttribute(&a->sm_count, cudaDevAttrMultiProcessorCount, d.device);
   if (e) return cuda_failed("cudaDeviceGetAttribute", e);
   const size_t ctas = (size_t)a->sm_count, dp = d.head_dim > 64 ? 128 : 64;
-  bool ok = alloc(a, &a->err, 1) && alloc(a, &a->counters, 2 * ctas) &&
-            alloc(a, &a->part_o, ctas * 4 * kAttnRows * dp) && alloc(a, &a->part_ml, ctas * 4 * kAttnRows);
+  a->mark_words = ((size_t)d.max_tokens * d.n_heads + 31) / 32;
+  bool ok = alloc(a, &a->marks, a->mark_words) && alloc(a, &a->err, 1) && alloc(a, &a->counters, 2 * ctas) &&
+            alloc(a, &a->part_o, ctas * 4 * kAttnRows * dp) && alloc(a, &a->part_ml, ctas * 4 * kAttnRows) &&
+            alloc(a, &a->part_odd, ctas * 4 * kAttnRows);
   if (d.max_shared_tokens > 0)
     ok = ok && alloc(a, &a->prefix_o, (size_t)d.max_shared_tokens * d.n_heads * d.head_dim) &&
          alloc(a, &a->prefix_lse, (size_t)d.max_shared_tokens * d.n_heads);
@@ -190,7 +194,8 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
     }
   }
   if (!ok) return report(nullptr, PW_ERR_OOM, "device memory exhausted");
-  if ((e = cudaMemset(a->err, 0, sizeof(int))) || (e = cudaMemset(a->counters, 0, 2 * ctas * sizeof(int))))
+  if ((e = cudaMemset(a->err, 0, sizeof(int))) || (e = cudaMemset(a->counters, 0, 2 * ctas * sizeof(int))) ||
+      (e = cudaMemset(a->marks, 0, a->mark_words * sizeof(uint32_t))))
     return cuda_failed("cudaMemset", e);
   for (Plan &p : a->plans)
     if ((e = cudaMemset(p.shape, 0, sizeof(AttnShape)))) return cuda_failed("cudaMemset", e);
@@ -455,12 +460,14 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   const double poly[5] = {1.0, -0.3333307206630707, 0.13324828445911407, -0.05298924073576927, 0.017141319811344147};
   double power = (double)g.cap2 * g.inv_cap;
   for (int i = 0; i < 5; ++i, power *= (double)g.inv_cap * g.inv_cap) g.cap_poly[i] = (float)(poly[i] * power);
+  g.marks = a->marks;
   g.err = a->err;
   g.wait_cycles = a->wait_cycles;
   g.withhold = a->fault_withhold;
   a->fault_withhold = 0;
   g.part_o = a->part_o;
   g.part_ml = a->part_ml;
+  g.part_odd = a->part_odd;
   g.counters = a->counters;
   g.ctas = a->sm_count;
   AttnMaps maps;
@@ -516,6 +523,7 @@ pw_status pw_attn_check(pw_attn *a, pw_stream stream) {
   if (!bits) return PW_OK;
   if ((e = cudaMemsetAsync(a->err, 0, sizeof bits, st)) ||
       (e = cudaMemsetAsync(a->counters, 0, 2 * sizeof(int) * (size_t)a->sm_count, st)) ||
+      (e = cudaMemsetAsync(a->marks, 0, a->mark_words * sizeof(uint32_t), st)) ||
       (e = cudaStreamSynchronize(st)))
     return cuda_failed("cudaMemsetAsync", e);
   if (bits & kAttnErrWait) return report(nullptr, PW_ERR_TIMEOUT, "a bounded device wait expired; outputs are invalid");

@@ -477,7 +477,8 @@ pw_status pw_kv_get_stats(pw_kv *kv, pw_kv_stats *out);
  * x_j -= slope[head] * |p - j| if slopes are given,
  *   o = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)  (natural logarithm).
  * A row that sees no key gets o = 0 and lse = -infinity.  Keys and values a row does not see do
- * not reach it, whatever bits they hold.  Products of q and k and the softmax sums are fp32; the
+ * not reach it, whatever bits they hold.  (Infinities and NaN among the values of a step's requests cost time: rows in
+ * whose key tiles they lie are computed again, key by key.)  Products of q and k and the softmax sums are fp32; the
  * probabilities are rounded to the cache's type for the product with v, which is summed in fp32. */
 enum { PW_BF16 = 0, PW_FP16 = 1 };
 
@@ -524,8 +525,8 @@ typedef struct {
     const int32_t *shared_len;  /* [n_groups] */
 } pw_kv_step;
 
-/* Create an attention handle: plans, split workspace (about 40 MB) and, with max_shared_tokens,
- * 4 * max_shared_tokens * n_heads * (head_dim + 1) bytes for the shared prefixes' results.  The calls
+/* Create an attention handle: plans, split workspace (about 40 MB), max_tokens * n_heads / 8 bytes of marks and, with
+ * max_shared_tokens, 4 * max_shared_tokens * n_heads * (head_dim + 1) bytes for the shared prefixes' results.  The calls
  * of one handle run on one stream at a time (its workspace is shared by them), and by one host
  * thread.  PW_ERR_INVALID on a shape outside the ranges above, PW_ERR_CUDA / PW_ERR_OOM otherwise. */
 pw_status pw_attn_create(const pw_attn_desc *desc, pw_attn **out);
