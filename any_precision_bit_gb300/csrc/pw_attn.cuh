@@ -1106,6 +1106,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         // times what the memory holds may be NaN
         if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
         hide_value<C>(smp + (NS + rv.st) * C::kTileBytes, thread, base, klo, khi);
+        __syncwarp();  // a warp without rows arrives below by one lane for all of them
       }
       if (active) {
         const int l0 = lo - base, h0 = hi - base;

@@ -135,3 +135,24 @@ def test_the_waits_of_a_call_do_not_depend_on_what_the_values_hold(shape):
     got, _ = s.forward(**fwd)
     assert (got == np.inf).all()
     s.close()
+
+
+@pytest.mark.parametrize("new", [9, 17, 32])
+@pytest.mark.parametrize("ctx", [3, 70, 250])
+@pytest.mark.parametrize("kw", [{}, dict(softcap=20.0)])
+def test_unwritten_values_beside_quarters_of_a_tile_without_rows(ctx, new, kw):
+    """Tiles of 18 to 64 rows: half or more of the warps that clear the values behind the last key have no rows of
+    their own.  The same bits whatever lies there."""
+    ref = None
+    for fill in (0.0, float("nan"), float("inf"), -2.0):
+        s = Step([ctx] * 40, [new] * 40, Hq=4, Hkv=2, D=128, seed=5)
+        for c in s.kv:
+            c[s.torch.isnan(c)] = fill
+        s.map_and_append()
+        for _ in range(5):
+            got = s.forward(**kw)
+            ref = ref or got
+            assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
+        if fill == 0.0:
+            s.compare(**kw)
+        s.close()
