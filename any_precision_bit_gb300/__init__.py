@@ -531,25 +531,44 @@ def pw_kv_get_stats(kv) -> dict:
 
 # ---------------------------------------------------------------- paged attention
 # (Called once or several times a layer, so argument marshalling is kept short here.)
-_attn_shapes = {}  # handle: (n_heads, n_kv_heads, head_dim, desc, {plan: its step's n_tokens})
+# handle: (n_heads, n_kv_heads, head_dim, the caches' and rows' type, device, desc, {plan: its step's n_tokens})
+_attn_shapes = {}
+_types = {}  # torch's, by name
 
 
-def _addr(t, size=4, n=0):
-    """Address of a contiguous device tensor of at least n elements of `size` bytes, or None."""
+def _load_types():
+    if not _types:
+        import torch
+        _types.update((n, getattr(torch, n)) for n in ("int32", "int64", "float32", "bfloat16", "float16"))
+
+
+def _addr(t, device, n=0, kind="int32"):
+    """Address of a contiguous tensor of at least n elements of a type on a CUDA device, or None."""
     if t is None:
         return None
-    if not t.is_contiguous() or t.element_size() != size or t.numel() < n or not t.is_cuda:
-        raise ValueError(f"needs a contiguous device tensor of {n} or more elements of {size} bytes")
+    if t.dtype is not _types[kind] or not t.is_contiguous() or t.numel() < n or t.get_device() != device:
+        raise ValueError(f"needs a contiguous {kind} tensor of {n} or more elements on device {device}, not {_what(t)}")
     return t.data_ptr()
 
 
-def _rows(t, n, heads, dim):
+def _rows(t, n, heads, dim, dtype, device):
     """Address and the strides of [n or more rows][heads][dim] (unit last stride)."""
     rows, h, d = t.shape
     a, b, c = t.stride()
-    if rows < n or h != heads or d != dim or c != 1 or t.element_size() != 2 or not t.is_cuda:
-        raise ValueError(f"needs a device tensor [{n}][{heads}][{dim}] of 16-bit elements, the last dimension contiguous")
+    if rows < n or h != heads or d != dim or c != 1 or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"needs a tensor [{n}][{heads}][{dim}] of {dtype} on device {device}, the last dimension "
+                         f"contiguous, not {_what(t)}")
     return t.data_ptr(), a, b
+
+
+def _what(t):
+    return f"{list(t.shape)} of {t.dtype} on {t.device}, strides {t.stride()}"
+
+
+def _step_on(step, device):
+    if step.device != device:
+        raise ValueError(f"the step's tensors are on device {step.device}, the handle is for {device}")
+    return step.address
 
 
 def _cuda_stream(s):
@@ -558,10 +577,12 @@ def _cuda_stream(s):
 
 def pw_attn_create(desc: pw_attn_desc):
     """An attention handle (pass it to the pw_attn_* calls and pw_kv_map)."""
+    _load_types()
     h = C.c_void_p()
     _check(lib().pw_attn_create(C.byref(desc), C.byref(h)))
     kept = pw_attn_desc.from_buffer_copy(desc)
-    _attn_shapes[h.value] = kept.n_heads, kept.n_kv_heads, kept.head_dim, kept, {}
+    dtype = _types["bfloat16" if kept.dtype == PW_BF16 else "float16"]
+    _attn_shapes[h.value] = kept.n_heads, kept.n_kv_heads, kept.head_dim, dtype, kept.device, kept, {}
     return h.value
 
 
@@ -573,10 +594,11 @@ def pw_attn_destroy(attn):
 def pw_attn_bind(attn, layer, k_cache, v_cache):
     """Caches as tensors [n_blocks][block_tokens][n_kv_heads][head_dim], views included, of the
     same strides and a unit last one."""
-    d = _attn_shapes[attn][3]
+    _, _, _, dtype, device, d, _ = _attn_shapes[attn]
     for c in (k_cache, v_cache):
-        if tuple(c.shape) != (d.n_blocks, d.block_tokens, d.n_kv_heads, d.head_dim) or c.element_size() != 2 or not c.is_cuda:
-            raise ValueError("the caches must be device tensors of the handle's shape and 16-bit elements")
+        if (tuple(c.shape) != (d.n_blocks, d.block_tokens, d.n_kv_heads, d.head_dim) or c.dtype is not dtype
+                or c.get_device() != device):
+            raise ValueError(f"the caches must be tensors of the handle's shape, {dtype} and on device {device}, not {_what(c)}")
     if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
         raise ValueError("the caches must have the same strides and a contiguous last dimension")
     _check(lib().pw_attn_bind(attn, layer, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3]))
@@ -585,37 +607,46 @@ def pw_attn_bind(attn, layer, k_cache, v_cache):
 def pw_make_step(ctx_len, new_len, table, q_start, kv_len, slot, pos, max_new, rows=None, groups=None, shared_len=None):
     """A pw_kv_step over device tensors, which it keeps alive: lengths int32 [R], table int32
     [rows][blocks], q_start int32 [R + 1], kv_len int32 [R], slot int64 and pos int32 [n_tokens];
-    groups int32 [n_groups + 1] and shared_len int32 [n_groups] for shared prefixes."""
+    groups int32 [n_groups + 1] and shared_len int32 [n_groups] for shared prefixes.  All on one device."""
+    _load_types()
+    dev = ctx_len.get_device()
+    if dev < 0:
+        raise ValueError("a step's tensors are on a CUDA device")
     R, n, n_groups = ctx_len.numel(), pos.numel(), 0 if groups is None else groups.numel() - 1
     s = pw_kv_step(R=R, n_tokens=n, max_new=int(max_new), table_rows=table.shape[0], table_stride=table.shape[1],
-                   ctx_len=_addr(ctx_len), new_len=_addr(new_len, n=R), rows=_addr(rows, n=R), table=_addr(table),
-                   q_start=_addr(q_start, n=R + 1), kv_len=_addr(kv_len, n=R), slot=_addr(slot, 8, n), pos=_addr(pos),
-                   n_groups=n_groups, group_start=_addr(groups), shared_len=_addr(shared_len, n=n_groups))
+                   ctx_len=_addr(ctx_len, dev), new_len=_addr(new_len, dev, R), rows=_addr(rows, dev, R),
+                   table=_addr(table, dev), q_start=_addr(q_start, dev, R + 1), kv_len=_addr(kv_len, dev, R),
+                   slot=_addr(slot, dev, n, "int64"), pos=_addr(pos, dev), n_groups=n_groups,
+                   group_start=_addr(groups, dev), shared_len=_addr(shared_len, dev, n_groups))
+    s.device = dev
     s.refs = (ctx_len, new_len, table, q_start, kv_len, slot, pos, rows, groups, shared_len)
     s.address = C.addressof(s)
     return s
 
 
 def pw_kv_map(attn, step, new_ids, stream=None):
-    st = lib().pw_kv_map(attn, step.address, _addr(new_ids), 0 if new_ids is None else new_ids.numel(),
+    dev = _attn_shapes[attn][4]
+    st = lib().pw_kv_map(attn, _step_on(step, dev), _addr(new_ids, dev), 0 if new_ids is None else new_ids.numel(),
                          _cuda_stream(stream))
     if st:
         _check(st)
 
 
 def pw_attn_plan(attn, plan, step, window=0, doc_start=None, bidir_len=None, stream=None):
-    st = lib().pw_attn_plan(attn, plan, step.address, window, _addr(doc_start, n=step.n_tokens), _addr(bidir_len, n=step.R),
-                            _cuda_stream(stream))
+    _, _, _, _, dev, _, plans = _attn_shapes[attn]
+    st = lib().pw_attn_plan(attn, plan, _step_on(step, dev), window, _addr(doc_start, dev, step.n_tokens),
+                            _addr(bidir_len, dev, step.R), _cuda_stream(stream))
     if st:
         _check(st)
-    _attn_shapes[attn][4][plan] = step.n_tokens
+    plans[plan] = step.n_tokens
 
 
 def pw_attn_append(attn, layer, step, k, v, stream=None):
     """k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last one."""
-    _, h, d, _, _ = _attn_shapes[attn]
+    _, h, d, dtype, dev, _, _ = _attn_shapes[attn]
     n = step.n_tokens
-    st = lib().pw_attn_append(attn, layer, step.address, *_rows(k, n, h, d), *_rows(v, n, h, d), _cuda_stream(stream))
+    st = lib().pw_attn_append(attn, layer, _step_on(step, dev), *_rows(k, n, h, d, dtype, dev), *_rows(v, n, h, d, dtype, dev),
+                              _cuda_stream(stream))
     if st:
         _check(st)
 
@@ -623,10 +654,11 @@ def pw_attn_append(attn, layer, step, k, v, stream=None):
 def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, slopes=None, stream=None):
     """q and o: [n_tokens][n_heads][head_dim], any strides with a unit last one; scale defaults to
     1 / sqrt(head_dim)."""
-    h, _, d, _, plans = _attn_shapes[attn]
+    h, _, d, dtype, dev, _, plans = _attn_shapes[attn]
     n = plans.get(plan, 0)
-    st = lib().pw_attn_forward(attn, layer, plan, *_rows(q, n, h, d), *_rows(o, n, h, d), _addr(lse, n=n * h),
-                               d ** -0.5 if scale is None else scale, softcap, _addr(slopes, n=h), _cuda_stream(stream))
+    st = lib().pw_attn_forward(attn, layer, plan, *_rows(q, n, h, d, dtype, dev), *_rows(o, n, h, d, dtype, dev),
+                               _addr(lse, dev, n * h, "float32"), d ** -0.5 if scale is None else scale, softcap,
+                               _addr(slopes, dev, h, "float32"), _cuda_stream(stream))
     if st:
         _check(st)
 
