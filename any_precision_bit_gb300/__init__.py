@@ -531,7 +531,8 @@ def pw_kv_get_stats(kv) -> dict:
 
 # ---------------------------------------------------------------- paged attention
 # (Called once or several times a layer, so argument marshalling is kept short here.)
-# handle: (n_heads, n_kv_heads, head_dim, the caches' and rows' type, device, desc, {plan: its step's n_tokens})
+# handle: (n_heads, n_kv_heads, head_dim, the caches' and rows' type, device, desc, plans, caches), with
+# {plan: (its step's n_tokens, the step's tensors)} and {layer: its caches}: the library keeps their addresses
 _attn_shapes = {}
 _types = {}  # torch's, by name
 
@@ -582,19 +583,19 @@ def pw_attn_create(desc: pw_attn_desc):
     _check(lib().pw_attn_create(C.byref(desc), C.byref(h)))
     kept = pw_attn_desc.from_buffer_copy(desc)
     dtype = _types["bfloat16" if kept.dtype == PW_BF16 else "float16"]
-    _attn_shapes[h.value] = kept.n_heads, kept.n_kv_heads, kept.head_dim, dtype, kept.device, kept, {}
+    _attn_shapes[h.value] = kept.n_heads, kept.n_kv_heads, kept.head_dim, dtype, kept.device, kept, {}, {}
     return h.value
 
 
 def pw_attn_destroy(attn):
-    _attn_shapes.pop(attn, None)
+    kept = _attn_shapes.pop(attn, None)  # noqa: F841 (until the device's work is done)
     lib().pw_attn_destroy(attn)
 
 
 def pw_attn_bind(attn, layer, k_cache, v_cache):
     """Caches as tensors [n_blocks][block_tokens][n_kv_heads][head_dim], views included, of the
-    same strides and a unit last one."""
-    _, _, _, dtype, device, d, _ = _attn_shapes[attn]
+    same strides and a unit last one.  The handle keeps them until others are bound to the layer."""
+    _, _, _, dtype, device, d, _, caches = _attn_shapes[attn]
     for c in (k_cache, v_cache):
         if (tuple(c.shape) != (d.n_blocks, d.block_tokens, d.n_kv_heads, d.head_dim) or c.dtype is not dtype
                 or c.get_device() != device):
@@ -602,6 +603,7 @@ def pw_attn_bind(attn, layer, k_cache, v_cache):
     if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
         raise ValueError("the caches must have the same strides and a contiguous last dimension")
     _check(lib().pw_attn_bind(attn, layer, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3]))
+    caches[layer] = k_cache, v_cache
 
 
 def pw_make_step(ctx_len, new_len, table, q_start, kv_len, slot, pos, max_new, rows=None, groups=None, shared_len=None):
@@ -633,17 +635,18 @@ def pw_kv_map(attn, step, new_ids, stream=None):
 
 
 def pw_attn_plan(attn, plan, step, window=0, doc_start=None, bidir_len=None, stream=None):
-    _, _, _, _, dev, _, plans = _attn_shapes[attn]
+    """The handle keeps the step's tensors until the plan is laid out again."""
+    _, _, _, _, dev, _, plans, _ = _attn_shapes[attn]
     st = lib().pw_attn_plan(attn, plan, _step_on(step, dev), window, _addr(doc_start, dev, step.n_tokens),
                             _addr(bidir_len, dev, step.R), _cuda_stream(stream))
     if st:
         _check(st)
-    plans[plan] = step.n_tokens
+    plans[plan] = step.n_tokens, step.refs
 
 
 def pw_attn_append(attn, layer, step, k, v, stream=None):
     """k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last one."""
-    _, h, d, dtype, dev, _, _ = _attn_shapes[attn]
+    _, h, d, dtype, dev, _, _, _ = _attn_shapes[attn]
     n = step.n_tokens
     st = lib().pw_attn_append(attn, layer, _step_on(step, dev), *_rows(k, n, h, d, dtype, dev), *_rows(v, n, h, d, dtype, dev),
                               _cuda_stream(stream))
@@ -654,8 +657,8 @@ def pw_attn_append(attn, layer, step, k, v, stream=None):
 def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, slopes=None, stream=None):
     """q and o: [n_tokens][n_heads][head_dim], any strides with a unit last one; scale defaults to
     1 / sqrt(head_dim)."""
-    h, _, d, dtype, dev, _, plans = _attn_shapes[attn]
-    n = plans.get(plan, 0)
+    h, _, d, dtype, dev, _, plans, _ = _attn_shapes[attn]
+    n = plans[plan][0] if plan in plans else 0
     st = lib().pw_attn_forward(attn, layer, plan, *_rows(q, n, h, d, dtype, dev), *_rows(o, n, h, d, dtype, dev),
                                _addr(lse, dev, n * h, "float32"), d ** -0.5 if scale is None else scale, softcap,
                                _addr(slopes, dev, h, "float32"), _cuda_stream(stream))

@@ -50,7 +50,7 @@ def test_calls_refuse_tensors_of_another_device_than_the_handle(monkeypatch):
                            max_requests=2, max_tokens=4, max_shared_tokens=0, n_plans=1, device=1)
     monkeypatch.setattr(pw, "lib", NoLibrary)
     step()  # (loads the types)
-    monkeypatch.setitem(pw._attn_shapes, 7, (4, 2, 8, torch.bfloat16, 1, desc, {}))
+    monkeypatch.setitem(pw._attn_shapes, 7, (4, 2, 8, torch.bfloat16, 1, desc, {}, {}))
 
     def rows(h, device=1, dtype=torch.bfloat16):
         return On(torch.zeros(4, h, 8, dtype=dtype), device)

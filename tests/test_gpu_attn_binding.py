@@ -59,3 +59,44 @@ def test_tensors_of_another_type_of_the_same_size_are_refused(dtype):
     make()
     s.compare()
     s.close()
+
+
+def test_a_plan_keeps_its_step_and_a_binding_its_caches():
+    """The caller's references may go: the table and the caches stay until another step is planned, others are
+    bound, or the handle is destroyed."""
+    import torch
+    import weakref
+    s = Step([100, 40], [1, 2], D=64, n_plans=2)
+    pw = s.pw
+    s.map_and_append()
+    want = s.forward()
+    kept = [weakref.ref(s.table), weakref.ref(s.kv[0]), weakref.ref(s.kv[1])]
+    q, attn, ctx, shapes = s.q, s.attn, (s.N, s.Hq, s.D), [c.shape for c in s.kv]
+    pw.pw_attn_plan(attn, 1, s.step)
+    new = dict(ctx_len=s.step.refs[0], new_len=s.step.refs[1], table=s.table.clone(), q_start=s.q_start, kv_len=s.kv_len,
+               slot=s.slot, pos=s.pos, max_new=2)
+    s.table = s.kv = s.step = None
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    junk = [torch.full(sh, float("nan"), dtype=s.dt, device="cuda") for sh in shapes for _ in range(4)]
+    o = torch.empty(*ctx, dtype=s.dt, device="cuda")
+    pw.pw_attn_forward(attn, 0, 0, q, o)
+    pw.pw_attn_check(attn)
+    assert np.array_equal(o.float().cpu().numpy(), want[0])
+    step = pw.pw_make_step(**new)
+    pw.pw_attn_plan(attn, 0, step)
+    gc.collect()
+    assert kept[0]() is not None  # plan 1 still has it
+    pw.pw_attn_plan(attn, 1, step)
+    gc.collect()
+    assert kept[0]() is None
+    pw.pw_attn_check(attn)
+    pw.pw_attn_bind(attn, 0, *[j for j in junk[:2]])
+    gc.collect()
+    assert kept[1]() is None and kept[2]() is None
+    table = weakref.ref(new.pop("table"))
+    junk = weakref.ref(junk.pop(0))
+    pw.pw_attn_destroy(attn)
+    step = None
+    gc.collect()
+    assert table() is None and junk() is None
