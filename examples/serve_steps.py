@@ -67,6 +67,7 @@ class Server:
         # the system prompt, request -1 of the allocator: its blocks head the tables of all requests
         self.system = system_tokens // BLOCK * BLOCK
         if self.system:
+            self.stream.wait_stream(torch.cuda.current_stream())  # the table is filled
             with torch.cuda.stream(self.stream):
                 x = torch.randn(self.system, sh.H, generator=g).to(torch.bfloat16).to(self.dev)
                 self._step([0], [0], [self.system], x, keys=[-1], share=False)
@@ -113,7 +114,8 @@ class Server:
         return x
 
     def step(self, hidden):
-        """hidden: {request: bf16 [new][H]}; the outputs, likewise."""
+        """hidden: {request: bf16 [new][H]}; the outputs, likewise, complete on return."""
+        self.stream.wait_stream(torch.cuda.current_stream())  # where the hidden states were made
         names = list(hidden)
         new = [hidden[r].shape[0] for r in names]
         with torch.cuda.stream(self.stream):

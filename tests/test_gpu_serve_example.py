@@ -45,3 +45,22 @@ def test_token_by_token_is_the_prompt_at_once(serve):
         s.close()
     err = (out[0] - out[1]).norm(dim=1) / out[0].norm(dim=1)
     assert (err < 0.03).float().mean() >= 0.8 and err.max() < 1.0, err
+
+
+def test_inputs_that_another_stream_is_still_writing(serve):
+    """Hidden states made on the caller's current stream just before the call are waited for."""
+    import torch
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn(5, 128, generator=g).to(torch.bfloat16).cuda()
+    out = []
+    for late in (False, True):
+        s = serve.Server(48, max_requests=4, max_tokens=64, n_blocks=32)
+        s.admit(0)
+        h = torch.zeros_like(x)
+        torch.cuda.synchronize()
+        if late:
+            torch.cuda._sleep(100_000_000)  # about 50 ms
+        h.copy_(x)
+        out.append(s.step({0: h})[0].float())
+        s.close()
+    assert torch.equal(out[0], out[1])
