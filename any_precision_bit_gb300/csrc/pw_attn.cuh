@@ -1960,7 +1960,7 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
     if (a.device < 64) done.fetch_or(bit, std::memory_order_relaxed);
   }
   if (cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(C::kThreads), (size_t)C::kSmem, st, maps, a)) return (int)e;
-  if (!a.join) return (int)cudaGetLastError();
+  if (!a.join) return 0;
   // (a split ends a CTA's share, so that there are at most a.ctas of them with two streams of 32 column groups each: not
   // more than 16 pieces of work for a CTA here, as redo_join counts on)
   return (int)launch_pdl(attn_join_kernel<FORM, DP, BF>, dim3(4 * a.ctas), dim3(128), 0, st, a);
