@@ -733,9 +733,8 @@ __device__ __forceinline__ float largest_magnitude(const float (&x)[N]) {
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 
-// kGeneral: scores of the keys base + i to log2 units with cap and bias.  tanh(y) = y P(y^2) with a polynomial of
-// degree 4 (fitted at Chebyshev nodes on |y| <= 1/2; largest error 3.8e-8), on the multiply-add pipe; a
-// warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, with two special-function
+// kGeneral: scores of the keys base + i to log2 units with cap and bias.  tanh(y) is a polynomial
+// (kTanhPoly, |y| <= 1/2) on the multiply-add pipe; a warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, with two special-function
 // operations for each score.  (tanh itself in one such operation is off by 2^-11: capped scores, and so
 // probabilities, would lose as much.)
 // Scores are consecutive keys, or (PAIRS) pairs of them eight apart.
@@ -750,8 +749,8 @@ __device__ __forceinline__ void transform(const AttnArgs &a, float (&x)[N], bool
       for (int i = 0; i < N; ++i) x[i] = cap2 - 2.f * cap2 * rcp(ex2(x[i] * t2) + 1.f);
     } else {
       const uint64_t s = pair(inv, inv);
-      const float c1 = -0.3333307206630707f * cap2, c2 = 0.13324828445911407f * cap2, c3 = -0.05298924073576927f * cap2,
-                  c4 = 0.017141319811344147f * cap2;
+      constexpr float p1 = (float)kTanhPoly[1], p2 = (float)kTanhPoly[2], p3 = (float)kTanhPoly[3], p4 = (float)kTanhPoly[4];
+      const float c1 = p1 * cap2, c2 = p2 * cap2, c3 = p3 * cap2, c4 = p4 * cap2;
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         const uint64_t y = mul2(pair(x[i], x[i + 1]), s), u = mul2(y, y);

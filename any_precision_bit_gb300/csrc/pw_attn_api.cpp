@@ -456,10 +456,8 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.scale2 = scale * 1.4426950408889634f;
   g.cap2 = softcap * 1.4426950408889634f;
   g.inv_cap = softcap > 0.f ? std::clamp(scale / softcap, -FLT_MAX, FLT_MAX) : 0.f;  // (0 scores stay 0)
-  // tanh(y) = y P(y^2), |y| <= 1/2 (see pw_attn.cuh)
-  const double poly[5] = {1.0, -0.3333307206630707, 0.13324828445911407, -0.05298924073576927, 0.017141319811344147};
   double power = (double)g.cap2 * g.inv_cap;
-  for (int i = 0; i < 5; ++i, power *= (double)g.inv_cap * g.inv_cap) g.cap_poly[i] = (float)(poly[i] * power);
+  for (int i = 0; i < 5; ++i, power *= (double)g.inv_cap * g.inv_cap) g.cap_poly[i] = (float)(kTanhPoly[i] * power);
   g.marks = a->marks;
   g.err = a->err;
   g.wait_cycles = a->wait_cycles;

@@ -34,14 +34,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t sbo
          (1ull << 46) | (2ull << 61);
 }
 
-// Descriptor of an operand that is contiguous along its M or N direction (64 elements = one 128-byte
-// swizzled row per K index): `block_bytes` between 64-element blocks of that direction, K indices in
-// groups of 8 rows of 128 bytes, 1 KB apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
 // Instruction descriptor of kind::f16 with fp16 A and B (K-major), fp32 accumulation.
 __host__ __device__ __forceinline__ uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
