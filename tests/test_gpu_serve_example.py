@@ -64,3 +64,48 @@ def test_inputs_that_another_stream_is_still_writing(serve):
         out.append(s.step({0: h})[0].float())
         s.close()
     assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("cuts", [[37], [20, 1, 1, 1, 9, 1, 1, 1, 2], [5] + [1] * 32])
+def test_attention_of_every_token_is_the_formula(serve, monkeypatch, cuts):
+    """Layer 0 of the example, whose attention comes before any expert: its outputs for every token of a prompt that
+    comes in parts, against float64 over all keys of the system prompt and the tokens before.  One rounding of each
+    probability and one of the result (2^-8 each), and 1e-4 for the fp32 steps."""
+    import numpy as np
+    import torch
+    seen = {"k": [], "v": [], "q": [], "o": []}
+    append, forward = serve.pw.pw_attn_append, serve.pw.pw_attn_forward
+
+    def keep(name, t):
+        seen[name].append(t.float().cpu().numpy().astype(np.float64))
+
+    def record_append(attn, layer, step, k, v, stream=None):
+        append(attn, layer, step, k, v, stream=stream)
+        if layer == 0:
+            keep("k", k), keep("v", v)
+
+    def record_forward(attn, layer, plan, q, o, stream=None, **kw):
+        forward(attn, layer, plan, q, o, stream=stream, **kw)
+        if layer == 0:
+            assert kw == dict(softcap=30.0)
+            keep("q", q), keep("o", o)
+
+    monkeypatch.setattr(serve.pw, "pw_attn_append", record_append)
+    monkeypatch.setattr(serve.pw, "pw_attn_forward", record_forward)
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn(37, 128, generator=g).to(torch.bfloat16).cuda()
+    s = serve.Server(48, max_requests=4, max_tokens=64, n_blocks=32)
+    s.admit(0)
+    for part in x.split(cuts):
+        s.step({0: part.contiguous()})
+    s.close()
+    k, v, q, o = (np.concatenate(seen[n]) for n in "kvqo")
+    assert len(k) == len(o) == 48 + 37
+    for t in range(48 + 37):
+        for h in range(serve.N_HEADS):
+            kv = h * serve.N_KV_HEADS // serve.N_HEADS
+            y = 30.0 * np.tanh(k[:t + 1, kv] @ q[t, h] / serve.HEAD_DIM ** 0.5 / 30.0)
+            p = np.exp(y - y.max())
+            p /= p.sum()
+            want, size = p @ v[:t + 1, kv], p @ np.abs(v[:t + 1, kv])
+            assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * (np.abs(want) + size) + 1e-4 * size).all(), (t, h)
