@@ -14,9 +14,9 @@
 //
 // Memory bounds the few-row form: 64 rows of 4 behind 0.26 to 8 thousand keys move 1.13 GB in 172 to 178 us, 6.4 to
 // 6.6 TB/s; two producer warps (one for K, one for V) reached 5.2 TB/s, the copies' issue being their limit.  The
-// two-tile form runs an 8192-token prompt of 32/8 heads of 128 at 1.42 PFLOP/s (387 us): a stream waits for its own
-// products (512 + 512 cycles and 350 of latency) behind its softmax (1800 cycles), and tensor memory has no room for a
-// second score buffer beside two streams' S and O.
+// two-tile form runs an 8192-token prompt of 32/8 heads of 128 at 1.42 PFLOP/s (388 us): a stream waits for its own
+// products (512 + 512 cycles and 350 of latency) behind its softmax (1800 cycles), and tensor memory has no room for
+// a second buffer of 128 scores beside two streams' S and O.
 #pragma once
 #include <cuda_runtime.h>
 

@@ -504,8 +504,8 @@ typedef struct {
     int R;                  /* requests, 1 .. max_requests */
     int n_tokens;           /* rows of slot and pos: at least the sum of new_len.  Rows past that sum
                                are padding: slot and pos -1, no cache write, o = 0 */
-    int max_new;            /* the largest new_len, or an upper bound of it (it chooses tile sizes;
-                               results do not depend on it) */
+    int max_new;            /* the largest new_len, or an upper bound of it (it chooses tile sizes, and
+                               with them the order in which sums are rounded) */
     int table_rows, table_stride; /* rows of table, and entries of a row */
     const int32_t *ctx_len; /* [R] */
     const int32_t *new_len; /* [R], each may be 0 */
