@@ -31,6 +31,12 @@ constexpr int kJoinTwo = 2, kJoinSpread = 16;
 // Rows of 256 bytes, or heads outermost: both alike (8 heads of 128 212 and 214).
 constexpr int64_t kReuseBytes = 48 << 20;
 
+// A forward over shared prefixes begins its last kernel while the one before adds results up, or computes rows again
+// there: at most 32 rows a warp in each of 16 pieces of work, at 0.24 us a key alone and 0.4 us with all warps at it.
+// That kernel's waits last so many SM cycles longer for each key that a row may see (16384 keys: 4 s).  (Waiting for the
+// other kernel in the waits themselves made prefix-64 1.4 us slower.)
+constexpr int64_t kRedoCycles = 32 * 16 * 1024;
+
 pw_status bad(const char *msg) { return report(nullptr, PW_ERR_INVALID, msg); }
 pw_status cuda_failed(const char *what, int e) {
   cudaGetLastError();
@@ -490,6 +496,7 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
     if (pw_status st = launch(p.groups)) return st;
     g.to_prefix = 0;
     g.after_prefix = 1;
+    g.wait_cycles += p.reach * kRedoCycles;
   }
   // Where tiles are few, each is split among many CTAs, and a kernel of its own adds up the pieces: from so many
   // pieces a tile on average.

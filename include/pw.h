@@ -575,7 +575,8 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
 /* Fault injection for testing (no GPU fault is ever made), as pw_set_fault's kinds: 4 = with n != 0, the next
  * pw_attn_forward withholds one barrier arrival, so that the bounded waits on it expire (its outputs are invalid
  * and pw_attn_check reports PW_ERR_TIMEOUT, after which the handle is usable as before); 5 = bounded device waits
- * give up after about n microseconds (0: the default, about 2 s).  PW_ERR_INVALID for another kind or n < 0. */
+ * give up after about n microseconds (0: the default, about 2 s; behind shared prefixes 0.3 ms later for each key that
+ * a row may see).  PW_ERR_INVALID for another kind or n < 0. */
 pw_status pw_attn_set_fault(pw_attn *a, int kind, int n);
 /* Wait for `stream` and report what the handle's calls found since the last check: PW_ERR_TIMEOUT if a
  * bounded device wait expired, PW_ERR_STATE for the findings of pw_kv_map and for a forward whose plan was laid out

@@ -156,3 +156,17 @@ def test_unwritten_values_beside_quarters_of_a_tile_without_rows(ctx, new, kw):
         if fill == 0.0:
             s.compare(**kw)
         s.close()
+
+
+@pytest.mark.parametrize("new,R", [(1, 40), (20, 10)])
+def test_the_waits_behind_a_shared_prefix_do_not_depend_on_what_its_values_hold(new, R):
+    """The kernel behind the prefix begins while that one's results are added up, and its waits of 3 ms with it; rows
+    that are computed again there take longer."""
+    s = Step([16384 + 10] * R, [new] * R, Hq=64, Hkv=64, D=8, bt=128, group_start=[0, R], prefix=16384)
+    s.map_and_append()
+    s.pw.pw_attn_set_fault(s.attn, 5, 3000)
+    s.forward()
+    bad_at(s, [100] + [None] * (R - 1), float("inf"))
+    got, _ = s.forward()
+    assert (got == np.inf).all()
+    s.close()
