@@ -170,3 +170,19 @@ def test_the_waits_behind_a_shared_prefix_do_not_depend_on_what_its_values_hold(
     got, _ = s.forward()
     assert (got == np.inf).all()
     s.close()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("prefix,per", [(256, 4), (1024, 2)])
+def test_a_bad_value_in_some_of_many_shared_prefixes(prefix, per, value):
+    """More tiles of prefixes than SMs, so that many of them are whole."""
+    groups = 100
+    R = groups * per
+    ctx = prefix + np.random.default_rng(4).integers(0, 120, size=R)
+    s = Step(ctx, [1 + r % 2 for r in range(R)], Hq=4, Hkv=2, D=64, bt=32, group_start=list(range(0, R + 1, per)), prefix=prefix)
+    s.map_and_append()
+    at = prefix - 30
+    bad_at(s, [at if r % (3 * per) == 0 else None for r in range(R)], value)
+    where = [at if r // per % 3 == 0 else None for r in range(R)]
+    check(s, where, value, dict(window=100))
+    s.close()
