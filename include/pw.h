@@ -478,7 +478,7 @@ pw_status pw_kv_get_stats(pw_kv *kv, pw_kv_stats *out);
  *   o = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)  (natural logarithm).
  * A row that sees no key gets o = 0 and lse = -infinity.  Keys and values a row does not see do
  * not reach it, whatever bits they hold.  (Infinities and NaN among the values of a step's requests cost time: rows in
- * whose key tiles they lie are computed again, key by key.)  Products of q and k and the softmax sums are fp32; the
+ * whose key tiles they lie are computed again, by one warp a row at 0.1 to 0.4 us a key.)  Products of q and k and the softmax sums are fp32; the
  * probabilities are rounded to the cache's type for the product with v, which is summed in fp32. */
 enum { PW_BF16 = 0, PW_FP16 = 1 };
 
