@@ -21,6 +21,7 @@ PW_ACCUMULATE = 1
 PW_PRENORM = 2
 PW_PAGE_GPU, PW_PAGE_CPU, PW_PAGE_TO_CPU, PW_PAGE_TO_GPU = range(4)
 PW_BF16, PW_FP16 = range(2)
+PW_TREE_NODES = 256
 STATUS_NAMES = {0: "PW_OK", 1: "PW_ERR_INVALID", 2: "PW_ERR_CUDA", 3: "PW_ERR_OOM",
                 4: "PW_ERR_STATE", 5: "PW_ERR_TIMEOUT", 6: "PW_ERR_BUSY",
                 7: "PW_ERR_RANGE"}
@@ -89,7 +90,7 @@ class pw_plan_problem(C.Structure):
 
 class pw_attn_desc(C.Structure):
     _fields_ = [(n, C.c_int) for n in ("L", "n_heads", "n_kv_heads", "head_dim", "dtype", "n_blocks", "block_tokens",
-                                       "max_requests", "max_tokens", "max_shared_tokens", "n_plans", "device")]
+                                       "max_requests", "max_tokens", "max_shared_tokens", "n_plans", "device", "max_tree_tokens")]
 
 
 class pw_kv_step(C.Structure):
@@ -97,6 +98,15 @@ class pw_kv_step(C.Structure):
                 ("table_stride", C.c_int), ("ctx_len", C.c_void_p), ("new_len", C.c_void_p), ("rows", C.c_void_p),
                 ("table", C.c_void_p), ("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("slot", C.c_void_p),
                 ("pos", C.c_void_p), ("n_groups", C.c_int), ("group_start", C.c_void_p), ("shared_len", C.c_void_p)]
+
+
+class pw_rope_desc(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("interleaved", C.c_int), ("n_axes", C.c_int), ("inv_freq", C.c_void_p),
+                ("axis", C.c_void_p), ("scale", C.c_float), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p), ("eps", C.c_float)]
+
+
+class pw_tree(C.Structure):
+    _fields_ = [("tree_len", C.c_void_p), ("parent", C.c_void_p), ("parent_stride", C.c_int), ("pos", C.c_void_p)]
 
 
 _P = C.c_void_p
@@ -143,6 +153,10 @@ _SIGS = {
     "pw_kv_request": [_P, C.c_int64, C.POINTER(C.c_int64), C.POINTER(C.c_int64)],
     "pw_kv_blocks": [_P, C.c_int64, _P, C.c_int64, C.POINTER(C.c_int64)],
     "pw_kv_get_stats": [_P, C.POINTER(pw_kv_stats)],
+    "pw_kv_fork": [_P, C.c_int64, C.c_int64, C.c_int64],
+    "pw_kv_unshare": [_P, C.c_int64, C.c_int64, C.POINTER(C.c_int32), C.POINTER(C.c_int32)],
+    "pw_kv_trim": [_P, C.c_int64, C.c_int64, C.POINTER(C.c_int64)],
+    "pw_kv_compact": [_P, C.c_int64, _P, _P, C.c_int64, C.POINTER(C.c_int64)],
     "pw_attn_create": [C.POINTER(pw_attn_desc), C.POINTER(C.c_void_p)],
     "pw_attn_destroy": [_P],
     "pw_attn_bind": [_P, _I, _P, _P, _L, _L, _L],
@@ -150,6 +164,11 @@ _SIGS = {
     "pw_attn_plan": [_P, _I, _P, _I, _P, _P, _P],
     "pw_attn_append": [_P, _I, _P, _P, _L, _L, _P, _L, _L, _P],
     "pw_attn_forward": [_P, _I, _I, _P, _L, _L, _P, _L, _L, _P, _F, _F, _P, _P],
+    "pw_attn_set_rope": [_P, _I, C.POINTER(pw_rope_desc)],
+    "pw_attn_rope_append": [_P, _I, _P, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _P],
+    "pw_attn_plan_tree": [_P, _I, _P, _I, C.POINTER(pw_tree), _P],
+    "pw_kv_keep": [_P, _P, _P, _P, _I, _P, _P, _P],
+    "pw_kv_copy": [_P, _P, _P, _I, _P, _I, _I, _P],
     "pw_attn_check": [_P, _P],
     "pw_attn_set_fault": [_P, _I, _I],
     "pw_set_profiling": [_P, _I],
@@ -508,6 +527,33 @@ def pw_kv_release(kv, request) -> int:
     return n.value
 
 
+def pw_kv_fork(kv, parent, child, n_blocks):
+    """`child` shares the first n_blocks blocks of `parent`."""
+    _check(lib().pw_kv_fork(kv, int(parent), int(child), int(n_blocks)))
+
+
+def pw_kv_unshare(kv, request, index):
+    """(source, destination) of the copy to make before the request writes to its block number `index`; the same where
+    the block is the request's alone."""
+    src, dst = C.c_int32(), C.c_int32()
+    _check(lib().pw_kv_unshare(kv, int(request), int(index), C.byref(src), C.byref(dst)))
+    return src.value, dst.value
+
+
+def pw_kv_trim(kv, request, n_keep) -> int:
+    n = C.c_int64()
+    _check(lib().pw_kv_trim(kv, int(request), int(n_keep), C.byref(n)))
+    return n.value
+
+
+def pw_kv_compact(kv, limit):
+    """Blocks that move below `limit`, as int32 arrays (sources, destinations)."""
+    cap = pw_kv_get_stats(kv)["used_blocks"]
+    src, dst, n = np.zeros(max(cap, 1), dtype=np.int32), np.zeros(max(cap, 1), dtype=np.int32), C.c_int64()
+    _check(lib().pw_kv_compact(kv, int(limit), src.ctypes.data, dst.ctypes.data, cap, C.byref(n)))
+    return src[:n.value], dst[:n.value]
+
+
 def pw_kv_request(kv, request):
     """(blocks held, blocks announced) of a request."""
     held, ann = C.c_int64(), C.c_int64()
@@ -534,6 +580,7 @@ def pw_kv_get_stats(kv) -> dict:
 # handle: (n_heads, n_kv_heads, head_dim, the caches' and rows' type, device, desc, plans, caches), with
 # {plan: (its step's n_tokens, the step's tensors)} and {layer: its caches}: the library keeps their addresses
 _attn_shapes = {}
+_rope_axes = {}  # axes of a (handle, layer)'s rotation
 _types = {}  # torch's, by name
 
 
@@ -589,6 +636,8 @@ def pw_attn_create(desc: pw_attn_desc):
 
 def pw_attn_destroy(attn):
     kept = _attn_shapes.pop(attn, None)  # noqa: F841 (until the device's work is done)
+    for key in [k for k in _rope_axes if k[0] == attn]:
+        del _rope_axes[key]
     lib().pw_attn_destroy(attn)
 
 
@@ -662,6 +711,74 @@ def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, 
     st = lib().pw_attn_forward(attn, layer, plan, *_rows(q, n, h, d, dtype, dev), *_rows(o, n, h, d, dtype, dev),
                                _addr(lse, dev, n * h, "float32"), d ** -0.5 if scale is None else scale, softcap,
                                _addr(slopes, dev, h, "float32"), _cuda_stream(stream))
+    if st:
+        _check(st)
+
+
+def pw_attn_set_rope(attn, layer, inv_freq, axis=None, n_axes=1, interleaved=False, scale=1.0, q_gain=None, k_gain=None,
+                     eps=1e-6):
+    """inv_freq: [rot_dim / 2] on the host (empty: no rotation); axis: as many ints; gains: fp32 [head_dim], host or device."""
+    _, _, d, _, dev, _, _, _ = _attn_shapes[attn]
+    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    axes = None if axis is None else np.ascontiguousarray(axis, dtype=np.int32)
+    if axes is not None and axes.size != freq.size:
+        raise ValueError("inv_freq and axis have an element for each pair")
+
+    def gain(g):
+        if g is None or hasattr(g, "get_device") and g.get_device() >= 0:
+            return _addr(g, dev, d, "float32")
+        g = np.ascontiguousarray(g, dtype=np.float32)
+        if g.size < d:
+            raise ValueError("a gain has an element for each of the head's")
+        keep.append(g)
+        return g.ctypes.data
+    keep = []
+    desc = pw_rope_desc(rot_dim=2 * freq.size, interleaved=int(interleaved), n_axes=int(n_axes), inv_freq=freq.ctypes.data,
+                        axis=None if axes is None else axes.ctypes.data, scale=float(scale), q_gain=gain(q_gain),
+                        k_gain=gain(k_gain), eps=float(eps))
+    _check(lib().pw_attn_set_rope(attn, layer, C.byref(desc)))
+    _rope_axes[attn, layer] = desc.n_axes
+
+
+def pw_attn_rope_append(attn, layer, step, q, q_out, k, v, pos=None, stream=None):
+    """q and q_out: [n_tokens][n_heads][head_dim], k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last
+    one; pos: int32 [n_axes][n_tokens], or None for the step's."""
+    hq, h, d, dtype, dev, _, _, _ = _attn_shapes[attn]
+    n = step.n_tokens
+    st = lib().pw_attn_rope_append(attn, layer, _step_on(step, dev), *_rows(q, n, hq, d, dtype, dev),
+                                   *_rows(q_out, n, hq, d, dtype, dev), *_rows(k, n, h, d, dtype, dev),
+                                   *_rows(v, n, h, d, dtype, dev), _addr(pos, dev, n * _rope_axes.get((attn, layer), 1)),
+                                   _cuda_stream(stream))
+    if st:
+        _check(st)
+
+
+def pw_attn_plan_tree(attn, plan, step, tree_len, parent, pos=None, window=0, stream=None):
+    """tree_len: int32 [R]; parent: int32 [R][nodes]; pos: int32 [n_tokens], filled.  The handle keeps the step's tensors
+    and these until the plan is laid out again."""
+    _, _, _, _, dev, _, plans, _ = _attn_shapes[attn]
+    tree = pw_tree(tree_len=_addr(tree_len, dev, step.R), parent=_addr(parent, dev, step.R * parent.shape[1]),
+                   parent_stride=parent.shape[1], pos=_addr(pos, dev, step.n_tokens))
+    st = lib().pw_attn_plan_tree(attn, plan, _step_on(step, dev), window, C.byref(tree), _cuda_stream(stream))
+    if st:
+        _check(st)
+    plans[plan] = step.n_tokens, (step.refs, tree_len, parent, pos)
+
+
+def pw_kv_keep(attn, step, tree_len, keep, n_keep, ctx_out=None, stream=None):
+    """tree_len and n_keep: int32 [R]; keep: int32 [R][nodes]; ctx_out: int32 [R], filled."""
+    dev, R = _attn_shapes[attn][4], step.R
+    st = lib().pw_kv_keep(attn, _step_on(step, dev), _addr(tree_len, dev, R), _addr(keep, dev, R * keep.shape[1]), keep.shape[1],
+                          _addr(n_keep, dev, R), _addr(ctx_out, dev, R), _cuda_stream(stream))
+    if st:
+        _check(st)
+
+
+def pw_kv_copy(attn, src, dst, table=None, stream=None):
+    """src and dst: int32 [n]; table: int32 [rows][blocks] whose entries src become dst."""
+    dev, n = _attn_shapes[attn][4], src.numel()
+    rows, stride = (0, 0) if table is None else table.shape
+    st = lib().pw_kv_copy(attn, _addr(src, dev), _addr(dst, dev, n), n, _addr(table, dev), rows, stride, _cuda_stream(stream))
     if st:
         _check(st)
 

@@ -1,5 +1,6 @@
 // pw_attn.cuh -- attention over the paged key/value cache: the kernel and its launch, instantiated form by
-// form in pw_attn_two.cu and pw_attn_spread.cu.
+// form in pw_attn_two.cu and pw_attn_spread.cu, and for trees of drafted tokens (TREE) in pw_attn_two_tree.cu and
+// pw_attn_spread_tree.cu.
 //
 // For a query row q with keys lo <= j < hi, x_j = scale q.k_j (capped, biased) and o = sum_j e^{x_j} v_j / sum_j
 // e^{x_j}, in one pass over the keys: with m a running reference, l = sum 2^{x_j log2 e - m} and O = sum
@@ -19,6 +20,7 @@
 // a second buffer of 128 scores beside two streams' S and O.
 #pragma once
 #include <cuda_runtime.h>
+#include <limits.h>
 
 #include <atomic>
 #include <type_traits>
@@ -628,6 +630,28 @@ __device__ __forceinline__ float largest_magnitude(const float (&x)[N]) {
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 
+// Trees of drafted tokens.  Bits of the keys from .. from + 31, `from` counted from the tree's first node: those that the
+// row of these words sees.  Keys before the tree count as `before`, all ones or zeros.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *seen, int from, uint32_t before) {
+  if (from <= -32) return before;
+  if (from >= PW_TREE_NODES) return 0;
+  const int w = from >> 5;
+  return __funnelshift_r(w < 0 ? before : seen[w], w + 1 < kTreeWords ? seen[w + 1] : 0u, from & 31);
+}
+// Nodes that the row sees among the first n of its tree.  (A node's distance from one of its ancestors is the number of its
+// ancestors behind that one, with itself and without that one: nodes ascend along a path.)
+__device__ __forceinline__ int tree_count(const uint32_t *seen, int n) {
+  int c = 0;
+#pragma unroll
+  for (int w = 0; w < kTreeWords; ++w) {
+    const int m = min(max(n - 32 * w, 0), 32);
+    if (m > 0) c += __popc(seen[w] & (m == 32 ? 0xffffffffu : (1u << m) - 1u));
+  }
+  return c;
+}
+// The row of a token that is in a tree; rows in none have their tree behind every key.
+__device__ __forceinline__ const uint32_t *tree_row(const AttnArgs &a, int tok) { return a.seen + (size_t)tok * kTreeWords; }
+
 // kGeneral: scores of the keys base + i to log2 units with cap and bias.  tanh(y) is a polynomial
 // (kTanhPoly, |y| <= 1/2) on the multiply-add pipe; a warp that meets a larger |y| takes 1 - 2 / (1 + e^(2y)) for the tile, with two special-function
 // operations for each score.  (tanh itself in one such operation is off by 2^-11: capped scores, and so
@@ -678,6 +702,23 @@ __device__ __forceinline__ void mask_out(float (&x)[N], int lo, int hi, float va
     const uint32_t seen = below_h & ~below_l;
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[32 * c + i] = seen >> i & 1u ? x[32 * c + i] : value;
+  }
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+// The same for rows in a tree: also the keys whose bit in `seen` is not set.
+template <int N>
+__device__ __forceinline__ void mask_tree(float (&x)[N], int lo, int hi, const Words<N / 32> &seen, float value) {
+#pragma unroll
+  for (int c = 0; c < N / 32; ++c) {
+    const int l = min(max(lo - 32 * c, 0), 32), h = min(max(hi - 32 * c, 0), 32);
+    const uint32_t below_h = h == 32 ? 0xffffffffu : (1u << h) - 1u, below_l = l == 32 ? 0xffffffffu : (1u << l) - 1u;
+    const uint32_t bits = below_h & ~below_l & seen.w[c];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[32 * c + i] = bits >> i & 1u ? x[32 * c + i] : value;
   }
 }
 
@@ -836,8 +877,8 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, const RowOut &r) {
 // keep within fp32 however many keys they meet).  Eight lanes share a key, lane l its elements 8 (l % 8) .. + 7 and 64 + 8
 // (l % 8) .. + 7, and 4 KEYS keys are under way at a time, KEYS to each quarter of the warp.  Only visible keys and
 // values count.  acc is the output in all lanes (zeros for a row without keys).
-template <bool BF, int KEYS>
-__device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, int trow, int pos, float lse2,
+template <bool BF, int KEYS, bool TREE>
+__device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, int trow, int pos, int tree0, float lse2,
                               float (&acc)[16]) {
   const int lane = threadIdx.x & 31, sub = lane >> 3, d = 8 * (lane & 7);
   const int hk = h / a.G, mask = (1 << a.log_bt) - 1;
@@ -861,6 +902,9 @@ __device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, i
     spread(zeros_but(has[half], *reinterpret_cast<const uint4 *>(a.q + t * a.q_token + h * a.q_head + col[half])), q + 8 * half);
   const int *table = a.table + (trow >= 0 ? (size_t)trow * a.table_stride : 0);
   const float slope = a.slopes ? a.slopes[h] : 0.f;
+  // what the row sees of its tree's nodes; all in all
+  auto node_seen = [&](int j) { return tree_row(a, t)[(j - tree0) >> 5] >> (j - tree0 & 31) & 1u; };
+  const int nodes = TREE && hi > tree0 && a.slopes ? tree_count(tree_row(a, t), PW_TREE_NODES) : 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll 1
@@ -871,7 +915,7 @@ __device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, i
 #pragma unroll
     for (int u = 0; u < KEYS; ++u) {
       const int j = j0 + 4 * u + sub, page = j >> a.log_bt;
-      const bool in = j < hi && trow >= 0 && page < a.table_stride;
+      const bool in = j < hi && trow >= 0 && page < a.table_stride && !(TREE && j >= tree0 && !node_seen(j));
       id[u] = table[in ? page : 0];
       there[u] = in && id[u] >= 0 && id[u] < a.n_blocks;
     }
@@ -896,8 +940,14 @@ __device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, i
       for (int o = 1; o < 8; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
       y *= a.scale;
       if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
-      if (a.slopes) y -= slope * fabsf((float)(pos - j));
-      const float w = j < hi ? ex2(fmaf(y, kLog2e, -lse2)) : 0.f;
+      float away = fabsf((float)(pos - j));
+      bool seen = j < hi;
+      if (TREE && seen && j >= tree0) {
+        seen = node_seen(j);
+        if (a.slopes) away = (float)(nodes - tree_count(tree_row(a, t), j - tree0 + 1));
+      }
+      if (a.slopes) y -= slope * away;
+      const float w = seen ? ex2(fmaf(y, kLog2e, -lse2)) : 0.f;
 #pragma unroll
       for (int half = 0; half < 2; ++half) spread(zeros_but(there[u] && has[half], v[u][half]), x + 8 * half);
 #pragma unroll
@@ -914,14 +964,14 @@ __device__ void row_attention(const AttnArgs &a, int t, int h, int lo, int hi, i
 // A row whose sum is finite but whose output is not: a value is infinite or NaN, possibly one that the row
 // does not see (0 times it in the product with v).  Again, from the row's visible keys alone, by the warp.
 // merge: over the shared prefix too.  lse2: the row's log2-sum-exp2, which is right.  Columns 4 g .. 4 g + 3 are written for the bits g of `groups`.
-template <bool BF, int KEYS>
+template <bool BF, int KEYS, bool TREE>
 static __device__ PW_RARE void redo_row(const AttnArgs &a, int tok, int head, int klo, int khi, int trow, bool merge,
                                         float lse2, uint32_t groups = ~0u) {
   const int lane = threadIdx.x & 31;
   const RowBound b = a.bounds[tok];
   float acc[16];
-  row_attention<BF, KEYS>(a, tok, head, merge ? b.lo : max(b.lo, klo), merge ? b.hi : min(b.hi, khi), trow, b.pos,
-                          lse2, acc);
+  row_attention<BF, KEYS, TREE>(a, tok, head, merge ? b.lo : max(b.lo, klo), merge ? b.hi : min(b.hi, khi), trow, b.pos,
+                                b.trow, lse2, acc);
   if (lane >= 8) return;
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
@@ -952,7 +1002,7 @@ static __device__ __forceinline__ void mark_row(const AttnArgs &a, int tok, int 
 }
 // By the first `warps` of a CTA whose pieces are done, rows dealt out among them.  A CTA looks at the rows of all its pieces;
 // the one that finished a tile has a piece of it, and whoever clears a row's mark computes it.
-template <bool BF, int KEYS>
+template <bool BF, int KEYS, bool TREE>
 static __device__ PW_RARE void redo_marked(const AttnArgs &a, int warps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Walk w(a, true);
@@ -978,7 +1028,7 @@ static __device__ PW_RARE void redo_marked(const AttnArgs &a, int warps) {
       while (flagged) {
         const int src = __ffs(flagged) - 1;
         flagged &= flagged - 1;
-        redo_row<BF, KEYS>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), t.klo, t.khi, t.trow,
+        redo_row<BF, KEYS, TREE>(a, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src), t.klo, t.khi, t.trow,
                            merge, __shfl_sync(0xffffffffu, lse2, src));
       }
     }
@@ -1027,7 +1077,7 @@ struct Group {
 };
 
 // kTwo: the softmax warps of two streams, which write their rows' results, too.
-template <int DP, bool BF, int MODE>
+template <int DP, bool BF, int MODE, bool TREE>
 __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
                        volatile int *abort_flag, volatile int *last_flag, volatile int *marked) {
   using C = Cfg<kTwo, DP>;
@@ -1054,11 +1104,12 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   const int row_tok = s * a.list.tpt + row_t;
   uint32_t pieces = 0;
   bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
-  RowBound rb{0, 0, -1, 0}, rb_ahead{0, 0, -1, 0};
+  const RowBound nobody{0, 0, TREE ? INT_MAX : -1, 0};
+  RowBound rb = nobody, rb_ahead = nobody;
   // the row's keys in a piece, fetched while the piece before is in work
   auto bound_of = [&](const volatile Piece &x) {
     if (x.n == 0 || !x.fresh) return rb;
-    return row_tok < min(x.ntok, (s + 1) * a.list.tpt) ? a.bounds[x.tok0 + row_tok] : RowBound{0, 0, -1, 0};
+    return row_tok < min(x.ntok, (s + 1) * a.list.tpt) ? a.bounds[x.tok0 + row_tok] : nobody;
   };
   if (ok) rb_ahead = bound_of(piece[0]);
   for (; ok; ++pieces) {
@@ -1095,7 +1146,28 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
       }
       if (active) {
         const int l0 = lo - base, h0 = hi - base;
-        const bool edge = __any_sync(0xffffffffu, valid && (l0 > 0 || h0 < NC));
+        // (a row in a tree sees all keys up to the tree, and few of the tree's)
+        const int t0 = TREE ? rb.trow - base : 0;
+        const bool edge = __any_sync(0xffffffffu, valid && (l0 > 0 || (TREE ? min(h0, t0) : h0) < NC));
+        uint32_t nodes[NC / 32];
+        if (TREE && edge) {
+          const uint32_t *of_row = tree_row(a, w.tok0 + row_tok);
+#pragma unroll
+          for (int c = 0; c < NC / 32; ++c) nodes[c] = tree_bits(of_row, 32 * c - t0, 0xffffffffu);
+        }
+        // (without a run-time index, which would put them in memory)
+        auto nodes_from = [&](int c) {
+          Words<CH / 32> r;
+#pragma unroll
+          for (int i = 0; i < CH / 32; ++i) r.w[i] = CH < NC && c ? nodes[(NC - CH) / 32 + i] : nodes[i];
+          return r;
+        };
+        auto hide = [&](float (&y)[CH], int c, float value) {
+          if constexpr (TREE)
+            mask_tree<CH>(y, l0 - c, h0 - c, nodes_from(c), value);
+          else
+            mask_out<CH>(y, l0 - c, h0 - c, value);
+        };
         float x[CH], mx = -INFINITY;
         auto load = [&](int c) {
 #pragma unroll
@@ -1107,10 +1179,23 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         for (int c = 0; c < NC; c += CH) {
           load(c);
           // (hidden scores, which may come from unwritten memory, have no say in how the tile's are capped)
-          if (MODE != kPlain && edge && a.softcap > 0.f) mask_out<CH>(x, l0 - c, h0 - c, 0.f);
+          if (MODE != kPlain && edge && a.softcap > 0.f) hide(x, c, 0.f);
           if (MODE == kCapped) top = fmaxf(top, largest_magnitude(x));
           if (MODE == kGeneral) transform<CH>(a, x, valid, slope, (float)(rb.pos - base - c));
-          if (edge) mask_out<CH>(x, l0 - c, h0 - c, -INFINITY);
+          if (TREE && MODE == kGeneral && edge && a.slopes && t0 < c + CH) {
+            // distances along the tree instead of those between the places in the cache
+            const uint32_t *of_row = tree_row(a, w.tok0 + row_tok);
+            int behind = tree_count(of_row, PW_TREE_NODES) - tree_count(of_row, c - t0);
+            const float d0 = (float)(rb.pos - base - c);
+            const Words<CH / 32> mine = nodes_from(c);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              if (c + i < t0) continue;
+              behind -= mine.w[i / 32] >> (i & 31) & 1u;
+              x[i] = fmaf(slope, fabsf(d0 - (float)i) - (float)behind, x[i]);
+            }
+          }
+          if (edge) hide(x, c, -INFINITY);
           mx = fmaxf(mx, max_of<CH>(x));
           if (MODE == kGeneral && CH < NC) {
 #pragma unroll
@@ -1148,7 +1233,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
           if (CH < NC) load(c0);  // (kGeneral: as transformed)
           if (MODE == kCapped) {
             cap_exponents<CH>(a, x, wide, ms);
-            if (edge) mask_out<CH>(x, l0 - c0, h0 - c0, -INFINITY);
+            if (edge) hide(x, c0, -INFINITY);
           }
 #pragma unroll
           for (int c = 0; c < CH / 32; ++c) {
@@ -1280,7 +1365,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 // thread t holds eight scores of row t / 4 and, where a tile has more than eight rows, eight of the row eight
 // below.  (A lane a row, half of a warp's lanes or more would have nothing to do.)  Four threads share a row: its
 // maximum is made common to them when it is renewed, which each of them may ask for, and its sum at a piece's end.
-template <int DP, bool BF, int MODE>
+template <int DP, bool BF, int MODE, bool TREE>
 __device__ void soften_few(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
                            volatile int *abort_flag) {
   using C = Cfg<kSpread, DP>;
@@ -1305,14 +1390,15 @@ __device__ void soften_few(const AttnArgs &a, const volatile Piece *piece, uint8
     row_h[h] = row - row_t[h] * a.G;
   }
   bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
-  RowBound rb[2] = {{0, 0, -1, 0}, {0, 0, -1, 0}}, ahead[2] = {{0, 0, -1, 0}, {0, 0, -1, 0}};
+  const RowBound nobody{0, 0, TREE ? INT_MAX : -1, 0};
+  RowBound rb[2] = {nobody, nobody}, ahead[2] = {nobody, nobody};
   // the rows' keys in a piece, fetched while the piece before is in work
   auto fetch = [&](const volatile Piece &x) {
     const bool fresh = x.n != 0 && x.fresh;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       ahead[h] = rb[h];
-      if (fresh) ahead[h] = row_t[h] < x.ntok ? a.bounds[x.tok0 + row_t[h]] : RowBound{0, 0, -1, 0};
+      if (fresh) ahead[h] = row_t[h] < x.ntok ? a.bounds[x.tok0 + row_t[h]] : nobody;
     }
   };
   if (ok) fetch(piece[0]);
@@ -1348,8 +1434,11 @@ __device__ void soften_few(const AttnArgs &a, const volatile Piece *piece, uint8
         const int from = min(max(l0, 0), 32), to = min(max(h0, 0), 32);
         const uint32_t below_to = to == 32 ? 0xffffffffu : (1u << to) - 1u;
         const uint32_t below_from = from == 32 ? 0xffffffffu : (1u << from) - 1u;
-        seen[h] = (below_to & ~below_from) >> (2 * (lane & 3));
-        edge = edge || (valid[h] && (l0 > 0 || h0 < 32));
+        const int t0 = TREE ? rb[h].trow - base - 32 * quarter : 0;
+        uint32_t all = below_to & ~below_from;
+        if (TREE && t0 < 32) all &= tree_bits(tree_row(a, w.tok0 + row_t[h]), -t0, 0xffffffffu);
+        seen[h] = all >> (2 * (lane & 3));
+        edge = edge || (valid[h] && (l0 > 0 || (TREE ? min(h0, t0) : h0) < 32));
       }
       edge = __any_sync(0xffffffffu, edge);
       auto hide = [&](int h, float value) {
@@ -1362,6 +1451,20 @@ __device__ void soften_few(const AttnArgs &a, const volatile Piece *piece, uint8
         if (MODE != kPlain && edge && a.softcap > 0.f) hide(h, 0.f);
         if (MODE == kCapped) wide = wide || (valid[h] && !(largest_magnitude(x[h]) * a.inv_cap <= 0.5f));
         if (MODE == kGeneral) transform<8, true>(a, x[h], valid[h], slope[h], (float)(rb[h].pos - base - col0));
+        if (TREE && MODE == kGeneral && a.slopes && rb[h].trow < base + 32 * (quarter + 1)) {
+          // distances along the tree instead of those between the places in the cache
+          const uint32_t *of_row = tree_row(a, w.tok0 + row_t[h]);
+          const int from = base + 32 * quarter - rb[h].trow;
+          const int behind = tree_count(of_row, PW_TREE_NODES) - tree_count(of_row, from);
+          const uint32_t nodes = tree_bits(of_row, from, 0);
+          const float d0 = (float)(rb[h].pos - base - col0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int b = 8 * (i / 2) + i % 2, key = 2 * (lane & 3) + b;
+            if (key + from >= 0)
+              x[h][i] = fmaf(slope[h], fabsf(d0 - (float)b) - (float)(behind - __popc(nodes & (2u << key) - 1u)), x[h][i]);
+          }
+        }
         if (edge) hide(h, -INFINITY);
         mx[h] = max_of(x[h]);
       }
@@ -1699,7 +1802,7 @@ __device__ void finish(const AttnArgs &a, const volatile Piece *piece, uint8_t *
 // Rows of this warp whose columns are not finite: bit `it` of `todo` for the CTA's piece of work number `it`.  Those columns
 // were not stored.  Where pieces of the row are not finite, all CTAs that have such columns of it find the same ones, and
 // one of them computes the row, once; where only the sum overflowed each does so for its columns.
-template <int COLS, bool BF>
+template <int COLS, bool BF, bool TREE>
 static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned todo, int streams) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -1728,7 +1831,7 @@ static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned todo, 
         l = fmaf(ex2(y.x - (m == -INFINITY ? 0.f : m)), y.y, l);
       }
       const float lse2 = row_out(a, tok, head, merge, merge ? a.prefix_lse[(size_t)tok * a.Hq + head] : 0.f, m, l).lse2;
-      redo_row<BF, 1>(a, tok, head, t.klo, t.khi, t.trow, merge, lse2, groups);
+      redo_row<BF, 1, TREE>(a, tok, head, t.klo, t.khi, t.trow, merge, lse2, groups);
     }
   }
 }
@@ -1739,7 +1842,7 @@ static __device__ __noinline__ void redo_join(const AttnArgs &a, unsigned todo, 
 // next kernel's CTAs find room beside these; rows to be computed again take few keys at a time for it, and are done
 // behind the loop.  With the 128 registers that four times as many keys take, 64 requests behind a shared prefix of
 // 4096 were 4 us slower.)
-template <int FORM, int DP, bool BF>
+template <int FORM, int DP, bool BF, bool TREE>
 static __global__ void __launch_bounds__(128, 7) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int kBatch = 8, kCols = DP / 4;
   constexpr int kRows = FORM == kSpread ? kSpreadRows : 128, kShare = 128 / kRows;
@@ -1843,10 +1946,10 @@ static __global__ void __launch_bounds__(128, 7) attn_join_kernel(const __grid_c
       if (c == 0) store_lse(a, out);
     }
   }
-  if (__any_sync(0xffffffffu, todo != 0)) redo_join<kCols, BF>(a, todo, streams);
+  if (__any_sync(0xffffffffu, todo != 0)) redo_join<kCols, BF, TREE>(a, todo, streams);
 }
 
-template <int FORM, int DP, bool BF, int MODE>
+template <int FORM, int DP, bool BF, int MODE, bool TREE>
 __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const __grid_constant__ AttnMaps maps,
                                                                        const __grid_constant__ AttnArgs a) {
   using C = Cfg<FORM, DP>;
@@ -1909,15 +2012,15 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
     if (FORM == kTwo) regs_inc<kRegsSoft>();
     if (!abort_flag) {
       if constexpr (FORM == kSpread)
-        soften_few<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag);
+        soften_few<DP, BF, MODE, TREE>(a, piece, smem, bars, tmem, &abort_flag);
       else
-        soften<DP, BF, MODE>(a, piece, smem, bars, tmem, &abort_flag, last_flag, &marked);
+        soften<DP, BF, MODE, TREE>(a, piece, smem, bars, tmem, &abort_flag, last_flag, &marked);
     }
     if constexpr (FORM == kTwo) {  // (here, where a warp has the registers for it)
       static_assert(FORM != kTwo || C::kSoftWarps == 8, "a barrier of 256 threads");
       __syncwarp();
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
-      if (__all_sync(0xffffffffu, marked && !abort_flag)) redo_marked<BF, 2>(a, C::kSoftWarps);
+      if (__all_sync(0xffffffffu, marked && !abort_flag)) redo_marked<BF, 2, TREE>(a, C::kSoftWarps);
     }
   } else if (warp < C::kProdWarp) {
     if constexpr (FORM == kSpread) {
@@ -1940,14 +2043,14 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
     tmem_dealloc(tmem, kTmemColsAttn);
     __syncwarp();
   }
-  if (FORM == kSpread && __all_sync(0xffffffffu, marked && !abort_flag)) redo_marked<BF, 1>(a, C::kThreads / 32);
+  if (FORM == kSpread && __all_sync(0xffffffffu, marked && !abort_flag)) redo_marked<BF, 1, TREE>(a, C::kThreads / 32);
 }
 
-template <int FORM, int DP, bool BF, int MODE>
+template <int FORM, int DP, bool BF, int MODE, bool TREE>
 static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
   using C = Cfg<FORM, DP>;
   static_assert(C::kStages >= 4, "two key tiles in flight");
-  auto kern = attn_kernel<FORM, DP, BF, MODE>;
+  auto kern = attn_kernel<FORM, DP, BF, MODE, TREE>;
   static std::atomic<uint64_t> done{0};  // devices whose limit has been raised
   const uint64_t bit = 1ull << (a.device & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
@@ -1958,25 +2061,25 @@ static int launch_one(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) 
   if (!a.join) return 0;
   // (a split ends a CTA's share, so that there are at most a.ctas of them with two streams of 32 column groups each: not
   // more than 16 pieces of work for a CTA here, as redo_join counts on)
-  return (int)launch_pdl(attn_join_kernel<FORM, DP, BF>, dim3(4 * a.ctas), dim3(128), 0, st, a);
+  return (int)launch_pdl(attn_join_kernel<FORM, DP, BF, TREE>, dim3(4 * a.ctas), dim3(128), 0, st, a);
 }
 
-template <int FORM, int DP, bool BF>
+template <int FORM, int DP, bool BF, bool TREE>
 static int launch_mode(const AttnArgs &a, const AttnMaps &maps, cudaStream_t st) {
   // kPlain folds a positive scale into the exponent's multiply-add; caps alone have the form above (for scales whose
   // ninth power is far from what fp32 holds), and everything else transforms the scores first
-  if (!(a.softcap > 0.f) && !a.slopes && a.scale > 0.f) return launch_one<FORM, DP, BF, kPlain>(a, maps, st);
-  if (!a.slopes && a.inv_cap >= 1e-3f && a.inv_cap <= 1e2f) return launch_one<FORM, DP, BF, kCapped>(a, maps, st);
-  return launch_one<FORM, DP, BF, kGeneral>(a, maps, st);
+  if (!(a.softcap > 0.f) && !a.slopes && a.scale > 0.f) return launch_one<FORM, DP, BF, kPlain, TREE>(a, maps, st);
+  if (!a.slopes && a.inv_cap >= 1e-3f && a.inv_cap <= 1e2f) return launch_one<FORM, DP, BF, kCapped, TREE>(a, maps, st);
+  return launch_one<FORM, DP, BF, kGeneral, TREE>(a, maps, st);
 }
-template <int FORM, int DP>
+template <int FORM, int DP, bool TREE>
 static int launch_type(const AttnArgs &a, const AttnMaps &maps, int bf16, cudaStream_t st) {
-  return bf16 ? launch_mode<FORM, DP, true>(a, maps, st) : launch_mode<FORM, DP, false>(a, maps, st);
+  return bf16 ? launch_mode<FORM, DP, true, TREE>(a, maps, st) : launch_mode<FORM, DP, false, TREE>(a, maps, st);
 }
 
-template <int FORM>
+template <int FORM, bool TREE>
 int launch_form(const AttnArgs &a, const AttnMaps &maps, int bf16, cudaStream_t st) {
-  return a.D > 64 ? launch_type<FORM, 128>(a, maps, bf16, st) : launch_type<FORM, 64>(a, maps, bf16, st);
+  return a.D > 64 ? launch_type<FORM, 128, TREE>(a, maps, bf16, st) : launch_type<FORM, 64, TREE>(a, maps, bf16, st);
 }
 
 }  // namespace pw

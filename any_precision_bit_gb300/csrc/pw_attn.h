@@ -37,6 +37,8 @@ enum {
   kAttnErrIds = 8,     // fewer new ids than opened blocks
   kAttnErrBlock = 16,  // a block id or a table row out of range
   kAttnErrPlan = 32,   // a forward met a plan of another shape than it was launched for
+  kAttnErrTree = 64,   // a tree's length or parent, or a node to be kept, out of range
+  kAttnErrCopy = 128,  // a block to be copied, or its new place, out of range
 };
 
 // What a forward's launch takes from the plan by value, beside the lists that lie on the device.  The plan's
@@ -44,17 +46,22 @@ enum {
 // plan was laid out again, or a captured plan that has not been replayed) would read past its tiles, the rows of
 // q and o or the table, so it writes nothing and reports kAttnErrPlan.
 struct alignas(16) AttnShape {
-  int tpt, streams;              // of the requests' list (streams 0: never laid out)
+  int tpt, streams;              // of the requests' list (streams 0: never laid out; kTreeShape more: of trees)
   int group_tpt, group_streams;  // of the groups' (0: no groups)
   int n_tokens, table_stride;
   const int *table;
 };
 static_assert(sizeof(AttnShape) == 32, "two 16-byte loads");
 
-// Keys a row may see, and where: [lo, hi) of table row trow (-1: none), at position pos.
+constexpr int kTreeShape = 16;
+
+// Keys a row may see, and where: [lo, hi) of table row trow (-1: none), at position pos.  In a plan of trees trow is the
+// cache position of the first node of the row's tree instead (INT_MAX: none); of the keys from there on the row sees those whose
+// bits are set in its kTreeWords words of TreeArgs::seen.
 struct RowBound {
   int lo, hi, trow, pos;
 };
+constexpr int kTreeWords = PW_TREE_NODES / 32;
 
 // A tile of query rows of one segment (a request's keys, or a group's shared prefix): tokens
 // tok0 .. tok0 + ntok - 1, each with its G = n_heads / n_kv_heads heads, against the keys
@@ -110,6 +117,15 @@ struct PlanArgs {
   int ctas, n_kv_heads;
 };
 
+struct TreeArgs {
+  PlanArgs plan;
+  const int *tree_len, *parent;
+  int parent_stride;
+  int *pos;
+  uint32_t *seen;  // [n_tokens][kTreeWords]
+  int *err;
+};
+
 struct MapArgs {
   int R, n_tokens, table_rows, table_stride, bt, n_blocks, n_ids;
   const int *ctx_len, *new_len, *rows, *new_ids;
@@ -125,6 +141,52 @@ struct AppendArgs {
   int64_t block_stride, token_stride, head_stride;
   const int64_t *slot;
   int n_tokens, n_heads, head_dim, bt, log_bt, n_blocks;
+};
+
+// A layer's rotation on the device.
+struct RopeTable {
+  uint64_t turn[64];   // of each pair: inv_freq / 2 pi, its part of a turn in units of 2^-64
+  int axis[64];
+  float gain[2][128];  // of q and k
+};
+
+struct RopeArgs {
+  const RopeTable *table;
+  const uint16_t *q, *k, *v;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  uint16_t *qo, *kc, *vc;
+  int64_t qo_token, qo_head;
+  int64_t block_stride, token_stride, head_stride;
+  const int64_t *slot;
+  const int *pos;     // [axes][n_tokens], or one for all axes
+  int64_t pos_axis;   // elements from axis to axis
+  int n_tokens, Hq, Hkv, D, bt, log_bt, n_blocks;
+  int rot, interleaved, norm_q, norm_k;
+  float scale, eps, inv_d;
+};
+
+// The caches of some layers, by value in a launch.
+constexpr int kMoveLayers = 64;
+struct CacheRef {
+  uint16_t *k, *v;
+  int64_t block_stride, token_stride, head_stride;
+};
+struct MoveLayers {
+  CacheRef layer[kMoveLayers];
+};
+
+struct KeepArgs {
+  int R, table_rows, table_stride, keep_stride, bt, log_bt, n_blocks, n_heads, head_dim;
+  const int *rows, *table, *kv_len, *tree_len, *keep, *n_keep;
+  int *ctx_out;  // (of the launch for the first layers, else null)
+  int *err;
+};
+
+struct CopyArgs {
+  const int *src, *dst;
+  int n, n_blocks, bt, log_bt, n_heads, head_dim;
+  int *where;  // [n_blocks] number of the pair that a block is the source of, where it is one; null: not asked for
+  int *err;
 };
 
 // Tensor maps of one forward launch: boxes of 64 elements of a head by (Q) the G heads of a
@@ -172,12 +234,18 @@ struct AttnArgs {
   int *err;
   long long wait_cycles;  // bounded device waits give up after this many SM cycles
   int withhold;           // testing: see produce()
+  const uint32_t *seen;   // [n_tokens][kTreeWords], of a plan of trees (else null): see RowBound
 };
 
 int launch_kv_map(const MapArgs &a, void *stream);
 int launch_attn_bounds(const PlanArgs &a, void *stream);
 int launch_attn_list(const PlanArgs &a, void *stream);
 int launch_attn_append(const AppendArgs &a, void *stream);
+int launch_tree_bounds(const TreeArgs &a, void *stream);
+int launch_rope(const RopeArgs &a, int bf16, void *stream);
+int launch_keep(const KeepArgs &a, const MoveLayers &m, int n_layers, void *stream);
+int launch_copy(const CopyArgs &a, const MoveLayers &m, int n_layers, void *stream);
+int launch_rename(const CopyArgs &a, int *table, int table_rows, int table_stride, void *stream);
 int launch_attn(const AttnArgs &a, const AttnMaps &maps, int bf16, void *stream);
 
 }  // namespace pw

@@ -76,6 +76,9 @@ struct Layer {
   uint16_t *k = nullptr, *v = nullptr;
   TmaDesc map_k[2], map_v[2];  // L2 fetches 256 bytes, or 64 (see kReuseBytes)
   int64_t block_stride = 0, token_stride = 0, head_stride = 0;
+  // its rotation; rope.table is null before pw_attn_set_rope
+  RopeArgs rope{};
+  int rope_axes = 0;
 };
 
 struct Plan {
@@ -84,10 +87,12 @@ struct Plan {
   int64_t reach = 0;           // keys that a row sees at most
   RowBound *bounds = nullptr;  // [max_tokens]
   AttnShape *shape = nullptr;  // as laid out on the device
+  uint32_t *seen = nullptr;    // [max_tree_tokens][kTreeWords]
+  bool tree = false;           // laid out by pw_attn_plan_tree
   AttnList requests{}, groups{};
 
   AttnShape launch_shape() const {
-    AttnShape s{requests.tpt, requests.streams, 0, 0, step.n_tokens, step.table_stride, step.table};
+    AttnShape s{requests.tpt, requests.streams + (tree ? kTreeShape : 0), 0, 0, step.n_tokens, step.table_stride, step.table};
     if (step.n_groups) {
       s.group_tpt = groups.tpt;
       s.group_streams = groups.streams;
@@ -131,6 +136,8 @@ struct pw_attn {
   float2 *part_ml = nullptr;
   int *counters = nullptr;
   uint32_t *marks = nullptr, *part_odd = nullptr;
+  RopeTable *rope = nullptr;  // [L]
+  int *where = nullptr;       // [n_blocks] see CopyArgs
   size_t mark_words = 0;
   long long wait_cycles = kWaitCyclesDefault;
   int fault_withhold = 0;  // testing: the next forward withholds one device barrier arrival
@@ -172,20 +179,22 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   a->d = d;
   a->layers.resize((size_t)d.L);
   a->plans.resize((size_t)d.n_plans);
-  a->allocs.reserve(64);
+  a->allocs.reserve(16 + 14 * (size_t)d.n_plans);
   int e = cudaDeviceGetAttribute(&a->sm_count, cudaDevAttrMultiProcessorCount, d.device);
   if (e) return cuda_failed("cudaDeviceGetAttribute", e);
   const size_t ctas = (size_t)a->sm_count, dp = d.head_dim > 64 ? 128 : 64;
   a->mark_words = ((size_t)d.max_tokens * d.n_heads + 31) / 32;
   bool ok = alloc(a, &a->marks, a->mark_words) && alloc(a, &a->err, 1) && alloc(a, &a->counters, 2 * ctas) &&
             alloc(a, &a->part_o, ctas * 4 * kAttnRows * dp) && alloc(a, &a->part_ml, ctas * 4 * kAttnRows) &&
-            alloc(a, &a->part_odd, ctas * 4 * kAttnRows);
+            alloc(a, &a->part_odd, ctas * 4 * kAttnRows) && alloc(a, &a->rope, (size_t)d.L) &&
+            alloc(a, &a->where, (size_t)d.n_blocks);
   if (d.max_shared_tokens > 0)
     ok = ok && alloc(a, &a->prefix_o, (size_t)d.max_shared_tokens * d.n_heads * d.head_dim) &&
          alloc(a, &a->prefix_lse, (size_t)d.max_shared_tokens * d.n_heads);
   // a tile holds a token at least, but the last of each segment may be short: requests and the padding, or groups
   for (Plan &p : a->plans) {
     ok = ok && alloc(a, &p.bounds, (size_t)d.max_tokens) && alloc(a, &p.shape, 1);
+    if (d.max_tree_tokens > 0) ok = ok && alloc(a, &p.seen, (size_t)d.max_tree_tokens * kTreeWords);
     for (AttnList *l : {&p.requests, &p.groups}) {
       if (l == &p.groups && d.max_shared_tokens == 0) continue;
       if (l == &p.groups) {
@@ -201,11 +210,106 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   }
   if (!ok) return report(nullptr, PW_ERR_OOM, "device memory exhausted");
   if ((e = cudaMemset(a->err, 0, sizeof(int))) || (e = cudaMemset(a->counters, 0, 2 * ctas * sizeof(int))) ||
-      (e = cudaMemset(a->marks, 0, a->mark_words * sizeof(uint32_t))))
+      (e = cudaMemset(a->marks, 0, a->mark_words * sizeof(uint32_t))) ||
+      (e = cudaMemset(a->where, 0, (size_t)d.n_blocks * sizeof(int))))
     return cuda_failed("cudaMemset", e);
   for (Plan &p : a->plans)
     if ((e = cudaMemset(p.shape, 0, sizeof(AttnShape)))) return cuda_failed("cudaMemset", e);
   if ((e = cudaDeviceSynchronize())) return cuda_failed("cudaDeviceSynchronize", e);
+  return PW_OK;
+}
+
+// All layers' caches, at most kMoveLayers of them a launch: launch(caches, their number, whether they are the first).
+template <class F>
+pw_status for_layers(const pw_attn *a, const char *what, F launch) {
+  for (const Layer &l : a->layers)
+    if (!l.k) return report(nullptr, PW_ERR_STATE, "a layer's cache is not bound");
+  MoveLayers m;
+  for (int at = 0; at < a->d.L; at += kMoveLayers) {
+    const int n = std::min(kMoveLayers, a->d.L - at);
+    for (int i = 0; i < n; ++i) {
+      const Layer &l = a->layers[(size_t)(at + i)];
+      m.layer[i] = CacheRef{l.k, l.v, l.block_stride, l.token_stride, l.head_stride};
+    }
+    if (int e = launch(m, n, at == 0)) return cuda_failed(what, e);
+  }
+  return PW_OK;
+}
+
+// pw_attn_plan, or with a tree pw_attn_plan_tree.
+pw_status lay_out(pw_attn *a, int plan, const pw_kv_step *s, int window, const int32_t *doc_start,
+                  const int32_t *bidir_len, const pw_tree *tree, pw_stream stream) {
+  if (pw_status st = check_step(a, s)) return st;
+  if (plan < 0 || plan >= a->d.n_plans) return bad("plan out of range");
+  if (window < 0) return bad("window must not be negative");
+  PlanArgs g{};
+  g.R = s->R;
+  g.n_tokens = s->n_tokens;
+  g.table_rows = s->table_rows;
+  g.table_stride = s->table_stride;
+  g.bt = a->d.block_tokens;
+  g.ctx_len = s->ctx_len;
+  g.rows = s->rows;
+  g.q_start = s->q_start;
+  g.kv_len = s->kv_len;
+  g.doc_start = doc_start;
+  g.bidir_len = bidir_len;
+  g.window = window;
+  g.n_groups = s->n_groups;
+  g.group_start = s->group_start;
+  g.shared_len = s->shared_len;
+  g.ctas = a->sm_count;
+  g.n_kv_heads = a->d.n_kv_heads;
+  const int G = a->d.n_heads / a->d.n_kv_heads, most = kAttnRows / G;
+  auto shape = [&](AttnList &l, int tokens) {
+    tokens = std::max(tokens, 1);
+    l.streams = (int64_t)tokens * G > kSpreadRows ? 2 : 1;  // the kernel's form: see pw_attn.h
+    l.tpt = std::min(most, tokens);
+    // measured: two tiles, 8192-token prompt 479, 417, 395, 397, 401 us at 1 to 5 and packed chunks 66, 66, 68,
+    // 71, 73 us; few rows, 160 windowed requests 137, 137, 138 us at 1 to 3
+    l.piece_cost = l.streams == 2 ? 3 : 2;
+  };
+  // The lists sum up key tiles (and a piece's cost) over all tiles of rows in 31 bits, as they do an SM's share over
+  // the heads.
+  const int64_t keys = ((int64_t)s->table_stride * a->d.block_tokens + kAttnKeys - 1) / kAttnKeys;
+  auto countable = [&](const AttnList &l, int segments) {
+    const int64_t sum = (s->n_tokens / (l.tpt * l.streams) + (int64_t)segments) * (keys + l.piece_cost);
+    return sum <= INT32_MAX && sum * a->d.n_kv_heads / a->sm_count < INT32_MAX;
+  };
+  AttnList requests = a->plans[(size_t)plan].requests, groups = a->plans[(size_t)plan].groups;
+  shape(requests, s->max_new);
+  shape(groups, s->n_tokens);
+  if (!countable(requests, s->R + 1) || (s->n_groups && !countable(groups, s->n_groups)))
+    return bad("table_stride is too long for this many tokens (2^31 key tiles or more)");
+  OnDevice dev(a->d.device);
+  Plan &p = a->plans[(size_t)plan];
+  p.reach = std::min((int64_t)s->table_stride * a->d.block_tokens,
+                     window ? (int64_t)window + s->max_new + (tree ? PW_TREE_NODES : 0) : INT64_MAX);
+  p.set = false;
+  p.tree = tree != nullptr;
+  p.requests = requests;
+  p.groups = groups;
+  p.step = *s;
+  g.bounds = p.bounds;
+  g.shape = p.launch_shape();
+  g.shape_out = p.shape;
+  int e;
+  if (tree) {
+    const TreeArgs t{g, tree->tree_len, tree->parent, tree->parent_stride, tree->pos, p.seen, a->err};
+    e = launch_tree_bounds(t, stream);
+  } else {
+    e = launch_attn_bounds(g, stream);
+  }
+  if (!e && s->n_groups) {
+    g.of_groups = 1;
+    g.list = p.groups;
+    e = launch_attn_list(g, stream);
+  }
+  g.of_groups = 0;
+  g.list = p.requests;
+  if (!e) e = launch_attn_list(g, stream);
+  if (e) return cuda_failed("pw_attn_plan launch", e);
+  p.set = true;
   return PW_OK;
 }
 
@@ -230,6 +334,7 @@ pw_status pw_attn_create(const pw_attn_desc *desc, pw_attn **out) {
   if (d.max_tokens < 1 || d.max_tokens > (1 << 20)) return bad("max_tokens must be in 1..2^20");
   if (d.max_shared_tokens < 0 || d.max_shared_tokens > d.max_tokens)
     return bad("max_shared_tokens must be in 0..max_tokens");
+  if (d.max_tree_tokens < 0 || d.max_tree_tokens > d.max_tokens) return bad("max_tree_tokens must be in 0..max_tokens");
   if (d.n_plans < 1 || d.n_plans > 16) return bad("n_plans must be in 1..16");
   OnDevice dev(d.device);
   if (!dev.ok) return cuda_failed("cudaSetDevice", cudaGetLastError());
@@ -314,70 +419,16 @@ pw_status pw_kv_map(pw_attn *a, const pw_kv_step *s, const int32_t *new_ids, int
 
 pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *s, int window, const int32_t *doc_start,
                        const int32_t *bidir_len, pw_stream stream) {
-  if (pw_status st = check_step(a, s)) return st;
-  if (plan < 0 || plan >= a->d.n_plans) return bad("plan out of range");
-  if (window < 0) return bad("window must not be negative");
-  PlanArgs g{};
-  g.R = s->R;
-  g.n_tokens = s->n_tokens;
-  g.table_rows = s->table_rows;
-  g.table_stride = s->table_stride;
-  g.bt = a->d.block_tokens;
-  g.ctx_len = s->ctx_len;
-  g.rows = s->rows;
-  g.q_start = s->q_start;
-  g.kv_len = s->kv_len;
-  g.doc_start = doc_start;
-  g.bidir_len = bidir_len;
-  g.window = window;
-  g.n_groups = s->n_groups;
-  g.group_start = s->group_start;
-  g.shared_len = s->shared_len;
-  g.ctas = a->sm_count;
-  g.n_kv_heads = a->d.n_kv_heads;
-  const int G = a->d.n_heads / a->d.n_kv_heads, most = kAttnRows / G;
-  auto shape = [&](AttnList &l, int tokens) {
-    tokens = std::max(tokens, 1);
-    l.streams = (int64_t)tokens * G > kSpreadRows ? 2 : 1;  // the kernel's form: see pw_attn.h
-    l.tpt = std::min(most, tokens);
-    // measured: two tiles, 8192-token prompt 479, 417, 395, 397, 401 us at 1 to 5 and packed chunks 66, 66, 68,
-    // 71, 73 us; few rows, 160 windowed requests 137, 137, 138 us at 1 to 3
-    l.piece_cost = l.streams == 2 ? 3 : 2;
-  };
-  // The lists sum up key tiles (and a piece's cost) over all tiles of rows in 31 bits, as they do an SM's share over
-  // the heads.
-  const int64_t keys = ((int64_t)s->table_stride * a->d.block_tokens + kAttnKeys - 1) / kAttnKeys;
-  auto countable = [&](const AttnList &l, int segments) {
-    const int64_t sum = (s->n_tokens / (l.tpt * l.streams) + (int64_t)segments) * (keys + l.piece_cost);
-    return sum <= INT32_MAX && sum * a->d.n_kv_heads / a->sm_count < INT32_MAX;
-  };
-  AttnList requests = a->plans[(size_t)plan].requests, groups = a->plans[(size_t)plan].groups;
-  shape(requests, s->max_new);
-  shape(groups, s->n_tokens);
-  if (!countable(requests, s->R + 1) || (s->n_groups && !countable(groups, s->n_groups)))
-    return bad("table_stride is too long for this many tokens (2^31 key tiles or more)");
-  OnDevice dev(a->d.device);
-  Plan &p = a->plans[(size_t)plan];
-  p.reach = std::min((int64_t)s->table_stride * a->d.block_tokens, window ? (int64_t)window + s->max_new : INT64_MAX);
-  p.set = false;
-  p.requests = requests;
-  p.groups = groups;
-  p.step = *s;
-  g.bounds = p.bounds;
-  g.shape = p.launch_shape();
-  g.shape_out = p.shape;
-  int e = launch_attn_bounds(g, stream);
-  if (!e && s->n_groups) {
-    g.of_groups = 1;
-    g.list = p.groups;
-    e = launch_attn_list(g, stream);
-  }
-  g.of_groups = 0;
-  g.list = p.requests;
-  if (!e) e = launch_attn_list(g, stream);
-  if (e) return cuda_failed("pw_attn_plan launch", e);
-  p.set = true;
-  return PW_OK;
+  return lay_out(a, plan, s, window, doc_start, bidir_len, nullptr, stream);
+}
+
+pw_status pw_attn_plan_tree(pw_attn *a, int plan, const pw_kv_step *s, int window, const pw_tree *tree, pw_stream stream) {
+  if (!a || !s || !tree || !tree->tree_len || !tree->parent) return bad("null argument");
+  if (tree->parent_stride < 1) return bad("parent_stride must be positive");
+  if (s->n_tokens > a->d.max_tree_tokens) return bad("n_tokens of a step with trees exceeds max_tree_tokens");
+  // (the kernels put the tree of a row that is in none at INT_MAX, behind every key)
+  if ((int64_t)s->table_stride * a->d.block_tokens > INT32_MAX - 1024) return bad("a table row holds nearly 2^31 tokens");
+  return lay_out(a, plan, s, window, nullptr, nullptr, tree, stream);
 }
 
 pw_status pw_attn_append(pw_attn *a, int layer, const pw_kv_step *s, const void *k, int64_t k_token,
@@ -474,6 +525,7 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   g.part_odd = a->part_odd;
   g.counters = a->counters;
   g.ctas = a->sm_count;
+  g.seen = p.tree ? p.seen : nullptr;
   AttnMaps maps;
   const bool apart = l.token_stride != g.D && g.D % 128;
   const int fetch = apart && p.reach * g.D * 4 * a->sm_count > kReuseBytes;
@@ -505,6 +557,153 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
   return launch(p.requests);
 }
 
+pw_status pw_attn_set_rope(pw_attn *a, int layer, const pw_rope_desc *r) {
+  if (!a || !r) return bad("null argument");
+  if (layer < 0 || layer >= a->d.L) return bad("layer out of range");
+  if (r->rot_dim < 0 || r->rot_dim % 8 || r->rot_dim > a->d.head_dim)
+    return bad("rot_dim must be a multiple of 8 in 0..head_dim");
+  if (r->n_axes < 1 || r->n_axes > 4) return bad("n_axes must be in 1..4");
+  if (r->rot_dim && !r->inv_freq) return bad("null argument");
+  if (!std::isfinite(r->scale)) return bad("scale must be finite");
+  if (!(r->eps >= 0.f) || !std::isfinite(r->eps)) return bad("eps must be finite and not negative");
+  RopeTable t{};
+  for (int i = 0; i < r->rot_dim / 2; ++i) {
+    if (!std::isfinite(r->inv_freq[i])) return bad("inv_freq must be finite");
+    if (r->axis && (r->axis[i] < 0 || r->axis[i] >= r->n_axes)) return bad("axis must be in 0..n_axes - 1");
+    // the fraction of a turn for each position; whole turns fall away, since positions are whole numbers
+    const double turns = r->inv_freq[i] / 6.283185307179586476925;
+    const double part = std::ldexp(turns - std::floor(turns), 64);  // up to 2^64 where turns is just below a whole number
+    t.turn[i] = part < 18446744073709551616.0 ? (uint64_t)part : 0;
+    t.axis[i] = r->axis ? r->axis[i] : 0;
+  }
+  OnDevice dev(a->d.device);
+  if (!dev.ok) return cuda_failed("cudaSetDevice", cudaGetLastError());
+  if (int e = cudaDeviceSynchronize()) return cuda_failed("cudaDeviceSynchronize", e);
+  const float *gains[2] = {r->q_gain, r->k_gain};
+  for (int i = 0; i < 2; ++i)
+    if (gains[i])
+      if (int e = cudaMemcpy(t.gain[i], gains[i], sizeof(float) * (size_t)a->d.head_dim, cudaMemcpyDefault))
+        return cuda_failed("cudaMemcpy", e);
+  RopeTable *table = a->rope + layer;
+  if (int e = cudaMemcpy(table, &t, sizeof t, cudaMemcpyHostToDevice)) return cuda_failed("cudaMemcpy", e);
+  Layer &l = a->layers[(size_t)layer];
+  l.rope_axes = r->n_axes;
+  l.rope.table = table;
+  l.rope.rot = r->rot_dim;
+  l.rope.interleaved = r->interleaved != 0;
+  l.rope.norm_q = r->q_gain != nullptr;
+  l.rope.norm_k = r->k_gain != nullptr;
+  l.rope.scale = r->scale;
+  l.rope.eps = r->eps;
+  return PW_OK;
+}
+
+pw_status pw_attn_rope_append(pw_attn *a, int layer, const pw_kv_step *s, const void *q, int64_t q_token, int64_t q_head,
+                              void *q_out, int64_t qo_token, int64_t qo_head, const void *k, int64_t k_token, int64_t k_head,
+                              const void *v, int64_t v_token, int64_t v_head, const int32_t *pos, pw_stream stream) {
+  if (pw_status st = check_step(a, s)) return st;
+  if (!q || !q_out || !k || !v) return bad("null argument");
+  if (layer < 0 || layer >= a->d.L) return bad("layer out of range");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v))
+    return bad("q, q_out, k and v must be multiples of 16 bytes");
+  for (int64_t stride : {q_token, q_head, qo_token, qo_head, k_token, k_head, v_token, v_head})
+    if (stride % 8) return bad("strides must be multiples of 8 elements");
+  const Layer &l = a->layers[(size_t)layer];
+  if (!l.k) return report(nullptr, PW_ERR_STATE, "the layer's cache is not bound");
+  if (!l.rope.table) return report(nullptr, PW_ERR_STATE, "the layer's rotation was never set");
+  OnDevice dev(a->d.device);
+  RopeArgs g = l.rope;
+  g.q = static_cast<const uint16_t *>(q);
+  g.q_token = q_token;
+  g.q_head = q_head;
+  g.qo = static_cast<uint16_t *>(q_out);
+  g.qo_token = qo_token;
+  g.qo_head = qo_head;
+  g.k = static_cast<const uint16_t *>(k);
+  g.k_token = k_token;
+  g.k_head = k_head;
+  g.v = static_cast<const uint16_t *>(v);
+  g.v_token = v_token;
+  g.v_head = v_head;
+  g.kc = l.k;
+  g.vc = l.v;
+  g.block_stride = l.block_stride;
+  g.token_stride = l.token_stride;
+  g.head_stride = l.head_stride;
+  g.slot = s->slot;
+  g.pos = pos ? pos : s->pos;
+  g.pos_axis = pos ? s->n_tokens : 0;
+  g.n_tokens = s->n_tokens;
+  g.Hq = a->d.n_heads;
+  g.Hkv = a->d.n_kv_heads;
+  g.D = a->d.head_dim;
+  g.inv_d = 1.f / (float)a->d.head_dim;
+  g.bt = a->d.block_tokens;
+  g.log_bt = log2_of(a->d.block_tokens);
+  g.n_blocks = a->d.n_blocks;
+  if (int e = launch_rope(g, a->d.dtype == PW_BF16, stream)) return cuda_failed("pw_attn_rope_append launch", e);
+  return PW_OK;
+}
+
+pw_status pw_kv_keep(pw_attn *a, const pw_kv_step *s, const int32_t *tree_len, const int32_t *keep, int keep_stride,
+                     const int32_t *n_keep, int32_t *ctx_out, pw_stream stream) {
+  if (pw_status st = check_step(a, s)) return st;
+  if (!tree_len || !keep || !n_keep) return bad("null argument");
+  if (keep_stride < 1) return bad("keep_stride must be positive");
+  OnDevice dev(a->d.device);
+  KeepArgs g{};
+  g.R = s->R;
+  g.table_rows = s->table_rows;
+  g.table_stride = s->table_stride;
+  g.keep_stride = keep_stride;
+  g.bt = a->d.block_tokens;
+  g.log_bt = log2_of(a->d.block_tokens);
+  g.n_blocks = a->d.n_blocks;
+  g.n_heads = a->d.n_kv_heads;
+  g.head_dim = a->d.head_dim;
+  g.rows = s->rows;
+  g.table = s->table;
+  g.kv_len = s->kv_len;
+  g.tree_len = tree_len;
+  g.keep = keep;
+  g.n_keep = n_keep;
+  g.err = a->err;
+  return for_layers(a, "pw_kv_keep launch", [&](const MoveLayers &m, int n, bool first) {
+    g.ctx_out = first ? ctx_out : nullptr;
+    return launch_keep(g, m, n, stream);
+  });
+}
+
+pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, int32_t *table, int table_rows, int table_stride,
+                     pw_stream stream) {
+  if (!a) return bad("null argument");
+  if (n < 0 || (n > 0 && (!src || !dst))) return bad("n pairs are needed");
+  if (table && (table_rows < 1 || table_stride < 1)) return bad("the table needs rows and entries");
+  if (n > a->d.n_blocks) return bad("more pairs than the cache has blocks");
+  if ((int64_t)n * ((int64_t)a->d.block_tokens * a->d.n_kv_heads * a->d.head_dim / 16384 + 1) > INT32_MAX)
+    return bad("too many pairs for one call");
+  OnDevice dev(a->d.device);
+  CopyArgs g{};
+  g.src = src;
+  g.dst = dst;
+  g.n = n;
+  g.n_blocks = a->d.n_blocks;
+  g.bt = a->d.block_tokens;
+  g.log_bt = log2_of(a->d.block_tokens);
+  g.n_heads = a->d.n_kv_heads;
+  g.head_dim = a->d.head_dim;
+  g.where = table ? a->where : nullptr;
+  g.err = a->err;
+  pw_status st = for_layers(a, "pw_kv_copy launch", [&](const MoveLayers &m, int layers, bool first) {
+    CopyArgs h = g;
+    if (!first) h.where = nullptr;
+    return n ? launch_copy(h, m, layers, stream) : 0;
+  });
+  if (st || !table || !n) return st;
+  if (int e = launch_rename(g, table, table_rows, table_stride, stream)) return cuda_failed("pw_kv_copy launch", e);
+  return PW_OK;
+}
+
 pw_status pw_attn_set_fault(pw_attn *a, int kind, int n) {
   if (!a) return bad("null argument");
   if (n < 0 || (kind != 4 && kind != 5)) return bad("kind 4 or 5 and n >= 0");
@@ -532,14 +731,17 @@ pw_status pw_attn_check(pw_attn *a, pw_stream stream) {
       (e = cudaStreamSynchronize(st)))
     return cuda_failed("cudaMemsetAsync", e);
   if (bits & kAttnErrWait) return report(nullptr, PW_ERR_TIMEOUT, "a bounded device wait expired; outputs are invalid");
-  char buf[384];
-  snprintf(buf, sizeof buf, "%s%s%s%s%s%s", bits & ~kAttnErrPlan ? "pw_kv_map found:" : "",
+  char buf[512];
+  constexpr int kMapErrs = kAttnErrLen | kAttnErrTokens | kAttnErrIds | kAttnErrBlock;
+  snprintf(buf, sizeof buf, "%s%s%s%s%s%s%s%s", bits & kMapErrs ? "pw_kv_map or pw_kv_keep found:" : "",
            bits & kAttnErrLen ? " a length out of range;" : "",
            bits & kAttnErrTokens ? " more new tokens than n_tokens;" : "",
            bits & kAttnErrIds ? " fewer new ids than opened blocks;" : "",
            bits & kAttnErrBlock ? " a block id or table row out of range;" : "",
            bits & kAttnErrPlan ? " a forward's plan is laid out for other tile sizes, n_tokens, table or groups than it was "
-                                 "launched with: it wrote nothing" : "");
+                                 "launched with: it wrote nothing;" : "",
+           bits & kAttnErrTree ? " a tree's length or parent, or a node to be kept, out of range;" : "",
+           bits & kAttnErrCopy ? " pw_kv_copy met a block id out of range" : "");
   return report(nullptr, PW_ERR_STATE, buf);
 }
 

@@ -2,5 +2,5 @@
 #include "pw_attn.cuh"
 
 namespace pw {
-template int launch_form<kSpread>(const AttnArgs &, const AttnMaps &, int, cudaStream_t);
+template int launch_form<kSpread, false>(const AttnArgs &, const AttnMaps &, int, cudaStream_t);
 }

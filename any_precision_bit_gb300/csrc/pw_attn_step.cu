@@ -178,6 +178,84 @@ int launch_attn_bounds(const PlanArgs &a, void *stream) {
                          reinterpret_cast<cudaStream_t>(stream), a);
 }
 
+// The same for a step with trees.  The first R CTAs take a request's tree each, a thread a node; the others take the rows that
+// stand in no tree as attn_bounds_kernel does.  A node's way up is in descending order (a parent comes before its children), so
+// that one word of its visible nodes after the other is finished; the parents lie in shared memory.
+__device__ __forceinline__ int tree_of(const TreeArgs &a, int r, int kv) {
+  const int tl = a.tree_len[r];
+  return tl > 0 && tl <= PW_TREE_NODES && tl <= a.parent_stride && tl <= kv ? tl : 0;
+}
+__global__ void __launch_bounds__(kStepThreads) tree_bounds_kernel(TreeArgs x) {
+  static_assert(kStepThreads == PW_TREE_NODES && kTreeWords == 8, "a thread a node, two 16-byte stores");
+  __shared__ int parent[PW_TREE_NODES];
+  const PlanArgs &a = x.plan;
+  const long long cap = (long long)a.table_stride * a.bt;
+  const int tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  if ((int)blockIdx.x < a.R) {
+    const int r = blockIdx.x, kv = (int)min((long long)a.kv_len[r], cap), tl = tree_of(x, r, kv);
+    if (tl != x.tree_len[r] && tid == 0) atomicOr(x.err, kAttnErrTree);
+    if (tl == 0) return;
+    if (tid < tl) {
+      int p = x.parent[(size_t)r * x.parent_stride + tid];
+      if (p < -1 || p >= tid) {
+        atomicOr(x.err, kAttnErrTree);
+        p = -1;
+      }
+      parent[tid] = p;
+    }
+    __syncthreads();
+    const int start = kv - tl, q0 = max(a.q_start[r], 0), q1 = min(a.q_start[r + 1], a.n_tokens);
+    const int t = q0 + (start + tid - a.ctx_len[r]);
+    if (tid >= tl || t < q0 || t >= q1) return;
+    uint32_t word[kTreeWords];
+    int node = tid, depth = 0;  // nodes passed so far
+#pragma unroll
+    for (int w = kTreeWords - 1; w >= 0; --w) {
+      uint32_t bits = 0;
+      while (node >= 32 * w) {  // (a root's parent is below every word)
+        if (a.window <= 0 || depth < a.window) bits |= 1u << (node & 31);
+        ++depth;
+        node = parent[node];
+      }
+      word[w] = bits;
+    }
+    uint4 *seen = reinterpret_cast<uint4 *>(x.seen + (size_t)t * kTreeWords);
+    seen[0] = make_uint4(word[0], word[1], word[2], word[3]);
+    seen[1] = make_uint4(word[4], word[5], word[6], word[7]);
+    RowBound b;
+    b.pos = start + depth - 1;
+    b.hi = start + tid + 1;
+    // (an ancestor within the window has no lower place than its position, which is not below this)
+    b.lo = a.window > 0 ? max(0, b.pos - a.window + 1) : 0;
+    b.trow = start;
+    a.bounds[t] = b;
+    if (x.pos) x.pos[t] = b.pos;
+    return;
+  }
+  const int t = (blockIdx.x - a.R) * kStepThreads + tid;
+  if (t >= a.n_tokens) return;
+  RowBound b{0, 0, INT_MAX, -1};
+  if (t < a.q_start[a.R]) {
+    const int r = seg_of(a.q_start, a.R, t);
+    const int kv = (int)min((long long)a.kv_len[r], cap), tl = tree_of(x, r, kv);
+    b.pos = a.ctx_len[r] + t - a.q_start[r];
+    if (tl && b.pos >= kv - tl) return;  // a node's row
+    b.hi = min(b.pos + 1, kv);
+    if (a.window > 0) b.lo = max(0, b.pos - a.window + 1);
+    b.lo = min(b.lo, b.hi);
+    if (b.hi <= 0) b.lo = b.hi = 0;
+  }
+  a.bounds[t] = b;
+  if (x.pos) x.pos[t] = b.pos;
+}
+
+int launch_tree_bounds(const TreeArgs &a, void *stream) {
+  return (int)launch_pdl(tree_bounds_kernel, dim3(a.plan.R + (a.plan.n_tokens + kStepThreads - 1) / kStepThreads),
+                         dim3(kStepThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+}
+
 // Segments of a list: requests (and, behind them, the rows that are padding), or groups.
 struct Segment {
   int tok0, tok1, trow, klo, khi, merge;

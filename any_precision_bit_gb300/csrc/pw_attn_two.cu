@@ -3,5 +3,5 @@
 #include "pw_attn.cuh"
 
 namespace pw {
-template int launch_form<kTwo>(const AttnArgs &, const AttnMaps &, int, cudaStream_t);
+template int launch_form<kTwo, false>(const AttnArgs &, const AttnMaps &, int, cudaStream_t);
 }

@@ -10,7 +10,8 @@
 // request's own announcement first and must otherwise fit in F_blk; it is all or nothing.
 // Ids are logical and the lowest free one is granted first: ids below the high-water mark
 // that were released are kept in an ordered set, so memory grows with the ids in use, not
-// with the budget.
+// with the budget.  Requests may share blocks (a fork holds its parent's); a shared block counts once, and comes free with
+// its last holder.
 #include <stdint.h>
 
 #include <iterator>
@@ -29,6 +30,7 @@ struct pw_kv {
   int32_t next_id = 0;              // ids >= next_id were never granted
   std::set<int32_t> freed;          // released ids below next_id
   std::unordered_map<int64_t, std::vector<int32_t>> held;
+  std::unordered_map<int32_t, int64_t> sharers;  // of a block that several requests hold: how many
   std::unordered_map<int64_t, int64_t> announced;
 };
 
@@ -51,6 +53,33 @@ int32_t take_lowest(pw_kv *kv) {
     return id;
   }
   return kv->next_id++;
+}
+
+// The high-water mark comes back down over released ids at its top.
+void lower_mark(pw_kv *kv) {
+  while (kv->next_id > 0 && !kv->freed.empty() && *kv->freed.rbegin() == kv->next_id - 1) {
+    kv->freed.erase(std::prev(kv->freed.end()));
+    --kv->next_id;
+  }
+}
+
+// One holder less of a block; true if it is free now.
+bool drop(pw_kv *kv, int32_t id) {
+  auto it = kv->sharers.find(id);
+  if (it != kv->sharers.end()) {
+    if (--it->second == 1) kv->sharers.erase(it);
+    return false;
+  }
+  kv->freed.insert(id);
+  --kv->U;
+  return true;
+}
+
+// A grow's room: the part of n blocks that request r's announcement covers, or -1 where the others do not fit.
+int64_t covered(const pw_kv *kv, int64_t request, int64_t n) {
+  auto it = kv->announced.find(request);
+  const int64_t own = it == kv->announced.end() ? 0 : it->second, c = n < own ? n : own;
+  return n - c > capacity(kv) - kv->U - kv->P ? -1 : c;
 }
 
 }  // namespace
@@ -102,11 +131,8 @@ extern "C" pw_status pw_kv_announce(pw_kv *kv, int64_t request, int64_t n_blocks
 extern "C" pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, int32_t *ids_out) {
   if (!kv || n_blocks < 0) return PW_ERR_INVALID;
   if (pw_status st = refresh_weights(kv)) return st;
-  auto it = kv->announced.find(request);
-  const int64_t own = it == kv->announced.end() ? 0 : it->second;
-  const int64_t c = n_blocks < own ? n_blocks : own;
-  const int64_t free_blocks = capacity(kv) - kv->U - kv->P;
-  if (n_blocks - c > free_blocks) return PW_ERR_OOM;
+  const int64_t c = covered(kv, request, n_blocks);
+  if (c < 0) return PW_ERR_OOM;
   // U + n <= C <= n_ids, so the ids below n_ids suffice
   std::vector<int32_t> &mine = kv->held[request];
   try {
@@ -120,7 +146,7 @@ extern "C" pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, in
     if (ids_out) ids_out[k] = id;
   }
   kv->U += n_blocks;
-  if (c > 0) pw_kv_announce(kv, request, own - c);
+  if (c > 0) pw_kv_announce(kv, request, kv->announced[request] - c);
   return PW_OK;
 }
 
@@ -129,18 +155,119 @@ extern "C" pw_status pw_kv_release(pw_kv *kv, int64_t request, int64_t *n_releas
   int64_t n = 0;
   auto it = kv->held.find(request);
   if (it != kv->held.end()) {
-    n = (int64_t)it->second.size();
-    for (int32_t id : it->second) kv->freed.insert(id);
+    for (int32_t id : it->second) n += drop(kv, id);
     kv->held.erase(it);
   }
-  // the high-water mark comes back down over released ids at its top
-  while (kv->next_id > 0 && !kv->freed.empty() && *kv->freed.rbegin() == kv->next_id - 1) {
-    kv->freed.erase(std::prev(kv->freed.end()));
-    --kv->next_id;
-  }
-  kv->U -= n;
+  lower_mark(kv);
   pw_kv_announce(kv, request, 0);
   if (n_released) *n_released = n;
+  return PW_OK;
+}
+
+extern "C" pw_status pw_kv_fork(pw_kv *kv, int64_t parent, int64_t child, int64_t n_blocks) {
+  if (!kv || n_blocks < 0 || parent == child) return PW_ERR_INVALID;
+  auto from = kv->held.find(parent), to = kv->held.find(child);
+  if (n_blocks > (from == kv->held.end() ? 0 : (int64_t)from->second.size())) return PW_ERR_INVALID;
+  if (to != kv->held.end() && !to->second.empty()) return PW_ERR_STATE;
+  if (n_blocks == 0) return PW_OK;
+  try {
+    std::vector<int32_t> ids(from->second.begin(), from->second.begin() + n_blocks);
+    for (int32_t id : ids) kv->sharers.emplace(id, 1);  // (of one that is not shared yet: its holder)
+    kv->held[child] = std::move(ids);
+  } catch (...) {
+    for (int64_t i = 0; i < n_blocks; ++i) {
+      auto it = kv->sharers.find(from->second[(size_t)i]);
+      if (it != kv->sharers.end() && it->second == 1) kv->sharers.erase(it);
+    }
+    return PW_ERR_OOM;
+  }
+  for (int32_t id : kv->held[child]) ++kv->sharers[id];
+  return PW_OK;
+}
+
+extern "C" pw_status pw_kv_unshare(pw_kv *kv, int64_t request, int64_t index, int32_t *src, int32_t *dst) {
+  if (!kv || !src || !dst || index < 0) return PW_ERR_INVALID;
+  if (pw_status st = refresh_weights(kv)) return st;
+  auto it = kv->held.find(request);
+  if (it == kv->held.end() || index >= (int64_t)it->second.size()) return PW_ERR_INVALID;
+  int32_t &id = it->second[(size_t)index];
+  if (kv->sharers.find(id) == kv->sharers.end()) {
+    *src = *dst = id;
+    return PW_OK;
+  }
+  const int64_t c = covered(kv, request, 1);
+  if (c < 0) return PW_ERR_OOM;
+  *src = id;
+  drop(kv, id);  // (shared: another holder keeps it)
+  *dst = id = take_lowest(kv);
+  ++kv->U;
+  if (c > 0) pw_kv_announce(kv, request, kv->announced[request] - c);
+  return PW_OK;
+}
+
+extern "C" pw_status pw_kv_trim(pw_kv *kv, int64_t request, int64_t n_keep, int64_t *n_released) {
+  if (!kv || n_keep < 0) return PW_ERR_INVALID;
+  int64_t n = 0;
+  auto it = kv->held.find(request);
+  if (it != kv->held.end())
+    while ((int64_t)it->second.size() > n_keep) {
+      n += drop(kv, it->second.back());
+      it->second.pop_back();
+    }
+  lower_mark(kv);
+  if (n_released) *n_released = n;
+  return PW_OK;
+}
+
+extern "C" pw_status pw_kv_compact(pw_kv *kv, int64_t limit, int32_t *src, int32_t *dst, int64_t capacity_out, int64_t *n) {
+  if (!kv || !n || limit < kv->U || capacity_out < 0 || (capacity_out > 0 && (!src || !dst))) return PW_ERR_INVALID;
+  try {
+    std::set<int32_t> used, above;
+    for (const auto &h : kv->held) used.insert(h.second.begin(), h.second.end());
+    for (int32_t id : used)
+      if (id >= limit) above.insert(id);
+    *n = (int64_t)above.size();
+    if (*n > capacity_out) return PW_ERR_INVALID;
+    std::unordered_map<int32_t, int32_t> to;
+    std::set<int32_t> freed;
+    int32_t place = 0;
+    for (int32_t id : above) {
+      while (used.count(place)) ++place;
+      to[id] = place++;
+    }
+    // what the moves leave free, below the new high-water mark
+    for (const auto &m : to) {
+      used.erase(m.first);
+      used.insert(m.second);
+    }
+    const int32_t top = used.empty() ? 0 : *used.rbegin() + 1;
+    int32_t at = 0;
+    for (int32_t id : used) {
+      for (; at < id; ++at) freed.insert(at);
+      at = id + 1;
+    }
+    std::unordered_map<int32_t, int64_t> sharers;
+    for (const auto &s : kv->sharers) {
+      auto m = to.find(s.first);
+      sharers[m == to.end() ? s.first : m->second] = s.second;
+    }
+    // (nothing below throws)
+    int64_t i = 0;
+    for (int32_t id : above) {
+      src[i] = id;
+      dst[i++] = to.find(id)->second;
+    }
+    for (auto &h : kv->held)
+      for (int32_t &id : h.second) {
+        auto m = to.find(id);
+        if (m != to.end()) id = m->second;
+      }
+    kv->sharers.swap(sharers);
+    kv->freed.swap(freed);
+    kv->next_id = top;
+  } catch (...) {
+    return PW_ERR_OOM;
+  }
   return PW_OK;
 }
 

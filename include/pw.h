@@ -447,8 +447,24 @@ pw_status pw_kv_announce(pw_kv *kv, int64_t request, int64_t n_blocks);
  * written). */
 pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, int32_t *ids_out);
 /* Return every block of request r and drop its announcement; the count to *n_released
- * (may be NULL).  An unknown request releases nothing. */
+ * (may be NULL).  An unknown request releases nothing.  (A block that other requests hold too, see pw_kv_fork, stays
+ * theirs and does not count.) */
 pw_status pw_kv_release(pw_kv *kv, int64_t request, int64_t *n_released);
+/* Request `child`, which holds no block (else PW_ERR_STATE), gets the first n_blocks blocks of `parent` (which holds as
+ * many, else PW_ERR_INVALID): both hold them from then on, a block counts once in U, and it is free when its last holder has
+ * returned it.  Costs no block.  A shared block is written to by nobody; pw_kv_unshare comes before that. */
+pw_status pw_kv_fork(pw_kv *kv, int64_t parent, int64_t child, int64_t n_blocks);
+/* Before request r writes to its block number `index` (PW_ERR_INVALID if it holds fewer): a block that others hold too is
+ * replaced by a fresh one, granted as by pw_kv_grow (one block, PW_ERR_OOM).  *src is the block before and *dst the one from
+ * now on, whose contents pw_kv_copy brings over; both the same where the block was the request's alone. */
+pw_status pw_kv_unshare(pw_kv *kv, int64_t request, int64_t index, int32_t *src, int32_t *dst);
+/* Return the blocks of request r behind its first n_keep (>= 0); how many became free to *n_released (may be NULL).
+ * Announcements stay. */
+pw_status pw_kv_trim(pw_kv *kv, int64_t request, int64_t n_keep, int64_t *n_released);
+/* Bring all blocks in use below the id `limit` (at least U, else PW_ERR_INVALID): those at or above it, ascending, go to
+ * src[0 .. *n - 1], and the lowest free ids, which take their places in every request, to dst.  pw_kv_copy moves the
+ * contents and renames the blocks in device tables.  With capacity < *n nothing is changed but *n (PW_ERR_INVALID). */
+pw_status pw_kv_compact(pw_kv *kv, int64_t limit, int32_t *src, int32_t *dst, int64_t capacity, int64_t *n);
 /* Blocks request r holds and has announced (0 and 0 for an unknown request); either
  * pointer may be NULL.  The held count is the request's weight in pw_merge_requests. */
 pw_status pw_kv_request(const pw_kv *kv, int64_t request, int64_t *held, int64_t *announced);
@@ -497,6 +513,7 @@ typedef struct {
     int max_shared_tokens;/* largest n_tokens of a step with n_groups > 0 (0: no such steps) */
     int n_plans;          /* plans kept at a time, 1..16 */
     int device;           /* CUDA device ordinal */
+    int max_tree_tokens;  /* largest n_tokens of a step planned by pw_attn_plan_tree (0: no such steps) */
 } pw_attn_desc;
 
 /* One engine step.  Every pointer is device memory that stays the caller's. */
@@ -526,7 +543,8 @@ typedef struct {
 } pw_kv_step;
 
 /* Create an attention handle: plans, split workspace (about 40 MB), max_tokens * n_heads / 8 bytes of marks and, with
- * max_shared_tokens, 4 * max_shared_tokens * n_heads * (head_dim + 1) bytes for the shared prefixes' results.  The calls
+ * max_shared_tokens, 4 * max_shared_tokens * n_heads * (head_dim + 1) bytes for the shared prefixes' results; 32 *
+ * max_tree_tokens bytes a plan, 4 * n_blocks bytes and 1792 * L bytes for trees, moved blocks and rotations.  The calls
  * of one handle run on one stream at a time (its workspace is shared by them), and by one host
  * thread.  PW_ERR_INVALID on a shape outside the ranges above, PW_ERR_CUDA / PW_ERR_OOM otherwise. */
 pw_status pw_attn_create(const pw_attn_desc *desc, pw_attn **out);
@@ -564,6 +582,64 @@ pw_status pw_attn_plan(pw_attn *a, int plan, const pw_kv_step *step, int window,
  * Rows with slot -1 are skipped. */
 pw_status pw_attn_append(pw_attn *a, int layer, const pw_kv_step *step, const void *k, int64_t k_token,
                          int64_t k_head, const void *v, int64_t v_token, int64_t v_head, pw_stream stream);
+/* Rotation of queries and keys by position, and norms of both before it.  Of each head the first rot_dim elements make
+ * rot_dim / 2 pairs; pair i of a token is turned by the angle f = p * inv_freq[i], p the token's position on axis axis[i]:
+ *   a' = scale (a cos f - b sin f),  b' = scale (a sin f + b cos f),
+ * which is exact to fp32 at every int32 position (the angle's part of a turn is computed in whole numbers).  Before that a
+ * head of q (k) is x / sqrt(mean x^2 + eps) * q_gain (k_gain), where gains are given.  All of it is fp32, rounded once. */
+typedef struct {
+    int rot_dim;            /* a multiple of 8, at most head_dim; 0: nothing is turned */
+    int interleaved;        /* pair i is the elements 2 i and 2 i + 1; else i and i + rot_dim / 2 */
+    int n_axes;             /* positions of a token, 1..4 (time, height, width) */
+    const double *inv_freq; /* host [rot_dim / 2], finite: radians for each position */
+    const int32_t *axis;    /* host [rot_dim / 2], or NULL: every pair follows axis 0 */
+    float scale;            /* of sine and cosine: 1 but where a long-context scheme says otherwise; finite */
+    const float *q_gain, *k_gain; /* [head_dim], host or device (detected), or NULL: no norm */
+    float eps;              /* >= 0, of the norms */
+} pw_rope_desc;
+/* Set a layer's rotation (everything in desc is copied).  Waits for the device's work, so not while a stream is captured; a
+ * pw_attn_rope_append captured before it is to be captured again. */
+pw_status pw_attn_set_rope(pw_attn *a, int layer, const pw_rope_desc *desc);
+/* Norms, rotation and cache write of the step's rows in one pass: q to q_out, k and v to the layer's cache (v as it is).
+ * q, q_out, k and v as in pw_attn_append, q and q_out with n_heads heads; q_out may be q itself (same strides) and overlaps
+ * nothing else.  pos: int32 [n_axes][n_tokens], or NULL: step->pos for every axis (for drafted trees: pw_tree's pos).  Rows with slot -1 are
+ * skipped: their rows of q_out stay as they were.  PW_ERR_STATE before pw_attn_set_rope and pw_attn_bind of the layer. */
+pw_status pw_attn_rope_append(pw_attn *a, int layer, const pw_kv_step *step, const void *q, int64_t q_token, int64_t q_head,
+                              void *q_out, int64_t qo_token, int64_t qo_head, const void *k, int64_t k_token, int64_t k_head,
+                              const void *v, int64_t v_token, int64_t v_head, const int32_t *pos, pw_stream stream);
+/* Drafted tokens that form a tree: the tree of request r is its last tree_len[r] keys, nodes 0, 1, ... from the tree's
+ * start s = kv_len[r] - tree_len[r], new ones or written by earlier steps.  Node i follows node parent[r][i] < i, or the token
+ * before the tree (-1).  Device memory that stays the caller's. */
+enum { PW_TREE_NODES = 256 };
+typedef struct {
+    const int32_t *tree_len; /* [R] at most PW_TREE_NODES, parent_stride and kv_len[r]; 0: no tree, the request's rows see what
+                                they see under pw_attn_plan */
+    const int32_t *parent;   /* [R][parent_stride] */
+    int parent_stride;
+    int32_t *pos;            /* out [n_tokens], or NULL: positions of the rows, s + the node's depth (roots: 0) for nodes,
+                                else as in step->pos; -1 for padding */
+} pw_tree;
+/* pw_attn_plan for a step with trees.  The row of a node sees the keys before the tree and, of the tree, the node itself and
+ * its ancestors.  Windows and distance biases go by positions: node i stands at s + its depth, as a row and as a key.  A
+ * length or a parent out of range is reported by pw_attn_check (PW_ERR_STATE): a tree_len counts as 0 then, a parent as -1.
+ * A captured pw_attn_forward is replayed under the rules of pw_attn_plan, and with a plan of the call that it was captured
+ * with.  PW_ERR_INVALID also where n_tokens exceeds max_tree_tokens. */
+pw_status pw_attn_plan_tree(pw_attn *a, int plan, const pw_kv_step *step, int window, const pw_tree *tree, pw_stream stream);
+/* Once drafts are verified: of each request's tree (as above; parents are not read) the nodes keep[r][0] < keep[r][1] < ...
+ * < keep[r][n_keep[r] - 1], a path from a root, move to the tree's start: key and value of position s + keep[r][i] go to s + i, in all
+ * layers' caches.  ctx_out [R] (NULL: not written): s + n_keep[r], the request's ctx_len in the next step; what lies
+ * behind is free to be written again.  keep [R][keep_stride] and n_keep [R] are device memory.  A length, or a node that does not
+ * ascend or lies outside the tree, is reported by pw_attn_check (PW_ERR_STATE); that request keeps what came before it.  Two
+ * requests' trees share no block.  PW_ERR_STATE if a layer's cache is not bound. */
+pw_status pw_kv_keep(pw_attn *a, const pw_kv_step *step, const int32_t *tree_len, const int32_t *keep, int keep_stride,
+                     const int32_t *n_keep, int32_t *ctx_out, pw_stream stream);
+/* Copy the blocks src[i] to dst[i], i < n, in all layers' caches (src and dst: device int32).  With a table (device
+ * [table_rows][table_stride], else NULL) its entries src[i] then become dst[i].  The dst are distinct and none of them is a
+ * src; with a table the src are distinct, too.  Where they are not, what lies in those blocks and entries afterwards is not
+ * specified.  Pairs with an id outside the cache are skipped and reported by pw_attn_check (PW_ERR_STATE).  n = 0 does
+ * nothing.  PW_ERR_STATE if a layer's cache is not bound. */
+pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, int32_t *table, int table_rows, int table_stride,
+                     pw_stream stream);
 /* Attention of the step's rows over the layer's cache, which holds the new tokens already: the formula
  * above.  q and o as k above, over n_heads heads; query head h reads key/value head h / (n_heads /
  * n_kv_heads).  lse: fp32 [n_tokens][n_heads] or NULL.  scale finite; softcap >= 0 (0: none); slopes: fp32
@@ -579,8 +655,8 @@ pw_status pw_attn_forward(pw_attn *a, int layer, int plan, const void *q, int64_
  * a row may see).  PW_ERR_INVALID for another kind or n < 0. */
 pw_status pw_attn_set_fault(pw_attn *a, int kind, int n);
 /* Wait for `stream` and report what the handle's calls found since the last check: PW_ERR_TIMEOUT if a
- * bounded device wait expired, PW_ERR_STATE for the findings of pw_kv_map and for a forward whose plan was laid out
- * anew for another shape (message in pw_last_error(NULL)).
+ * bounded device wait expired, PW_ERR_STATE for the findings of pw_kv_map, pw_attn_plan_tree, pw_kv_keep and pw_kv_copy and
+ * for a forward whose plan was laid out anew for another shape (message in pw_last_error(NULL)).
  * Clears what it reports. */
 pw_status pw_attn_check(pw_attn *a, pw_stream stream);
 
