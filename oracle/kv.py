@@ -21,6 +21,8 @@ The pages give no formula for how those three signals make F_blk.  Readings take
   other n - c blocks must fit in F_blk.  A grow is all or nothing.  A release returns all of
   r's blocks and drops its announcement.
 * Block ids are logical, in [0, floor(S / B)), and the lowest free id is granted first.
+* Requests may share blocks: a fork holds the first blocks of its parent.  U counts a shared block once, and it is free
+  when nobody holds it.
 
 Parity: pinned by a hand-worked sequence (tests/golden/kv_hand.json) computed from these
 readings; the pages print no numbers for it.
@@ -54,7 +56,7 @@ class KVAllocator:
         return max(0, self.S - self.W) // self.B
 
     def used(self) -> int:
-        return sum(len(ids) for ids in self.held.values())
+        return len({i for ids in self.held.values() for i in ids})
 
     def pending(self) -> int:
         return sum(self.announced.values())
@@ -96,9 +98,54 @@ class KVAllocator:
 
     def release(self, r: int) -> int:
         ids = self.held.pop(r, [])
-        self.free_ids.update(ids)
         self.announced.pop(r, None)
+        return self._free(ids)
+
+    def _free(self, ids) -> int:
+        ids = set(ids) - {i for h in self.held.values() for i in h}
+        self.free_ids.update(ids)
         return len(ids)
+
+    # ---- shared blocks
+    def fork(self, parent: int, child: int, n: int):
+        if n < 0 or parent == child or n > len(self.held.get(parent, [])):
+            raise KVError("the parent holds fewer blocks")
+        if self.held.get(child):
+            raise KVError("the child holds blocks")
+        if n:
+            self.held[child] = self.held[parent][:n]
+
+    def unshare(self, r: int, index: int):
+        """(block before, block from now on) of r's block number index."""
+        ids = self.held.get(r, [])
+        if not 0 <= index < len(ids):
+            raise KVError("no such block")
+        old = ids[index]
+        if sum(old in h for h in self.held.values()) == 1:
+            return old, old
+        self.grow(r, 1)
+        ids = self.held[r]
+        ids[index] = ids.pop()
+        return old, ids[index]
+
+    def trim(self, r: int, n_keep: int) -> int:
+        if n_keep < 0:
+            raise KVError("blocks to keep must be >= 0")
+        ids = self.held.get(r, [])
+        gone, ids[n_keep:] = ids[n_keep:], []
+        return self._free(gone)
+
+    def compact(self, limit: int):
+        """[(block, its new id)] of the blocks at or above limit, ascending."""
+        used = {i for ids in self.held.values() for i in ids}
+        if limit < len(used):
+            raise KVError("more blocks are in use than fit below the limit")
+        above = sorted(i for i in used if i >= limit)
+        to = dict(zip(above, sorted(self.free_ids)))
+        for ids in self.held.values():
+            ids[:] = [to.get(i, i) for i in ids]
+        self.free_ids = (self.free_ids | set(above)) - set(to.values())
+        return sorted(to.items())
 
     def request(self, r: int):
         """(blocks held, blocks announced) of request r."""
