@@ -678,7 +678,8 @@ pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, 
                      pw_stream stream) {
   if (!a) return bad("null argument");
   if (n < 0 || (n > 0 && (!src || !dst))) return bad("n pairs are needed");
-  if (table && (table_rows < 1 || table_stride < 1)) return bad("the table needs rows and entries");
+  if ((table || table_rows || table_stride) && (!table || table_rows < 1 || table_stride < 1))
+    return bad("the table needs rows and entries");
   if (n > a->d.n_blocks) return bad("more pairs than the cache has blocks");
   if ((int64_t)n * ((int64_t)a->d.block_tokens * a->d.n_kv_heads * a->d.head_dim / 16384 + 1) > INT32_MAX)
     return bad("too many pairs for one call");
