@@ -12,7 +12,7 @@
 
 namespace pw {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // Sine and cosine of 2 pi h 2^-32: their Taylor polynomials in x, |x| <= pi / 4 (x^11 / 11! < 2^-29, x^10 / 10! < 2^-25),
 // turned back by quarters.
@@ -30,22 +30,6 @@ __device__ __forceinline__ void sincos_turn(uint32_t h, float &s, float &c) {
   const float a = quarter & 1 ? pc : ps, b = quarter & 1 ? ps : pc;
   s = quarter & 2 ? -a : a;
   c = (quarter + 1) & 2 ? -b : b;
-}
-
-template <bool BF>
-__device__ __forceinline__ float2 to_floats(uint32_t w) {
-  if (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  const __half2 h = *reinterpret_cast<const __half2 *>(&w);
-  return __half22float2(h);
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t from_floats(float lo, float hi) {
-  uint32_t r;
-  if (BF)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // P elements, in one load or store.
@@ -73,126 +57,179 @@ __device__ __forceinline__ void store_piece(uint16_t *p, const Piece16<P> &r) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
 }
 
-// GL lanes to a head, each with two pieces of P elements: the two halves of P pairs (IL: or, side by side, 2 P elements that
-// are P pairs).  A warp takes U of its 32 / GL heads at a time, all of them heads of q, or of k, or of v; `parts` warps
-// share a token's.
+// 2 N floats as pairs, or zeros.
+template <int N>
+__device__ __forceinline__ void load_pairs(const float *p, bool there, uint64_t (&out)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float4 x = there ? *reinterpret_cast<const float4 *>(p + 2 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    out[i] = pair(x.x, x.y);
+    out[i + 1] = pair(x.z, x.w);
+  }
+}
+
+// A CTA takes a few tokens.  Their angles' sines and cosines, which all heads share, come first, to shared memory (computed by
+// every warp for its heads they were a third of the instructions); the rows' first loads are under way by then.  GL lanes
+// have a head, each two pieces of P elements: the two halves of P pairs (IL: or, side by side, 2 P elements that are P
+// pairs).  A warp takes kRopeHeads heads for each GL lanes at a time, all of q, or of k, or of v, so that it has one kind of
+// address and of work.
+//
+// Memory bounds it: 8205 tokens of 32/8 heads of 128 with norms, 202 MB, take 37 us (5.4 TB/s, 80 % of the copy rate; a
+// copy of that size has the same beginning and end), 5003 of 16/16 heads of 96 17.6 us.  The same by 2 heads at a time 39 and
+// 21 us, by 3 or 6 CTAs an SM 38 to 41 and 19; one token to a CTA 39 and 21, 5 or 8 tokens 42 and 18 to 20, where the last CTAs
+// run alone.  With the slot's, the positions' and the rows' loads behind each other it took 62 us.
+constexpr int kRopeHeads = 4, kRopeTokens = 4, kPairs = 64, kRopeCtas = 5;
 template <bool BF, int P, int GL, bool IL>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a, int parts) {
-  constexpr int U = 2, kHeads = 32 / GL * U;  // heads that a warp takes at a time
-  const int lane = threadIdx.x & 31, sub = lane / GL, l = lane % GL;
-  const unsigned item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);  // at most 2^20 tokens, 768 parts
-  const int t = (int)(item / (unsigned)parts), part = (int)(item - (unsigned)t * parts);
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeArgs a, int tokens) {
+  constexpr int U = kRopeHeads, S = 32 / GL, Q = P / 2;
+  __shared__ __align__(16) float cos_of[kRopeTokens][kPairs], sin_of[kRopeTokens][kPairs];
+  const int lane = threadIdx.x & 31, sub = lane / GL, l = lane % GL, pair_of = threadIdx.x % kPairs;
   // this lane's pieces, and whether they are turned
-  const int rot_lanes = IL ? 0 : a.rot / (2 * P);
-  const bool turn0 = IL ? 2 * P * l < a.rot : l < rot_lanes, turn1 = IL ? 2 * P * l + P < a.rot : turn0;
+  const bool turn0 = 2 * P * l < a.rot, turn1 = IL ? 2 * P * l + P < a.rot : turn0;
   const int at0 = !IL && turn0 ? P * l : 2 * P * l;  // (behind the turned ones: rot + 2 P (l - rot / 2 P))
   const int at1 = !IL && turn0 ? a.rot / 2 + P * l : 2 * P * l + P;
   const bool has0 = at0 < a.D, has1 = at1 < a.D;
+  const int t0 = blockIdx.x * tokens, n = min(tokens, a.n_tokens - t0);
   pdl_trigger();
-  uint64_t f[P];
-  int axis[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {  // (set long before this launch)
-    const bool on = IL && i >= P / 2 ? turn1 : turn0;
-    f[i] = on ? a.table->turn[P * l + i] : 0;
-    axis[i] = on ? a.table->axis[P * l + i] : 0;
+  uint64_t turn = 0;
+  int axis = 0;
+  if (pair_of < a.rot / 2) {  // (set long before this launch)
+    turn = a.table->turn[pair_of];
+    axis = a.table->axis[pair_of];
   }
   pdl_wait();
-  if (t >= a.n_tokens) return;
-  const int64_t slot = a.slot[t];
-  if (slot < 0) return;
-  const bool stored = slot >> a.log_bt < a.n_blocks;
-  const int64_t place = (slot >> a.log_bt) * a.block_stride + (slot & (a.bt - 1)) * a.token_stride;
-  float sn[P], cs[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int p = a.pos[axis[i] * a.pos_axis + t];
-    sincos_turn((uint32_t)(f[i] * (uint64_t)(int64_t)p >> 32), sn[i], cs[i]);
-    sn[i] *= a.scale;
-    cs[i] *= a.scale;
-  }
-  const int nq = (a.Hq + kHeads - 1) / kHeads, nk = (a.Hkv + kHeads - 1) / kHeads;
-  for (int c = part; c < nq + 2 * nk; c += parts) {
-    const int kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
-    const int h0 = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * kHeads + sub, H = kind == 0 ? a.Hq : a.Hkv;
-    const uint16_t *src = kind == 0 ? a.q + t * a.q_token : kind == 1 ? a.k + t * a.k_token : a.v + t * a.v_token;
-    const int64_t src_head = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
-    uint16_t *dst = kind == 0 ? a.qo + t * a.qo_token : kind == 1 ? a.kc + place : a.vc + place;
-    const int64_t dst_head = kind == 0 ? a.qo_head : a.head_stride;
-    Piece16<P> x[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * (32 / GL);
-      x[u][0] = x[u][1] = Piece16<P>{};
-      if (h < H && has0) x[u][0] = load_piece<P>(src + h * src_head + at0);
-      if (h < H && has1) x[u][1] = load_piece<P>(src + h * src_head + at1);
+  // this warp's share of the work: chunks of S U heads of q, k and v, token by token
+  const int nq = (a.Hq + S * U - 1) / (S * U), nk = (a.Hkv + S * U - 1) / (S * U);
+  int tok = 0, chunk = threadIdx.x >> 5;
+  Piece16<P> x[U][2];
+  int64_t slot = -1;
+  int kind = 0, left = 0;  // q, k or v; heads from this lane's first one on
+  auto load = [&] {
+    while (chunk >= nq + 2 * nk) {
+      chunk -= nq + 2 * nk;
+      ++tok;
     }
-    const bool norm = kind == 0 ? a.norm_q : kind == 1 && a.norm_k;
+    if (tok >= n) return;
+    const int64_t t = t0 + tok;
+    kind = chunk < nq ? 0 : chunk < nq + nk ? 1 : 2;
+    const int h = (kind == 0 ? chunk : kind == 1 ? chunk - nq : chunk - nq - nk) * (S * U) + sub;
+    left = (kind == 0 ? a.Hq : a.Hkv) - h;
+    const int64_t head = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
+    const uint16_t *src = (kind == 0 ? a.q + t * a.q_token : kind == 1 ? a.k + t * a.k_token : a.v + t * a.v_token) + h * head;
+    slot = a.slot[t];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * (32 / GL);
-      if (kind < 2) {
-        float y[2][P];
+      x[u][0] = x[u][1] = Piece16<P>{};
+      if (u * S < left && has0) x[u][0] = load_piece<P>(src + at0);
+      if (u * S < left && has1) x[u][1] = load_piece<P>(src + at1);
+      src += S * head;
+    }
+  };
+  load();
+  if (pair_of < a.rot / 2)
+    for (int k = threadIdx.x / kPairs; k < n; k += kRopeThreads / kPairs) {
+      float s, c;
+      sincos_turn((uint32_t)(turn * (uint64_t)(int64_t)a.pos[axis * a.pos_axis + t0 + k] >> 32), s, c);
+      sin_of[k][pair_of] = s * a.scale;
+      cos_of[k][pair_of] = c * a.scale;
+    }
+  __syncthreads();
+  while (tok < n) {
+    if (kind < 2) {
+      // pairs of pairs: cosines, sines, and the gains of either piece
+      uint64_t cs[Q], sn[Q], minus_sn[Q], g[2][Q];
+      load_pairs<Q>(&cos_of[tok][P * l], turn0, cs);
+      load_pairs<Q>(&sin_of[tok][P * l], turn0, sn);
+#pragma unroll
+      for (int i = 0; i < Q; ++i) minus_sn[i] = sn[i] ^ 0x8000000080000000ull;
+      const bool norm = kind ? a.norm_k : a.norm_q;
+      if (norm) {
+        load_pairs<Q>(a.table->gain[kind] + at0, has0, g[0]);
+        load_pairs<Q>(a.table->gain[kind] + at1, has1, g[1]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!__any_sync(0xffffffffu, u * S < left)) break;
+        uint64_t y[2][Q];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int i = 0; i < P; i += 2) {
-            const float2 z = to_floats<BF>(x[u][s].w[i / 2]);
-            y[s][i] = z.x, y[s][i + 1] = z.y;
+          for (int i = 0; i < Q; ++i) {
+            const float2 z = unpack2<BF>(x[u][s].w[i]);
+            y[s][i] = pair(z.x, z.y);
           }
         if (norm) {
-          float ss = 0.f;
+          uint64_t sq = 0;
 #pragma unroll
-          for (int i = 0; i < P; ++i) ss = fmaf(y[0][i], y[0][i], fmaf(y[1][i], y[1][i], ss));
+          for (int i = 0; i < Q; ++i) sq = fma2(y[0][i], y[0][i], fma2(y[1][i], y[1][i], sq));
+          float ss, s1;
+          unpair(sq, ss, s1);
+          ss += s1;
 #pragma unroll
           for (int o = 1; o < GL; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
-          const float *g = a.table->gain[kind];
+          const uint64_t rr = pair(r, r);
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            if (has0) y[0][i] *= r * g[at0 + i];
-            if (has1) y[1][i] *= r * g[at1 + i];
-          }
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < Q; ++i) y[s][i] = mul2(y[s][i], mul2(rr, g[s][i]));
         }
         if (IL) {
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < P; i += 2) {
+            for (int i = 0; i < Q; ++i) {
               if (!(s ? turn1 : turn0)) continue;  // (0 times what is not turned may be NaN)
-              const int j = s * (P / 2) + i / 2;
-              const float p = y[s][i], q = y[s][i + 1];
-              y[s][i] = fmaf(p, cs[j], -q * sn[j]);
-              y[s][i + 1] = fmaf(p, sn[j], q * cs[j]);
+              const int j = s * Q + i;
+              float p, q, c0, c1, s0, s1;
+              unpair(y[s][i], p, q);
+              unpair(cs[j / 2], c0, c1);
+              unpair(sn[j / 2], s0, s1);
+              const float c = j & 1 ? c1 : c0, z = j & 1 ? s1 : s0;
+              y[s][i] = pair(fmaf(p, c, -q * z), fmaf(p, z, q * c));
             }
         } else if (turn0) {
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float p = y[0][i], q = y[1][i];
-            y[0][i] = fmaf(p, cs[i], -q * sn[i]);
-            y[1][i] = fmaf(p, sn[i], q * cs[i]);
+          for (int i = 0; i < Q; ++i) {
+            const uint64_t p = y[0][i], q = y[1][i];
+            y[0][i] = fma2(p, cs[i], mul2(q, minus_sn[i]));
+            y[1][i] = fma2(p, sn[i], mul2(q, cs[i]));
           }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int i = 0; i < P; i += 2) x[u][s].w[i / 2] = from_floats<BF>(y[s][i], y[s][i + 1]);
-      }
-      if (h < H && (kind == 0 || stored)) {
-        if (has0) store_piece<P>(dst + h * dst_head + at0, x[u][0]);
-        if (has1) store_piece<P>(dst + h * dst_head + at1, x[u][1]);
+          for (int i = 0; i < Q; ++i) {
+            float p, q;
+            unpair(y[s][i], p, q);
+            x[u][s].w[i] = pack_pair<BF>(p, q);
+          }
       }
     }
+    const int64_t t = t0 + tok, block = slot >> a.log_bt, head = kind == 0 ? a.qo_head : a.head_stride;
+    const int h = (kind == 0 ? a.Hq : a.Hkv) - left;
+    uint16_t *dst = (kind == 0 ? a.qo + t * a.qo_token
+                               : (kind == 1 ? a.kc : a.vc) + block * a.block_stride + (slot & (a.bt - 1)) * a.token_stride) +
+                    h * head;
+    if (slot >= 0 && (kind == 0 || block < a.n_blocks)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * S < left && has0) store_piece<P>(dst + at0, x[u][0]);
+        if (u * S < left && has1) store_piece<P>(dst + at1, x[u][1]);
+        dst += S * head;
+      }
+    }
+    chunk += kRopeThreads / 32;
+    load();
   }
 }
 
 template <bool BF, int P, int GL, bool IL>
 static int launch_one(const RopeArgs &a, cudaStream_t st) {
-  constexpr int kHeads = 32 / GL * 2;
-  const int parts = (a.Hq + kHeads - 1) / kHeads + 2 * ((a.Hkv + kHeads - 1) / kHeads);
-  const int64_t warps = (int64_t)a.n_tokens * parts, per = kRopeThreads / 32;
-  return (int)launch_pdl(rope_kernel<BF, P, GL, IL>, dim3((unsigned)((warps + per - 1) / per)), dim3(kRopeThreads), 0, st, a,
-                         parts);
+  // as few tokens to a CTA as keep the SMs in work, for the shortest way, and no more than make the tables worth their while
+  const int tokens = a.n_tokens >= 152 * 8 * kRopeTokens ? kRopeTokens : a.n_tokens >= 152 * 16 ? 2 : 1;
+  return (int)launch_pdl(rope_kernel<BF, P, GL, IL>, dim3((a.n_tokens + tokens - 1) / tokens), dim3(kRopeThreads), 0, st, a,
+                         tokens);
 }
 template <bool BF>
 static int launch_type(const RopeArgs &a, cudaStream_t st) {
