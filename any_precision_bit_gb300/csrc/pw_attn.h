@@ -125,6 +125,12 @@ struct TreeArgs {
   uint32_t *seen;  // [n_tokens][kTreeWords]
   int *err;
 };
+// Blocks of 256 threads that find the bounds of such a plan: one for each request, and one for each 256 rows.  With at most
+// kTreeListBlocks the work is laid out in the same launch, by one CTA.  Measured, one launch and two (us, in a row of captured
+// plans): one request of 24 nodes 7.5 and 8.3, four of up to 64 8.7 and 9.1, four of up to 200 9.8 and 9.9, six of up to 40 9.6 and
+// 9.3, twelve of up to 64 (15 blocks) 12.2 and 9.9; called from Python one launch takes 2 us less.
+constexpr int kTreeRows = 256, kTreeListBlocks = 8;
+inline int tree_blocks(const TreeArgs &a) { return a.plan.R + (a.plan.n_tokens + kTreeRows - 1) / kTreeRows; }
 
 struct MapArgs {
   int R, n_tokens, table_rows, table_stride, bt, n_blocks, n_ids;
@@ -186,8 +192,11 @@ struct CopyArgs {
   const int *src, *dst;
   int n, n_blocks, bt, log_bt, n_heads, head_dim;
   int *where;  // [n_blocks] number of the pair that a block is the source of, where it is one; null: not asked for
+  int *table;  // whose entries are renamed in the same launch (few pairs, the first layers), else null
+  int64_t entries;
   int *err;
 };
+constexpr int kRenamePairs = 64;  // at most so many pairs are looked for one by one
 
 // Tensor maps of one forward launch: boxes of 64 elements of a head by (Q) the G heads of a
 // key/value head by a tile's tokens, or (K, V) the tokens of a block; 128-byte swizzle, the K-major
@@ -242,10 +251,11 @@ int launch_attn_bounds(const PlanArgs &a, void *stream);
 int launch_attn_list(const PlanArgs &a, void *stream);
 int launch_attn_append(const AppendArgs &a, void *stream);
 int launch_tree_bounds(const TreeArgs &a, void *stream);
+int launch_tree_list(const TreeArgs &a, void *stream);
 int launch_rope(const RopeArgs &a, int bf16, void *stream);
 int launch_keep(const KeepArgs &a, const MoveLayers &m, int n_layers, void *stream);
 int launch_copy(const CopyArgs &a, const MoveLayers &m, int n_layers, void *stream);
-int launch_rename(const CopyArgs &a, int *table, int table_rows, int table_stride, void *stream);
+int launch_rename(const CopyArgs &a, void *stream);
 int launch_attn(const AttnArgs &a, const AttnMaps &maps, int bf16, void *stream);
 
 }  // namespace pw

@@ -295,7 +295,13 @@ pw_status lay_out(pw_attn *a, int plan, const pw_kv_step *s, int window, const i
   g.shape_out = p.shape;
   int e;
   if (tree) {
-    const TreeArgs t{g, tree->tree_len, tree->parent, tree->parent_stride, tree->pos, p.seen, a->err};
+    TreeArgs t{g, tree->tree_len, tree->parent, tree->parent_stride, tree->pos, p.seen, a->err};
+    if (!s->n_groups && tree_blocks(t) <= kTreeListBlocks) {
+      t.plan.list = p.requests;
+      if ((e = launch_tree_list(t, stream))) return cuda_failed("pw_attn_plan_tree launch", e);
+      p.set = true;
+      return PW_OK;
+    }
     e = launch_tree_bounds(t, stream);
   } else {
     e = launch_attn_bounds(g, stream);
@@ -681,7 +687,7 @@ pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, 
   if ((table || table_rows || table_stride) && (!table || table_rows < 1 || table_stride < 1))
     return bad("the table needs rows and entries");
   if (n > a->d.n_blocks) return bad("more pairs than the cache has blocks");
-  if ((int64_t)n * ((int64_t)a->d.block_tokens * a->d.n_kv_heads * a->d.head_dim / 16384 + 1) > INT32_MAX)
+  if ((int64_t)n * ((int64_t)a->d.block_tokens * a->d.n_kv_heads * a->d.head_dim / 16384 + 1) > INT32_MAX - 1024)
     return bad("too many pairs for one call");
   OnDevice dev(a->d.device);
   CopyArgs g{};
@@ -693,15 +699,19 @@ pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, 
   g.log_bt = log2_of(a->d.block_tokens);
   g.n_heads = a->d.n_kv_heads;
   g.head_dim = a->d.head_dim;
-  g.where = table ? a->where : nullptr;
   g.err = a->err;
+  g.entries = (int64_t)table_rows * table_stride;
+  const bool few = n <= kRenamePairs && g.entries <= (1 << 20);
+  if (!n) return for_layers(a, "", [](const MoveLayers &, int, bool) { return 0; });
   pw_status st = for_layers(a, "pw_kv_copy launch", [&](const MoveLayers &m, int layers, bool first) {
-    CopyArgs h = g;
-    if (!first) h.where = nullptr;
-    return n ? launch_copy(h, m, layers, stream) : 0;
+    g.table = first && few ? table : nullptr;
+    g.where = first && table && !few ? a->where : nullptr;
+    return launch_copy(g, m, layers, stream);
   });
-  if (st || !table || !n) return st;
-  if (int e = launch_rename(g, table, table_rows, table_stride, stream)) return cuda_failed("pw_kv_copy launch", e);
+  if (st || !table || few) return st;
+  g.table = table;
+  g.where = a->where;
+  if (int e = launch_rename(g, stream)) return cuda_failed("pw_kv_copy launch", e);
   return PW_OK;
 }
 

@@ -178,34 +178,32 @@ int launch_attn_bounds(const PlanArgs &a, void *stream) {
                          reinterpret_cast<cudaStream_t>(stream), a);
 }
 
-// The same for a step with trees.  The first R CTAs take a request's tree each, a thread a node; the others take the rows that
-// stand in no tree as attn_bounds_kernel does.  A node's way up is in descending order (a parent comes before its children), so
+// The same for a step with trees.  The first R blocks of threads take a request's tree each, a thread a node; the others take the
+// rows that stand in no tree as attn_bounds_kernel does.  A node's way up is in descending order (a parent comes before its children), so
 // that one word of its visible nodes after the other is finished; the parents lie in shared memory.
 __device__ __forceinline__ int tree_of(const TreeArgs &a, int r, int kv) {
   const int tl = a.tree_len[r];
   return tl > 0 && tl <= PW_TREE_NODES && tl <= a.parent_stride && tl <= kv ? tl : 0;
 }
-__global__ void __launch_bounds__(kStepThreads) tree_bounds_kernel(TreeArgs x) {
-  static_assert(kStepThreads == PW_TREE_NODES && kTreeWords == 8, "a thread a node, two 16-byte stores");
-  __shared__ int parent[PW_TREE_NODES];
+// One of them (`block`), in two phases with a meeting of the CTA between them: parents to shared memory, and the rows.
+__device__ __forceinline__ void tree_parents(const TreeArgs &x, int block, int tid, int *parent) {
+  const PlanArgs &a = x.plan;
+  if (block >= a.R) return;
+  const int kv = (int)min((long long)a.kv_len[block], (long long)a.table_stride * a.bt), tl = tree_of(x, block, kv);
+  if (tl != x.tree_len[block] && tid == 0) atomicOr(x.err, kAttnErrTree);
+  if (tid >= tl) return;
+  int p = x.parent[(size_t)block * x.parent_stride + tid];
+  if (p < -1 || p >= tid) {
+    atomicOr(x.err, kAttnErrTree);
+    p = -1;
+  }
+  parent[tid] = p;
+}
+__device__ __forceinline__ void tree_rows(const TreeArgs &x, int block, int tid, const int *parent) {
   const PlanArgs &a = x.plan;
   const long long cap = (long long)a.table_stride * a.bt;
-  const int tid = threadIdx.x;
-  pdl_trigger();
-  pdl_wait();
-  if ((int)blockIdx.x < a.R) {
-    const int r = blockIdx.x, kv = (int)min((long long)a.kv_len[r], cap), tl = tree_of(x, r, kv);
-    if (tl != x.tree_len[r] && tid == 0) atomicOr(x.err, kAttnErrTree);
-    if (tl == 0) return;
-    if (tid < tl) {
-      int p = x.parent[(size_t)r * x.parent_stride + tid];
-      if (p < -1 || p >= tid) {
-        atomicOr(x.err, kAttnErrTree);
-        p = -1;
-      }
-      parent[tid] = p;
-    }
-    __syncthreads();
+  if (block < a.R) {
+    const int r = block, kv = (int)min((long long)a.kv_len[r], cap), tl = tree_of(x, r, kv);
     const int start = kv - tl, q0 = max(a.q_start[r], 0), q1 = min(a.q_start[r + 1], a.n_tokens);
     const int t = q0 + (start + tid - a.ctx_len[r]);
     if (tid >= tl || t < q0 || t >= q1) return;
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kStepThreads) tree_bounds_kernel(TreeArgs x) {
     if (x.pos) x.pos[t] = b.pos;
     return;
   }
-  const int t = (blockIdx.x - a.R) * kStepThreads + tid;
+  const int t = (block - a.R) * kTreeRows + tid;
   if (t >= a.n_tokens) return;
   RowBound b{0, 0, INT_MAX, -1};
   if (t < a.q_start[a.R]) {
@@ -250,10 +248,18 @@ __global__ void __launch_bounds__(kStepThreads) tree_bounds_kernel(TreeArgs x) {
   a.bounds[t] = b;
   if (x.pos) x.pos[t] = b.pos;
 }
+__global__ void __launch_bounds__(kTreeRows) tree_bounds_kernel(TreeArgs x) {
+  static_assert(kTreeRows == PW_TREE_NODES && kTreeWords == 8, "a thread a node, two 16-byte stores");
+  __shared__ int parent[PW_TREE_NODES];
+  pdl_trigger();
+  pdl_wait();
+  tree_parents(x, blockIdx.x, threadIdx.x, parent);
+  __syncthreads();
+  tree_rows(x, blockIdx.x, threadIdx.x, parent);
+}
 
 int launch_tree_bounds(const TreeArgs &a, void *stream) {
-  return (int)launch_pdl(tree_bounds_kernel, dim3(a.plan.R + (a.plan.n_tokens + kStepThreads - 1) / kStepThreads),
-                         dim3(kStepThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  return (int)launch_pdl(tree_bounds_kernel, dim3(tree_blocks(a)), dim3(kTreeRows), 0, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 // Segments of a list: requests (and, behind them, the rows that are padding), or groups.
@@ -294,13 +300,12 @@ __device__ __forceinline__ Segment segment_of(const PlanArgs &a, int i) {
 // One list of work, by one CTA: tiles per segment and their sum; per tile (one warp each) the key
 // tiles that some row of it sees; their sum; and where each of the forward's CTAs begins.
 constexpr int kListThreads = 1024;
-__global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
-  extern __shared__ int cum_tiles[];
-  const int tid = threadIdx.x, lane = tid & 31;
+constexpr int kListTiles = 1024;  // with at most so many tiles their sums are searched in shared memory
+__device__ __forceinline__ void lay_out_list(const PlanArgs &a, int *cum_tiles) {
+  __shared__ int near_cum[kListTiles + 1];
+  const int tid = threadIdx.x;
   const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
   const int tt = a.list.tpt * a.list.streams;
-  pdl_trigger();
-  pdl_wait();
   long long before = 0;
   for (int s0 = 0; s0 < n_seg; s0 += kListThreads) {
     const int s = s0 + tid;
@@ -316,36 +321,48 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
   }
   const int n_tiles = (int)min(before, (long long)a.list.max_tiles);
   __syncthreads();
-  // lanes that look through a tile's tokens: one where they are few (a decode step's)
-  const int wide = tt > 4 ? 32 : 1;
+  // lanes that look through a tile's tokens: one where they are few (a decode step's), else as many as leave one round of
+  // tiles, or four, with eight loads a lane under way (32 lanes each and one load at a time: 96 tiles of 64 tokens 13.7 us for
+  // the whole plan instead of 11.2, a prompt of 8192 13 instead of 10.2)
+  int wide = tt > 4 ? 32 : 1;
+  while (wide > 4 && n_tiles * wide > kListThreads) wide >>= 1;
   for (int i0 = 0; i0 < n_tiles; i0 += kListThreads / wide) {
     const int i = i0 + tid / wide;
-    if (i >= n_tiles) break;  // (whole warps, or with one lane to a tile nothing that meets follows)
-    const int s = seg_of(cum_tiles, n_seg, i);
+    const bool some = i < n_tiles;
+    const int s = some ? seg_of(cum_tiles, n_seg, i) : 0;
     const Segment g = segment_of(a, s);
     AttnTile t;
     t.tok0 = g.tok0 + (i - cum_tiles[s]) * tt;
-    t.ntok = min(tt, g.tok1 - t.tok0);
+    t.ntok = some ? min(tt, g.tok1 - t.tok0) : 0;
     t.trow = g.trow;
     t.klo = g.klo;
     t.khi = g.khi;
     t.merge = g.merge;
     int lo = INT_MAX, hi = 0;
-    for (int j = wide == 32 ? lane : 0; j < t.ntok; j += wide) {
-      const RowBound b = a.bounds[t.tok0 + j];
-      const int l = max(b.lo, g.klo), h = min(b.hi, g.khi);
-      if (l < h) {
-        lo = min(lo, l);
-        hi = max(hi, h);
+    constexpr int kAhead = 8;  // rows whose bounds are under way at once
+    for (int j0 = tid & (wide - 1); j0 < t.ntok; j0 += kAhead * wide) {
+      int2 b[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int j = j0 + k * wide;
+        b[k] = j < t.ntok ? *reinterpret_cast<const int2 *>(a.bounds + t.tok0 + j) : make_int2(0, 0);  // lo and hi
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int l = max(b[k].x, g.klo), h = min(b[k].y, g.khi);
+        if (l < h) {
+          lo = min(lo, l);
+          hi = max(hi, h);
+        }
       }
     }
-    if (wide == 32) {
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
+    for (int o = wide >> 1; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     t.kv0 = hi > 0 ? lo / kAttnKeys : g.klo / kAttnKeys;
     t.kv1 = hi > 0 ? (hi - 1) / kAttnKeys + 1 : t.kv0 + 1;
-    if (wide == 1 || lane == 0) {
+    if (some && (tid & (wide - 1)) == 0) {
       a.list.tiles[i] = t;
       a.list.cum[i + 1] = t.kv1 - t.kv0 + a.list.piece_cost;
     }
@@ -357,10 +374,15 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     const int n = i < n_tiles ? a.list.cum[i + 1] : 0;
     long long total;
     const long long at = block_scan<kListThreads>(n, &total);
-    if (i < n_tiles) a.list.cum[i + 1] = sat(before + at + n);
+    if (i < n_tiles) {
+      a.list.cum[i + 1] = sat(before + at + n);
+      if (n_tiles <= kListTiles) near_cum[i + 1] = sat(before + at + n);
+    }
     before += total;
   }
+  const int *cum = n_tiles <= kListTiles ? near_cum : a.list.cum;
   if (tid == 0) {
+    near_cum[0] = 0;
     a.list.cum[0] = 0;
     a.list.meta[0] = n_tiles;
     a.list.meta[1] = sat(before);
@@ -383,13 +405,13 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
       int lo = 0, hi = n_tiles - 1;  // the last tile whose units begin at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((long long)a.list.cum[mid] * a.n_kv_heads <= u)
+        if ((long long)cum[mid] * a.n_kv_heads <= u)
           lo = mid;
         else
           hi = mid - 1;
       }
-      const int cost = a.list.cum[lo + 1] - a.list.cum[lo];
-      const long long rem = u - (long long)a.list.cum[lo] * a.n_kv_heads;
+      const int cost = cum[lo + 1] - cum[lo];
+      const long long rem = u - (long long)cum[lo] * a.n_kv_heads;
       tile = lo;
       head = (int)(rem / cost);
       off = (int)(rem - (long long)head * cost);
@@ -411,10 +433,38 @@ __global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
     if (!a.of_groups) *a.shape_out = a.shape;
   }
 }
+__global__ void __launch_bounds__(kListThreads) attn_list_kernel(PlanArgs a) {
+  extern __shared__ int cum_tiles[];
+  pdl_trigger();
+  pdl_wait();
+  lay_out_list(a, cum_tiles);
+}
+// Bounds and list of a small step with trees.
+__global__ void __launch_bounds__(kListThreads) tree_list_kernel(TreeArgs x) {
+  extern __shared__ int cum_tiles[];
+  constexpr int kBlocks = kListThreads / kTreeRows;
+  __shared__ int parent[kBlocks][PW_TREE_NODES];
+  const int blocks = x.plan.R + (x.plan.n_tokens + kTreeRows - 1) / kTreeRows, part = threadIdx.x / kTreeRows;
+  pdl_trigger();
+  pdl_wait();
+  for (int b0 = 0; b0 < blocks; b0 += kBlocks) {
+    const int block = b0 + part;
+    if (block < blocks) tree_parents(x, block, threadIdx.x % kTreeRows, parent[part]);
+    __syncthreads();
+    if (block < blocks) tree_rows(x, block, threadIdx.x % kTreeRows, parent[part]);
+    __syncthreads();
+  }
+  lay_out_list(x.plan, cum_tiles);
+}
 
 int launch_attn_list(const PlanArgs &a, void *stream) {
   const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
   return (int)launch_pdl(attn_list_kernel, dim3(1), dim3(kListThreads), sizeof(int) * (size_t)n_seg,
+                         reinterpret_cast<cudaStream_t>(stream), a);
+}
+
+int launch_tree_list(const TreeArgs &a, void *stream) {
+  return (int)launch_pdl(tree_list_kernel, dim3(1), dim3(kListThreads), sizeof(int) * (size_t)(a.plan.R + 1),
                          reinterpret_cast<cudaStream_t>(stream), a);
 }
 

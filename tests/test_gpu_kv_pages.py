@@ -175,9 +175,9 @@ def test_paths_that_are_wrong_are_reported():
 
 
 @pytest.mark.parametrize("layout,D,bt", [("nhd", 64, 16), ("hnd", 64, 32), ("apart", 72, 16), ("nhd", 8, 128), ("nhd", 128, 128)])
-@pytest.mark.parametrize("n", [1, 2, 37])
+@pytest.mark.parametrize("n", [1, 2, 37, 64, 65, 150])
 def test_copies(layout, D, bt, n):
-    s = Cache([40 * bt, 3 * bt], D=D, bt=bt, layout=layout, spare=50)
+    s = Cache([160 * bt, 3 * bt], D=D, bt=bt, layout=layout, spare=160)
     try:
         rng = np.random.default_rng(n)
         src, dst = rng.choice(s.used, n, replace=False), s.free[:n]
