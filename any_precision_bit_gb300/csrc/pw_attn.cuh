@@ -109,6 +109,7 @@ struct Bars {
     kDF = kJoin + 2,         // a piece has been handed over
     kDE = kDF + kPieces,     // ... every reader is done with it
     kDrain = kDE + kPieces,  // the MMA warp's last commit
+    kMerge,                  // TREE, kTwo: the softmax warps of both streams meet
     kNum
   };
 };
@@ -374,7 +375,16 @@ struct Mma {
   }
 };
 
-template <int FORM, int DP, bool BF>
+// Trees are small, and often one 128-row tile holds one (of at most 32 nodes with four query heads to a key/value head).
+// The two streams of kTwo then take every other key tile of the same rows, each with maxima, sums and outputs of its own,
+// which stream 0 adds up at the end of a piece: one's products run during the other's softmax again.  (Measured for trees
+// alone, ALT_MEASURED.)
+template <bool TREE>
+__device__ __forceinline__ bool alternates(bool two, int n) {
+  return TREE && !two && n > 1;
+}
+
+template <int FORM, int DP, bool BF, bool TREE>
 __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t sm, uint32_t bars, uint32_t tmem, volatile int *abort_flag) {
   using C = Cfg<FORM, DP>;
   constexpr int NS = C::NS;
@@ -412,6 +422,50 @@ __device__ void issue(const AttnArgs &a, const volatile Piece *piece, uint32_t s
   if constexpr (!SP) {
     for (; more_pieces; more_pieces = next_piece(++pieces, n, two)) {
       const uint32_t q0 = M::lo_k(sm);
+      if (alternates<TREE>(two, n)) {  // stream t & 1 has the key tile t
+        Ring<C::kStages> rk = r, rv = r;
+        rv.next();
+        auto scores = [&](int t) {
+          if (!(ok = full(rk))) return false;
+          const uint32_t st = rk.st, u = t & 1;
+          rk.next();
+          rk.next();
+          if (elect_one()) {
+            M::qk(tmem + 128 * u, q0, ring_k + st * kStep);
+            tc_commit(bars + 8 * (B::kSF + u));
+            release(st);
+            if (t + 1 == n) tc_commit(bars + 8 * B::kQE);
+          }
+          __syncwarp();
+          return true;
+        };
+        if (!scores(0) || !scores(1)) break;
+        for (int t = 0; t < n; ++t) {
+          const uint32_t u = t & 1, par = u ? p2_par : p_par;
+          if (!(ok = full(rv))) break;
+          const uint32_t v_st = rv.st, v = ring_v + v_st * kStep;
+          rv.next();
+          rv.next();
+          if (!(ok = wait(B::kPE + u, par))) break;
+          if (elect_one()) M::template pv<0, kEarly>(o0 + 128 * u, tmem + 128 * u, v, t > 1);
+          __syncwarp();
+          if (!(ok = wait(B::kPF + u, par))) break;
+          if (u)
+            p2_par ^= 1;
+          else
+            p_par ^= 1;
+          if (elect_one()) {
+            M::template pv<kEarly, kAttnKeys / 16>(o0 + 128 * u, tmem + 128 * u, v, 1);
+            if (t + 2 >= n) tc_commit(bars + 8 * (B::kOD + u));
+            release(v_st);
+          }
+          __syncwarp();
+          if (t + 2 < n && !scores(t + 2)) break;
+        }
+        if (!ok) break;
+        r = rk;
+        continue;
+      }
       if (!(ok = full(r))) break;
       uint32_t k_st = r.st;
       r.next();
@@ -1039,7 +1093,7 @@ struct Group {
 // kTwo: the softmax warps of two streams, which write their rows' results, too.
 template <int DP, bool BF, int MODE, bool TREE>
 __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *smp, uint32_t bars, uint32_t tmem,
-                       volatile int *abort_flag, volatile int *last_flag, volatile int *marked) {
+                       volatile int *abort_flag, volatile int *last_flag, volatile int *marked, volatile float2 *other) {
   using C = Cfg<kTwo, DP>;
   using B = Bars<C::kStages>;
   constexpr int NS = C::NS;
@@ -1056,12 +1110,20 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   Ring<C::kStages> rv;    // the current tile's V
   rv.next();
   uint32_t o_done = 0;    // pieces of this stream so far
+  uint32_t o1_done = 0;   // (TREE) of stream 1
+  uint32_t merges = 0;
   Group<C::kStages> group{bars, s, 0, abort_flag};
+  auto merge_meet = [&] {  // all eight warps, bounded as every wait
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * B::kMerge);
+    return wait_for_all(bars + 8 * B::kMerge, merges++ & 1, abort_flag, a);
+  };
   constexpr int kPart = DP * 128;
   auto slot_of = [&](int c, int c0) { return part_slot(c, c0, NS, s); };
   const float sl2 = a.scale2;
   const int row_t = over_g(a, row), row_h = row - row_t * a.G;  // the row's token in its tile, and head
-  const int row_tok = s * a.list.tpt + row_t;
+  // the row in a tile of ntok tokens: a stream of its own, or (TREE) the same in both
+  auto tok_of = [&](int ntok) { return (TREE && ntok <= a.list.tpt ? 0 : s * a.list.tpt) + row_t; };
   uint32_t pieces = 0;
   bool ok = wait_for_all(bars + 8 * B::kDF, 0, abort_flag, a);
   const RowBound nobody{0, 0, TREE ? INT_MAX : -1, 0};
@@ -1069,14 +1131,18 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
   // the row's keys in a piece, fetched while the piece before is in work
   auto bound_of = [&](const volatile Piece &x) {
     if (x.n == 0 || !x.fresh) return rb;
-    return row_tok < min(x.ntok, (s + 1) * a.list.tpt) ? a.bounds[x.tok0 + row_tok] : nobody;
+    const int nt = x.ntok, r = tok_of(nt);
+    return r < min(nt, (s + 1) * a.list.tpt) ? a.bounds[x.tok0 + r] : nobody;
   };
   if (ok) rb_ahead = bound_of(piece[0]);
   for (; ok; ++pieces) {
     const volatile Piece &w = piece[pieces % kPieces];
     const int n = w.n, first = w.first;
     if (n == 0) break;
-    const int ntok = min(a.list.tpt, w.ntok - s * a.list.tpt), nrows = ntok * a.G;
+    const int row_tok = tok_of(w.ntok);
+    const bool alt = alternates<TREE>(w.ntok > a.list.tpt, n);
+    const int ntok = alt ? w.ntok : min(a.list.tpt, w.ntok - s * a.list.tpt), nrows = ntok * a.G;
+    if (TREE && (alt || w.ntok > a.list.tpt)) ++o1_done;
     rb = rb_ahead;
     const uint32_t dn = (pieces + 1) % kPieces;
     if (ntok <= 0) {
@@ -1093,11 +1159,12 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     const float slope = MODE == kGeneral && a.slopes && valid ? a.slopes[w.head * a.G + row_h] * kLog2e : 0.f;
     const uint32_t tmem_o = tmem + 256 + 128 * (uint32_t)s + lanes, ts = tmem + 128 * (uint32_t)s + lanes;
     float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j, ++it, rv.next(), rv.next()) {
+    for (int j = 0; j < n; ++j, rv.next(), rv.next()) {
+      if (alt && (j & 1) != s) continue;
       const int base = (first + j) * kAttnKeys;
-      if (!(ok = wait_for_all(bars + 8 * (B::kSF + s), it & 1, abort_flag, a))) break;
+      if (!(ok = wait_for_all(bars + 8 * (B::kSF + s), it++ & 1, abort_flag, a))) break;
       tc_fence_after();
-      if (s == 0 && (base < klo || base + kAttnKeys > khi)) {
+      if ((s == 0 || alt) && (base < klo || base + kAttnKeys > khi)) {
         // keys outside the segment (unwritten cache, blocks not loaded): their values must be zeros, since 0
         // times what the memory holds may be NaN
         if (!(ok = wait_for_all(bars + 8 * (B::kFull + rv.st), rv.ph, abort_flag, a))) break;
@@ -1168,7 +1235,7 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
         if (MODE == kCapped) mx = mx == -INFINITY ? mx : cap_one(a, mx, wide);
         if (!valid) mx = INFINITY;  // rows of nobody: no rescaling on their account
         mx -= kAbove<BF>;
-        if (j == 0) {
+        if (j == (alt ? s : 0)) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
           // (these scores were issued behind the product before, which is therefore done)
@@ -1226,6 +1293,41 @@ __device__ void soften(const AttnArgs &a, const volatile Piece *piece, uint8_t *
     // the piece's last product
     if (!(ok = wait_for_all(bars + 8 * (B::kOD + s), o_done++ & 1, abort_flag, a))) break;
     tc_fence_after();
+    if (TREE && alt) {
+      if (s == 1 && valid) {
+        other[row].x = m;
+        other[row].y = l;
+      }
+      if (!(ok = merge_meet())) break;
+      if (s == 0) {
+        if (!(ok = wait_for_all(bars + 8 * (B::kOD + 1), (o1_done - 1) & 1, abort_flag, a))) break;
+        tc_fence_after();
+        if (active) {
+          const float m1 = other[row].x, l1 = other[row].y, mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
+          const float f0 = ex2(m - ms), f1 = ex2(m1 - ms);
+          m = mm;
+          l = fmaf(l1, f1, l * f0);
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c) {
+            float o[32], o1[32];
+            __syncwarp();
+            tmem_ld32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
+            tmem_ld32(tmem_o + 128 + 32 * c, reinterpret_cast<uint32_t *>(o1));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], f1, o[i] * f0);
+            tmem_st32(tmem_o + 32 * c, reinterpret_cast<uint32_t *>(o));
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+      }
+      if (!(ok = merge_meet())) break;  // stream 1's outputs have been read
+      if (s == 1) {
+        if (lane == 0) mbar_arrive(bars + 8 * (B::kDE + pieces % kPieces));
+        continue;
+      }
+    }
     if (a.after_prefix) pdl_wait();  // (returns at once but the first time)
     auto from_tmem = [&](int c, float (&v)[32]) {
       __syncwarp();  // a load of the whole warp: lanes without a row come from other branches
@@ -1919,6 +2021,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, last_flag[2], marked;
   __shared__ Piece piece[kPieces];
+  __shared__ float2 other[TREE && FORM == kTwo ? kAttnRows : 1];  // maxima and sums of stream 1, where it has the same rows
   const int warp = threadIdx.x >> 5;
   const uint32_t bars = smem_u32(bar_mem), sm = smem_u32(smem);
   if (threadIdx.x == 0) {
@@ -1939,6 +2042,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
       mbar_init(bars + 8 * (B::kPE + i), 4);
     }
     mbar_init(bars + 8 * B::kDrain, 1);
+    mbar_init(bars + 8 * B::kMerge, 8);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bars + 8 * (B::kDF + i), 1);
       mbar_init(bars + 8 * (B::kDE + i), C::kProdWarp + 1);  // the softmax and finishing warps and the MMA warp
@@ -1974,7 +2078,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
       if constexpr (FORM == kSpread)
         soften_few<DP, BF, MODE, TREE>(a, piece, smem, bars, tmem, &abort_flag);
       else
-        soften<DP, BF, MODE, TREE>(a, piece, smem, bars, tmem, &abort_flag, last_flag, &marked);
+        soften<DP, BF, MODE, TREE>(a, piece, smem, bars, tmem, &abort_flag, last_flag, &marked, other);
     }
     if constexpr (FORM == kTwo) {  // (here, where a warp has the registers for it)
       static_assert(FORM != kTwo || C::kSoftWarps == 8, "a barrier of 256 threads");
@@ -1992,7 +2096,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
     } else if (warp < C::kMmaWarp) {
       produce<FORM, DP>(a, maps, warp - C::kProdWarp, piece, sm, bars, &abort_flag);
     } else if (warp == C::kMmaWarp) {
-      issue<FORM, DP, BF>(a, piece, sm, bars, tmem, &abort_flag);
+      issue<FORM, DP, BF, TREE>(a, piece, sm, bars, tmem, &abort_flag);
     }
   }
   __syncwarp();

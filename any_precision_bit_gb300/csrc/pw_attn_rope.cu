@@ -74,8 +74,8 @@ __device__ __forceinline__ void load_pairs(const float *p, bool there, uint64_t 
 // pairs).  A warp takes kRopeHeads heads for each GL lanes at a time, all of q, or of k, or of v, so that it has one kind of
 // address and of work.
 //
-// Memory bounds it: 8205 tokens of 32/8 heads of 128 with norms, 202 MB, take 37 us (5.4 TB/s, 80 % of the copy rate; a
-// copy of that size has the same beginning and end), 5003 of 16/16 heads of 96 17.6 us.  The same by 2 heads at a time 39 and
+// Memory bounds it: 8205 tokens of 32/8 heads of 128 with norms, 202 MB, take 37.3 us (5.4 TB/s), 5003 of 16/16 heads of 96,
+// 92 MB, 17.6 us; a plain copy that moves 202 MB takes 37.2 us here, one that moves 92 MB 21.  The same by 2 heads at a time 39 and
 // 21 us, by 3 or 6 CTAs an SM 38 to 41 and 19; one token to a CTA 39 and 21, 5 or 8 tokens 42 and 18 to 20, where the last CTAs
 // run alone.  With the slot's, the positions' and the rows' loads behind each other it took 62 us.
 constexpr int kRopeHeads = 4, kRopeTokens = 4, kPairs = 64, kRopeCtas = 5;

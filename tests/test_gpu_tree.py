@@ -128,15 +128,17 @@ def test_an_infinite_value_of_an_ancestor_reaches_its_descendants(n, ctx):
         s.close()
 
 
-def test_a_chain_and_no_tree_give_what_a_plain_plan_gives():
+def test_a_chain_and_no_tree_are_what_a_plain_plan_is():
+    """The plain plan's formula with Step.compare's tolerances, and its positions."""
     ctx, new = [70, 5, 300], [20, 33, 1]
     for trees in ([chain(n) for n in new], [[], [], []], [chain(25), [], chain(1)]):
         s = TreeStep(ctx, new, trees)
         try:
             s.map_and_append()
             got, lse = s.forward(window=50)
-            want = super(TreeStep, s).forward(window=50)
-            assert np.array_equal(got, want[0]) and np.array_equal(lse, want[1])
+            o, want_lse, absum, xmax, _ = super(TreeStep, s).expect(window=50)
+            s.near(got, o, absum, 50)
+            assert (np.abs(lse - want_lse) <= 2.0 ** -23 * (s.D + 16) * (4.0 + xmax)).all()
             assert s.tree_pos.tolist() == s.pos.tolist()
         finally:
             s.close()
@@ -253,6 +255,16 @@ def test_captured_steps_follow_new_trees():
         assert e.value.status == pw.PW_ERR_STATE and bool((o == 7).all())
     finally:
         s.close()
+
+
+@pytest.mark.parametrize("ctx", [0, 120, 130, 250, 260, 390, 1000, 1100])
+@pytest.mark.parametrize("kind", [{}, dict(window=140), dict(softcap=3.0), dict(slopes=[0.5, 0.25, 0.1, 3.0])], ids=str)
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_tile_of_rows_behind_several_of_keys(ctx, kind, D):
+    """Odd and even numbers of key tiles, of which two streams take turns; beside rows of two tiles."""
+    run([ctx, ctx + 60, ctx // 2], [24, 40, 17], [random_tree(24, ctx), random_tree(40, ctx + 1), random_tree(20, ctx + 2)][:3],
+        Hq=8, Hkv=2, D=D, **{**kind, **({"slopes": kind["slopes"] * 2} if "slopes" in kind else {})}) if ctx > 5 else \
+        run([ctx], [24], [random_tree(24, ctx)], D=D, **kind)
 
 
 def test_results_repeat_bit_by_bit():
