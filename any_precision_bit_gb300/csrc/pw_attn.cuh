@@ -147,9 +147,11 @@ __device__ __forceinline__ AttnTile load_tile(const AttnTile *p) {
 __device__ __forceinline__ size_t part_slot(int cta, int c0, int streams, int s) {
   return ((size_t)cta * 2 + (cta == c0 ? 1 : 0)) * streams + s;
 }
+template <bool TREE>
 struct Walk {
   int tile, head, off, left;  // off and left in units
   int cost;                   // units that lead each (tile, head)
+  int tpt, one, two;
   AttnTile t, ahead;
   int j0, n;  // first key tile of this piece within the tile's, and their number
   int2 first_ctas, last_ctas;  // see AttnStart
@@ -161,25 +163,35 @@ struct Walk {
     tile = x.x, head = x.y, off = x.z, left = fits ? x.w : 0;
     first_ctas = s->first, last_ctas = s->last;
     cost = a.list.piece_cost;
+    tpt = a.list.tpt;
+    one = a.list.one, two = a.list.two;
     fresh = true;
     if (left > 0) ahead = load_tile(a.list.tiles + tile + 1);
   }
-  __device__ __forceinline__ bool load() {
-    if (off < cost) {
-      const int skip = min(cost - off, left);
-      off += skip;
-      left -= skip;
+  __device__ __forceinline__ int units() const { return TREE ? (t.ntok > tpt ? two : one) : 1; }  // of a key tile
+  __device__ __forceinline__ bool load(const AttnArgs &a) {
+    for (;;) {
+      if (off < cost) {
+        const int skip = min(cost - off, left);
+        off += skip;
+        left -= skip;
+      }
+      if (left <= 0) return false;
+      const int u = units(), o = off - cost;
+      j0 = (o + u - 1) / u;
+      n = min(t.kv1 - t.kv0, (o + left + u - 1) / u) - j0;
+      if (!TREE || n > 0) return true;
+      const bool f = fresh;  // the rest of a key tile that is the CTA's before
+      next(a);
+      fresh = fresh || f;
     }
-    if (left <= 0) return false;
-    j0 = off - cost;
-    n = min(t.kv1 - t.kv0 - j0, left);
-    return true;
   }
   __device__ __forceinline__ void next(const AttnArgs &a) {
-    left -= n;
-    off += n;
+    const int all = (t.kv1 - t.kv0) * units(), used = min(left, all - (off - cost));
+    left -= used;
+    off += used;
     fresh = false;
-    if (off == t.kv1 - t.kv0 + cost) {
+    if (off == all + cost) {
       off = 0;
       if (++head == a.Hkv) {
         head = 0;
@@ -229,7 +241,7 @@ constexpr uint32_t kQBufferStep = kSpreadRows * 128;  // bytes between the two
 
 // A producer warp: the keys (kv = 0) or values of every key tile, or every other box of them; the last of
 // the warps also loads the queries and hands the pieces over.
-template <int FORM, int DP>
+template <int FORM, int DP, bool TREE>
 __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece *piece, uint32_t sm, uint32_t bars,
                         volatile int *abort_flag) {
   using C = Cfg<FORM, DP>;
@@ -251,7 +263,7 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
   if (kv) r.next();
   // (where the plan does not fit there are no pieces, and the other warps find none)
   const bool fits = plan_fits(a);
-  Walk w(a, fits);
+  Walk<TREE> w(a, fits);
   if (!fits && leads) {
     if (a.after_prefix) pdl_wait();  // as every launch before its end
     if (lane == 0) atomicOr(a.err, kAttnErrPlan);
@@ -267,7 +279,7 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
     if (t.trow >= 0 && p < a.table_stride) id = a.table[(size_t)t.trow * a.table_stride + p];
     return id >= 0 && id < a.n_blocks ? id : a.n_blocks;  // out of the map's range: zeros
   };
-  bool more = w.load();
+  bool more = w.load(a);
   int id = more ? block_of(w.t, w.first()) : -1;
   // hand over piece `i`, the one the walk is at (or the end)
   auto publish = [&](uint32_t i) {
@@ -309,7 +321,7 @@ __device__ void produce(const AttnArgs &a, const AttnMaps &maps, int self, Piece
         id = block_of(w.t, w.first() + j + 1);
       } else {  // the next piece's first
         w.next(a);
-        more = w.load();
+        more = w.load(a);
         id = more ? block_of(w.t, w.first()) : -1;
       }
       const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, cur >= 0)) * bt * 128);
@@ -377,8 +389,9 @@ struct Mma {
 
 // Trees are small, and often one 128-row tile holds one (of at most 32 nodes with four query heads to a key/value head).
 // The two streams of kTwo then take every other key tile of the same rows, each with maxima, sums and outputs of its own,
-// which stream 0 adds up at the end of a piece: one's products run during the other's softmax again.  (Measured for trees
-// alone, ALT_MEASURED.)
+// which stream 0 adds up at the end of a piece: one's products run during the other's softmax again.  Measured (us, without and
+// with): 64 trees of up to 32 nodes behind up to 4000 tokens, heads of 64 90 and 72, of 128 115 and 108 (memory: 86); 8 of up to
+// 24 behind up to 8000, heads of 64, capped 47 and 36; one of 24 11.0 both.
 template <bool TREE>
 __device__ __forceinline__ bool alternates(bool two, int n) {
   return TREE && !two && n > 1;
@@ -1019,8 +1032,8 @@ static __device__ __forceinline__ void mark_row(const AttnArgs &a, int tok, int 
 template <bool BF, int KEYS, bool TREE>
 static __device__ PW_RARE void redo_marked(const AttnArgs &a, int warps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk w(a, true);
-  while (w.load()) {
+  Walk<TREE> w(a, true);
+  while (w.load(a)) {
     const AttnTile t = w.t;
     const bool merge = t.merge && !a.to_prefix;
     const int rows = t.ntok * a.G;
@@ -2094,7 +2107,7 @@ __global__ void __launch_bounds__(Cfg<FORM, DP>::kThreads, 1) attn_kernel(const 
     if (FORM == kTwo) regs_dec<kRegsOther>();
     if (abort_flag) {
     } else if (warp < C::kMmaWarp) {
-      produce<FORM, DP>(a, maps, warp - C::kProdWarp, piece, sm, bars, &abort_flag);
+      produce<FORM, DP, TREE>(a, maps, warp - C::kProdWarp, piece, sm, bars, &abort_flag);
     } else if (warp == C::kMmaWarp) {
       issue<FORM, DP, BF, TREE>(a, piece, sm, bars, tmem, &abort_flag);
     }

@@ -88,8 +88,8 @@ struct AttnSplit {
   int head, c0, c1, pad;
 };
 
-// One list of work.  In the order (tile, head), each has piece_cost units without keys and then one for
-// each of its key tiles; of the W units CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W if that is less (the rest idle).
+// One list of work.  In the order (tile, head), each has piece_cost units without keys and then `one` or `two` for
+// each of its key tiles, which is the CTA's that has the first of them; of the W units CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W / two if that is less (the rest idle).
 struct AttnList {
   AttnTile *tiles;
   int *cum;          // [tiles + 1] units of one head before each tile
@@ -100,6 +100,8 @@ struct AttnList {
   int streams;       // 128-row tiles of one AttnTile (1 or 2)
   int piece_cost;    // units that a (tile, head) counts for beside its key tiles when the work is divided: the
                      // queries' way in, the pipeline's filling and draining, the result's way out
+  int one, two;      // units of a key tile of an AttnTile of one 128-row tile and of two: 1, but for plans of trees in kTwo,
+                     // where the streams share the key tiles of one 128-row tile
   int max_tiles;
 };
 

@@ -268,12 +268,22 @@ pw_status lay_out(pw_attn *a, int plan, const pw_kv_step *s, int window, const i
     // measured: two tiles, 8192-token prompt 479, 417, 395, 397, 401 us at 1 to 5 and packed chunks 66, 66, 68,
     // 71, 73 us; few rows, 160 windowed requests 137, 137, 138 us at 1 to 3
     l.piece_cost = l.streams == 2 ? 3 : 2;
+    l.one = l.two = 1;
+    // A key tile of one 128-row tile, which the streams take in turns, is memory's or the copies' more often than theirs.
+    // Measured, weights 1 : 1, 2 : 3 and 1 : 2 (us): prompt chunks among trees 54, 47 and 46, 32 trees of up to 33 nodes 122,
+    // 109 and 112, of up to 64 127, 130 and 153; a piece at 6, 9 and 12: one tree of 24 nodes 11.2, 12.1 and 12.1, chunks among
+    // trees 47.7, 47.1 and 47.8, 64 trees of up to 32 nodes of heads of 64 72.7, 70.8 and 71.1.
+    if (tree && l.streams == 2) {
+      l.one = 2;
+      l.two = 3;
+      l.piece_cost = 8;
+    }
   };
   // The lists sum up key tiles (and a piece's cost) over all tiles of rows in 31 bits, as they do an SM's share over
   // the heads.
   const int64_t keys = ((int64_t)s->table_stride * a->d.block_tokens + kAttnKeys - 1) / kAttnKeys;
   auto countable = [&](const AttnList &l, int segments) {
-    const int64_t sum = (s->n_tokens / (l.tpt * l.streams) + (int64_t)segments) * (keys + l.piece_cost);
+    const int64_t sum = (s->n_tokens / (l.tpt * l.streams) + (int64_t)segments) * (keys * l.two + l.piece_cost);
     return sum <= INT32_MAX && sum * a->d.n_kv_heads / a->sm_count < INT32_MAX;
   };
   AttnList requests = a->plans[(size_t)plan].requests, groups = a->plans[(size_t)plan].groups;

@@ -306,6 +306,7 @@ __device__ __forceinline__ void lay_out_list(const PlanArgs &a, int *cum_tiles) 
   const int tid = threadIdx.x;
   const int n_seg = a.of_groups ? a.n_groups : a.R + 1;
   const int tt = a.list.tpt * a.list.streams;
+  auto units_of = [&](const AttnTile &t) { return t.ntok > a.list.tpt ? a.list.two : a.list.one; };  // of a key tile
   long long before = 0;
   for (int s0 = 0; s0 < n_seg; s0 += kListThreads) {
     const int s = s0 + tid;
@@ -364,7 +365,7 @@ __device__ __forceinline__ void lay_out_list(const PlanArgs &a, int *cum_tiles) 
     t.kv1 = hi > 0 ? (hi - 1) / kAttnKeys + 1 : t.kv0 + 1;
     if (some && (tid & (wide - 1)) == 0) {
       a.list.tiles[i] = t;
-      a.list.cum[i + 1] = t.kv1 - t.kv0 + a.list.piece_cost;
+      a.list.cum[i + 1] = (t.kv1 - t.kv0) * units_of(t) + a.list.piece_cost;
     }
   }
   __syncthreads();
@@ -389,10 +390,11 @@ __device__ __forceinline__ void lay_out_list(const PlanArgs &a, int *cum_tiles) 
   }
   __syncthreads();
   const long long W = before * a.n_kv_heads;  // (0 for groups without new tokens)
-  const long long P = max(1LL, min((long long)a.ctas, W));
+  // (a share is a key tile's units at least, so that every CTA between a (tile, head)'s first and last has a piece of it)
+  const long long P = max(1LL, min((long long)a.ctas, W / a.list.two));
   // CTAs of the first and the last key tile of a (tile, head) whose units begin at ub
-  auto ctas_of = [&](long long ub, int cost) {
-    return make_int2((int)(((ub + a.list.piece_cost + 1) * P - 1) / W), (int)(((ub + cost) * P - 1) / W));
+  auto ctas_of = [&](long long ub, int cost, int units) {
+    return make_int2((int)(((ub + a.list.piece_cost + 1) * P - 1) / W), (int)(((ub + cost - units + 1) * P - 1) / W));
   };
   __shared__ int n_splits;
   if (tid == 0) n_splits = 0;
@@ -415,7 +417,7 @@ __device__ __forceinline__ void lay_out_list(const PlanArgs &a, int *cum_tiles) 
       tile = lo;
       head = (int)(rem / cost);
       off = (int)(rem - (long long)head * cost);
-      return ctas_of(u - off, cost);
+      return ctas_of(u - off, cost, a.list.two > 1 ? units_of(a.list.tiles[lo]) : 1);
     };
     if (u1 > u0) {
       st.first = find(u0, st.tile, st.head, st.off);

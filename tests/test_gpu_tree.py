@@ -267,6 +267,22 @@ def test_one_tile_of_rows_behind_several_of_keys(ctx, kind, D):
         run([ctx], [24], [random_tree(24, ctx)], D=D, **kind)
 
 
+@pytest.mark.parametrize("n", [3, 24, 40])
+@pytest.mark.parametrize("heads", [(2, 1), (8, 2)], ids=str)
+def test_short_steps_behind_long_ones_in_one_handle(n, heads):
+    """What earlier steps left in the workspace has no say."""
+    s = TreeStep([5000], [n], [random_tree(n, 1)], Hq=heads[0], Hkv=heads[1], bt=16, spare_ids=4)
+    try:
+        for ctx in (5000, 120, 4000, 130, 250, 700, 1500, 20, 0, 380):
+            s.ctx = [ctx]
+            s.step.refs[0].fill_(ctx)
+            s.table.copy_(s.torch.as_tensor(s.table0))  # without the block that the step before opened
+            s.map_and_append()
+            s.compare()
+    finally:
+        s.close()
+
+
 def test_results_repeat_bit_by_bit():
     s = TreeStep([3000, 500, 9000], [64, 13, 40], [random_tree(64, 1), random_tree(13, 2), random_tree(40, 3)], Hq=8, Hkv=2, D=128)
     try:
