@@ -599,6 +599,14 @@ def _addr(t, device, n=0, kind="int32"):
     return t.data_ptr()
 
 
+def _nodes(t, device, R):
+    """Address of a contiguous int32 tensor of at least R rows, and the length of a row."""
+    if t.dim() != 2:
+        raise ValueError(f"needs a tensor [{R}][nodes], not {_what(t)}")
+    n = t.shape[1]
+    return _addr(t, device, R * n), n
+
+
 def _rows(t, n, heads, dim, dtype, device):
     """Address and the strides of [n or more rows][heads][dim] (unit last stride)."""
     rows, h, d = t.shape
@@ -757,8 +765,8 @@ def pw_attn_plan_tree(attn, plan, step, tree_len, parent, pos=None, window=0, st
     """tree_len: int32 [R]; parent: int32 [R][nodes]; pos: int32 [n_tokens], filled.  The handle keeps the step's tensors
     and these until the plan is laid out again."""
     _, _, _, _, dev, _, plans, _ = _attn_shapes[attn]
-    tree = pw_tree(tree_len=_addr(tree_len, dev, step.R), parent=_addr(parent, dev, step.R * parent.shape[1]),
-                   parent_stride=parent.shape[1], pos=_addr(pos, dev, step.n_tokens))
+    nodes, stride = _nodes(parent, dev, step.R)
+    tree = pw_tree(tree_len=_addr(tree_len, dev, step.R), parent=nodes, parent_stride=stride, pos=_addr(pos, dev, step.n_tokens))
     st = lib().pw_attn_plan_tree(attn, plan, _step_on(step, dev), window, C.byref(tree), _cuda_stream(stream))
     if st:
         _check(st)
@@ -768,8 +776,8 @@ def pw_attn_plan_tree(attn, plan, step, tree_len, parent, pos=None, window=0, st
 def pw_kv_keep(attn, step, tree_len, keep, n_keep, ctx_out=None, stream=None):
     """tree_len and n_keep: int32 [R]; keep: int32 [R][nodes]; ctx_out: int32 [R], filled."""
     dev, R = _attn_shapes[attn][4], step.R
-    st = lib().pw_kv_keep(attn, _step_on(step, dev), _addr(tree_len, dev, R), _addr(keep, dev, R * keep.shape[1]), keep.shape[1],
-                          _addr(n_keep, dev, R), _addr(ctx_out, dev, R), _cuda_stream(stream))
+    st = lib().pw_kv_keep(attn, _step_on(step, dev), _addr(tree_len, dev, R), *_nodes(keep, dev, R), _addr(n_keep, dev, R),
+                          _addr(ctx_out, dev, R), _cuda_stream(stream))
     if st:
         _check(st)
 

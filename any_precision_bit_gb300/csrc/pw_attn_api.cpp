@@ -269,11 +269,11 @@ pw_status lay_out(pw_attn *a, int plan, const pw_kv_step *s, int window, const i
     // 71, 73 us; few rows, 160 windowed requests 137, 137, 138 us at 1 to 3
     l.piece_cost = l.streams == 2 ? 3 : 2;
     l.one = l.two = 1;
-    // A key tile of one 128-row tile, which the streams take in turns, is memory's or the copies' more often than theirs.
+    // Where some tiles hold two 128-row tiles and others one: a key tile of the latter, which the streams take in turns, is
+    // memory's or the copies' more often than theirs.
     // Measured, weights 1 : 1, 2 : 3 and 1 : 2 (us): prompt chunks among trees 54, 47 and 46, 32 trees of up to 33 nodes 122,
-    // 109 and 112, of up to 64 127, 130 and 153; a piece at 6, 9 and 12: one tree of 24 nodes 11.2, 12.1 and 12.1, chunks among
-    // trees 47.7, 47.1 and 47.8, 64 trees of up to 32 nodes of heads of 64 72.7, 70.8 and 71.1.
-    if (tree && l.streams == 2) {
+    // 109 and 112, of up to 64 127, 130 and 153; a piece at 6, 9 and 12: chunks among trees 47.7, 47.1 and 47.8.
+    if (tree && l.streams == 2 && tokens > most) {
       l.one = 2;
       l.two = 3;
       l.piece_cost = 8;

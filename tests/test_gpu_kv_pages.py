@@ -238,6 +238,40 @@ def test_copies_of_bad_ids_are_reported():
         s.close()
 
 
+def test_offsets_beyond_32_bits():
+    """Blocks 2^31 elements apart: a rotation's cache write, a kept path and a copy."""
+    import torch
+
+    import any_precision_bit_gb300 as pw
+    far = 1 << 31
+    store = torch.empty(2 * far + 4096, dtype=torch.bfloat16, device="cuda")
+    k = store.as_strided((3, 16, 1, 64), (far, 64, 64, 1))
+    v = store.as_strided((3, 16, 1, 64), (far, 64, 64, 1), 2048)
+    k.zero_(), v.zero_()
+    i32 = lambda a: torch.as_tensor(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    attn = pw.pw_attn_create(pw.pw_attn_desc(L=1, n_heads=1, n_kv_heads=1, head_dim=64, dtype=0, n_blocks=3, block_tokens=16,
+                                             max_requests=1, max_tokens=20, n_plans=1, device=0))
+    try:
+        pw.pw_attn_bind(attn, 0, k, v)
+        pw.pw_attn_set_rope(attn, 0, [])
+        table, slot = i32([[2, 1]]), torch.tensor([*range(32, 48), *range(16, 20)]).cuda()
+        step = pw.pw_make_step(i32([0]), i32([20]), table, i32([0, 20]), i32([20]), slot, i32(range(20)), max_new=20)
+        x = torch.randn(3, 20, 1, 64, device="cuda").bfloat16()
+        q_out = torch.empty_like(x[0])
+        pw.pw_attn_rope_append(attn, 0, step, x[0], q_out, x[1], x[2])
+        pw.pw_kv_keep(attn, step, i32([8]), i32([[0, 2, 7]]), i32([3]))
+        pw.pw_kv_copy(attn, i32([2]), i32([0]), table=table)
+        pw.pw_attn_check(attn)
+        assert torch.equal(q_out, x[0]) and table.tolist() == [[0, 1]]
+        for c, new in ((k, x[1]), (v, x[2])):
+            want = new.clone()
+            want[13], want[14] = new[14], new[19]
+            assert torch.equal(c[2], want[:16]) and torch.equal(c[0], want[:16]) and torch.equal(c[1, :4], want[16:])
+            assert not c[1, 4:].any()
+    finally:
+        pw.pw_attn_destroy(attn)
+
+
 def test_captured_calls():
     import torch
     s = Cache([100, 100], D=64)
