@@ -46,7 +46,7 @@ enum {
 // plan was laid out again, or a captured plan that has not been replayed) would read past its tiles, the rows of
 // q and o or the table, so it writes nothing and reports kAttnErrPlan.
 struct alignas(16) AttnShape {
-  int tpt, streams;              // of the requests' list (streams 0: never laid out; kTreeShape more: of trees)
+  int tpt, streams;              // of the requests' list (streams 0: never laid out; kTreeShape * AttnList::two more: of trees)
   int group_tpt, group_streams;  // of the groups' (0: no groups)
   int n_tokens, table_stride;
   const int *table;

@@ -92,10 +92,10 @@ struct Plan {
   AttnList requests{}, groups{};
 
   AttnShape launch_shape() const {
-    AttnShape s{requests.tpt, requests.streams + (tree ? kTreeShape : 0), 0, 0, step.n_tokens, step.table_stride, step.table};
+    AttnShape s{requests.tpt, requests.streams + (tree ? kTreeShape * requests.two : 0), 0, 0, step.n_tokens, step.table_stride, step.table};
     if (step.n_groups) {
       s.group_tpt = groups.tpt;
-      s.group_streams = groups.streams;
+      s.group_streams = groups.streams + (tree ? kTreeShape * groups.two : 0);
     }
     return s;
   }

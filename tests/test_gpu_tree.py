@@ -267,6 +267,40 @@ def test_one_tile_of_rows_behind_several_of_keys(ctx, kind, D):
         run([ctx], [24], [random_tree(24, ctx)], D=D, **kind)
 
 
+def test_a_captured_forward_does_not_fit_a_plan_that_divides_otherwise():
+    """Tiles of as many tokens, but with key tiles that weigh otherwise since a request may bring more."""
+    import torch
+    s = TreeStep([700, 300], [20, 12], [random_tree(20, 1), random_tree(12, 2)], Hq=4, Hkv=1)
+    pw = s.pw
+    try:
+        s.map_and_append()
+        o = torch.empty(s.N, s.Hq, s.D, dtype=s.dt, device="cuda")
+        ctx, new, table, q_start, kv_len, slot, pos = s.step.refs[:7]
+        wide, narrow = (pw.pw_make_step(ctx, new, table, q_start, kv_len, slot, pos, max_new=n) for n in (64, 32))
+
+        def plan(step):
+            pw.pw_attn_plan_tree(s.attn, 0, step, s.tree_len, s.parent, pos=s.tree_pos)
+            torch.cuda.synchronize()
+        for first, second in ((wide, narrow), (narrow, wide)):
+            plan(first)
+            pw.pw_attn_forward(s.attn, 0, 0, s.q, o)
+            pw.pw_attn_check(s.attn)
+            want, _, absum, _, _ = s.expect()
+            s.near(o.float().cpu().numpy(), want, absum, 720)
+            graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+            with torch.cuda.graph(graph, stream=stream):
+                pw.pw_attn_forward(s.attn, 0, 0, s.q, o, stream=stream)
+            plan(second)
+            o.fill_(7.0)
+            torch.cuda.synchronize()
+            graph.replay()
+            with pytest.raises(pw.PwError) as e:
+                pw.pw_attn_check(s.attn)
+            assert e.value.status == pw.PW_ERR_STATE and bool((o == 7).all())
+    finally:
+        s.close()
+
+
 @pytest.mark.parametrize("n", [3, 24, 40])
 @pytest.mark.parametrize("heads", [(2, 1), (8, 2)], ids=str)
 def test_short_steps_behind_long_ones_in_one_handle(n, heads):
