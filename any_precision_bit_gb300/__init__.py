@@ -753,6 +753,8 @@ def pw_attn_rope_append(attn, layer, step, q, q_out, k, v, pos=None, stream=None
     one; pos: int32 [n_axes][n_tokens], or None for the step's."""
     hq, h, d, dtype, dev, _, _, _ = _attn_shapes[attn]
     n = step.n_tokens
+    if pos is not None and pos.dim() > 1 and pos.shape[-1] != n:
+        raise ValueError(f"needs positions [n_axes][{n}], not {_what(pos)}")
     st = lib().pw_attn_rope_append(attn, layer, _step_on(step, dev), *_rows(q, n, hq, d, dtype, dev),
                                    *_rows(q_out, n, hq, d, dtype, dev), *_rows(k, n, h, d, dtype, dev),
                                    *_rows(v, n, h, d, dtype, dev), _addr(pos, dev, n * _rope_axes.get((attn, layer), 1)),

@@ -267,6 +267,27 @@ def test_one_tile_of_rows_behind_several_of_keys(ctx, kind, D):
         run([ctx], [24], [random_tree(24, ctx)], D=D, **kind)
 
 
+@pytest.mark.parametrize("n", [3, 24, 70])
+def test_an_expired_wait_is_reported_and_the_handle_usable(n):
+    s = TreeStep([100, 400, 64], [n] * 3, [random_tree(n, r) for r in range(3)])
+    pw = s.pw
+    try:
+        s.map_and_append()
+        s.compare()
+        pw.pw_attn_set_fault(s.attn, 5, 2000)
+        pw.pw_attn_set_fault(s.attn, 4, 1)
+        o = s.torch.empty(s.N, s.Hq, s.D, dtype=s.dt, device="cuda")
+        pw.pw_attn_forward(s.attn, 0, 0, s.q, o)
+        with pytest.raises(pw.PwError) as e:
+            pw.pw_attn_check(s.attn)
+        assert e.value.status == pw.PW_ERR_TIMEOUT
+        pw.pw_attn_check(s.attn)
+        pw.pw_attn_set_fault(s.attn, 5, 0)
+        s.compare()
+    finally:
+        s.close()
+
+
 def test_a_captured_forward_does_not_fit_a_plan_that_divides_otherwise():
     """Tiles of as many tokens, but with key tiles that weigh otherwise since a request may bring more."""
     import torch

@@ -63,7 +63,7 @@ def test_calls_refuse_tensors_of_another_device_than_the_handle(monkeypatch):
         return lambda: pw.pw_kv_copy(7, a["src"], a["dst"], table=a["table"])
 
     calls = [rope(step=there), rope(q=rows(4, 0)), rope(q_out=rows(4, 0)), rope(k=rows(2, 0)), rope(v=rows(2, 0)),
-             rope(v=rows(2, dtype=torch.float16)), rope(q_out=rows(2)), rope(pos=ints(8, 0)), rope(pos=ints(7)),
+             rope(v=rows(2, dtype=torch.float16)), rope(q_out=rows(2)), rope(pos=ints(8, 0)), rope(pos=ints(7)), rope(pos=ints((4, 2))),
              tree(step=there), tree(tree_len=ints(2, 0)), tree(parent=ints((2, 3), 0)), tree(pos=ints(4, 0)), tree(pos=ints(3)),
              tree(parent=ints((1, 3))), tree(parent=ints(6)), keep(keep=ints(6)),
              keep(step=there), keep(tree_len=ints(1)), keep(keep=ints((2, 3), 0)), keep(n_keep=ints(2, 0)), keep(ctx_out=ints(1)),
