@@ -192,7 +192,7 @@ struct KeepArgs {
 
 struct CopyArgs {
   const int *src, *dst;
-  int n, n_blocks, bt, log_bt, n_heads, head_dim;
+  int n, n_blocks, bt, n_heads, head_dim;
   int *where;  // [n_blocks] number of the pair that a block is the source of, where it is one; null: not asked for
   int *table;  // whose entries are renamed in the same launch (few pairs, the first layers), else null
   int64_t entries;

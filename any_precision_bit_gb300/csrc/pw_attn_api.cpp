@@ -706,7 +706,6 @@ pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, 
   g.n = n;
   g.n_blocks = a->d.n_blocks;
   g.bt = a->d.block_tokens;
-  g.log_bt = log2_of(a->d.block_tokens);
   g.n_heads = a->d.n_kv_heads;
   g.head_dim = a->d.head_dim;
   g.err = a->err;
