@@ -75,6 +75,20 @@ bool drop(pw_kv *kv, int32_t id) {
   return true;
 }
 
+// The blocks behind the first n_keep of a request's are returned, the last one first; how many are free now.  Where memory
+// for the free ids runs out, those that are left are still the request's.
+bool give_back(pw_kv *kv, std::vector<int32_t> &ids, int64_t n_keep, int64_t *n) {
+  try {
+    while ((int64_t)ids.size() > n_keep) {
+      *n += drop(kv, ids.back());
+      ids.pop_back();
+    }
+  } catch (...) {
+    return false;
+  }
+  return true;
+}
+
 // A grow's room: the part of n blocks that request r's announcement covers, or -1 where the others do not fit.
 int64_t covered(const pw_kv *kv, int64_t request, int64_t n) {
   auto it = kv->announced.find(request);
@@ -155,7 +169,7 @@ extern "C" pw_status pw_kv_release(pw_kv *kv, int64_t request, int64_t *n_releas
   int64_t n = 0;
   auto it = kv->held.find(request);
   if (it != kv->held.end()) {
-    for (int32_t id : it->second) n += drop(kv, id);
+    if (!give_back(kv, it->second, 0, &n)) return PW_ERR_OOM;
     kv->held.erase(it);
   }
   lower_mark(kv);
@@ -209,11 +223,7 @@ extern "C" pw_status pw_kv_trim(pw_kv *kv, int64_t request, int64_t n_keep, int6
   if (!kv || n_keep < 0) return PW_ERR_INVALID;
   int64_t n = 0;
   auto it = kv->held.find(request);
-  if (it != kv->held.end())
-    while ((int64_t)it->second.size() > n_keep) {
-      n += drop(kv, it->second.back());
-      it->second.pop_back();
-    }
+  if (it != kv->held.end() && !give_back(kv, it->second, n_keep, &n)) return PW_ERR_OOM;
   lower_mark(kv);
   if (n_released) *n_released = n;
   return PW_OK;
