@@ -239,7 +239,7 @@ __device__ __forceinline__ void tree_rows(const TreeArgs &x, int block, int tid,
     const int r = seg_of(a.q_start, a.R, t);
     const int kv = (int)min((long long)a.kv_len[r], cap), tl = tree_of(x, r, kv);
     b.pos = a.ctx_len[r] + t - a.q_start[r];
-    if (tl && b.pos >= kv - tl) return;  // a node's row
+    if (tl && b.pos >= kv - tl && b.pos < kv) return;  // a node's row
     b.hi = min(b.pos + 1, kv);
     if (a.window > 0) b.lo = max(0, b.pos - a.window + 1);
     b.lo = min(b.lo, b.hi);
