@@ -602,6 +602,8 @@ pw_status pw_attn_set_rope(pw_attn *a, int layer, const pw_rope_desc *r) {
         return cuda_failed("cudaMemcpy", e);
   RopeTable *table = a->rope + layer;
   if (int e = cudaMemcpy(table, &t, sizeof t, cudaMemcpyHostToDevice)) return cuda_failed("cudaMemcpy", e);
+  // (the copy may return while its bytes are on their way, on a stream that the caller's need not wait for)
+  if (int e = cudaDeviceSynchronize()) return cuda_failed("cudaDeviceSynchronize", e);
   Layer &l = a->layers[(size_t)layer];
   l.rope_axes = r->n_axes;
   l.rope.table = table;

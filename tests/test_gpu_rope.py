@@ -194,6 +194,28 @@ def test_what_is_not_turned_stays_as_it_is():
             s.close()
 
 
+def test_a_rotation_holds_for_every_stream_once_it_is_set():
+    """Launches on a stream that waits for no other, right behind pw_attn_set_rope."""
+    import torch
+    s = Rope(300, D=128)
+    stream = torch.cuda.Stream()
+    gain = np.random.default_rng(0).normal(1, 0.2, (12, 128))
+    torch.cuda.synchronize()
+    try:
+        for k in range(12):
+            s.pw.pw_attn_set_rope(s.attn, 0, freqs(128) * (k + 1), q_gain=gain[k], k_gain=gain[k])
+            s.pw.pw_attn_rope_append(s.attn, 0, s.step, s.q, s.out[:, :, 0], s.k, s.v, stream=stream)
+            torch.cuda.synchronize()
+            got, held = s.out[:, :, 0].clone(), s.cache[0].clone()
+            torch.cuda.synchronize()
+            s.pw.pw_attn_rope_append(s.attn, 0, s.step, s.q, s.out[:, :, 0], s.k, s.v, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got, s.out[:, :, 0])
+            assert torch.equal(held.nan_to_num(nan=7.0), s.cache[0].nan_to_num(nan=7.0))
+    finally:
+        s.close()
+
+
 def test_a_captured_call_on_a_stream_of_its_own():
     import torch
     s = Rope(10, D=128)
