@@ -173,20 +173,21 @@ struct RopeArgs {
   float scale, eps, inv_d;
 };
 
-// The caches of some layers, by value in a launch.
-constexpr int kMoveLayers = 64;
+// Some of the layers' caches, of keys or of values, by value in a launch.  Each of a handle's caches is in one launch once,
+// however many layers are bound to it: its tokens are moved in place.
+constexpr int kMoveCaches = 128;
 struct CacheRef {
-  uint16_t *k, *v;
+  uint16_t *base;
   int64_t block_stride, token_stride, head_stride;
 };
-struct MoveLayers {
-  CacheRef layer[kMoveLayers];
+struct MoveCaches {
+  CacheRef cache[kMoveCaches];
 };
 
 struct KeepArgs {
   int R, table_rows, table_stride, keep_stride, bt, log_bt, n_blocks, n_heads, head_dim;
   const int *rows, *table, *kv_len, *tree_len, *keep, *n_keep;
-  int *ctx_out;  // (of the launch for the first layers, else null)
+  int *ctx_out;  // (of the launch for the first caches, else null)
   int *err;
 };
 
@@ -194,7 +195,7 @@ struct CopyArgs {
   const int *src, *dst;
   int n, n_blocks, bt, n_heads, head_dim;
   int *where;  // [n_blocks] number of the pair that a block is the source of, where it is one; null: not asked for
-  int *table;  // whose entries are renamed in the same launch (few pairs, the first layers), else null
+  int *table;  // whose entries are renamed in the same launch (few pairs, the first caches), else null
   int64_t entries;
   int *err;
 };
@@ -255,8 +256,8 @@ int launch_attn_append(const AppendArgs &a, void *stream);
 int launch_tree_bounds(const TreeArgs &a, void *stream);
 int launch_tree_list(const TreeArgs &a, void *stream);
 int launch_rope(const RopeArgs &a, int bf16, void *stream);
-int launch_keep(const KeepArgs &a, const MoveLayers &m, int n_layers, void *stream);
-int launch_copy(const CopyArgs &a, const MoveLayers &m, int n_layers, void *stream);
+int launch_keep(const KeepArgs &a, const MoveCaches &m, int n_caches, void *stream);
+int launch_copy(const CopyArgs &a, const MoveCaches &m, int n_caches, void *stream);
 int launch_rename(const CopyArgs &a, void *stream);
 int launch_attn(const AttnArgs &a, const AttnMaps &maps, int bf16, void *stream);
 

@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <cstring>
 #include <new>
+#include <tuple>
 #include <vector>
 
 #include "pw_attn.h"
@@ -131,6 +132,8 @@ struct pw_attn {
   std::vector<Layer> layers;
   std::vector<Plan> plans;
   std::vector<void *> allocs;
+  std::vector<CacheRef> caches;  // what the layers are bound to, each once; empty since a layer was bound anew
+  bool caches_mixed = false;     // some of them begin at one address with other strides
   int *err = nullptr;
   float *part_o = nullptr, *prefix_o = nullptr, *prefix_lse = nullptr;
   float2 *part_ml = nullptr;
@@ -180,6 +183,7 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   a->layers.resize((size_t)d.L);
   a->plans.resize((size_t)d.n_plans);
   a->allocs.reserve(16 + 14 * (size_t)d.n_plans);
+  a->caches.reserve(2 * (size_t)d.L);
   int e = cudaDeviceGetAttribute(&a->sm_count, cudaDevAttrMultiProcessorCount, d.device);
   if (e) return cuda_failed("cudaDeviceGetAttribute", e);
   const size_t ctas = (size_t)a->sm_count, dp = d.head_dim > 64 ? 128 : 64;
@@ -219,18 +223,33 @@ pw_status create(const pw_attn_desc &d, pw_attn *a) {
   return PW_OK;
 }
 
-// All layers' caches, at most kMoveLayers of them a launch: launch(caches, their number, whether they are the first).
-template <class F>
-pw_status for_layers(const pw_attn *a, const char *what, F launch) {
+// Lists the caches of all layers, each once: layers may share them, and keys and values may be one.
+pw_status list_caches(pw_attn *a) {
+  if (!a->caches.empty()) return PW_OK;
   for (const Layer &l : a->layers)
     if (!l.k) return report(nullptr, PW_ERR_STATE, "a layer's cache is not bound");
-  MoveLayers m;
-  for (int at = 0; at < a->d.L; at += kMoveLayers) {
-    const int n = std::min(kMoveLayers, a->d.L - at);
-    for (int i = 0; i < n; ++i) {
-      const Layer &l = a->layers[(size_t)(at + i)];
-      m.layer[i] = CacheRef{l.k, l.v, l.block_stride, l.token_stride, l.head_stride};
-    }
+  for (const Layer &l : a->layers)
+    for (uint16_t *base : {l.k, l.v})  // (strides along a length of one say nothing; the room is reserved at creation)
+      a->caches.push_back(CacheRef{base, a->d.n_blocks > 1 ? l.block_stride : 0, l.token_stride,
+                                   a->d.n_kv_heads > 1 ? l.head_stride : a->d.head_dim});
+  auto key = [](const CacheRef &c) {
+    return std::make_tuple(reinterpret_cast<uintptr_t>(c.base), c.block_stride, c.token_stride, c.head_stride);
+  };
+  std::sort(a->caches.begin(), a->caches.end(), [&](const CacheRef &x, const CacheRef &y) { return key(x) < key(y); });
+  auto same = [&](const CacheRef &x, const CacheRef &y) { return key(x) == key(y); };
+  a->caches.erase(std::unique(a->caches.begin(), a->caches.end(), same), a->caches.end());
+  auto meet = [](const CacheRef &x, const CacheRef &y) { return x.base == y.base; };
+  a->caches_mixed = std::adjacent_find(a->caches.begin(), a->caches.end(), meet) != a->caches.end();
+  return PW_OK;
+}
+
+// At most kMoveCaches of the listed caches a launch: launch(caches, their number, whether they are the first).
+template <class F>
+pw_status for_caches(const pw_attn *a, const char *what, F launch) {
+  MoveCaches m;
+  for (size_t at = 0; at < a->caches.size(); at += kMoveCaches) {
+    const int n = (int)std::min((size_t)kMoveCaches, a->caches.size() - at);
+    std::copy_n(a->caches.begin() + (ptrdiff_t)at, n, m.cache);
     if (int e = launch(m, n, at == 0)) return cuda_failed(what, e);
   }
   return PW_OK;
@@ -404,6 +423,7 @@ pw_status pw_attn_bind(pw_attn *a, int layer, void *k, void *v, int64_t block_st
   l.block_stride = block_stride;
   l.token_stride = token_stride;
   l.head_stride = head_stride;
+  a->caches.clear();
   return PW_OK;
 }
 
@@ -668,6 +688,8 @@ pw_status pw_kv_keep(pw_attn *a, const pw_kv_step *s, const int32_t *tree_len, c
   if (pw_status st = check_step(a, s)) return st;
   if (!tree_len || !keep || !n_keep) return bad("null argument");
   if (keep_stride < 1) return bad("keep_stride must be positive");
+  if (pw_status st = list_caches(a)) return st;
+  if (a->caches_mixed) return report(nullptr, PW_ERR_STATE, "two layers' caches begin at one address with other strides");
   OnDevice dev(a->d.device);
   KeepArgs g{};
   g.R = s->R;
@@ -686,7 +708,7 @@ pw_status pw_kv_keep(pw_attn *a, const pw_kv_step *s, const int32_t *tree_len, c
   g.keep = keep;
   g.n_keep = n_keep;
   g.err = a->err;
-  return for_layers(a, "pw_kv_keep launch", [&](const MoveLayers &m, int n, bool first) {
+  return for_caches(a, "pw_kv_keep launch", [&](const MoveCaches &m, int n, bool first) {
     g.ctx_out = first ? ctx_out : nullptr;
     return launch_keep(g, m, n, stream);
   });
@@ -701,6 +723,8 @@ pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, 
   if (n > a->d.n_blocks) return bad("more pairs than the cache has blocks");
   if ((int64_t)n * ((int64_t)a->d.block_tokens * a->d.n_kv_heads * a->d.head_dim / 16384 + 1) > INT32_MAX - 1024)
     return bad("too many pairs for one call");
+  if (pw_status st = list_caches(a)) return st;
+  if (!n) return PW_OK;
   OnDevice dev(a->d.device);
   CopyArgs g{};
   g.src = src;
@@ -713,11 +737,10 @@ pw_status pw_kv_copy(pw_attn *a, const int32_t *src, const int32_t *dst, int n, 
   g.err = a->err;
   g.entries = (int64_t)table_rows * table_stride;
   const bool few = n <= kRenamePairs && g.entries <= (1 << 20);
-  if (!n) return for_layers(a, "", [](const MoveLayers &, int, bool) { return 0; });
-  pw_status st = for_layers(a, "pw_kv_copy launch", [&](const MoveLayers &m, int layers, bool first) {
+  pw_status st = for_caches(a, "pw_kv_copy launch", [&](const MoveCaches &m, int caches, bool first) {
     g.table = first && few ? table : nullptr;
     g.where = first && table && !few ? a->where : nullptr;
-    return launch_copy(g, m, layers, stream);
+    return launch_copy(g, m, caches, stream);
   });
   if (st || !table || few) return st;
   g.table = table;

@@ -1,5 +1,5 @@
 // pw_kv_pages.cu -- keys and values that change their place: an accepted path of drafted tokens moves to the front of its
-// tree, and blocks are copied and renamed.  All layers' caches in one launch (of at most kMoveLayers).
+// tree, and blocks are copied and renamed.  All layers' caches in one launch (of at most kMoveCaches).
 #include <cuda_runtime.h>
 #include <limits.h>
 
@@ -10,18 +10,17 @@ namespace pw {
 
 constexpr int kKeepThreads = 128;
 
-// A CTA moves one request's tokens in one layer's keys or values.  Ids and addresses come once for the CTA; a thread then
+// A CTA moves one request's tokens in one cache, a layer's keys or values.  Ids and addresses come once for the CTA; a thread then
 // has 16 bytes of a token and goes through the moves in ascending order, four loads ahead of their stores: a place lies
 // at or before where its token comes from, and so before everything that is loaded later.  96 requests' paths of up to 6
 // tokens in 32 caches, 23.5 MB moved, take 5.5 us: latency (ids, addresses, and two rounds of loads in turn).
 __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_constant__ KeepArgs a,
-                                                               const __grid_constant__ MoveLayers m) {
+                                                               const __grid_constant__ MoveCaches m) {
   __shared__ int from[PW_TREE_NODES], end;
   __shared__ int64_t src[PW_TREE_NODES], dst[PW_TREE_NODES];
   __shared__ int n_moves, warp_moves[kKeepThreads / 32];
-  const int r = blockIdx.x, layer = blockIdx.y >> 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const CacheRef &c = m.layer[layer];
-  uint16_t *base = blockIdx.y & 1 ? c.v : c.k;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const CacheRef &c = m.cache[blockIdx.y];
   pdl_trigger();
   pdl_wait();
   const long long cap = (long long)a.table_stride * a.bt;
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
   const int moves = n_moves, vec = a.head_dim / 8;
   for (int p = tid; p < a.n_heads * vec; p += kKeepThreads) {
     const int h = p / vec;
-    uint16_t *col = base + h * c.head_stride + 8 * (p - h * vec);
+    uint16_t *col = c.base + h * c.head_stride + 8 * (p - h * vec);
     for (int i = 0; i < moves; i += 4) {
       uint4 x[4];
 #pragma unroll
@@ -95,11 +94,11 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
   }
 }
 
-int launch_keep(const KeepArgs &a, const MoveLayers &m, int n_layers, void *stream) {
-  return (int)launch_pdl(kv_keep_kernel, dim3(a.R, 2 * n_layers), dim3(kKeepThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, m);
+int launch_keep(const KeepArgs &a, const MoveCaches &m, int n_caches, void *stream) {
+  return (int)launch_pdl(kv_keep_kernel, dim3(a.R, n_caches), dim3(kKeepThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, m);
 }
 
-// A CTA copies a part of one block's keys or values in one layer, kCopyPieces pieces of 16 bytes a thread.  The pieces are
+// A CTA copies a part of one block of one cache, kCopyPieces pieces of 16 bytes a thread.  The pieces are
 // numbered in the order in which they lie in memory where the block is one run of it (`whole`), else token by token.  700
 // blocks of 32 KB in 24 caches, 1.1 GB moved, take 163 us, a copy's rate.  CTAs behind the copies' rename the table's entries
 // where pairs are few (3 pairs with a launch of its own for that: 1.5 us later).
@@ -125,9 +124,8 @@ __device__ void rename_few(const CopyArgs &a, int64_t e0) {
   }
 }
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyArgs a,
-                                                               const __grid_constant__ MoveLayers m, int splits) {
-  const CacheRef &c = m.layer[blockIdx.y >> 1];
-  uint16_t *base = blockIdx.y & 1 ? c.v : c.k;
+                                                               const __grid_constant__ MoveCaches m, int splits) {
+  const CacheRef &c = m.cache[blockIdx.y];
   const int pair = blockIdx.x / splits, split = blockIdx.x - pair * splits;
   const int vec = a.head_dim / 8, row = a.n_heads * vec, total = a.bt * row;
   const bool whole = (c.head_stride == a.head_dim && c.token_stride == (int64_t)a.n_heads * a.head_dim) ||
@@ -145,8 +143,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
     if (a.where && good) a.where[s] = pair;
   }
   if (!good) return;
-  const uint16_t *from = base + s * c.block_stride;
-  uint16_t *to = base + d * c.block_stride;
+  const uint16_t *from = c.base + s * c.block_stride;
+  uint16_t *to = c.base + d * c.block_stride;
   const int p0 = split * (kCopyThreads * kCopyPieces) + threadIdx.x;
   int64_t at[kCopyPieces];
   uint4 x[kCopyPieces];
@@ -165,11 +163,11 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
     if (p0 + k * kCopyThreads < total) *reinterpret_cast<uint4 *>(to + at[k]) = x[k];
 }
 
-int launch_copy(const CopyArgs &a, const MoveLayers &m, int n_layers, void *stream) {
+int launch_copy(const CopyArgs &a, const MoveCaches &m, int n_caches, void *stream) {
   const int per = kCopyThreads * kCopyPieces;
   const int splits = (a.bt * a.n_heads * (a.head_dim / 8) + per - 1) / per;
   const int64_t each = kCopyThreads * kRenameEntries, rename = a.table ? (a.entries + each - 1) / each : 0;
-  return (int)launch_pdl(kv_copy_kernel, dim3((unsigned)(a.n * splits + rename), 2 * n_layers), dim3(kCopyThreads), 0,
+  return (int)launch_pdl(kv_copy_kernel, dim3((unsigned)(a.n * splits + rename), n_caches), dim3(kCopyThreads), 0,
                          reinterpret_cast<cudaStream_t>(stream), a, m, splits);
 }
 

@@ -553,7 +553,8 @@ void pw_attn_destroy(pw_attn *a);
 /* The caches of a layer: element (block, token, head, d) of k is k[block * block_stride + token *
  * token_stride + head * head_stride + d] (strides in elements; v likewise), so a block may keep its
  * heads or its tokens outermost.  Addresses are multiples of 16 bytes, strides positive multiples of 8.
- * The memory stays the caller's and outlives the binding; k and v may be bound again. */
+ * The memory stays the caller's and outlives the binding; k and v may be bound again.  Layers may share a cache, and k and v
+ * may be one (the same address and strides); caches that are not the same share no element. */
 pw_status pw_attn_bind(pw_attn *a, int layer, void *k, void *v, int64_t block_stride, int64_t token_stride,
                        int64_t head_stride);
 /* Block tables and slot maps of a step, on the device from the lengths: q_start, kv_len, slot, pos, and
@@ -630,7 +631,8 @@ pw_status pw_attn_plan_tree(pw_attn *a, int plan, const pw_kv_step *step, int wi
  * layers' caches.  ctx_out [R] (NULL: not written): s + n_keep[r], the request's ctx_len in the next step; what lies
  * behind is free to be written again.  keep [R][keep_stride] and n_keep [R] are device memory.  A length, or a node that does not
  * ascend or lies outside the tree, is reported by pw_attn_check (PW_ERR_STATE); that request keeps what came before it.  Two
- * requests' trees share no block.  PW_ERR_STATE if a layer's cache is not bound. */
+ * requests' trees share no block.  A cache that several layers share is moved once.  PW_ERR_STATE if a layer's cache is not
+ * bound, or if two begin at one address with other strides. */
 pw_status pw_kv_keep(pw_attn *a, const pw_kv_step *step, const int32_t *tree_len, const int32_t *keep, int keep_stride,
                      const int32_t *n_keep, int32_t *ctx_out, pw_stream stream);
 /* Copy the blocks src[i] to dst[i], i < n, in all layers' caches (src and dst: device int32).  With a table (device

@@ -142,6 +142,59 @@ def test_more_layers_than_one_launch_takes():
         s.close()
 
 
+@pytest.mark.parametrize("L", [4, 150])
+def test_caches_that_several_layers_share(L):
+    """Layers bound to caches of others, and keys that are the values: each cache is moved once, more of them than a launch
+    takes among them."""
+    s = Cache([90, 50, 130], L=L, Hkv=2, D=16)
+    nodes, paths = [40, 30, 100], [[1, 3, 4, 9, 30], [1, 3], list(range(1, 100, 2))]
+    bind = lambda layer, k, v: s.pw.pw_attn_bind(s.attn, layer, k, v)  # noqa: E731
+    try:
+        bind(1, s.cache[0, 0], s.cache[0, 1])  # as layer 0
+        bind(2, s.cache[0, 1], s.cache[0, 0])  # the other way round
+        bind(3, s.cache[3, 0], s.cache[3, 0])  # one for both
+        untouched = [(1, 0), (1, 1), (2, 0), (2, 1), (3, 1)]
+        for _ in range(2):
+            before = s.bits()
+            ctx = s.keep(nodes, paths)
+            s.pw.pw_attn_check(s.attn)
+            want, want_ctx = s.expect_kept(before, nodes, paths)
+            for at in untouched:
+                want[at] = before[at]
+            assert np.array_equal(s.bits(), want) and ctx == want_ctx.tolist()
+            before = s.bits()
+            src, dst = s.i32(s.used[:3]), s.i32(s.free[:3])
+            s.torch.cuda.synchronize()
+            s.pw.pw_kv_copy(s.attn, src, dst)
+            want = before.copy()
+            want[:, :, s.free[:3]] = before[:, :, s.used[:3]]
+            for at in untouched:
+                want[at] = before[at]
+            assert np.array_equal(s.bits(), want)
+            # bound again: the caches are listed anew
+            bind(1, s.cache[1, 0], s.cache[1, 1])
+            untouched = [(2, 0), (2, 1), (3, 1)]
+    finally:
+        s.close()
+
+
+def test_shared_caches_of_other_strides_are_refused():
+    s = Cache([40], L=2, Hkv=2, D=16)
+    try:
+        k, v = s.cache[0, 0], s.cache[0, 1]
+        a, b = ((s.bt * 2 * 16, 16, s.bt * 16, 1), k.shape)
+        s.pw.pw_attn_bind(s.attn, 1, k.as_strided(b, a, k.storage_offset()), v.as_strided(b, a, v.storage_offset()))
+        before = s.bits()
+        with pytest.raises(s.pw.PwError) as e:
+            s.keep([20], [[3, 5]])
+        assert e.value.status == s.pw.PW_ERR_STATE and "strides" in str(e.value)
+        assert np.array_equal(s.bits(), before)
+        s.pw.pw_attn_bind(s.attn, 1, s.cache[1, 0], s.cache[1, 1])
+        s.compare_kept([20], [[3, 5]])
+    finally:
+        s.close()
+
+
 def test_paths_that_are_wrong_are_reported():
     s = Cache([100, 100, 100], D=8)
     good = [3, 7, 12]
