@@ -63,29 +63,30 @@ void lower_mark(pw_kv *kv) {
   }
 }
 
-// One holder less of a block; true if it is free now.
-bool drop(pw_kv *kv, int32_t id) {
+// One holder less of a block that several requests hold; false if it is one request's alone.
+bool leave(pw_kv *kv, int32_t id) {
   auto it = kv->sharers.find(id);
-  if (it != kv->sharers.end()) {
-    if (--it->second == 1) kv->sharers.erase(it);
-    return false;
-  }
-  kv->freed.insert(id);
-  --kv->U;
+  if (it == kv->sharers.end()) return false;
+  if (--it->second == 1) kv->sharers.erase(it);
   return true;
 }
 
-// The blocks behind the first n_keep of a request's are returned, the last one first; how many are free now.  Where memory
-// for the free ids runs out, those that are left are still the request's.
+// The blocks behind the first n_keep of a request's are returned; how many are free now.  Where memory for the free ids
+// runs out nothing changes: theirs is taken first, and the rest allocates nothing.
 bool give_back(pw_kv *kv, std::vector<int32_t> &ids, int64_t n_keep, int64_t *n) {
+  if ((int64_t)ids.size() <= n_keep) return true;
+  std::set<int32_t> free_now;
   try {
-    while ((int64_t)ids.size() > n_keep) {
-      *n += drop(kv, ids.back());
-      ids.pop_back();
-    }
+    for (size_t i = (size_t)n_keep; i < ids.size(); ++i)
+      if (!kv->sharers.count(ids[i])) free_now.insert(ids[i]);
   } catch (...) {
     return false;
   }
+  for (size_t i = (size_t)n_keep; i < ids.size(); ++i) leave(kv, ids[i]);
+  *n = (int64_t)free_now.size();
+  kv->U -= *n;
+  kv->freed.merge(free_now);
+  ids.resize((size_t)n_keep);
   return true;
 }
 
@@ -212,7 +213,7 @@ extern "C" pw_status pw_kv_unshare(pw_kv *kv, int64_t request, int64_t index, in
   const int64_t c = covered(kv, request, 1);
   if (c < 0) return PW_ERR_OOM;
   *src = id;
-  drop(kv, id);  // (shared: another holder keeps it)
+  leave(kv, id);
   *dst = id = take_lowest(kv);
   ++kv->U;
   if (c > 0) pw_kv_announce(kv, request, kv->announced[request] - c);

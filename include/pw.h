@@ -448,7 +448,7 @@ pw_status pw_kv_announce(pw_kv *kv, int64_t request, int64_t n_blocks);
 pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, int32_t *ids_out);
 /* Return every block of request r and drop its announcement; the count to *n_released
  * (may be NULL).  An unknown request releases nothing.  (A block that other requests hold too, see pw_kv_fork, stays
- * theirs and does not count.) */
+ * theirs and does not count.)  PW_ERR_OOM if host memory for the free ids runs out; nothing has changed then. */
 pw_status pw_kv_release(pw_kv *kv, int64_t request, int64_t *n_released);
 /* Request `child`, which holds no block (else PW_ERR_STATE), gets the first n_blocks blocks of `parent` (which holds as
  * many, else PW_ERR_INVALID): both hold them from then on, a block counts once in U, and it is free when its last holder has
@@ -459,7 +459,7 @@ pw_status pw_kv_fork(pw_kv *kv, int64_t parent, int64_t child, int64_t n_blocks)
  * now on, whose contents pw_kv_copy brings over; both the same where the block was the request's alone. */
 pw_status pw_kv_unshare(pw_kv *kv, int64_t request, int64_t index, int32_t *src, int32_t *dst);
 /* Return the blocks of request r behind its first n_keep (>= 0); how many became free to *n_released (may be NULL).
- * Announcements stay. */
+ * Announcements stay.  PW_ERR_OOM as by pw_kv_release. */
 pw_status pw_kv_trim(pw_kv *kv, int64_t request, int64_t n_keep, int64_t *n_released);
 /* Bring all blocks in use below the id `limit` (at least U, else PW_ERR_INVALID): those at or above it, ascending, go to
  * src[0 .. *n - 1], and the lowest free ids, which take their places in every request, to dst.  pw_kv_copy moves the
