@@ -149,12 +149,14 @@ extern "C" pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, in
   const int64_t c = covered(kv, request, n_blocks);
   if (c < 0) return PW_ERR_OOM;
   // U + n <= C <= n_ids, so the ids below n_ids suffice
-  std::vector<int32_t> &mine = kv->held[request];
+  std::vector<int32_t> *held;
   try {
-    mine.reserve(mine.size() + (size_t)n_blocks);
+    held = &kv->held[request];
+    held->reserve(held->size() + (size_t)n_blocks);
   } catch (...) {
     return PW_ERR_OOM;
   }
+  std::vector<int32_t> &mine = *held;
   for (int64_t k = 0; k < n_blocks; ++k) {
     const int32_t id = take_lowest(kv);
     mine.push_back(id);

@@ -442,7 +442,7 @@ pw_status pw_kv_attach(pw_kv *kv, pw_ctx *ctx);
  * announcement.  The announced blocks count as taken in F_blk. */
 pw_status pw_kv_announce(pw_kv *kv, int64_t request, int64_t n_blocks);
 /* Grow request r by n_blocks (>= 0): c = min(n, r's announcement) of them come out of the
- * announcement, the other n - c must fit in F_blk, else PW_ERR_OOM and nothing changes.
+ * announcement, the other n - c must fit in F_blk (and their ids in host memory), else PW_ERR_OOM and nothing changes.
  * The granted ids -- the lowest free ones, ascending -- go to ids_out[0..n-1] (NULL: not
  * written). */
 pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, int32_t *ids_out);
