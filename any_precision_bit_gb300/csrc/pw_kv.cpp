@@ -134,12 +134,16 @@ extern "C" pw_status pw_kv_announce(pw_kv *kv, int64_t request, int64_t n_blocks
   if (!kv || n_blocks < 0) return PW_ERR_INVALID;
   auto it = kv->announced.find(request);
   const int64_t old = it == kv->announced.end() ? 0 : it->second;
-  kv->P += n_blocks - old;
   if (n_blocks == 0) {
     if (it != kv->announced.end()) kv->announced.erase(it);
   } else {
-    kv->announced[request] = n_blocks;
+    try {
+      kv->announced[request] = n_blocks;
+    } catch (...) {
+      return PW_ERR_OOM;
+    }
   }
+  kv->P += n_blocks - old;
   return PW_OK;
 }
 

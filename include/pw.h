@@ -439,7 +439,8 @@ pw_status pw_kv_set_weight_bytes(pw_kv *kv, int64_t weight_bytes);
  * detaches and keeps the last value read).  PW_ERR_* of pw_memory when reading fails. */
 pw_status pw_kv_attach(pw_kv *kv, pw_ctx *ctx);
 /* Request r expects to need n_blocks (>= 0) more blocks soon; replaces its previous
- * announcement.  The announced blocks count as taken in F_blk. */
+ * announcement.  The announced blocks count as taken in F_blk.  PW_ERR_OOM if host memory runs out; nothing has changed
+ * then. */
 pw_status pw_kv_announce(pw_kv *kv, int64_t request, int64_t n_blocks);
 /* Grow request r by n_blocks (>= 0): c = min(n, r's announcement) of them come out of the
  * announcement, the other n - c must fit in F_blk (and their ids in host memory), else PW_ERR_OOM and nothing changes.

@@ -19,7 +19,7 @@ def program(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("call", ["release", "trim", "grow", "fork", "compact"])
+@pytest.mark.parametrize("call", ["release", "trim", "grow", "fork", "compact", "announce"])
 def test_a_call_out_of_memory_changes_nothing(program, call):
     out = subprocess.run([program, "".join("1" if c == call else "0" for c in CALLS)], capture_output=True, text=True, timeout=120)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout + out.stderr
