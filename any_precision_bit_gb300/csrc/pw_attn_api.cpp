@@ -111,6 +111,29 @@ int log2_of(int v) {
   return l;
 }
 
+// f / 2 pi modulo one turn, in units of 2^-64 to the nearest (f finite): for f = m 2^e with a whole m the bits of 1 / 2 pi from the
+// (e + 1)st behind the point on, all that is left of 2^e / 2 pi, times m (the reduction of Payne and Hanek, 1983).  128 of
+// those bits are enough: m < 2^53.  (In double f / 2 pi has 53 bits at best, which 2^31 positions later is 2^-22 of a turn and
+// more; negative and large f lose more than that.)
+uint64_t turn_of(double f) {
+  static const uint64_t kBits[18] = {  // of 1 / 2 pi behind the point, computed by Machin's formula
+    0x28be60db9391054a, 0x7f09d5f47d4d3770, 0x36d8a5664f10e410, 0x7f9458eaf7aef158, 0x6dc91b8e909374b8,
+    0x01924bba82746487, 0x3f877ac72c4a69cf, 0xba208d7d4baed121, 0x3a671c09ad17df90, 0x4e64758e60d4ce7d,
+    0x272117e2ef7e4a0e, 0xc7fe25fff7816603, 0xfbcbc462d6829b47, 0xdb4d9fb3c9f2c26d, 0xd3d18fd9a797fa8b,
+    0x5d49eeb1faf97c5e, 0xcf41ce7de294a4ba, 0x9afed7ec47e35742};
+  using u128 = unsigned __int128;
+  int e;
+  const double m = std::frexp(std::fabs(f), &e);
+  const uint64_t whole = (uint64_t)std::ldexp(m, 53);
+  e -= 53;  // at most 971: 128 bits from there on are in the table
+  const int at = e >= 0 ? e / 64 : -((63 - e) / 64), shift = e - 64 * at;
+  auto word = [&](int i) { return i >= 0 && i < 18 ? kBits[i] : 0; };
+  auto from = [&](int i) { return shift ? word(i) << shift | word(i + 1) >> (64 - shift) : word(i); };
+  const u128 turns = ((u128)from(at) << 64 | from(at + 1)) * whole;
+  const uint64_t turn = (uint64_t)((turns + ((u128)1 << 63)) >> 64);
+  return f < 0 ? 0 - turn : turn;
+}
+
 // Makes the handle's device current for a call and puts the caller's back.
 struct OnDevice {
   int before = -1;
@@ -606,10 +629,7 @@ pw_status pw_attn_set_rope(pw_attn *a, int layer, const pw_rope_desc *r) {
   for (int i = 0; i < r->rot_dim / 2; ++i) {
     if (!std::isfinite(r->inv_freq[i])) return bad("inv_freq must be finite");
     if (r->axis && (r->axis[i] < 0 || r->axis[i] >= r->n_axes)) return bad("axis must be in 0..n_axes - 1");
-    // the fraction of a turn for each position; whole turns fall away, since positions are whole numbers
-    const double turns = r->inv_freq[i] / 6.283185307179586476925;
-    const double part = std::ldexp(turns - std::floor(turns), 64);  // up to 2^64 where turns is just below a whole number
-    t.turn[i] = part < 18446744073709551616.0 ? (uint64_t)part : 0;
+    t.turn[i] = turn_of(r->inv_freq[i]);  // (whole turns fall away, since positions are whole numbers)
     t.axis[i] = r->axis ? r->axis[i] : 0;
   }
   OnDevice dev(a->d.device);

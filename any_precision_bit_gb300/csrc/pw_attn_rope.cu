@@ -1,10 +1,11 @@
 // pw_attn_rope.cu -- norms and rotation of queries and keys, and the cache write, in one pass over a step's rows.
 //
 // A head x of q or k becomes y = x rsqrt(mean x^2 + eps) gain, and each of its pairs (a, b) becomes s (a cos f - b sin f,
-// a sin f + b cos f), f = p inv_freq.  The host turns inv_freq / 2 pi into a 64-bit fraction of a turn, so that the product
-// with the integer position modulo 2^64 is the angle's fraction of a turn at any position, exactly; in fp32 the product alone is
-// off by 2^-24 p radians.  Its upper 32 bits give the nearest quarter turn and a rest of at most 1/8 turn for two short
-// polynomials.
+// a sin f + b cos f), f = p inv_freq.  The host turns inv_freq / 2 pi into the nearest 64-bit fraction of a turn, off by at most 2^-65,
+// so that the product with the integer position modulo 2^64 is the angle's fraction of a turn to 2^-34 at any position; in fp32 the
+// product alone is off by 2^-24 p radians.  Its upper 32 bits give the nearest quarter turn and a rest of at most 1/8 turn for
+// two short polynomials.  What was cut off is less than 2^-31.6 of a turn, 2 10^-9; with the polynomials' fp32 steps sine and cosine are
+// off by less than 2^-22 (2^-23.3 at most among 4 10^7 random angles, the same steps restated on the host).
 #include <cuda_runtime.h>
 
 #include "pw_attn.h"

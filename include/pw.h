@@ -587,8 +587,9 @@ pw_status pw_attn_append(pw_attn *a, int layer, const pw_kv_step *step, const vo
 /* Rotation of queries and keys by position, and norms of both before it.  Of each head the first rot_dim elements make
  * rot_dim / 2 pairs; pair i of a token is turned by the angle f = p * inv_freq[i], p the token's position on axis axis[i]:
  *   a' = scale (a cos f - b sin f),  b' = scale (a sin f + b cos f),
- * which is exact to fp32 at every int32 position (the angle's part of a turn is computed in whole numbers).  Before that a
- * head of q (k) is x / sqrt(mean x^2 + eps) * q_gain (k_gain), where gains are given.  All of it is fp32, rounded once. */
+ * with sine and cosine off by less than 2^-22 at every int32 position and for every finite inv_freq (the angle's part of a
+ * turn is computed in whole numbers, to 2 10^-9 radians).  Before that a head of q (k) is x / sqrt(mean x^2 + eps) *
+ * q_gain (k_gain), where gains are given.  All of it is fp32, rounded once. */
 typedef struct {
     int rot_dim;            /* a multiple of 8, at most head_dim; 0: nothing is turned */
     int interleaved;        /* pair i is the elements 2 i and 2 i + 1; else i and i + rot_dim / 2 */

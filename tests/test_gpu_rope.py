@@ -1,4 +1,6 @@
 """Norms, rotation and cache write in one pass against the float64 oracle."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -129,6 +131,57 @@ def test_far_positions(top, interleaved):
     pos = np.array([[0, 1, top - 1, top // 3, top // 7 * 2, -top + 1, -1]])
     run(7, dict(D=128, dtype="fp16"), pos=pos, interleaved=interleaved)
     run(7, dict(D=128, dtype="fp16"), pos=pos, interleaved=interleaved, freq=-freqs(128, 500000.0) * 3)
+
+
+def two_pi(bits=1400):
+    """2 pi as a fraction, by Machin's formula."""
+    def atan_of_inverse(n):
+        x = total = (1 << bits) // n
+        k, sign = 1, -1
+        while x:
+            x //= n * n
+            k += 2
+            total += sign * (x // k)
+            sign = -sign
+        return total
+    return Fraction(8 * (4 * atan_of_inverse(5) - atan_of_inverse(239)), 1 << bits)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_angles_far_away(sign):
+    """Sines of angles next to a multiple of pi, which show an angle to a small part of fp32's step: for each frequency the
+    position among the farthest 200000 whose sine is the smallest.  The angle is off by what 32 bits of a turn cut off and
+    2^31 / 2 steps of 2^-64; sine, scale and result are rounded once or a few times, relative to a sine that small."""
+    some = [1.0, 0.3, 2.5, 7.0, 1000.0, 1e5, 1e12, 1e30, 1e300, 2.0 ** 53, 2.0 ** 100 / 3, 5e-324]
+    freq = np.array([sign * f for f in [*some, *freqs(128)[:26], *freqs(128, 5e5)[:26]]])
+    turn, top, places, want = two_pi(), (1 << 31) - 1, [], []
+    near = top - np.arange(200000, dtype=np.uint64)
+    for f in freq:
+        part = Fraction(float(f)) / turn % 1
+        angle = (near * np.uint64(int(part * 2 ** 64))) & np.uint64(2 ** 63 - 1)  # modulo half a turn
+        p = int(near[np.argmin(np.minimum(angle, np.uint64(2 ** 63) - angle))])
+        halves = 2 * part * p
+        whole = round(halves)
+        places.append(p)
+        want.append((-1) ** whole * np.sin(float((halves - whole) * turn / 2)))
+    want, n = np.array(want), len(freq)
+    s = Rope(n, Hq=1, Hkv=1, D=128, dtype="fp16")
+    try:
+        for x in (s.q, s.k):
+            x[..., :64], x[..., 64:] = 1, 0
+        for way in (1, -1):
+            pos = s.torch.as_tensor(way * np.array([places], dtype=np.int32)).cuda()
+            s.pw.pw_attn_set_rope(s.attn, 0, freq, scale=1024.0)
+            s.torch.cuda.synchronize()
+            s.pw.pw_attn_rope_append(s.attn, 0, s.step, s.q, s.out[:, :, 0], s.k, s.v, pos=pos)
+            s.pw.pw_attn_check(s.attn)
+            held = s.cache[0, 0].reshape(-1, 1, 128)[s.slot]
+            for got in (s.out[:, 0, 0], held[:, 0]):
+                err = np.abs(got.double().cpu().numpy()[np.arange(n), 64 + np.arange(n)] / 1024 - way * want)
+                lim = 2 * np.pi * (2.0 ** -32 + 2.0 ** -33) + (2.0 ** -11 + 2.0 ** -22) * np.abs(want) + 2.0 ** -35
+                assert (err <= lim).all(), (freq[err > lim].tolist(), err[err > lim].tolist(), lim[err > lim].tolist())
+    finally:
+        s.close()
 
 
 @pytest.mark.parametrize("n_axes", [2, 3, 4])
