@@ -82,6 +82,13 @@ struct Layer {
   int rope_axes = 0;
 };
 
+// A cache of keys or of values.
+struct CacheRef {
+  uint16_t *base;
+  int64_t block_stride, token_stride, head_stride;
+  auto strides() const { return std::tie(block_stride, token_stride, head_stride); }
+};
+
 struct Plan {
   bool set = false;
   pw_kv_step step{};
@@ -255,24 +262,29 @@ pw_status list_caches(pw_attn *a) {
     for (uint16_t *base : {l.k, l.v})  // (strides along a length of one say nothing; the room is reserved at creation)
       a->caches.push_back(CacheRef{base, a->d.n_blocks > 1 ? l.block_stride : 0, l.token_stride,
                                    a->d.n_kv_heads > 1 ? l.head_stride : a->d.head_dim});
-  auto key = [](const CacheRef &c) {
-    return std::make_tuple(reinterpret_cast<uintptr_t>(c.base), c.block_stride, c.token_stride, c.head_stride);
-  };
-  std::sort(a->caches.begin(), a->caches.end(), [&](const CacheRef &x, const CacheRef &y) { return key(x) < key(y); });
-  auto same = [&](const CacheRef &x, const CacheRef &y) { return key(x) == key(y); };
-  a->caches.erase(std::unique(a->caches.begin(), a->caches.end(), same), a->caches.end());
+  auto at = [](const CacheRef &c) { return reinterpret_cast<uintptr_t>(c.base); };
   auto meet = [](const CacheRef &x, const CacheRef &y) { return x.base == y.base; };
+  auto same = [&](const CacheRef &x, const CacheRef &y) { return meet(x, y) && x.strides() == y.strides(); };
+  std::sort(a->caches.begin(), a->caches.end(), [&](const CacheRef &x, const CacheRef &y) {
+    return at(x) != at(y) ? at(x) < at(y) : x.strides() < y.strides();
+  });
+  a->caches.erase(std::unique(a->caches.begin(), a->caches.end(), same), a->caches.end());
   a->caches_mixed = std::adjacent_find(a->caches.begin(), a->caches.end(), meet) != a->caches.end();
+  std::sort(a->caches.begin(), a->caches.end(), [&](const CacheRef &x, const CacheRef &y) {
+    return x.strides() != y.strides() ? x.strides() < y.strides() : at(x) < at(y);
+  });
   return PW_OK;
 }
 
-// At most kMoveCaches of the listed caches a launch: launch(caches, their number, whether they are the first).
+// The listed caches, at most kMoveCaches of the same strides a launch: launch(caches, their number, whether they are the first).
 template <class F>
 pw_status for_caches(const pw_attn *a, const char *what, F launch) {
   MoveCaches m;
-  for (size_t at = 0; at < a->caches.size(); at += kMoveCaches) {
-    const int n = (int)std::min((size_t)kMoveCaches, a->caches.size() - at);
-    std::copy_n(a->caches.begin() + (ptrdiff_t)at, n, m.cache);
+  const std::vector<CacheRef> &c = a->caches;
+  int n = 0;
+  for (size_t at = 0; at < c.size(); at += (size_t)n) {
+    for (n = 0; n < kMoveCaches && at + n < c.size() && c[at + n].strides() == c[at].strides(); ++n) m.base[n] = c[at + n].base;
+    std::tie(m.block_stride, m.token_stride, m.head_stride) = c[at].strides();
     if (int e = launch(m, n, at == 0)) return cuda_failed(what, e);
   }
   return PW_OK;

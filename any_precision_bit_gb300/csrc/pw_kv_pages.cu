@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
   __shared__ int64_t src[PW_TREE_NODES], dst[PW_TREE_NODES];
   __shared__ int n_moves, warp_moves[kKeepThreads / 32];
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const CacheRef &c = m.cache[blockIdx.y];
+  uint16_t *base = m.base[blockIdx.y];
   pdl_trigger();
   pdl_wait();
   const long long cap = (long long)a.table_stride * a.bt;
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
   // the moves of tokens that are not in their place, in order
   auto address = [&](int p) {
     const int id = a.table[(size_t)row * a.table_stride + (p >> a.log_bt)];
-    return id >= 0 && id < a.n_blocks ? id * c.block_stride + (p & (a.bt - 1)) * c.token_stride : (int64_t)-1;
+    return id >= 0 && id < a.n_blocks ? id * m.block_stride + (p & (a.bt - 1)) * m.token_stride : (int64_t)-1;
   };
   for (int i0 = 0; i0 < n; i0 += kKeepThreads) {
     const int i = i0 + tid;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
   const int moves = n_moves, vec = a.head_dim / 8;
   for (int p = tid; p < a.n_heads * vec; p += kKeepThreads) {
     const int h = p / vec;
-    uint16_t *col = c.base + h * c.head_stride + 8 * (p - h * vec);
+    uint16_t *col = base + h * m.head_stride + 8 * (p - h * vec);
     for (int i = 0; i < moves; i += 4) {
       uint4 x[4];
 #pragma unroll
@@ -125,11 +125,11 @@ __device__ void rename_few(const CopyArgs &a, int64_t e0) {
 }
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyArgs a,
                                                                const __grid_constant__ MoveCaches m, int splits) {
-  const CacheRef &c = m.cache[blockIdx.y];
+  uint16_t *base = m.base[blockIdx.y];
   const int pair = blockIdx.x / splits, split = blockIdx.x - pair * splits;
   const int vec = a.head_dim / 8, row = a.n_heads * vec, total = a.bt * row;
-  const bool whole = (c.head_stride == a.head_dim && c.token_stride == (int64_t)a.n_heads * a.head_dim) ||
-                     (c.token_stride == a.head_dim && c.head_stride == (int64_t)a.bt * a.head_dim);
+  const bool whole = (m.head_stride == a.head_dim && m.token_stride == (int64_t)a.n_heads * a.head_dim) ||
+                     (m.token_stride == a.head_dim && m.head_stride == (int64_t)a.bt * a.head_dim);
   pdl_trigger();
   pdl_wait();
   if (pair >= a.n) {
@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
     if (a.where && good) a.where[s] = pair;
   }
   if (!good) return;
-  const uint16_t *from = c.base + s * c.block_stride;
-  uint16_t *to = c.base + d * c.block_stride;
+  const uint16_t *from = base + s * m.block_stride;
+  uint16_t *to = base + d * m.block_stride;
   const int p0 = split * (kCopyThreads * kCopyPieces) + threadIdx.x;
   int64_t at[kCopyPieces];
   uint4 x[kCopyPieces];
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
     at[k] = 8 * (int64_t)p;
     if (!whole) {
       const int t = p / row, q = p - t * row, h = q / vec;
-      at[k] = t * c.token_stride + h * c.head_stride + 8 * (q - h * vec);
+      at[k] = t * m.token_stride + h * m.head_stride + 8 * (q - h * vec);
     }
     if (p < total) x[k] = *reinterpret_cast<const uint4 *>(from + at[k]);
   }

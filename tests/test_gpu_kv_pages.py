@@ -178,6 +178,35 @@ def test_caches_that_several_layers_share(L):
         s.close()
 
 
+def test_layers_of_different_strides():
+    """Heads outermost in one layer, tokens in the others: each is moved by its own strides, and the table renamed once."""
+    s = Cache([90, 50], L=4, Hkv=2, D=16)
+    try:
+        hnd = s.cache[1].reshape(2, s.nb, 2, s.bt, 16).transpose(2, 3)
+        s.pw.pw_attn_bind(s.attn, 1, hnd[0], hnd[1])
+        view = lambda bits: bits[1].reshape(2, s.nb, 2, s.bt, 16).transpose(0, 1, 3, 2, 4)  # noqa: E731
+        nodes, paths = [40, 30], [[1, 3, 4, 9, 30], [1, 3]]
+        before = s.bits()
+        ctx = s.keep(nodes, paths)
+        s.pw.pw_attn_check(s.attn)
+        want, want_ctx = s.expect_kept(before, nodes, paths)
+        want[1] = before[1]
+        for kind in range(2):
+            view(want)[kind], _ = oa.keep(view(before)[kind], s.table0, s.kv_len, nodes, paths, s.bt)
+        assert np.array_equal(s.bits(), want) and ctx == want_ctx.tolist()
+        before = s.bits()
+        src, dst = s.i32(s.used[:2]), s.i32(s.free[:2])
+        s.torch.cuda.synchronize()
+        s.pw.pw_kv_copy(s.attn, src, dst, table=s.table)
+        want, renamed = before.copy(), s.table0.copy()
+        want[:, :, s.free[:2]] = before[:, :, s.used[:2]]
+        for a, b in zip(s.used[:2], s.free[:2]):
+            renamed[s.table0 == a] = b
+        assert np.array_equal(s.bits(), want) and np.array_equal(s.table.cpu().numpy(), renamed)
+    finally:
+        s.close()
+
+
 def test_shared_caches_of_other_strides_are_refused():
     s = Cache([40], L=2, Hkv=2, D=16)
     try:
