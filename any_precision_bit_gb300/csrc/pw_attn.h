@@ -169,7 +169,7 @@ struct RopeArgs {
   const int *pos;     // [axes][n_tokens], or one for all axes
   int64_t pos_axis;   // elements from axis to axis
   int n_tokens, Hq, Hkv, D, bt, log_bt, n_blocks;
-  int rot, interleaved, norm_q, norm_k;
+  int rot, interleaved, norm_q, norm_k, sms;
   float scale, eps, inv_d;
 };
 

@@ -704,6 +704,7 @@ pw_status pw_attn_rope_append(pw_attn *a, int layer, const pw_kv_step *s, const 
   g.pos = pos ? pos : s->pos;
   g.pos_axis = pos ? s->n_tokens : 0;
   g.n_tokens = s->n_tokens;
+  g.sms = a->sm_count;
   g.Hq = a->d.n_heads;
   g.Hkv = a->d.n_kv_heads;
   g.D = a->d.head_dim;

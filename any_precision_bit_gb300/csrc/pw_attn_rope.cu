@@ -227,8 +227,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
 
 template <bool BF, int P, int GL, bool IL>
 static int launch_one(const RopeArgs &a, cudaStream_t st) {
-  // as few tokens to a CTA as keep the SMs in work, for the shortest way, and no more than make the tables worth their while
-  const int tokens = a.n_tokens >= 152 * 8 * kRopeTokens ? kRopeTokens : a.n_tokens >= 152 * 16 ? 2 : 1;
+  // As few tokens to a CTA as keep the SMs in work, for the shortest way, and no more than make the tables worth their while.  Both
+  // borders are measured: tokens and us with 1, 2 and 4 to a CTA on 152 SMs,
+  //            1200             2432             4000             4864             8000
+  //   32/8 x 128  9.1 8.2 12.1  14.9 14.3 13.8   21.3 20.2 23.0   25.0 24.7 24.5   38.2 36.7 36.5
+  //   16/16 x 96  8.3 7.7 9.7   13.8 13.5 10.9   19.8 19.1 17.4   23.0 23.4 19.0   34.4 34.4 28.0
+  //   8/1 x 128   4.5 4.0 5.4   9.2 7.9 6.4      14.0 11.9 10.8   16.3 14.5 11.5   24.8 21.3 16.7
+  //   28/4 x 72   8.5 8.7 14.7  13.3 13.2 15.9   18.2 16.2 16.3   21.7 19.9 23.5   33.0 29.3 29.8
+  // (600 tokens: 1 is the best of all four by a third; halves of a head)
+  const int tokens = a.n_tokens >= a.sms * 8 * kRopeTokens ? kRopeTokens : a.n_tokens >= a.sms * 16 ? 2 : 1;
   return (int)launch_pdl(rope_kernel<BF, P, GL, IL>, dim3((a.n_tokens + tokens - 1) / tokens), dim3(kRopeThreads), 0, st, a,
                          tokens);
 }
