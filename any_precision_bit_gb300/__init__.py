@@ -579,14 +579,20 @@ def pw_kv_get_stats(kv) -> dict:
 # (Called once or several times a layer, so argument marshalling is kept short here.)
 # handle: (n_heads, n_kv_heads, head_dim, the caches' and rows' type, device, desc, plans, caches), with
 # {plan: (its step's n_tokens, the step's tensors)} and {layer: its caches}: the library keeps their addresses
+# Every call works on `stream` (None: the device's default stream) and returns before it has run.  Its tensors are lent to that
+# stream where it is not torch's current one, so that a tensor made for the call alone is not given out again too early; other
+# tensors of a foreign stream are the caller's to keep or to record, as with torch's own operators.
 _attn_shapes = {}
 _rope_axes = {}  # axes of a (handle, layer)'s rotation
 _types = {}  # torch's, by name
+_raw_stream = None  # torch's current stream of a device, as a number
 
 
 def _load_types():
+    global _raw_stream
     if not _types:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
         _types.update((n, getattr(torch, n)) for n in ("int32", "int64", "float32", "bfloat16", "float16"))
 
 
@@ -628,7 +634,21 @@ def _step_on(step, device):
 
 
 def _cuda_stream(s):
-    return None if s is None else getattr(s, "cuda_stream", s)
+    return 0 if s is None else getattr(s, "cuda_stream", s)
+
+
+def _lend(stream, device, *tensors):
+    """Tensors that a call uses on a stream that is not torch's current one (whose freed tensors are given out again at once):
+    their memory stays theirs until the stream has come past the call."""
+    if not hasattr(stream, "cuda_stream"):
+        import torch
+        raw = getattr(stream, "value", stream) or 0
+        if raw == _raw_stream(device):
+            return
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def pw_attn_create(desc: pw_attn_desc):
@@ -651,7 +671,8 @@ def pw_attn_destroy(attn):
 
 def pw_attn_bind(attn, layer, k_cache, v_cache):
     """Caches as tensors [n_blocks][block_tokens][n_kv_heads][head_dim], views included, of the
-    same strides and a unit last one.  The handle keeps them until others are bound to the layer."""
+    same strides and a unit last one.  The handle keeps them until others are bound to the layer (which does not wait for
+    work on them)."""
     _, _, _, dtype, device, d, _, caches = _attn_shapes[attn]
     for c in (k_cache, v_cache):
         if (tuple(c.shape) != (d.n_blocks, d.block_tokens, d.n_kv_heads, d.head_dim) or c.dtype is not dtype
@@ -685,19 +706,24 @@ def pw_make_step(ctx_len, new_len, table, q_start, kv_len, slot, pos, max_new, r
 
 def pw_kv_map(attn, step, new_ids, stream=None):
     dev = _attn_shapes[attn][4]
-    st = lib().pw_kv_map(attn, _step_on(step, dev), _addr(new_ids, dev), 0 if new_ids is None else new_ids.numel(),
-                         _cuda_stream(stream))
+    raw = _cuda_stream(stream)
+    st = lib().pw_kv_map(attn, _step_on(step, dev), _addr(new_ids, dev), 0 if new_ids is None else new_ids.numel(), raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, new_ids, *step.refs)
 
 
 def pw_attn_plan(attn, plan, step, window=0, doc_start=None, bidir_len=None, stream=None):
     """The handle keeps the step's tensors until the plan is laid out again."""
     _, _, _, _, dev, _, plans, _ = _attn_shapes[attn]
+    raw = _cuda_stream(stream)
     st = lib().pw_attn_plan(attn, plan, _step_on(step, dev), window, _addr(doc_start, dev, step.n_tokens),
-                            _addr(bidir_len, dev, step.R), _cuda_stream(stream))
+                            _addr(bidir_len, dev, step.R), raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, doc_start, bidir_len, *step.refs)
     plans[plan] = step.n_tokens, step.refs
 
 
@@ -705,10 +731,13 @@ def pw_attn_append(attn, layer, step, k, v, stream=None):
     """k and v: [n_tokens][n_kv_heads][head_dim], any strides with a unit last one."""
     _, h, d, dtype, dev, _, _, _ = _attn_shapes[attn]
     n = step.n_tokens
+    raw = _cuda_stream(stream)
     st = lib().pw_attn_append(attn, layer, _step_on(step, dev), *_rows(k, n, h, d, dtype, dev), *_rows(v, n, h, d, dtype, dev),
-                              _cuda_stream(stream))
+                              raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, k, v, *step.refs)
 
 
 def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, slopes=None, stream=None):
@@ -716,11 +745,14 @@ def pw_attn_forward(attn, layer, plan, q, o, lse=None, scale=None, softcap=0.0, 
     1 / sqrt(head_dim)."""
     h, _, d, dtype, dev, _, plans, _ = _attn_shapes[attn]
     n = plans[plan][0] if plan in plans else 0
+    raw = _cuda_stream(stream)
     st = lib().pw_attn_forward(attn, layer, plan, *_rows(q, n, h, d, dtype, dev), *_rows(o, n, h, d, dtype, dev),
                                _addr(lse, dev, n * h, "float32"), d ** -0.5 if scale is None else scale, softcap,
-                               _addr(slopes, dev, h, "float32"), _cuda_stream(stream))
+                               _addr(slopes, dev, h, "float32"), raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, q, o, lse, slopes, *plans[plan][1])
 
 
 def pw_attn_set_rope(attn, layer, inv_freq, axis=None, n_axes=1, interleaved=False, scale=1.0, q_gain=None, k_gain=None,
@@ -755,12 +787,15 @@ def pw_attn_rope_append(attn, layer, step, q, q_out, k, v, pos=None, stream=None
     n = step.n_tokens
     if pos is not None and pos.dim() > 1 and pos.shape[-1] != n:
         raise ValueError(f"needs positions [n_axes][{n}], not {_what(pos)}")
+    raw = _cuda_stream(stream)
     st = lib().pw_attn_rope_append(attn, layer, _step_on(step, dev), *_rows(q, n, hq, d, dtype, dev),
                                    *_rows(q_out, n, hq, d, dtype, dev), *_rows(k, n, h, d, dtype, dev),
                                    *_rows(v, n, h, d, dtype, dev), _addr(pos, dev, n * _rope_axes.get((attn, layer), 1)),
-                                   _cuda_stream(stream))
+                                   raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, q, q_out, k, v, pos, *step.refs)
 
 
 def pw_attn_plan_tree(attn, plan, step, tree_len, parent, pos=None, window=0, stream=None):
@@ -769,28 +804,37 @@ def pw_attn_plan_tree(attn, plan, step, tree_len, parent, pos=None, window=0, st
     _, _, _, _, dev, _, plans, _ = _attn_shapes[attn]
     nodes, stride = _nodes(parent, dev, step.R)
     tree = pw_tree(tree_len=_addr(tree_len, dev, step.R), parent=nodes, parent_stride=stride, pos=_addr(pos, dev, step.n_tokens))
-    st = lib().pw_attn_plan_tree(attn, plan, _step_on(step, dev), window, C.byref(tree), _cuda_stream(stream))
+    raw = _cuda_stream(stream)
+    st = lib().pw_attn_plan_tree(attn, plan, _step_on(step, dev), window, C.byref(tree), raw)
     if st:
         _check(st)
-    plans[plan] = step.n_tokens, (step.refs, tree_len, parent, pos)
+    plans[plan] = step.n_tokens, (*step.refs, tree_len, parent, pos)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, *plans[plan][1])
 
 
 def pw_kv_keep(attn, step, tree_len, keep, n_keep, ctx_out=None, stream=None):
     """tree_len and n_keep: int32 [R]; keep: int32 [R][nodes]; ctx_out: int32 [R], filled."""
     dev, R = _attn_shapes[attn][4], step.R
+    raw = _cuda_stream(stream)
     st = lib().pw_kv_keep(attn, _step_on(step, dev), _addr(tree_len, dev, R), *_nodes(keep, dev, R), _addr(n_keep, dev, R),
-                          _addr(ctx_out, dev, R), _cuda_stream(stream))
+                          _addr(ctx_out, dev, R), raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, tree_len, keep, n_keep, ctx_out, *step.refs)
 
 
 def pw_kv_copy(attn, src, dst, table=None, stream=None):
     """src and dst: int32 [n]; table: int32 [rows][blocks] whose entries src become dst."""
     dev, n = _attn_shapes[attn][4], src.numel()
     rows, stride = (0, 0) if table is None else table.shape
-    st = lib().pw_kv_copy(attn, _addr(src, dev), _addr(dst, dev, n), n, _addr(table, dev), rows, stride, _cuda_stream(stream))
+    raw = _cuda_stream(stream)
+    st = lib().pw_kv_copy(attn, _addr(src, dev), _addr(dst, dev, n), n, _addr(table, dev), rows, stride, raw)
     if st:
         _check(st)
+    if raw != _raw_stream(dev):
+        _lend(stream, dev, src, dst, table)
 
 
 def pw_attn_check(attn, stream=None):

@@ -380,6 +380,36 @@ def test_captured_calls():
         s.close()
 
 
+def test_tensors_made_for_a_call_on_another_stream():
+    """While that stream is busy their memory is not given out again."""
+    import torch
+    s = Cache([100, 100], D=64)
+    stream = torch.cuda.Stream()
+
+    def addresses(call):
+        t = torch.zeros(2000, dtype=torch.int32, device="cuda")  # (of a size that nothing else here has)
+        at = t.data_ptr()
+        call(t)
+        del t
+        return at, torch.zeros(2000, dtype=torch.int32, device="cuda").data_ptr()
+    try:
+        first, second = addresses(lambda t: None)
+        assert first == second  # as a rule it comes back at once
+        none, used, free = s.i32([0, 0]), s.i32(s.used[:2]), s.i32(s.free[:2])
+        for call in (lambda t: s.pw.pw_kv_keep(s.attn, s.step, none, t.view(2, 1000), none, stream=stream),
+                     lambda t: s.pw.pw_kv_copy(s.attn, used, free, table=t.view(2, 1000), stream=stream)):
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(200_000_000)
+            first, second = addresses(call)
+            assert first != second
+        torch.cuda.synchronize()
+        s.pw.pw_attn_check(s.attn)
+    finally:
+        torch.cuda.synchronize()
+        s.close()
+
+
 def test_refusals():
     import torch
     s = Cache([40])
