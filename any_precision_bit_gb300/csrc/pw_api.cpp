@@ -620,6 +620,8 @@ pw_status pw_set_router(pw_ctx *c, int layer, const float *Wr, const float *bias
     l.bias = nullptr;
     drop_graphs(c);
   }
+  // (copies from pageable or device memory may return while they are under way, on a stream that forwards do not wait for)
+  CU(c, cudaStreamSynchronize(nullptr));
   c->router_set[layer] = 1;
   return PW_OK;
 }
@@ -1156,7 +1158,7 @@ static pw_status readback(pw_ctx *c, int block, int b, uint8_t *idx_out, uint16_
   BlockDev *drow = reinterpret_cast<BlockDev *>(stg + out_al);
   BlockDev v = dev_entry(c, hb, c->d.bmax);
   v.q = b;
-  CU(c, cudaMemcpy(drow, &v, sizeof v, cudaMemcpyHostToDevice));
+  CU(c, cudaMemcpyAsync(drow, &v, sizeof v, cudaMemcpyHostToDevice, c->compute));
   if (int e = launch_unpack(drow, 0, b, hb.u, c->d.I, hb.N, hb.KC, idx_out ? reinterpret_cast<uint8_t *>(stg) : nullptr,
                             w_out ? reinterpret_cast<uint16_t *>(stg) : nullptr, c->compute))
     return fail(c, PW_ERR_CUDA, "unpack kernel: %s", cudaGetErrorString((cudaError_t)e));
