@@ -82,6 +82,15 @@ def test_behind_shared_prefixes(n, kind):
     run(ctx, [n] * R, [random_tree(n + (3 if r == 0 else 0), r) for r in range(R)], group_start=[0, 3, 5], prefix=[64, 128], **kind)
 
 
+@pytest.mark.parametrize("kind", [{}, dict(window=9), dict(softcap=3.0), dict(slopes=[0.5, 0.25, 0.1, 3.0])], ids=str)
+@pytest.mark.parametrize("n,held", [(2, 5), (4, 90), (19, 30), (40, 60)])
+def test_trees_that_begin_within_a_shared_prefix(n, held, kind):
+    """Nodes of earlier steps, in blocks that the requests share."""
+    ctx = [64 + 2, 64 + 1, 64, 128 + 10, 128]
+    trees = [random_tree(n + min(held, c), r, back=20) for r, c in enumerate(ctx)]
+    run(ctx, [n] * 5, trees, group_start=[0, 3, 5], prefix=[64, 128], **kind)
+
+
 def test_many_requests():
     rng = np.random.default_rng(0)
     R = 150
