@@ -89,7 +89,8 @@ struct AttnSplit {
 };
 
 // One list of work.  In the order (tile, head), each has piece_cost units without keys and then `one` or `two` for
-// each of its key tiles, which is the CTA's that has the first of them; of the W units CTA c takes [c W / P, (c + 1) W / P), P the number of CTAs or W / two if that is less (the rest idle).
+// each of its key tiles, which is the CTA's that has the first of them; of the W units CTA c takes [c W / P, (c + 1) W / P),
+// P the number of CTAs or W / two if that is less (the rest idle).
 struct AttnList {
   AttnTile *tiles;
   int *cum;          // [tiles + 1] units of one head before each tile

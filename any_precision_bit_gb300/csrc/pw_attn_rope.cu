@@ -75,9 +75,11 @@ __device__ __forceinline__ void load_pairs(const float *p, bool there, uint64_t 
 // pairs).  A warp takes kRopeHeads heads for each GL lanes at a time, all of q, or of k, or of v, so that it has one kind of
 // address and of work.
 //
-// Memory bounds it: 8205 tokens of 32/8 heads of 128 with norms, 202 MB, take 37.3 us (5.4 TB/s), 5003 of 16/16 heads of 96,
-// 92 MB, 17.6 us; a plain copy that moves 202 MB takes 37.2 us here, one that moves 92 MB 21.  The same by 2 heads at a time 39 and
-// 21 us, by 3 or 6 CTAs an SM 38 to 41 and 19; one token to a CTA 39 and 21, 5 or 8 tokens 42 and 18 to 20, where the last CTAs
+// Memory bounds it where heads are many: 8205 tokens of 32/8 heads of 128 with norms, 202 MB, take 37.3 us (5.4 TB/s;
+// interleaved 38.7), 30000 tokens 121 us (6.1 TB/s, 90 % of a copy's rate: the rest of the shorter kernel is its beginning and end),
+// 5003 of 16/16 heads of 96, 92 MB, 17.6 us.  With few heads most places of a chunk are empty, one key/value head in 16 or 32:
+// 8/1 heads of 128 and 16/2 of 64 2.5 to 3.0 TB/s; heads of 72 fill five lanes of eight, 28/4 of them 2.8 to 3.2.
+// The first two by 2 heads at a time 39 and 21 us, by 3 or 6 CTAs an SM 38 to 41 and 19; one token to a CTA 39 and 21, 5 or 8 tokens 42 and 18 to 20, where the last CTAs
 // run alone.  With the slot's, the positions' and the rows' loads behind each other it took 62 us.
 constexpr int kRopeHeads = 4, kRopeTokens = 4, kPairs = 64, kRopeCtas = 5;
 template <bool BF, int P, int GL, bool IL>

@@ -453,7 +453,8 @@ pw_status pw_kv_grow(pw_kv *kv, int64_t request, int64_t n_blocks, int32_t *ids_
 pw_status pw_kv_release(pw_kv *kv, int64_t request, int64_t *n_released);
 /* Request `child`, which holds no block (else PW_ERR_STATE), gets the first n_blocks blocks of `parent` (which holds as
  * many, else PW_ERR_INVALID): both hold them from then on, a block counts once in U, and it is free when its last holder has
- * returned it.  Costs no block.  A shared block is written to by nobody; pw_kv_unshare comes before that. */
+ * returned it.  Costs no block.  A shared block is written to by nobody; pw_kv_unshare comes before that.  PW_ERR_OOM as by
+ * pw_kv_release. */
 pw_status pw_kv_fork(pw_kv *kv, int64_t parent, int64_t child, int64_t n_blocks);
 /* Before request r writes to its block number `index` (PW_ERR_INVALID if it holds fewer): a block that others hold too is
  * replaced by a fresh one, granted as by pw_kv_grow (one block, PW_ERR_OOM).  *src is the block before and *dst the one from
@@ -464,7 +465,8 @@ pw_status pw_kv_unshare(pw_kv *kv, int64_t request, int64_t index, int32_t *src,
 pw_status pw_kv_trim(pw_kv *kv, int64_t request, int64_t n_keep, int64_t *n_released);
 /* Bring all blocks in use below the id `limit` (at least U, else PW_ERR_INVALID): those at or above it, ascending, go to
  * src[0 .. *n - 1], and the lowest free ids, which take their places in every request, to dst.  pw_kv_copy moves the
- * contents and renames the blocks in device tables.  With capacity < *n nothing is changed but *n (PW_ERR_INVALID). */
+ * contents and renames the blocks in device tables.  With capacity < *n nothing is changed but *n (PW_ERR_INVALID).
+ * PW_ERR_OOM as by pw_kv_release. */
 pw_status pw_kv_compact(pw_kv *kv, int64_t limit, int32_t *src, int32_t *dst, int64_t capacity, int64_t *n);
 /* Blocks request r holds and has announced (0 and 0 for an unknown request); either
  * pointer may be NULL.  The held count is the request's weight in pw_merge_requests. */
