@@ -72,21 +72,24 @@ bool leave(pw_kv *kv, int32_t id) {
 }
 
 // The blocks behind the first n_keep of a request's are returned; how many are free now.  Where memory for the free ids
-// runs out nothing changes: theirs is taken first, and the rest allocates nothing.
+// runs out nothing changes: those that were entered are taken out again, and what comes behind allocates nothing.
 bool give_back(pw_kv *kv, std::vector<int32_t> &ids, int64_t n_keep, int64_t *n) {
   if ((int64_t)ids.size() <= n_keep) return true;
-  std::set<int32_t> free_now;
+  const size_t keep = (size_t)n_keep;
+  size_t i = keep;
   try {
-    for (size_t i = (size_t)n_keep; i < ids.size(); ++i)
-      if (!kv->sharers.count(ids[i])) free_now.insert(ids[i]);
+    for (; i < ids.size(); ++i)
+      if (!kv->sharers.count(ids[i])) {
+        kv->freed.insert(ids[i]);
+        ++*n;
+      }
   } catch (...) {
+    while (i-- > keep) kv->freed.erase(ids[i]);
     return false;
   }
-  for (size_t i = (size_t)n_keep; i < ids.size(); ++i) leave(kv, ids[i]);
-  *n = (int64_t)free_now.size();
+  for (i = keep; i < ids.size(); ++i) leave(kv, ids[i]);
   kv->U -= *n;
-  kv->freed.merge(free_now);
-  ids.resize((size_t)n_keep);
+  ids.resize(keep);
   return true;
 }
 
