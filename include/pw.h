@@ -634,7 +634,8 @@ pw_status pw_attn_plan_tree(pw_attn *a, int plan, const pw_kv_step *step, int wi
  * < keep[r][n_keep[r] - 1], a path from a root, move to the tree's start: key and value of position s + keep[r][i] go to s + i, in all
  * layers' caches.  ctx_out [R] (NULL: not written): s + n_keep[r], the request's ctx_len in the next step; what lies
  * behind is free to be written again.  keep [R][keep_stride] and n_keep [R] are device memory.  A length, or a node that does not
- * ascend or lies outside the tree, is reported by pw_attn_check (PW_ERR_STATE); that request keeps what came before it.  Two
+ * ascend or lies outside the tree, is reported by pw_attn_check (PW_ERR_STATE); that request keeps what came before it.  (So is
+ * a block id outside the cache; the tokens that would move there or from there stay, and ctx_out counts them.)  Two
  * requests' trees share no block.  A cache that several layers share is moved once.  PW_ERR_STATE if a layer's cache is not
  * bound, or if two begin at one address with other strides. */
 pw_status pw_kv_keep(pw_attn *a, const pw_kv_step *step, const int32_t *tree_len, const int32_t *keep, int keep_stride,
