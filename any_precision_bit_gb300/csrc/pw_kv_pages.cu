@@ -13,7 +13,7 @@ constexpr int kKeepThreads = 128;
 // A CTA moves one request's tokens in one cache, a layer's keys or values.  Ids and addresses come once for the CTA; a thread then
 // has 16 bytes of a token and goes through the moves in ascending order, four loads ahead of their stores: a place lies
 // at or before where its token comes from, and so before everything that is loaded later.  96 requests' paths of up to 6
-// tokens in 32 caches, 23.5 MB moved, take 5.5 us: latency (ids, addresses, and two rounds of loads in turn).
+// tokens in 32 caches, 23.5 MB moved, take 5.5 to 5.9 us: latency (ids, addresses, and two rounds of loads in turn).
 __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_constant__ KeepArgs a,
                                                                const __grid_constant__ MoveCaches m) {
   __shared__ int from[PW_TREE_NODES], end;
